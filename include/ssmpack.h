@@ -45,10 +45,11 @@ typedef enum {
     SSMP_ERR_NULL = 1,        /* a required pointer is NULL */
     SSMP_ERR_SHAPE = 2,       /* a size is out of range, or sizes overflow */
     SSMP_ERR_CU_SEQLENS = 3,  /* cu_seqlens invalid (written to dev_err) */
-    SSMP_ERR_UNSUPPORTED = 4, /* dtype, d_state or conv width not supported */
+    SSMP_ERR_UNSUPPORTED = 4, /* dtype, d_state, conv width or head size not supported */
     SSMP_ERR_HIP = 5,         /* a kernel launch failed */
     SSMP_ERR_WORKSPACE = 6,   /* workspace missing or smaller than queried */
-    SSMP_ERR_TOO_LARGE = 7    /* needs more than the library's own scratch */
+    SSMP_ERR_TOO_LARGE = 7,   /* needs more than the library's own scratch */
+    SSMP_ERR_ALIGN = 8        /* a pointer is not a multiple of 16 bytes */
 } ssmp_status;
 
 typedef enum { SSMP_F32 = 0, SSMP_BF16 = 1 } ssmp_dtype;
@@ -60,7 +61,9 @@ const char *ssmp_status_string(int status);
  * or their meaning; 2 added the _ex scan entry points, 3 the host packer
  * varlen_pack_plan, 4 the scan and conv entry points with sequence states,
  * 5 the scan entry points with a checkpoint interval, 6 the forward scan
- * without allocation). */
+ * without allocation). qk_norm_pack_* and gated_delta_pack_* were added
+ * beside version 6: they change nothing in it, and a caller that may meet a
+ * library without them looks their symbols up. */
 int ssmp_abi_version(void);
 
 /*
@@ -356,6 +359,130 @@ int selective_scan_pack_fwd_noalloc(const void *u, const void *delta, const floa
                                     int32_t dtype, const float *delta_bias, int32_t delta_softplus,
                                     float gate_floor, const int32_t *cu_seqlens, int32_t nseq,
                                     const float *initial_state, float *final_state, void *stream);
+
+/* Norms of qk_norm_pack. */
+enum ssmp_norm {
+    SSMP_NORM_RMS = 0,  /* r = (mean_d x_d^2 + eps)^(-1/2) */
+    SSMP_NORM_L2 = 1    /* r = (sum_d x_d^2 + eps)^(-1/2) */
+};
+
+/*
+ * qk_norm_pack_fwd / qk_norm_pack_bwd — the norms of the query and the key
+ * heads of a packed batch, with the position rotation in the same pass:
+ *   y = R(pos[t]) (x r w),  r by `norm` over the head's D components
+ * R turns pairs of the head's first `rot` components: component i with
+ * i + rot/2 (interleaved = 0), or 2i with 2i + 1 (interleaved = 1), by the
+ * angle pos[t] * inv_freq[i], the product formed in 64 bits. Components from
+ * rot on are not turned. Positions are taken as they are (any int32): those of
+ * varlen_pack_indices start anew with each sequence; a caller that continues
+ * a sequence adds what precedes it.
+ *   q (T, Hq, D), k (T, Hk, D) dtype; Hq or Hk may be 0 (its pointers are
+ *                              then not read)
+ *   wq, wk    fp32 (D), nullable (ones)
+ *   pos       int32 (T); inv_freq fp32 (rot/2); both unused when rot = 0
+ *   yq, yk    as q, k, out; may be the same buffers as q, k
+ *   dyq, dyk  the gradients of yq, yk; dq, dk out, may be the same buffers as
+ *             dyq, dyk. q and k are the forward's inputs.
+ *   dwq, dwk  fp32 (D) out, nullable; must be NULL where the weight is.
+ *             Their sums over tokens and heads are deterministic.
+ * The backward's workspace, qk_norm_pack_bwd_workspace_bytes(T, Hq, Hk, D)
+ * bytes, is used only when dwq or dwk is given.
+ * Supports D a multiple of 8 up to 512, rot a multiple of 16 (of 2 when
+ * interleaved) up to D. Activation pointers must be multiples of 16 bytes.
+ * A row of zeros with eps = 0 gives NaN, as the formula does.
+ * Errors: SSMP_ERR_SHAPE, SSMP_ERR_UNSUPPORTED, SSMP_ERR_NULL, SSMP_ERR_ALIGN,
+ * SSMP_ERR_WORKSPACE.
+ */
+int qk_norm_pack_fwd(const void *q, const void *k, const float *wq, const float *wk, const int32_t *pos,
+                     const float *inv_freq, void *yq, void *yk, int64_t T, int32_t Hq, int32_t Hk,
+                     int32_t D, int32_t rot, int32_t dtype, int32_t norm, float eps, int32_t interleaved,
+                     void *stream);
+size_t qk_norm_pack_bwd_workspace_bytes(int64_t T, int32_t Hq, int32_t Hk, int32_t D);
+int qk_norm_pack_bwd(const void *q, const void *k, const float *wq, const float *wk, const int32_t *pos,
+                     const float *inv_freq, const void *dyq, const void *dyk, void *dq, void *dk,
+                     float *dwq, float *dwk, void *workspace, size_t workspace_bytes, int64_t T,
+                     int32_t Hq, int32_t Hk, int32_t D, int32_t rot, int32_t dtype, int32_t norm,
+                     float eps, int32_t interleaved, void *stream);
+
+/*
+ * gated_delta_pack_fwd — the gated delta rule over packed sequences, the
+ * state reset (or taken from initial_state) at the start of each. Per value
+ * head h with key head h / (Hv / Hk), a_t = exp(g_t):
+ *   e_t = v_t - (a_t S_{t-1})^T k_t
+ *   S_t = a_t S_{t-1} + beta_t k_t e_t^T          (S: Dk x Dv)
+ *   out_t = scale * S_t^T q_t
+ *   q, k     (T, Hk, Dk) dtype; as given (no norm is applied here)
+ *   v, out   (T, Hv, Dv) dtype
+ *   g, beta  fp32 (T, Hv); g is the log of the decay (-infinity: a reset)
+ *   cu_seqlens  device int32 [nseq+1]: non-decreasing, cu[0] = 0; cu[nseq] may
+ *            be less than T, and tokens from it on are neither read nor
+ *            written. Any other content gives meaningless values, but no
+ *            access outside the buffers.
+ *   initial_state  fp32 (nseq, Hv, Dk, Dv), nullable (zero)
+ *   final_state    fp32 (nseq, Hv, Dk, Dv) out, nullable
+ *   saved    nullable; with it the forward keeps what gated_delta_pack_bwd
+ *            reads, gated_delta_pack_saved_bytes(T, nseq, Hk, Hv, Dk, Dv) bytes
+ *            (fp32: the state that enters every chunk of 64 tokens, and the
+ *            errors e): the only memory between the two calls
+ *   scratch  used during the call only,
+ *            gated_delta_pack_fwd_scratch_bytes(T, nseq, Hk, Hv, Dk, Dv, dtype)
+ * States, and everything that enters them, are fp32 whatever the dtype.
+ * Results are deterministic. Within a sequence, a NaN or an infinity of a
+ * token may reach outputs up to 63 tokens before it (they share a chunk);
+ * other sequences are not touched.
+ * Supports Dk a multiple of 8 up to 128, Dv a multiple of 8, Hv a multiple
+ * of Hk. Pointers other than g, beta, cu_seqlens must be multiples of 16 bytes.
+ * Buffers must not overlap.
+ * Errors: SSMP_ERR_SHAPE, SSMP_ERR_UNSUPPORTED, SSMP_ERR_NULL, SSMP_ERR_ALIGN,
+ * SSMP_ERR_WORKSPACE. The size queries return 0 for arguments out of range.
+ */
+size_t gated_delta_pack_saved_bytes(int64_t T, int32_t nseq, int32_t Hk, int32_t Hv, int32_t Dk, int32_t Dv);
+size_t gated_delta_pack_fwd_scratch_bytes(int64_t T, int32_t nseq, int32_t Hk, int32_t Hv, int32_t Dk,
+                                          int32_t Dv, int32_t dtype);
+int gated_delta_pack_fwd(const void *q, const void *k, const void *v, const float *g, const float *beta,
+                         const int32_t *cu_seqlens, int32_t nseq, void *out, int64_t T, int32_t Hk,
+                         int32_t Hv, int32_t Dk, int32_t Dv, int32_t dtype, float scale,
+                         const float *initial_state, float *final_state, void *saved, size_t saved_bytes,
+                         void *scratch, size_t scratch_bytes, void *stream);
+
+/*
+ * gated_delta_pack_bwd — gradients of gated_delta_pack_fwd given dout, from
+ * what the forward kept in `saved` (same inputs, untouched since).
+ *   dfinal_state    fp32 (nseq, Hv, Dk, Dv), nullable (zero)
+ *   dinitial_state  fp32 (nseq, Hv, Dk, Dv) out, nullable
+ *   dq, dk (T, Hk, Dk) dtype out, summed over the value heads of a key head;
+ *   dv (T, Hv, Dv) dtype out; dg, dbeta fp32 (T, Hv) out
+ *   scratch  gated_delta_pack_bwd_scratch_bytes(T, nseq, Hk, Hv, Dk, Dv, dtype)
+ * Other arguments, conditions and errors as gated_delta_pack_fwd.
+ */
+size_t gated_delta_pack_bwd_scratch_bytes(int64_t T, int32_t nseq, int32_t Hk, int32_t Hv, int32_t Dk,
+                                          int32_t Dv, int32_t dtype);
+int gated_delta_pack_bwd(const void *q, const void *k, const float *g, const float *beta,
+                         const int32_t *cu_seqlens, int32_t nseq, const void *dout, int64_t T, int32_t Hk,
+                         int32_t Hv, int32_t Dk, int32_t Dv, int32_t dtype, float scale,
+                         const float *dfinal_state, float *dinitial_state, void *dq, void *dk, void *dv,
+                         float *dg, float *dbeta, const void *saved, size_t saved_bytes, void *scratch,
+                         size_t scratch_bytes, void *stream);
+
+/*
+ * gated_delta_pack_step — one new token for each of B rows of a serving batch,
+ * on states in a pool, updated in place (a workspace-free form of
+ * gated_delta_pack_fwd for sequences of one token).
+ *   q, k (B, Hk, Dk), v, out (B, Hv, Dv) dtype; g, beta fp32 (B, Hv)
+ *   state  fp32 (nslots, Hv, Dk, Dv), read and written: the states of the
+ *          slots that are named, no others
+ *   slots  device int32 [B], nullable (row b uses slot b): the state of each
+ *          row. Rows that name the same slot are applied in their order. A row
+ *          whose slot is outside [0, nslots) is skipped: its out is left as
+ *          it was.
+ * Supports Dk a multiple of 8 up to 128, Dv a multiple of 8. Allocates and
+ * needs nothing. Errors: SSMP_ERR_SHAPE (also B > nslots without slots),
+ * SSMP_ERR_UNSUPPORTED, SSMP_ERR_NULL, SSMP_ERR_ALIGN.
+ */
+int gated_delta_pack_step(const void *q, const void *k, const void *v, const float *g, const float *beta,
+                          float *state, const int32_t *slots, void *out, int32_t B, int32_t nslots,
+                          int32_t Hk, int32_t Hv, int32_t Dk, int32_t Dv, int32_t dtype, float scale,
+                          void *stream);
 
 /* Packing strategies of varlen_pack_plan. */
 enum ssmp_pack_strategy {

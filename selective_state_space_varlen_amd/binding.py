@@ -21,7 +21,9 @@ LIB_PATH = os.path.join(_HERE, "libssmpack.so")
 
 SSMP_F32, SSMP_BF16 = 0, 1
 SSMP_PACK_SEQUENTIAL, SSMP_PACK_LOCAL_GREEDY = 0, 1
+SSMP_NORM_RMS, SSMP_NORM_L2 = 0, 1
 
+_c_f32 = ctypes.c_float
 _c_i32, _c_i64, _c_sz, _c_vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_void_p
 
 _SIGNATURES = {
@@ -76,6 +78,17 @@ _SIGNATURES = {
     "conv1d_pack_bwd_states": (ctypes.c_int, [_c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_sz,
                                               _c_i64, _c_i32, _c_i32, _c_i32, _c_i32, _c_vp, _c_i32, _c_vp, _c_vp,
                                               _c_vp, _c_vp]),
+    "qk_norm_pack_fwd": (ctypes.c_int, [_c_vp] * 8 + [_c_i64] + [_c_i32] * 6 + [_c_f32, _c_i32, _c_vp]),
+    "qk_norm_pack_bwd_workspace_bytes": (_c_sz, [_c_i64, _c_i32, _c_i32, _c_i32]),
+    "qk_norm_pack_bwd": (ctypes.c_int, [_c_vp] * 13 + [_c_sz, _c_i64] + [_c_i32] * 6 + [_c_f32, _c_i32, _c_vp]),
+    "gated_delta_pack_saved_bytes": (_c_sz, [_c_i64] + [_c_i32] * 5),
+    "gated_delta_pack_fwd_scratch_bytes": (_c_sz, [_c_i64] + [_c_i32] * 6),
+    "gated_delta_pack_fwd": (ctypes.c_int, [_c_vp] * 6 + [_c_i32, _c_vp, _c_i64] + [_c_i32] * 5
+                             + [_c_f32, _c_vp, _c_vp, _c_vp, _c_sz, _c_vp, _c_sz, _c_vp]),
+    "gated_delta_pack_bwd_scratch_bytes": (_c_sz, [_c_i64] + [_c_i32] * 6),
+    "gated_delta_pack_bwd": (ctypes.c_int, [_c_vp] * 5 + [_c_i32, _c_vp, _c_i64] + [_c_i32] * 5
+                             + [_c_f32] + [_c_vp] * 8 + [_c_sz, _c_vp, _c_sz, _c_vp]),
+    "gated_delta_pack_step": (ctypes.c_int, [_c_vp] * 8 + [_c_i32] * 7 + [_c_f32, _c_vp]),
     "varlen_pack_plan": (ctypes.c_int, [_c_vp, _c_i32, _c_i32, _c_i32, _c_i32, _c_vp, _c_vp, _c_vp, _c_vp,
                                         _c_vp, _c_vp]),
 }
@@ -558,3 +571,188 @@ def selective_scan_pack_fwd_noalloc(u, delta, A, B, C, Dskip, z, pos, out: Optio
           _ptr(z), _ptr(pos), _ptr(o), T, D, N, _dtype_code(u), _ptr(delta_bias), int(bool(delta_softplus)),
           float(gate_floor), _ptr(cu_seqlens), nseq, _ptr(initial_state), _ptr(fs), _stream(u))
     return o, fs
+
+
+# ---------------------------------------------------------------------------
+# Head norms and the gated delta rule
+def _call_on(dev, name: str, *args):
+    """_call with the tensors' device current: their stream takes no launch
+    from another one."""
+    with torch.cuda.device(dev):
+        _call(name, *args)
+
+
+def _heads(t: torch.Tensor, name: str):
+    if t.dim() != 3:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected (tokens, heads, size)")
+    return t.shape
+
+
+def _qk_norm_args(q, k, wq, wk, pos, inv_freq, interleaved):
+    """Checks of what the forward and the backward share; (T, Hq, Hk, D, rot)."""
+    T, Hq, D = _heads(q, "q")
+    Hk = _heads(k, "k")[1]
+    dev = q.device
+    _check(q, "q"); _check(k, "k", (T, Hk, D), q.dtype, dev)
+    _check(wq, "wq", (D,), torch.float32, dev); _check(wk, "wk", (D,), torch.float32, dev)
+    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
+    if rot:
+        if pos is None:
+            raise ValueError("the rotation (inv_freq) needs pos")
+        _check(inv_freq, "inv_freq", (rot // 2,), torch.float32, dev); _check(pos, "pos", (T,), torch.int32, dev)
+    return T, Hq, Hk, D, rot
+
+
+def qk_norm_pack_fwd(q: torch.Tensor, k: torch.Tensor, wq: Optional[torch.Tensor] = None,
+                     wk: Optional[torch.Tensor] = None, pos: Optional[torch.Tensor] = None,
+                     inv_freq: Optional[torch.Tensor] = None, norm: int = SSMP_NORM_L2, eps: float = 1e-6,
+                     interleaved: bool = False, out: Optional[tuple] = None):
+    """Norms of the heads of q (T, Hq, D) and k (T, Hk, D), times the weights
+    (D,), the first 2 * len(inv_freq) components turned by pos * inv_freq.
+    Returns (yq, yk); `out` may supply them (q and k themselves included)."""
+    T, Hq, Hk, D, rot = _qk_norm_args(q, k, wq, wk, pos, inv_freq, interleaved)
+    yq, yk = (torch.empty_like(q), torch.empty_like(k)) if out is None else out
+    _check(yq, "yq", q.shape, q.dtype, q.device); _check(yk, "yk", k.shape, q.dtype, q.device)
+    _call_on(q.device, "qk_norm_pack_fwd", _ptr(q), _ptr(k), _ptr(wq), _ptr(wk), _ptr(pos), _ptr(inv_freq), _ptr(yq),
+             _ptr(yk), T, Hq, Hk, D, rot, _dtype_code(q), int(norm), float(eps), int(bool(interleaved)), _stream(q))
+    return yq, yk
+
+
+def qk_norm_pack_bwd_workspace_bytes(T: int, Hq: int, Hk: int, D: int) -> int:
+    return int(load().qk_norm_pack_bwd_workspace_bytes(T, Hq, Hk, D))
+
+
+def qk_norm_pack_bwd(q: torch.Tensor, k: torch.Tensor, dyq: torch.Tensor, dyk: torch.Tensor,
+                     wq: Optional[torch.Tensor] = None, wk: Optional[torch.Tensor] = None,
+                     pos: Optional[torch.Tensor] = None, inv_freq: Optional[torch.Tensor] = None,
+                     norm: int = SSMP_NORM_L2, eps: float = 1e-6, interleaved: bool = False,
+                     workspace: Optional[torch.Tensor] = None, out: Optional[dict] = None) -> dict:
+    """Gradients of sum(dyq * yq) + sum(dyk * yk): {"dq", "dk", "dwq", "dwk"}
+    (the last two None without weights). q and k are the forward's inputs."""
+    T, Hq, Hk, D, rot = _qk_norm_args(q, k, wq, wk, pos, inv_freq, interleaved)
+    dev = q.device
+    _check(dyq, "dyq", q.shape, q.dtype, dev); _check(dyk, "dyk", k.shape, q.dtype, dev)
+    if out is None:
+        new = lambda w: None if w is None else torch.empty_like(w)  # noqa: E731
+        out = {"dq": torch.empty_like(q), "dk": torch.empty_like(k), "dwq": new(wq), "dwk": new(wk)}
+    dq, dk, dwq, dwk = (out[n] for n in ("dq", "dk", "dwq", "dwk"))
+    _check(dq, "dq", q.shape, q.dtype, dev); _check(dk, "dk", k.shape, q.dtype, dev)
+    _check(dwq, "dwq", (D,), torch.float32, dev); _check(dwk, "dwk", (D,), torch.float32, dev)
+    if workspace is None and (dwq is not None or dwk is not None):
+        workspace = torch.empty(max(qk_norm_pack_bwd_workspace_bytes(T, Hq, Hk, D), 1), dtype=torch.uint8, device=dev)
+    _check(workspace, "workspace", device=dev)
+    _call_on(dev, "qk_norm_pack_bwd", _ptr(q), _ptr(k), _ptr(wq), _ptr(wk), _ptr(pos), _ptr(inv_freq), _ptr(dyq),
+             _ptr(dyk), _ptr(dq), _ptr(dk), _ptr(dwq), _ptr(dwk), _ptr(workspace), _nbytes(workspace), T, Hq, Hk, D,
+             rot, _dtype_code(q), int(norm), float(eps), int(bool(interleaved)), _stream(q))
+    return {"dq": dq, "dk": dk, "dwq": dwq, "dwk": dwk}
+
+
+def _delta_sizes(q, k, heads_v, g, beta):
+    """Checks of what the delta-rule calls share; (tokens, Hk, Hv, Dk, Dv).
+    heads_v: the tensor that has v's shape, with its name."""
+    t, name = heads_v
+    T, Hk, Dk = _heads(q, "q")
+    _, Hv, Dv = _heads(t, name)
+    dev = q.device
+    _check(q, "q"); _check(k, "k", (T, Hk, Dk), q.dtype, dev); _check(t, name, (T, Hv, Dv), q.dtype, dev)
+    _check(g, "g", (T, Hv), torch.float32, dev); _check(beta, "beta", (T, Hv), torch.float32, dev)
+    return T, Hk, Hv, Dk, Dv
+
+
+def gated_delta_pack_saved_bytes(T: int, nseq: int, Hk: int, Hv: int, Dk: int, Dv: int) -> int:
+    return int(load().gated_delta_pack_saved_bytes(T, nseq, Hk, Hv, Dk, Dv))
+
+
+def gated_delta_pack_fwd_scratch_bytes(T: int, nseq: int, Hk: int, Hv: int, Dk: int, Dv: int,
+                                       dtype: torch.dtype) -> int:
+    code = SSMP_BF16 if dtype == torch.bfloat16 else SSMP_F32
+    return int(load().gated_delta_pack_fwd_scratch_bytes(T, nseq, Hk, Hv, Dk, Dv, code))
+
+
+def gated_delta_pack_bwd_scratch_bytes(T: int, nseq: int, Hk: int, Hv: int, Dk: int, Dv: int,
+                                       dtype: torch.dtype) -> int:
+    code = SSMP_BF16 if dtype == torch.bfloat16 else SSMP_F32
+    return int(load().gated_delta_pack_bwd_scratch_bytes(T, nseq, Hk, Hv, Dk, Dv, code))
+
+
+def gated_delta_pack_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor,
+                         cu_seqlens: torch.Tensor, scale: Optional[float] = None,
+                         initial_state: Optional[torch.Tensor] = None, final_state=False, save: bool = False,
+                         saved: Optional[torch.Tensor] = None, scratch: Optional[torch.Tensor] = None,
+                         out: Optional[torch.Tensor] = None):
+    """The gated delta rule over the sequences of cu_seqlens: q, k (T, Hk, Dk),
+    v (T, Hv, Dv), log decay g and beta fp32 (T, Hv), states fp32
+    (nseq, Hv, Dk, Dv). scale defaults to Dk ** -0.5. Returns (out, saved or
+    None, final_state or None); save=True (or a `saved` buffer) keeps what the
+    backward reads. The scratch is free again once the call's work on the
+    current stream is done."""
+    T, Hk, Hv, Dk, Dv = _delta_sizes(q, k, (v, "v"), g, beta)
+    dev = q.device
+    nseq = _nseq(cu_seqlens, dev)
+    fs = _out_or_new(final_state, (nseq, Hv, Dk, Dv), torch.float32, dev)
+    for name, t in (("initial_state", initial_state), ("final_state", fs)):
+        _check(t, name, (nseq, Hv, Dk, Dv), torch.float32, dev)
+    if saved is None and save:
+        saved = torch.empty(max(gated_delta_pack_saved_bytes(T, nseq, Hk, Hv, Dk, Dv), 1), dtype=torch.uint8,
+                            device=dev)
+    _check(saved, "saved", device=dev)
+    scratch = _scratch(scratch, gated_delta_pack_fwd_scratch_bytes(T, nseq, Hk, Hv, Dk, Dv, q.dtype), dev)
+    o = torch.empty_like(v) if out is None else out
+    _check(o, "out", (T, Hv, Dv), q.dtype, dev)
+    _call_on(dev, "gated_delta_pack_fwd", _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(cu_seqlens), nseq,
+             _ptr(o), T, Hk, Hv, Dk, Dv, _dtype_code(q), float(Dk ** -0.5 if scale is None else scale),
+             _ptr(initial_state), _ptr(fs), _ptr(saved), _nbytes(saved), _ptr(scratch), _nbytes(scratch), _stream(q))
+    return o, saved, fs
+
+
+def gated_delta_pack_bwd(q: torch.Tensor, k: torch.Tensor, g: torch.Tensor, beta: torch.Tensor,
+                         cu_seqlens: torch.Tensor, dout: torch.Tensor, saved: torch.Tensor,
+                         scale: Optional[float] = None, dfinal_state: Optional[torch.Tensor] = None,
+                         dinitial_state=False, scratch: Optional[torch.Tensor] = None,
+                         out: Optional[dict] = None) -> dict:
+    """Gradients of sum(dout * out) (+ sum(dfinal_state * final_state)) from
+    what the forward saved: {"dq", "dk", "dv", "dg", "dbeta",
+    "dinitial_state"} (the last None unless asked for: True, or an output
+    tensor). `out` may supply the first five."""
+    T, Hk, Hv, Dk, Dv = _delta_sizes(q, k, (dout, "dout"), g, beta)
+    dev = q.device
+    nseq = _nseq(cu_seqlens, dev)
+    di = _out_or_new(dinitial_state, (nseq, Hv, Dk, Dv), torch.float32, dev)
+    for name, t in (("dfinal_state", dfinal_state), ("dinitial_state", di)):
+        _check(t, name, (nseq, Hv, Dk, Dv), torch.float32, dev)
+    _check(saved, "saved", device=dev)
+    scratch = _scratch(scratch, gated_delta_pack_bwd_scratch_bytes(T, nseq, Hk, Hv, Dk, Dv, q.dtype), dev)
+    if out is None:
+        out = {"dq": torch.empty_like(q), "dk": torch.empty_like(k), "dv": torch.empty_like(dout),
+               "dg": torch.empty_like(g), "dbeta": torch.empty_like(beta)}
+    dq, dk, dv, dg, dbeta = (out[n] for n in ("dq", "dk", "dv", "dg", "dbeta"))
+    _check(dq, "dq", q.shape, q.dtype, dev); _check(dk, "dk", q.shape, q.dtype, dev)
+    _check(dv, "dv", dout.shape, q.dtype, dev); _check(dg, "dg", g.shape, torch.float32, dev)
+    _check(dbeta, "dbeta", g.shape, torch.float32, dev)
+    _call_on(dev, "gated_delta_pack_bwd", _ptr(q), _ptr(k), _ptr(g), _ptr(beta), _ptr(cu_seqlens), nseq, _ptr(dout),
+             T, Hk, Hv, Dk, Dv, _dtype_code(q), float(Dk ** -0.5 if scale is None else scale), _ptr(dfinal_state),
+             _ptr(di), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dg), _ptr(dbeta), _ptr(saved), _nbytes(saved),
+             _ptr(scratch), _nbytes(scratch), _stream(q))
+    return {"dq": dq, "dk": dk, "dv": dv, "dg": dg, "dbeta": dbeta, "dinitial_state": di}
+
+
+def gated_delta_pack_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor,
+                          state: torch.Tensor, slots: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                          out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """One token for each row: q, k (B, Hk, Dk), v (B, Hv, Dv), g, beta
+    (B, Hv); state fp32 (nslots, Hv, Dk, Dv) is updated in place at slots
+    (int32 (B); None: row b uses slot b). Returns out (B, Hv, Dv); a row whose
+    slot lies outside the pool keeps what `out` held (zeros, if it is made here)."""
+    B, Hk, Hv, Dk, Dv = _delta_sizes(q, k, (v, "v"), g, beta)
+    dev = q.device
+    if state.dim() != 4:
+        raise ValueError(f"state has shape {tuple(state.shape)}, expected (slots, heads, Dk, Dv)")
+    _check(state, "state", (state.shape[0], Hv, Dk, Dv), torch.float32, dev)
+    _check(slots, "slots", (B,), torch.int32, dev)
+    if out is None:
+        out = torch.empty_like(v) if slots is None else torch.zeros_like(v)
+    _check(out, "out", (B, Hv, Dv), q.dtype, dev)
+    _call_on(dev, "gated_delta_pack_step", _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(state), _ptr(slots),
+             _ptr(out), B, state.shape[0], Hk, Hv, Dk, Dv, _dtype_code(q),
+             float(Dk ** -0.5 if scale is None else scale), _stream(q))
+    return out

@@ -1,0 +1,331 @@
+// Shared by the delta-rule and head-norm kernels: chunk numbering, operands
+// of the matrix instructions, and the small 64-token matrices of a chunk.
+#pragma once
+
+#include "common.h"
+
+namespace ssmp {
+
+// Host-side: whether every pointer is a multiple of 16 (wide loads want that).
+template <typename... P>
+inline bool aligned16(P... p) {
+    return ((reinterpret_cast<uintptr_t>(p) % 16 == 0) && ...);
+}
+
+// ---------------------------------------------------------------------------
+// Chunks. A chunk is up to 64 tokens of one sequence, counted from its first
+// token. Sequence s has its chunks in the slots floor(cu[s] / 64) + s + c,
+// c = 0 .. ceil(len / 64) - 1: since floor((x + len) / 64) + 1 >= floor(x / 64)
+// + ceil(len / 64), the slots of two sequences never meet, and T / 64 + nseq
+// slots are enough for any division of T tokens, so no prefix sum over the
+// sequences is needed. cu_seqlens is clamped to [0, T], so that no content of
+// it leads outside the tensors or slots.
+constexpr int kC = 64;
+
+__host__ __device__ inline int64_t delta_slots(int64_t T, int32_t nseq) { return T / kC + nseq; }
+
+struct Seq {
+    int64_t start;
+    int32_t len;
+    int64_t slot0;
+};
+__device__ __forceinline__ Seq seq_at(const int32_t* __restrict__ cu, int s, int64_t T) {
+    int64_t a = cu[s], b = cu[s + 1];
+    a = a < 0 ? 0 : (a > T ? T : a);
+    b = b < a ? a : (b > T ? T : b);
+    return {a, (int32_t)(b - a), a / kC + s};
+}
+
+// The chunk in a slot: false where the slot holds none. Called by whole waves;
+// 64 boundaries are looked at in one step, so 2 steps find a sequence among 4096.
+struct Chunk {
+    int64_t start;  // its first token
+    int32_t n;      // tokens
+    bool last;      // of its sequence
+    int32_t seq;
+};
+__device__ __forceinline__ bool chunk_at(const int32_t* __restrict__ cu, int32_t nseq, int64_t T, int64_t slot,
+                                         Chunk& c) {
+    int lo = 0, hi = nseq;
+    const int lane = lane_id();
+    while (hi - lo > 1) {
+        const int step = (hi - lo + 63) / 64, i = lo + lane * step;
+        bool below = false;
+        if (i < hi) {
+            int64_t a = cu[i];
+            a = a < 0 ? 0 : (a > T ? T : a);
+            below = a / kC + i <= slot;
+        }
+        int n = __popcll(__ballot(below));
+        n = n < 1 ? 1 : n;
+        lo += (n - 1) * step;
+        hi = lo + step < hi ? lo + step : hi;
+    }
+    lo = __builtin_amdgcn_readfirstlane(lo);
+    const Seq q = seq_at(cu, lo, T);
+    const int64_t at = (slot - q.slot0) * kC;
+    if (at < 0 || at >= q.len) return false;
+    c.start = q.start + at;
+    c.n = q.len - at < kC ? (int32_t)(q.len - at) : kC;
+    c.last = at + kC >= q.len;
+    c.seq = lo;
+    return true;
+}
+
+// ---------------------------------------------------------------------------
+// Matrix products. States, the chunk's inverse and every value derived from
+// them are fp32; v_mfma_f32_16x16x32_bf16 multiplies bf16. An fp32 operand is
+// split into bf16 planes x = x0 + x1 + x2 (8 bits each, together fp32's 24),
+// and a product adds the plane products down to the bits that count: with
+// three planes a side 6 of 9 (error 2^-24 relative to the factors), with one
+// side exactly bf16 3. That is 2.7 to 5.3 times the rate of the fp32 matrix
+// instruction, whose rate is a sixteenth of bf16's.
+//
+// Operands: lane l of A holds row l % 16, elements k = 8 (l / 16) .. + 7; of B
+// column l % 16, the same k; the result D has column l % 16, rows 4 (l / 16)
+// .. + 3. Both operands want their k contiguous, so in memory A is [m][k] and
+// B is [n][k].
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+template <int NP>
+struct Frag {
+    bf16x8 p[NP];
+};
+
+// d += a b, the terms i + j < LIM of the plane products, small ones first
+template <int LIM, int NA, int NB>
+__device__ __forceinline__ void mma(f32x4& d, const Frag<NA>& a, const Frag<NB>& b) {
+#pragma unroll
+    for (int s = LIM - 1; s >= 0; --s)
+#pragma unroll
+        for (int i = 0; i < NA; ++i)
+            if (s - i >= 0 && s - i < NB) d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.p[i], b.p[s - i], d, 0, 0, 0);
+}
+
+// v as bf16 planes: v = p[0] + p[1] + p[2] up to fp32's last bit
+template <int NP>
+__device__ __forceinline__ void split(float v, __bf16 (&p)[NP]) {
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+        p[i] = (__bf16)v;
+        if (i + 1 < NP) v -= (float)p[i];
+    }
+}
+template <int NP>
+__device__ __forceinline__ Frag<NP> split8(const float (&v)[8]) {
+    Frag<NP> f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        __bf16 p[NP];
+        split<NP>(v[e], p);
+#pragma unroll
+        for (int i = 0; i < NP; ++i) f.p[i][e] = p[i];
+    }
+    return f;
+}
+
+// planes that hold an input of this type exactly
+template <typename T>
+constexpr int kExact = std::is_same<T, float>::value ? 3 : 1;
+
+// 8 contiguous elements at p as an operand (zeros where off)
+__device__ __forceinline__ Frag<1> load_frag(const uint16_t* p, bool on) {
+    u32x4 w = {0, 0, 0, 0};
+    if (on) w = *reinterpret_cast<const u32x4*>(p);
+    return {{__builtin_bit_cast(bf16x8, w)}};
+}
+__device__ __forceinline__ void load8(const float* p, bool on, float (&v)[8]) {
+    f32x4 a = {0, 0, 0, 0}, b = {0, 0, 0, 0};
+    if (on) {
+        a = reinterpret_cast<const f32x4*>(p)[0];
+        b = reinterpret_cast<const f32x4*>(p)[1];
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        v[e] = a[e];
+        v[4 + e] = b[e];
+    }
+}
+__device__ __forceinline__ Frag<3> load_frag(const float* p, bool on) {
+    float v[8];
+    load8(p, on, v);
+    return split8<3>(v);
+}
+
+// Planes: [plane][row][ld] bf16; in LDS ld = k length + 8 so that the 16
+// rows of a 16-byte read fall into different banks.
+template <int NP>
+__device__ __forceinline__ Frag<NP> plane_frag(const __bf16* base, int plane, int ld, int row, int k) {
+    Frag<NP> f;
+#pragma unroll
+    for (int i = 0; i < NP; ++i)
+        f.p[i] = __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4*>(base + i * plane + row * ld + k));
+    return f;
+}
+// four values along k (a lane's rows of a result) into the planes
+template <int NP>
+__device__ __forceinline__ void lds_put4(__bf16* base, int plane, int ld, int row, int k, const float (&v)[4]) {
+    __bf16 p[4][NP];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) split<NP>(v[e], p[e]);
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+        typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+        const bf16x4 w = {p[0][i], p[1][i], p[2][i], p[3][i]};
+        *reinterpret_cast<bf16x4*>(base + i * plane + row * ld + k) = w;
+    }
+}
+
+// four contiguous elements
+__device__ __forceinline__ void load4(const uint16_t* p, float (&v)[4]) {
+    const u32x2 w = *reinterpret_cast<const u32x2*>(p);
+    v[0] = bf16_to_f32(w[0]);
+    v[1] = bf16_hi_to_f32(w[0]);
+    v[2] = bf16_to_f32(w[1]);
+    v[3] = bf16_hi_to_f32(w[1]);
+}
+__device__ __forceinline__ void load4(const float* p, float (&v)[4]) {
+    const f32x4 w = *reinterpret_cast<const f32x4*>(p);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = w[e];
+}
+
+// ---------------------------------------------------------------------------
+// Decays of a chunk: G = running sum of g in 64 bits (32-bit sums would lose
+// the small steps behind a large one), lane l holding token l. g below
+// kGMin is taken as kGMin: e^g is zero all the same, and a full reset
+// (g = -infinity) does not turn G's differences into NaN.
+constexpr double kGMin = -4096.0;
+__device__ __forceinline__ double chunk_decay_sum(const float* __restrict__ g, int64_t start, int n, int H, int h) {
+    const int lane = lane_id();
+    double v = 0.0;
+    if (lane < n) {
+        v = (double)g[(size_t)(start + lane) * H + h];
+        v = v < kGMin ? kGMin : v;
+    }
+#pragma unroll
+    for (int m = 1; m < kC; m <<= 1) {
+        const double o = __shfl_up(v, m);
+        if (lane >= m) v += o;
+    }
+    return v;
+}
+
+// The inverse of I + A for strictly lower triangular A (64 x 64, fp32 in LDS
+// with row length kLdA): X = (I + A)^-1 in X. By forward substitution in the
+// four 16 x 16 blocks of the diagonal (lane = block and column), then
+//   X_ba = -X_bb (A_ba X_aa)
+// for the blocks between them, twice, with the fp32 matrix instruction, whose
+// k order is free: a result's rows 4 (l / 16) + r serve as the next product's
+// k without leaving their registers. Called by workgroups of 256.
+constexpr int kLdA = 68;
+__device__ __forceinline__ f32x4 mma16(const float* a, const f32x4& b, f32x4 d) {
+    // d += A b, A 16 x 16 at a (row length kLdA), b as a result of this layout
+    const int l = lane_id();
+    const f32x4 r = *reinterpret_cast<const f32x4*>(a + (l & 15) * kLdA + (l >> 4) * 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) d = __builtin_amdgcn_mfma_f32_16x16x4f32(r[i], b[i], d, 0, 0, 0);
+    return d;
+}
+__device__ __forceinline__ f32x4 tile16(const float* x) {
+    const int l = lane_id();
+    f32x4 r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = x[((l >> 4) * 4 + i) * kLdA + (l & 15)];
+    return r;
+}
+__device__ __forceinline__ void put_tile16(float* x, const f32x4& v) {
+    const int l = lane_id();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[((l >> 4) * 4 + i) * kLdA + (l & 15)] = v[i];
+}
+__device__ __forceinline__ void chunk_inverse(const float* A, float* X) {
+    const int tid = threadIdx.x, wave = tid >> 6, l = tid & 63;
+    // zero the blocks above the diagonal's
+    for (int i = tid; i < kC * kC; i += 256) {
+        const int r = i >> 6, c = i & 63;
+        if ((c >> 4) > (r >> 4)) X[r * kLdA + c] = 0.0f;
+    }
+    if (wave == 0) {
+        const int at = (l >> 4) * 16, c = l & 15;
+        float x[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            float s = i == c ? 1.0f : 0.0f;
+#pragma unroll
+            for (int j = 0; j < i; ++j) s = fmaf(-A[(at + i) * kLdA + at + j], x[j], s);
+            x[i] = s;
+            X[(at + i) * kLdA + at + c] = s;
+        }
+    }
+    __syncthreads();
+    if (wave < 2) {  // blocks (1, 0) and (3, 2)
+        const int a = wave * 32, b = a + 16;
+        const f32x4 zero = {0, 0, 0, 0};
+        const f32x4 y = mma16(A + b * kLdA + a, tile16(X + a * kLdA + a), zero);
+        const f32x4 z = mma16(X + b * kLdA + b, y, zero);
+        put_tile16(X + b * kLdA + a, -z);
+    }
+    __syncthreads();
+    if (wave < 2) {  // the lower left 32 x 32, one column of blocks a wave
+        const int n = wave * 16;
+        f32x4 y[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const f32x4 b = tile16(X + k * 16 * kLdA + n);
+#pragma unroll
+            for (int m = 0; m < 2; ++m) y[m] = mma16(A + (32 + m * 16) * kLdA + k * 16, b, y[m]);
+        }
+        const f32x4 zero = {0, 0, 0, 0};
+        f32x4 z0 = mma16(X + 32 * kLdA + 32, y[0], zero);
+        f32x4 z1 = mma16(X + 48 * kLdA + 32, y[0], zero);
+        z1 = mma16(X + 48 * kLdA + 48, y[1], z1);
+        put_tile16(X + 32 * kLdA + n, -z0);
+        put_tile16(X + 48 * kLdA + n, -z1);
+    }
+    __syncthreads();
+}
+
+// ---------------------------------------------------------------------------
+// Sizes and buffers
+constexpr int kMaxDk = 128;
+constexpr int kCols = 32;  // state columns a workgroup of the chunk chains takes
+
+inline int delta_dkp(int Dk) { return Dk <= 64 ? 64 : 128; }
+inline size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+
+struct DeltaArgs {
+    const void *q, *k, *v, *dout;
+    const float *g, *beta;
+    const int32_t* cu;
+    void *out, *dq, *dk, *dv;
+    float *dg, *dbeta;
+    const float *h0, *dhT;
+    float *hT, *dh0;
+    int64_t T;
+    int32_t nseq, Hk, Hv, Dk, Dv;
+    float scale;
+    // kept from the forward to the backward, by slot and value head
+    float *S0, *E;   // the state that enters the chunk (Dk, Dv); the errors (64, Dv)
+    // scratch, by slot and head
+    float* dec;      // e^{G_i} and e^{G_last - G_i}: (2, 64)
+    __bf16* inv;     // the chunk's inverse: (planes, 64, 64)
+    __bf16* att;     // the decayed products of q and k: (planes, 64, 64)
+    void *kt, *qt;   // keys and queries, transposed: (Dk padded, 64)
+    float *dS1, *dU; // backward: gradients of the state that leaves the chunk, and of U
+};
+
+inline int delta_check(int64_t T, int32_t nseq, int32_t Hk, int32_t Hv, int32_t Dk, int32_t Dv, int32_t dtype) {
+    if (T < 0 || T >= (int64_t(1) << 31) || nseq < 1 || Hk < 1 || Hv < 1 || Dk < 1 || Dv < 1) return SSMP_ERR_SHAPE;
+    if (Hv % Hk || Hv > 65535 || Dv > 65536 || nseq > (1 << 24)) return SSMP_ERR_SHAPE;
+    if (T * Hv * (int64_t)(Dv > Dk ? Dv : Dk) >= (int64_t(1) << 40)) return SSMP_ERR_SHAPE;
+    if ((int64_t)nseq * Hv * ((Dv + kCols - 1) / kCols) >= (int64_t(1) << 31)) return SSMP_ERR_SHAPE;
+    if (dtype != SSMP_F32 && dtype != SSMP_BF16) return SSMP_ERR_UNSUPPORTED;
+    if (Dk % 8 || Dv % 8 || Dk > kMaxDk) return SSMP_ERR_UNSUPPORTED;
+    return SSMP_OK;
+}
+
+}  // namespace ssmp

@@ -68,10 +68,11 @@ extern "C" const char* ssmp_status_string(int status) {
         case SSMP_ERR_NULL: return "a required pointer is NULL";
         case SSMP_ERR_SHAPE: return "a size is out of range or sizes overflow";
         case SSMP_ERR_CU_SEQLENS: return "cu_seqlens is invalid (cu[0] != 0, decreasing, or cu[nseq] != T)";
-        case SSMP_ERR_UNSUPPORTED: return "dtype, d_state or conv width not supported";
+        case SSMP_ERR_UNSUPPORTED: return "dtype, d_state, conv width or head size not supported";
         case SSMP_ERR_HIP: return "a HIP kernel launch failed";
         case SSMP_ERR_WORKSPACE: return "workspace missing or too small";
         case SSMP_ERR_TOO_LARGE: return "the problem needs more scratch than the library's own buffer holds";
+        case SSMP_ERR_ALIGN: return "a pointer is not a multiple of 16 bytes";
         default: return "unknown status";
     }
 }

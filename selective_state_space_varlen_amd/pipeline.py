@@ -1,8 +1,14 @@
-"""The sequence-wise part of one Mamba-1 block on a packed batch, as a chain
-of library calls (no arithmetic here):
+"""The sequence-wise part of one block on a packed batch, as a chain of library
+calls (no arithmetic here). A Mamba-1 block:
 
   forward:  varlen_pack_indices -> conv1d_pack_fwd (SiLU) -> selective_scan_pack_fwd
   backward: selective_scan_pack_bwd -> conv1d_pack_bwd
+
+A gated delta rule block (delta_forward, delta_backward), whose queries, keys
+and values each pass a conv and whose query and key heads are normalised:
+
+  forward:  varlen_pack_indices -> conv1d_pack_fwd (SiLU, three) -> qk_norm_pack_fwd -> gated_delta_pack_fwd
+  backward: gated_delta_pack_bwd -> qk_norm_pack_bwd -> conv1d_pack_bwd (three)
 
 Shanghai AI Lab article on packed variable-length Mamba-1 training
 (gitcode.csdn.net/69d8cc1b54b52172bc6872cb.html), section "Mamba block中的步骤":
@@ -85,3 +91,72 @@ def backward(x: torch.Tensor, w: torch.Tensor, b: Optional[torch.Tensor], delta:
                                          dconv_final=dfs.get("conv"), dconv_initial=True)
     g.update({"dx": dx, "dw": dw, "db": db, "dinitial_states": {"ssm": g.pop("dinitial_state"), "conv": dci}})
     return g
+
+
+def delta_forward(x: tuple, w: tuple, b: Optional[tuple], g: torch.Tensor, beta: torch.Tensor,
+                  cu_seqlens: torch.Tensor, Hk: int, Hv: int, pos: Optional[torch.Tensor] = None,
+                  scale: Optional[float] = None, norm: int = _b.SSMP_NORM_L2, eps: float = 1e-6,
+                  norm_weights: tuple = (None, None), inv_freq: Optional[torch.Tensor] = None,
+                  initial_states: Optional[dict] = None, final_states: bool = False, save: bool = True) -> dict:
+    """x = (xq (T, Hk * Dk), xk (T, Hk * Dk), xv (T, Hv * Dv)) with conv weights w
+    and biases b (None, or a tuple) in the same order; g, beta fp32 (T, Hv).
+    Returns {'out' (T, Hv, Dv), ...}; keep it for delta_backward (save=True).
+
+    Sequences continued from an earlier pack take initial_states = {'delta':
+    (nseq, Hv, Dk, Dv) fp32, 'conv': three contexts (nseq, W-1, .)} (either may
+    be None: zeros); with final_states=True, or with initial states, the result
+    also holds 'final_states' in the same form. pos then still counts inside
+    the pack; a rotation (inv_freq) that goes on is given its own pos."""
+    T = x[0].shape[0]
+    starts, _, _ = _b.varlen_pack_indices(cu_seqlens, T, heads=False, dev_err=False)
+    carry = initial_states is not None or final_states
+    st = initial_states or {}
+    u, cf = [], []
+    for i in range(3):
+        bias = None if b is None else b[i]
+        if carry:
+            ctx = st.get("conv")
+            y, f = _b.conv1d_pack_fwd(x[i], w[i], bias, starts, silu=True, cu_seqlens=cu_seqlens,
+                                      conv_initial=None if ctx is None else ctx[i], conv_final=True)
+            cf.append(f)
+        else:
+            y = _b.conv1d_pack_fwd(x[i], w[i], bias, starts, silu=True)
+        u.append(y)
+    q, k, v = u[0].view(T, Hk, -1), u[1].view(T, Hk, -1), u[2].view(T, Hv, -1)
+    nk = dict(wq=norm_weights[0], wk=norm_weights[1], pos=starts if pos is None else pos, inv_freq=inv_freq,
+              norm=norm, eps=eps)
+    qn, kn = _b.qk_norm_pack_fwd(q, k, **nk)
+    out, saved, hT = _b.gated_delta_pack_fwd(qn, kn, v, g, beta, cu_seqlens, scale=scale,
+                                             initial_state=st.get("delta"), final_state=carry, save=save)
+    res = {"out": out, "starts": starts, "q": q, "k": k, "qn": qn, "kn": kn, "saved": saved, "norm": nk,
+           "scale": scale, "cu_seqlens": cu_seqlens, "carry": carry, "initial_states": st}
+    if carry:
+        res["final_states"] = {"delta": hT, "conv": tuple(cf)}
+    return res
+
+
+def delta_backward(x: tuple, w: tuple, b: Optional[tuple], g: torch.Tensor, beta: torch.Tensor, fwd: dict,
+                   dout: torch.Tensor, dfinal_states: Optional[dict] = None) -> dict:
+    """Gradients of sum(dout * out) (+ sum(dfinal * final) for carried states):
+    'dx', 'dw', 'db' (tuples in the order q, k, v; db None without biases),
+    'dg', 'dbeta', 'dwq', 'dwk' (the norm weights'), and with carried states
+    'dinitial_states', to hand to the earlier pack's backward."""
+    cu, carry, st, dfs = fwd["cu_seqlens"], fwd["carry"], fwd["initial_states"], dfinal_states or {}
+    G = _b.gated_delta_pack_bwd(fwd["qn"], fwd["kn"], g, beta, cu, dout, fwd["saved"], scale=fwd["scale"],
+                                dfinal_state=dfs.get("delta"), dinitial_state=carry)
+    N = _b.qk_norm_pack_bwd(fwd["q"], fwd["k"], G["dq"], G["dk"], **fwd["norm"])
+    dx, dw, db, dci = [], [], [], []
+    for i, du in enumerate((N["dq"], N["dk"], G["dv"])):
+        bias = None if b is None else b[i]
+        ctx, dctx = st.get("conv"), dfs.get("conv")
+        kw = dict(cu_seqlens=cu, conv_initial=None if ctx is None else ctx[i],
+                  dconv_final=None if dctx is None else dctx[i], dconv_initial=True) if carry else {}
+        r = _b.conv1d_pack_bwd(x[i], w[i], bias, fwd["starts"], du.view(x[i].shape), silu=True,
+                               want_db=bias is not None, **kw)
+        for to, t in zip((dx, dw, db, dci), r):
+            to.append(t)
+    res = {"dx": tuple(dx), "dw": tuple(dw), "db": None if b is None else tuple(db), "dg": G["dg"],
+           "dbeta": G["dbeta"], "dwq": N["dwq"], "dwk": N["dwk"]}
+    if carry:
+        res["dinitial_states"] = {"delta": G["dinitial_state"], "conv": tuple(dci)}
+    return res
