@@ -23,350 +23,330 @@ namespace ssmp {
 
 // As k_delta_chain, from the last chunk to the first.
 template <typename T, int DKP>
-__global__ __launch_bounds__(256) void k_delta_chain_bwd(DeltaArgs a) {
+__global__ __launch_bounds__(256, NWG<T>) void k_delta_chain_bwd(DeltaArgs a) {
     constexpr int NX = kExact<T>;
-    constexpr int MT = DKP / 64;
-    constexpr int LS = DKP + 8, LT = kC + 8;
-    constexpr int PS = kCols * LS, PT = kCols * LT;
-    __shared__ alignas(16) __bf16 St[3 * PS];   // dS', [column][row]
-    __shared__ alignas(16) __bf16 Ot[NX * PT];  // dOut, [column][token]
-    __shared__ alignas(16) __bf16 Gt[3 * PT];   // e^G scale dOut
-    __shared__ alignas(16) __bf16 Yt[3 * PT];   // Y
-    __shared__ alignas(16) __bf16 Wt[3 * PT];   // -e^G dE
-    const int ncb = (a.Dv + kCols - 1) / kCols;
-    const int cb = blockIdx.x % ncb, hv = (blockIdx.x / ncb) % a.Hv, seq = blockIdx.x / (ncb * a.Hv);
-    const int hk = hv / (a.Hv / a.Hk);
-    const int tid = threadIdx.x, wave = tid >> 6, l = tid & 63, l16 = l & 15, l4 = l >> 4;
+    constexpr int MT = DKP / 16;
+    using Loads = ChainLoads<T, DKP, 1, 2, 3>;
+    __shared__ alignas(16) typename Loads::Tiles lds;
+    const int ncb = (a.Dv + kCols - 1) / kCols, group = a.Hv / a.Hk;
+    const Spread sp = spread(blockIdx.x, ncb * group);
+    if (sp.group >= (int64_t)a.nseq * a.Hk) return;
+    const int seq = (int)(sp.group / a.Hk), hk = (int)(sp.group % a.Hk);
+    const int hv = hk * group + sp.member / ncb, cb = sp.member % ncb;
+    const int wave = wave_id(), l = lane_id(), l16 = l & 15, l4 = l >> 4;
+    const int col = cb * kCols + wave * 16 + l16;
+    const bool busy = cb * kCols + wave * 16 < a.Dv;
     const Seq q = seq_at(a.cu, seq, a.T);
     const int chunks = (q.len + kC - 1) / kC;
-    f32x4 S[MT][2];
-    const auto state_row = [&](int m, int r) { return wave * (DKP / 4) + m * 16 + l4 * 4 + r; };
-    const auto state_col = [&](int n) { return cb * kCols + n * 16 + l16; };
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int d = state_row(m, r), e = state_col(n);
-                S[m][n][r] = a.dhT && d < a.Dk && e < a.Dv
-                                 ? a.dhT[(((size_t)seq * a.Hv + hv) * a.Dk + d) * a.Dv + e] : 0.0f;
-            }
+    const Column cs = column_of<float>(1, a.Dv, col), cv = column_of<T>(a.Hv, a.Dv, col);
+    const size_t state = ((size_t)seq * a.Hv + hv) * a.Dk * a.Dv;
+    f32x4 S[MT];
+    load_matrix(a.dhT ? a.dhT + state : nullptr, a.Dk, a.Dv, cs, S);
+    Loads next;
+    uint32_t onext[16];
+    if (chunks > 0) {
+        const int64_t start = q.start + (int64_t)(chunks - 1) * kC;
+        const int n = q.len - (chunks - 1) * kC;
+        next.load(a, q.slot0 + chunks - 1, start, n, hk, hv);
+        load_column<T>(a.dout, start, n, a.Hv, hv, a.Dv, cv, onext);
+    }
     for (int ch = chunks - 1; ch >= 0; --ch) {
         const int64_t slot = q.slot0 + ch, start = q.start + (int64_t)ch * kC;
-        const int cn = q.len - ch * kC < kC ? q.len - ch * kC : kC;
         const size_t sh = (size_t)slot * a.Hv + hv;
-        const float* const dec = a.dec + sh * 2 * kC;
+        __syncthreads();  // the last chunk's operands have been read
+        next.put(lds);
+        f32x4 o[4];
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int n = 0; n < 2; ++n) {
-                float v[4];
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    v[r] = S[m][n][r];
-                    const int d = state_row(m, r), e = state_col(n);
-                    if (d < a.Dk && e < a.Dv) a.dS1[(sh * a.Dk + d) * a.Dv + e] = v[r];
-                }
-                lds_put4<3>(St, PS, LS, n * 16 + l16, state_row(m, 0), v);
-            }
-        {  // the chunk's dOut: token tid / 4, 8 columns
-            const int i = tid >> 2, e = cb * kCols + (tid & 3) * 8;
-            const bool on = i < cn && e < a.Dv;
-            const auto f = load_frag(static_cast<const T*>(a.dout) + ((size_t)(start + i) * a.Hv + hv) * a.Dv + e, on);
-            const float w = dec[i] * a.scale;
-#pragma unroll
-            for (int x = 0; x < 8; ++x) {
-                const int at = ((tid & 3) * 8 + x) * LT + i;
-                float v = 0.0f;
-#pragma unroll
-                for (int p = NX - 1; p >= 0; --p) v += (float)f.p[p][x];
-                __bf16 g[3];
-                split<3>(v * w, g);
-#pragma unroll
-                for (int p = 0; p < NX; ++p) Ot[p * PT + at] = f.p[p][x];
-#pragma unroll
-                for (int p = 0; p < 3; ++p) Gt[p * PT + at] = g[p];
-            }
-        }
+        for (int i = 0; i < 16; ++i) o[i >> 2][i & 3] = Elt<T>::cvt(onext[i]);
         __syncthreads();
-        f32x4 y[2] = {}, x[2] = {};
-        const int i0 = wave * 16 + l16;
-        const size_t row = ((size_t)(start + i0) * a.Hk + hk) * a.Dk;
+        if (ch > 0) {
+            next.load(a, slot - 1, start - kC, kC, hk, hv);
+            load_column<T>(a.dout, start - kC, kC, a.Hv, hv, a.Dv, cv, onext);
+        }
+        if (!busy) continue;
+        store_matrix(a.dS1 + sh * a.Dk * a.Dv, a.Dk, a.Dv, cs, S);
+        f32x4 x[4] = {}, y[4] = {};  // K dS', scale P^T dOut
 #pragma unroll
         for (int s = 0; s < DKP / 32; ++s) {
-            const int k0 = s * 32 + l4 * 8;
-            const auto ka = load_frag(static_cast<const T*>(a.k) + row + k0, i0 < cn && k0 < a.Dk);
+            __builtin_amdgcn_sched_barrier(0);
+            const auto sb = split_tiles<3>(S[2 * s], S[2 * s + 1]);
 #pragma unroll
-            for (int n = 0; n < 2; ++n) mma<3>(x[n], ka, plane_frag<3>(St, PS, LS, n * 16 + l16, k0));
+            for (int m = 0; m < 4; ++m) mma<3>(x[m], lds.row_frag(0, m * 16 + l16, s * 4 + l4), sb);
         }
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            const int k0 = s * 32 + l4 * 8;
-            const auto pa = plane_frag<3>(a.att + sh * 3 * kC * kC, kC * kC, kC, i0, k0);
+            __builtin_amdgcn_sched_barrier(0);
+            const auto ob = split_tiles<NX>(o[2 * s], o[2 * s + 1]);
 #pragma unroll
-            for (int n = 0; n < 2; ++n) mma<3>(y[n], pa, plane_frag<NX>(Ot, PT, LT, n * 16 + l16, k0));
+            for (int m = 0; m < 2 + 2 * s; ++m)
+                mma<3>(y[m], tri_frag<3>(lds.att, (s ? 0 : 64) + m * 16 + l16, l4), ob);
         }
-        float eg[4], el[4], bt[4];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int i = wave * 16 + l4 * 4 + r;
-            eg[r] = dec[i];
-            el[r] = dec[kC + i];
-            bt[r] = i < cn ? a.beta[(size_t)(start + i) * a.Hv + hv] : 0.0f;
+        for (int m = 0; m < 4; ++m) {
+            const f32x4 el = *reinterpret_cast<const f32x4*>(lds.el + m * 16 + l4 * 4);
+            y[m] += el * x[m];
         }
-        const float ec = dec[kC - 1];
-#pragma unroll
-        for (int n = 0; n < 2; ++n) {
-            float v[4];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) v[r] = fmaf(el[r], x[n][r], y[n][r]);
-            lds_put4<3>(Yt, PT, LT, n * 16 + l16, wave * 16 + l4 * 4, v);
-        }
-        __syncthreads();
-        f32x4 u[2] = {};
+        f32x4 u[4] = {};
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            const int k0 = s * 32 + l4 * 8;
-            const auto ia = plane_frag<3>(a.inv + sh * 3 * kC * kC, kC * kC, kC, i0, k0);
+            __builtin_amdgcn_sched_barrier(0);
+            const auto yb = split_tiles<3>(y[2 * s], y[2 * s + 1]);
 #pragma unroll
-            for (int n = 0; n < 2; ++n) mma<3>(u[n], ia, plane_frag<3>(Yt, PT, LT, n * 16 + l16, k0));
+            for (int m = 0; m < 2 + 2 * s; ++m)
+                mma<3>(u[m], tri_frag<3>(lds.inv, (s ? 0 : 64) + m * 16 + l16, l4), yb);
         }
+        store_matrix(a.dU + sh * kC * a.Dv, kC, a.Dv, cs, u);
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
-            float w[4];
+        for (int m = 0; m < 4; ++m) {
+            const f32x4 be = *reinterpret_cast<const f32x4*>(lds.beta + m * 16 + l4 * 4);
+            const f32x4 eg = *reinterpret_cast<const f32x4*>(lds.eg + m * 16 + l4 * 4);
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                w[r] = -eg[r] * (bt[r] * u[n][r]);
-                const int i = wave * 16 + l4 * 4 + r, e = state_col(n);
-                if (e < a.Dv) a.dU[(sh * kC + i) * a.Dv + e] = u[n][r];
+                u[m][r] *= -eg[r] * be[r];         // -e^G dE
+                o[m][r] *= eg[r] * a.scale;        // e^G scale dOut
             }
-            lds_put4<3>(Wt, PT, LT, n * 16 + l16, wave * 16 + l4 * 4, w);
         }
-        __syncthreads();
-        const size_t tr = ((size_t)slot * a.Hk + hk) * DKP * kC;
+        const float ec = lds.eg[kC - 1];
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int n = 0; n < 2; ++n) S[m][n] *= ec;
+        for (int m = 0; m < MT; ++m) S[m] *= ec;
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            const int k0 = s * 32 + l4 * 8;
+            __builtin_amdgcn_sched_barrier(0);
+            const auto ob = split_tiles<3>(o[2 * s], o[2 * s + 1]);
+            const auto ub = split_tiles<3>(u[2 * s], u[2 * s + 1]);
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
-                const size_t at = tr + (wave * (DKP / 4) + m * 16 + l16) * kC + k0;
-                const auto ka = load_frag(static_cast<const T*>(a.kt) + at, true);
-                const auto qa = load_frag(static_cast<const T*>(a.qt) + at, true);
-#pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                    mma<3>(S[m][n], qa, plane_frag<3>(Gt, PT, LT, n * 16 + l16, k0));
-                    mma<3>(S[m][n], ka, plane_frag<3>(Wt, PT, LT, n * 16 + l16, k0));
-                }
+                mma<3>(S[m], lds.col_frag(1, m * 16 + l16, s * 4 + l4), ob);
+                mma<3>(S[m], lds.col_frag(0, m * 16 + l16, s * 4 + l4), ub);
             }
         }
-        __syncthreads();  // Gt and Wt have been read
     }
-    if (a.dh0) {
+    if (a.dh0 && busy) store_matrix(a.dh0 + state, a.Dk, a.Dv, cs, S);
+}
+
+// dq and dk of one column, from the tiles of 64 tokens
+template <typename T, typename F>
+__device__ __forceinline__ void store_qk_t(const DeltaArgs& a, const Chunk& c, int hk, int d, const f32x4 (&dq)[4], F dk) {
+    const int l4 = lane_id() >> 4;
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+    for (int m = 0; m < 4; ++m) {
+        const f32x4 k = dk(m);
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int d = state_row(m, r), e = state_col(n);
-                    if (d < a.Dk && e < a.Dv) a.dh0[(((size_t)seq * a.Hv + hv) * a.Dk + d) * a.Dv + e] = S[m][n][r];
-                }
+        for (int r = 0; r < 4; ++r) {
+            const int i = m * 16 + l4 * 4 + r;
+            if (i < c.n && d < a.Dk) {
+                const size_t o = ((size_t)(c.start + i) * a.Hk + hk) * a.Dk + d;
+                Elt<T>::st(static_cast<T*>(a.dq), o, dq[m][r]);
+                Elt<T>::st(static_cast<T*>(a.dk), o, k[r]);
+            }
+        }
     }
 }
 
 // One workgroup per (slot, key head), over the value heads of its group, whose
-// dq and dk it adds in registers. Wave w holds columns w DKP / 4 .. of dq and
-// dk for all 64 tokens, so its rows of S and dS' come straight from memory,
-// and rows 16 w .. of a^T and b^T.
-template <typename T, int DKP>
-__global__ __launch_bounds__(256, 1) void k_delta_grads(DeltaArgs a) {
+// dq and dk it adds in registers (GROUP; a head that has its keys to itself
+// needs no second set). Wave w of DKP / 16 holds columns 16 w .. of dq and dk
+// for all 64 tokens, so its rows of S and dS' come straight from memory, and
+// some of the tiles of a^T and b^T. The next 64 columns of dOut, E and dU are
+// under way in registers while the present ones are multiplied.
+template <typename T, int DKP, bool GROUP>
+__global__ __launch_bounds__(DKP * 4) void k_delta_grads(DeltaArgs a) {
     constexpr int NX = kExact<T>;
-    constexpr int NT = DKP / 64;  // 16-column tiles of dq and dk a wave holds
+    constexpr int kThreads = DKP * 4, kWaves = DKP / 16;
+    constexpr int SG = 512 / kThreads;    // 8-column units a thread stages
+    constexpr int TT = 16 / kWaves;       // tiles of a^T a wave holds: row tile w / (4 / TT)
     constexpr int LT = kC + 8, PT = kC * LT;
     // planes of dOut, dE and U (64 columns at a time, [token][column]), then of
     // a or -b and its transpose
     __shared__ alignas(16) __bf16 lds[(NX + 6) * PT];
     __shared__ double G[kC];
-    __shared__ float decay[2][kC], red[4][kC], ends[4];
+    __shared__ alignas(16) float decay[2][kC];
+    __shared__ float red[kWaves][kC], ends[kWaves];
     const int64_t slot = blockIdx.x;
-    const int hk = blockIdx.y;
+    const int hk = blockIdx.y, group = a.Hv / a.Hk;
     Chunk c;
     if (!chunk_at(a.cu, a.nseq, a.T, slot, c)) return;
-    const int tid = threadIdx.x, wave = tid >> 6, l = tid & 63, l16 = l & 15, l4 = l >> 4;
+    const int tid = threadIdx.x, wave = wave_id(), l = lane_id(), l16 = l & 15, l4 = l >> 4;
     __bf16* const Op = lds;
     __bf16* const Ep = lds + NX * PT;
     __bf16* const Up = Ep + 3 * PT;
     __bf16* const M = lds;
     __bf16* const Mt = lds + 3 * PT;
     const size_t tr = ((size_t)slot * a.Hk + hk) * DKP * kC;
-    f32x4 tq[4][NT] = {}, tk[4][NT] = {};
-    for (int hv = hk * (a.Hv / a.Hk); hv < (hk + 1) * (a.Hv / a.Hk); ++hv) {
+    const int d = wave * 16 + l16;                       // this lane's column of dq and dk
+    const int tj = wave / (4 / TT), ti0 = (wave % (4 / TT)) * TT;  // tiles (tj, ti0 + x) of a^T: rows j, columns i
+    f32x4 tq[GROUP ? 4 : 1], tk[GROUP ? 4 : 1];
+    if constexpr (GROUP)
+#pragma unroll
+        for (int m = 0; m < 4; ++m) tq[m] = tk[m] = f32x4{0, 0, 0, 0};
+    for (int hv = hk * group; hv < (hk + 1) * group; ++hv) {
         const size_t sh = (size_t)slot * a.Hv + hv;
-        __syncthreads();
+        Unit<T> fo[SG];
+        Unit<float> fE[SG], fU[SG];
+        float beta[SG], db[SG];
+        const auto stage_load = [&](int v0) {
+#pragma unroll
+            for (int x = 0; x < SG; ++x) {
+                const int u = tid + x * kThreads, t = u >> 3, e = (u & 7) * 8;
+                const bool on = v0 + e < a.Dv;
+                const size_t ws = (sh * kC + t) * a.Dv + v0 + e;
+                fo[x].load(static_cast<const T*>(a.dout) + ((size_t)(c.start + t) * a.Hv + hv) * a.Dv + v0 + e,
+                           on && t < c.n);
+                fE[x].load(a.E + ws, on);
+                fU[x].load(a.dU + ws, on);
+            }
+        };
+        stage_load(0);
+#pragma unroll
+        for (int x = 0; x < SG; ++x) {
+            const int t = (tid + x * kThreads) >> 3;
+            beta[x] = t < c.n ? a.beta[(size_t)(c.start + t) * a.Hv + hv] : 0.0f;
+            db[x] = 0.0f;
+        }
+        __syncthreads();  // the last head's sums have been read
         if (wave == 0) {
             G[l] = chunk_decay_sum(a.g, c.start, c.n, a.Hv, hv);
             decay[0][l] = a.dec[sh * 2 * kC + l];
             decay[1][l] = a.dec[sh * 2 * kC + kC + l];
         }
-        f32x4 dq[4][NT] = {}, dr[4][NT] = {}, dw[4][NT] = {};  // dq, dk read, dk write
-        f32x4 at[4] = {}, bt[4] = {};                          // rows j of tile `wave`, columns i of tile n
-        float sd = 0.0f;                                       // <dS', S>
-        const int ti = tid >> 2;
-        const float beta = ti < c.n ? a.beta[(size_t)(c.start + ti) * a.Hv + hv] : 0.0f;
-        float db = 0.0f;
+        f32x4 dq[4] = {}, dr[4] = {}, dw[4] = {};  // dq, dk read, dk write
+        f32x4 at[TT] = {}, bt[TT] = {};
+        float sd = 0.0f;                           // <dS', S>
         for (int v0 = 0; v0 < a.Dv; v0 += 64) {
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {  // token tid / 4, 16 columns
-                const int e = (tid & 3) * 16 + x * 8;
-                const bool on = v0 + e < a.Dv;
-                const size_t io = ((size_t)(c.start + ti) * a.Hv + hv) * a.Dv + v0 + e;
-                const size_t ws = (sh * kC + ti) * a.Dv + v0 + e;
-                const auto fo = load_frag(static_cast<const T*>(a.dout) + io, on && ti < c.n);
-                float E[8], dU[8];
-                load8(a.E + ws, on, E);
-                load8(a.dU + ws, on, dU);
-#pragma unroll
-                for (int p = 0; p < 8; ++p) {
-                    db = fmaf(dU[p], E[p], db);
-                    E[p] *= beta;
-                    dU[p] *= beta;
-                    if (on && ti < c.n) Elt<T>::st(static_cast<T*>(a.dv), io + p, dU[p]);
-                }
-                const auto fe = split8<3>(dU), fu = split8<3>(E);
-                const int o = ti * LT + e;
-#pragma unroll
-                for (int p = 0; p < NX; ++p) *reinterpret_cast<bf16x8*>(Op + p * PT + o) = fo.p[p];
-#pragma unroll
-                for (int p = 0; p < 3; ++p) {
-                    *reinterpret_cast<bf16x8*>(Ep + p * PT + o) = fe.p[p];
-                    *reinterpret_cast<bf16x8*>(Up + p * PT + o) = fu.p[p];
-                }
-            }
-            __syncthreads();
+            Unit<float> s0[2], s1[2];              // this lane's row of S and dS'
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
                 const int k0 = s * 32 + l4 * 8;
-                Frag<3> sb[NT], db1[NT];
+                const bool on = d < a.Dk && v0 + k0 < a.Dv;
+                const size_t o = (sh * a.Dk + d) * a.Dv + v0 + k0;
+                s0[s].load(a.S0 + o, on);
+                s1[s].load(a.dS1 + o, on);
+            }
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    const int d = wave * (DKP / 4) + n * 16 + l16;
-                    const bool on = d < a.Dk && v0 + k0 < a.Dv;
-                    const size_t o = (sh * a.Dk + d) * a.Dv + v0 + k0;
-                    float s0[8], s1[8];
-                    load8(a.S0 + o, on, s0);
-                    load8(a.dS1 + o, on, s1);
+            for (int x = 0; x < SG; ++x) {
+                const int u = tid + x * kThreads, t = u >> 3, e = (u & 7) * 8;
+                float E[8], dU[8];
+                T dv[8];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) sd = fmaf(s0[e], s1[e], sd);
-                    sb[n] = split8<3>(s0);
-                    db1[n] = split8<3>(s1);
+                for (int p = 0; p < 8; ++p) {
+                    E[p] = fE[x].w[p >> 2][p & 3];
+                    dU[p] = fU[x].w[p >> 2][p & 3];
+                    db[x] = fmaf(dU[p], E[p], db[x]);
+                    E[p] *= beta[x];
+                    dU[p] *= beta[x];
+                    Elt<T>::st(dv, p, dU[p]);
                 }
-                const auto uw = plane_frag<3>(Up, PT, LT, wave * 16 + l16, k0);
+                if (v0 + e < a.Dv && t < c.n)
+                    put8(static_cast<T*>(a.dv) + ((size_t)(c.start + t) * a.Hv + hv) * a.Dv + v0 + e, dv);
+                const auto po = unit_planes(fo[x]);
+                const auto pe = split8<3>(dU), pu = split8<3>(E);
+                const int o = t * LT + e;
+#pragma unroll
+                for (int p = 0; p < NX; ++p) *reinterpret_cast<bf16x8*>(Op + p * PT + o) = po.p[p];
+#pragma unroll
+                for (int p = 0; p < 3; ++p) {
+                    *reinterpret_cast<bf16x8*>(Ep + p * PT + o) = pe.p[p];
+                    *reinterpret_cast<bf16x8*>(Up + p * PT + o) = pu.p[p];
+                }
+            }
+            __syncthreads();
+            if (v0 + 64 < a.Dv) stage_load(v0 + 64);
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const int k0 = s * 32 + l4 * 8;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) sd = fmaf(s0[s].w[e >> 2][e & 3], s1[s].w[e >> 2][e & 3], sd);
+                const auto sb = unit_planes(s0[s]), db1 = unit_planes(s1[s]);
 #pragma unroll
                 for (int m = 0; m < 4; ++m) {
-                    const auto fo = plane_frag<NX>(Op, PT, LT, m * 16 + l16, k0);
-                    const auto fe = plane_frag<3>(Ep, PT, LT, m * 16 + l16, k0);
-                    const auto fu = plane_frag<3>(Up, PT, LT, m * 16 + l16, k0);
+                    mma<3>(dq[m], plane_frag<NX>(Op, PT, LT, m * 16 + l16, k0), sb);
+                    mma<3>(dr[m], plane_frag<3>(Ep, PT, LT, m * 16 + l16, k0), sb);
+                    mma<3>(dw[m], plane_frag<3>(Up, PT, LT, m * 16 + l16, k0), db1);
+                }
+                const auto uw = plane_frag<3>(Up, PT, LT, tj * 16 + l16, k0);
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        mma<3>(dq[m][n], fo, sb[n]);
-                        mma<3>(dr[m][n], fe, sb[n]);
-                        mma<3>(dw[m][n], fu, db1[n]);
+                for (int x = 0; x < TT; ++x) {
+                    const int i = ti0 + x;
+                    if (i >= tj) {  // below the diagonal of a and b
+                        mma<3>(at[x], uw, plane_frag<NX>(Op, PT, LT, i * 16 + l16, k0));
+                        mma<3>(bt[x], uw, plane_frag<3>(Ep, PT, LT, i * 16 + l16, k0));
                     }
-                    mma<3>(at[m], uw, fo);
-                    mma<3>(bt[m], uw, fe);
                 }
             }
             __syncthreads();
         }
-        db += __shfl_xor(db, 1);
-        db += __shfl_xor(db, 2);
-        if ((tid & 3) == 0 && ti < c.n) a.dbeta[(size_t)(c.start + ti) * a.Hv + hv] = db;
+#pragma unroll
+        for (int x = 0; x < SG; ++x) {
+            const int u = tid + x * kThreads, t = u >> 3;
+            float s = db[x];
+            s += __shfl_xor(s, 1);
+            s += __shfl_xor(s, 2);
+            s += __shfl_xor(s, 4);
+            if ((u & 7) == 0 && t < c.n) a.dbeta[(size_t)(c.start + t) * a.Hv + hv] = s;
+        }
         float end = decay[0][kC - 1] * sd;
+        float kv[4][4], qv[4][4];  // this lane's column of K and Q: tokens 16 m + 4 l4 + r
 #pragma unroll
-        for (int m = 0; m < 4; ++m)
+        for (int m = 0; m < 4; ++m) {
+            const int i = m * 16 + l4 * 4;
+            load4(static_cast<const T*>(a.kt) + tr + d * kC + kplace(i), kv[m]);
+            load4(static_cast<const T*>(a.qt) + tr + d * kC + kplace(i), qv[m]);
+            const f32x4 eg = *reinterpret_cast<const f32x4*>(&decay[0][i]);
+            const f32x4 el = *reinterpret_cast<const f32x4*>(&decay[1][i]);
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const int i = m * 16 + l4 * 4, d = wave * (DKP / 4) + n * 16 + l16;
-                float kv[4];
-                load4(static_cast<const T*>(a.kt) + tr + d * kC + i, kv);
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    dq[m][n][r] *= decay[0][i + r] * a.scale;
-                    dr[m][n][r] *= -decay[0][i + r];
-                    dw[m][n][r] *= decay[1][i + r];
-                    end = fmaf(kv[r], dw[m][n][r], end);
-                }
+            for (int r = 0; r < 4; ++r) {
+                dq[m][r] *= eg[r] * a.scale;
+                dr[m][r] *= -eg[r];
+                dw[m][r] *= el[r];
+                end = fmaf(kv[m][r], dw[m][r], end);
             }
-        for (int x = 0; x < 2; ++x) {  // a, then -b
+        }
 #pragma unroll
-            for (int n = 0; n < 4; ++n) {
-                const int i = n * 16 + l16, j = wave * 16 + l4 * 4;
+        for (int pass = 0; pass < 2; ++pass) {  // a, then -b
+#pragma unroll
+            for (int x = 0; x < TT; ++x) {
+                const int i = (ti0 + x) * 16 + l16, j = tj * 16 + l4 * 4;
                 float v[4];
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    const bool on = x ? i > j + r : i >= j + r;
+                    const bool on = pass ? i > j + r : i >= j + r;
                     const float w = on ? expf((float)(G[i] - G[j + r])) : 0.0f;
-                    v[r] = on ? (x ? -w * bt[n][r] : w * a.scale * at[n][r]) : 0.0f;
+                    v[r] = on ? (pass ? -w * bt[x][r] : w * a.scale * at[x][r]) : 0.0f;
                     __bf16 p[3];
                     split<3>(v[r], p);
 #pragma unroll
-                    for (int y = 0; y < 3; ++y) Mt[y * PT + (j + r) * LT + i] = p[y];
+                    for (int y = 0; y < 3; ++y) Mt[y * PT + (j + r) * LT + kplace(i)] = p[y];
                 }
-                lds_put4<3>(M, PT, LT, i, j, v);
+                lds_put4<3>(M, PT, LT, i, kplace(j), v);
             }
             __syncthreads();
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
                 const int k0 = s * 32 + l4 * 8;
+                const size_t o = tr + d * kC + k0;
+                const auto kb = load_frag(static_cast<const T*>(a.kt) + o, true);
+                const auto qb = load_frag(static_cast<const T*>(a.qt) + o, true);
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    const size_t o = tr + (wave * (DKP / 4) + n * 16 + l16) * kC + k0;
-                    const auto kb = load_frag(static_cast<const T*>(a.kt) + o, true);
-                    const auto qb = load_frag(static_cast<const T*>(a.qt) + o, true);
-#pragma unroll
-                    for (int m = 0; m < 4; ++m) {
-                        const auto fm = plane_frag<3>(M, PT, LT, m * 16 + l16, k0);
-                        const auto ft = plane_frag<3>(Mt, PT, LT, m * 16 + l16, k0);
-                        if (x == 0) {
-                            mma<3>(dq[m][n], fm, kb);
-                            mma<3>(dw[m][n], ft, qb);
-                        } else {
-                            mma<3>(dr[m][n], fm, kb);
-                            mma<3>(dw[m][n], ft, kb);
-                        }
-                    }
+                for (int m = 0; m < 4; ++m) {
+                    if (m >= 2 * s) mma<3>(pass ? dr[m] : dq[m], plane_frag<3>(M, PT, LT, m * 16 + l16, k0), kb);
+                    if (m < 2 + 2 * s) mma<3>(dw[m], plane_frag<3>(Mt, PT, LT, m * 16 + l16, k0), pass ? kb : qb);
                 }
             }
             __syncthreads();
         }
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
-            float s[4] = {};
             const int i = m * 16 + l4 * 4;
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const int d = wave * (DKP / 4) + n * 16 + l16;
-                float kv[4], qv[4];
-                load4(static_cast<const T*>(a.kt) + tr + d * kC + i, kv);
-                load4(static_cast<const T*>(a.qt) + tr + d * kC + i, qv);
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    s[r] = fmaf(qv[r], dq[m][n][r], s[r]);
-                    s[r] = fmaf(kv[r], dr[m][n][r] - dw[m][n][r], s[r]);
-                }
-                tq[m][n] += dq[m][n];
-                tk[m][n] += dr[m][n] + dw[m][n];
-            }
-#pragma unroll
             for (int r = 0; r < 4; ++r) {
+                float s = fmaf(qv[m][r], dq[m][r], kv[m][r] * (dr[m][r] - dw[m][r]));
 #pragma unroll
-                for (int x = 1; x < 16; x <<= 1) s[r] += __shfl_xor(s[r], x);
-                if (l16 == 0) red[wave][i + r] = s[r];
+                for (int x = 1; x < 16; x <<= 1) s += __shfl_xor(s, x);
+                if (l16 == 0) red[wave][i + r] = s;
+            }
+            if constexpr (GROUP) {
+                tq[m] += dq[m];
+                tk[m] += dr[m] + dw[m];
             }
         }
 #pragma unroll
@@ -374,8 +354,13 @@ __global__ __launch_bounds__(256, 1) void k_delta_grads(DeltaArgs a) {
         if (l == 0) ends[wave] = end;
         __syncthreads();
         if (wave == 0) {
-            double s = (double)red[0][l] + red[1][l] + red[2][l] + red[3][l];
-            if (l == kC - 1) s += (double)ends[0] + ends[1] + ends[2] + ends[3];
+            double s = 0.0, e = 0.0;
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) {
+                s += (double)red[w][l];
+                e += (double)ends[w];
+            }
+            if (l == kC - 1) s += e;
 #pragma unroll
             for (int x = 1; x < kC; x <<= 1) {
                 const double o = __shfl_down(s, x);
@@ -383,36 +368,25 @@ __global__ __launch_bounds__(256, 1) void k_delta_grads(DeltaArgs a) {
             }
             if (l < c.n) a.dg[(size_t)(c.start + l) * a.Hv + hv] = (float)s;
         }
+        if constexpr (!GROUP) store_qk_t<T>(a, c, hk, d, dq, [&](int m) { return dr[m] + dw[m]; });
     }
-#pragma unroll
-    for (int m = 0; m < 4; ++m)
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int i = m * 16 + l4 * 4 + r, d = wave * (DKP / 4) + n * 16 + l16;
-                if (i < c.n && d < a.Dk) {
-                    const size_t o = ((size_t)(c.start + i) * a.Hk + hk) * a.Dk + d;
-                    Elt<T>::st(static_cast<T*>(a.dq), o, tq[m][n][r]);
-                    Elt<T>::st(static_cast<T*>(a.dk), o, tk[m][n][r]);
-                }
-            }
+    if constexpr (GROUP) store_qk_t<T>(a, c, hk, d, tq, [&](int m) { return tk[m]; });
 }
 
 template <typename T, int DKP>
 int launch_delta_bwd(const DeltaArgs& a, hipStream_t s) {
-    const int64_t slots = delta_slots(a.T, a.nseq);
-    if (a.T > 0) {
-        k_delta_prepare<T, DKP, true><<<dim3((unsigned)slots, a.Hk), 256, 0, s>>>(a);
-        SSMP_LAUNCH_CHECK();
-    }
+    if (a.T > 0)
+        if (const int st = launch_delta_prepare<T, DKP, true>(a, s)) return st;
     if (a.T > 0 || a.dh0) {
-        const unsigned blocks = (unsigned)((int64_t)a.nseq * a.Hv * ((a.Dv + kCols - 1) / kCols));
+        const int ncb = (a.Dv + kCols - 1) / kCols;
+        const unsigned blocks = (unsigned)spread_blocks((int64_t)a.nseq * a.Hk, ncb * (a.Hv / a.Hk));
         k_delta_chain_bwd<T, DKP><<<blocks, 256, 0, s>>>(a);
         SSMP_LAUNCH_CHECK();
     }
     if (a.T > 0) {
-        k_delta_grads<T, DKP><<<dim3((unsigned)slots, a.Hk), 256, 0, s>>>(a);
+        const dim3 grid((unsigned)delta_slots(a.T, a.nseq), a.Hk);
+        if (a.Hv > a.Hk) k_delta_grads<T, DKP, true><<<grid, DKP * 4, 0, s>>>(a);
+        else k_delta_grads<T, DKP, false><<<grid, DKP * 4, 0, s>>>(a);
         SSMP_LAUNCH_CHECK();
     }
     return SSMP_OK;
@@ -427,8 +401,8 @@ inline DeltaBwdLayout delta_bwd_layout(int64_t T, int32_t nseq, int32_t Hk, int3
     DeltaBwdLayout L;
     L.dec = 0;
     L.inv = L.dec + round256(n * Hv * 2 * kC * 4);
-    L.att = L.inv + round256(n * Hv * 3 * kC * kC * 2);
-    L.kt = L.att + round256(n * Hv * 3 * kC * kC * 2);
+    L.att = L.inv + round256(n * Hv * kTri * 4);
+    L.kt = L.att + round256(n * Hv * kTri * 4);
     L.qt = L.kt + round256(n * Hk * delta_dkp(Dk) * kC * elt);
     L.dS1 = L.qt + round256(n * Hk * delta_dkp(Dk) * kC * elt);
     L.dU = L.dS1 + round256(n * Hv * Dk * Dv * 4);
@@ -489,8 +463,8 @@ extern "C" int gated_delta_pack_bwd(const void* q, const void* k, const float* g
         a.S0 = reinterpret_cast<float*>(kept);
         a.E = reinterpret_cast<float*>(kept + round256((size_t)delta_slots(T, nseq) * Hv * Dk * Dv * 4));
         a.dec = reinterpret_cast<float*>(ws + L.dec);
-        a.inv = reinterpret_cast<__bf16*>(ws + L.inv);
-        a.att = reinterpret_cast<__bf16*>(ws + L.att);
+        a.inv = reinterpret_cast<float*>(ws + L.inv);
+        a.att = reinterpret_cast<float*>(ws + L.att);
         a.kt = ws + L.kt;
         a.qt = ws + L.qt;
         a.dS1 = reinterpret_cast<float*>(ws + L.dS1);

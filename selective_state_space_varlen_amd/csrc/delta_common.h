@@ -12,6 +12,10 @@ inline bool aligned16(P... p) {
     return ((reinterpret_cast<uintptr_t>(p) % 16 == 0) && ...);
 }
 
+// The wave's number in its workgroup, as a scalar: branches on it are the
+// wave's own, as matrix instructions, which heed no lane mask, need them to be.
+__device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)); }
+
 // ---------------------------------------------------------------------------
 // Chunks. A chunk is up to 64 tokens of one sequence, counted from its first
 // token. Sequence s has its chunks in the slots floor(cu[s] / 64) + s + c,
@@ -193,6 +197,150 @@ __device__ __forceinline__ void load4(const float* p, float (&v)[4]) {
     for (int e = 0; e < 4; ++e) v[e] = w[e];
 }
 
+// Results as operands. The order of a product's k is free as long as both
+// operands have the same, so k = 4 g + e (g < 8) of each block of 32 is put at
+// place 8 (g % 4) + 4 (g / 4) + e: lane group l / 16 then holds as operand the
+// very rows 4 (l / 16) + e and 16 + 4 (l / 16) + e that two tiles of a result
+// left with it, and a result becomes the next product's right operand by
+// rounding alone, without a trip through LDS. Left operands are stored in
+// this order.
+__host__ __device__ constexpr int kplace(int k) { return (k & ~31) | (((k >> 2) & 3) << 3) | (((k >> 4) & 1) << 2) | (k & 3); }
+template <int NP>
+__device__ __forceinline__ Frag<NP> split_tiles(const f32x4& lo, const f32x4& hi) {
+    const float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+    return split8<NP>(v);
+}
+
+// Rows of a chunk through a buffer resource: 32-bit lane offsets, and what
+// lies behind the chunk's last row, or is marked kNowhere, reads as zero and
+// is not written. Rows of up to kMaxRow elements keep offsets below 2^31.
+constexpr uint32_t kNowhere = 0x80000000u;
+constexpr int64_t kMaxRow = int64_t(1) << 20;
+template <typename T>
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const T* first, int rows, int stride, int width) {
+    return bytes_rsrc(first, rows > 0 ? (uint32_t)((rows - 1) * stride + width) * (uint32_t)sizeof(T) : 0u);
+}
+
+// 8 elements on their way from memory to LDS
+template <typename T>
+struct Unit;
+template <>
+struct Unit<uint16_t> {
+    u32x4 w;
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t o) {
+        w = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)o, 0, 0));
+    }
+    __device__ __forceinline__ void load(const uint16_t* p, bool on) {
+        w = u32x4{0, 0, 0, 0};
+        if (on) w = *reinterpret_cast<const u32x4*>(p);
+    }
+    __device__ __forceinline__ void put_half(uint16_t* p, int h) const {
+        *reinterpret_cast<u32x2*>(p) = h ? u32x2{w[2], w[3]} : u32x2{w[0], w[1]};
+    }
+};
+template <>
+struct Unit<float> {
+    f32x4 w[2];
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t o) {
+        w[0] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)o, 0, 0));
+        w[1] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)(o + 16), 0, 0));
+    }
+    __device__ __forceinline__ void load(const float* p, bool on) {
+        w[0] = w[1] = f32x4{0, 0, 0, 0};
+        if (on) {
+            w[0] = reinterpret_cast<const f32x4*>(p)[0];
+            w[1] = reinterpret_cast<const f32x4*>(p)[1];
+        }
+    }
+    __device__ __forceinline__ void put_half(float* p, int h) const { *reinterpret_cast<f32x4*>(p) = w[h]; }
+};
+__device__ __forceinline__ Frag<1> unit_planes(const Unit<uint16_t>& u) { return {{__builtin_bit_cast(bf16x8, u.w)}}; }
+__device__ __forceinline__ Frag<3> unit_planes(const Unit<float>& u) { return split_tiles<3>(u.w[0], u.w[1]); }
+template <typename T>
+__device__ __forceinline__ void copy8(T* to, const T* from, bool on) {
+    Unit<T> u;
+    u.load(from, on);
+    u.put_half(to, 0);
+    u.put_half(to + 4, 1);
+}
+__device__ __forceinline__ void put8(uint16_t* p, const uint16_t (&v)[8]) {
+    u32x4 w;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) w[e] = (uint32_t)v[2 * e] | ((uint32_t)v[2 * e + 1] << 16);
+    *reinterpret_cast<u32x4*>(p) = w;
+}
+__device__ __forceinline__ void put8(float* p, const float (&v)[8]) {
+    reinterpret_cast<f32x4*>(p)[0] = f32x4{v[0], v[1], v[2], v[3]};
+    reinterpret_cast<f32x4*>(p)[1] = f32x4{v[4], v[5], v[6], v[7]};
+}
+
+// Left operands in LDS: rows of W elements of E in 16-byte units (32 for fp32:
+// what one lane reads), without padding; unit u of row r lies at u ^ swz(r),
+// so that the 16 rows a read touches fall into different banks.
+template <typename E, int W>
+struct Tile {
+    static constexpr int kUnits = W / 8;
+    static constexpr int kPer = W * (int)sizeof(E) >= 256 ? 1 : 256 / (W * (int)sizeof(E));  // rows to a turn of the banks
+    static __device__ __forceinline__ int at(int row, int unit) {
+        return row * W + ((unit ^ ((row / kPer) & (kUnits - 1))) << 3);
+    }
+};
+__device__ __forceinline__ Frag<1> tile_frag(const uint16_t* p) {
+    return {{__builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4*>(p))}};
+}
+__device__ __forceinline__ Frag<3> tile_frag(const float* p) {
+    float v[8];
+    load8(p, true, v);
+    return split8<3>(v);
+}
+
+// The triangular matrices of a chunk (the inverse, the decayed products) in
+// memory: fp32, in places, the blocks of 32 columns that hold anything:
+// lower: columns 0-31 of all 64 rows, then 32-63 of rows 32-63;
+// upper: columns 32-63 of all 64 rows, then 0-31 of rows 0-31.
+constexpr int kTriRows = 96, kTri = kTriRows * 32;
+template <bool UPPER>
+__device__ __forceinline__ int tri_row(int row, int col) {
+    if constexpr (UPPER) return col >= 32 ? row : 64 + row;
+    else return col < 32 ? row : 32 + row;
+}
+// the same in LDS: NP planes of 96 rows of 32 places
+template <int NP>
+__device__ __forceinline__ void tri_put4(__bf16* base, int idx4, const f32x4& v) {
+    typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+    const int row = idx4 >> 3, q = idx4 & 7;
+    __bf16 p[4][NP];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) split<NP>(v[e], p[e]);
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+        const bf16x4 w = {p[0][i], p[1][i], p[2][i], p[3][i]};
+        *reinterpret_cast<bf16x4*>(base + i * kTri + Tile<uint16_t, 32>::at(row, q >> 1) + (q & 1) * 4) = w;
+    }
+}
+template <int NP>
+__device__ __forceinline__ Frag<NP> tri_frag(const __bf16* base, int row, int unit) {
+    Frag<NP> f;
+#pragma unroll
+    for (int i = 0; i < NP; ++i)
+        f.p[i] = __builtin_bit_cast(
+            bf16x8, *reinterpret_cast<const u32x4*>(base + i * kTri + Tile<uint16_t, 32>::at(row, unit)));
+    return f;
+}
+
+// The workgroups that share keys and queries (the column blocks of a head,
+// the value heads of a key head) on one XCD, one after another: workgroups go
+// to the 8 XCDs in turn, and each has its own L2.
+struct Spread {
+    int64_t group;
+    int member;
+};
+__device__ __forceinline__ Spread spread(int64_t block, int members) {
+    const int64_t i = block >> 3;
+    return {(i / members) * 8 + (block & 7), (int)(i % members)};
+}
+inline int64_t spread_blocks(int64_t groups, int members) { return (groups + 7) / 8 * 8 * members; }
+
 // ---------------------------------------------------------------------------
 // Decays of a chunk: G = running sum of g in 64 bits (32-bit sums would lose
 // the small steps behind a large one), lane l holding token l. g below
@@ -243,7 +391,7 @@ __device__ __forceinline__ void put_tile16(float* x, const f32x4& v) {
     for (int i = 0; i < 4; ++i) x[((l >> 4) * 4 + i) * kLdA + (l & 15)] = v[i];
 }
 __device__ __forceinline__ void chunk_inverse(const float* A, float* X) {
-    const int tid = threadIdx.x, wave = tid >> 6, l = tid & 63;
+    const int tid = threadIdx.x, wave = wave_id(), l = lane_id();
     // zero the blocks above the diagonal's
     for (int i = tid; i < kC * kC; i += 256) {
         const int r = i >> 6, c = i & 63;
@@ -292,7 +440,7 @@ __device__ __forceinline__ void chunk_inverse(const float* A, float* X) {
 // ---------------------------------------------------------------------------
 // Sizes and buffers
 constexpr int kMaxDk = 128;
-constexpr int kCols = 32;  // state columns a workgroup of the chunk chains takes
+constexpr int kCols = 64;  // state columns a workgroup of the chunk chains takes: 16 a wave
 
 inline int delta_dkp(int Dk) { return Dk <= 64 ? 64 : 128; }
 inline size_t round256(size_t n) { return (n + 255) / 256 * 256; }
@@ -312,17 +460,19 @@ struct DeltaArgs {
     float *S0, *E;   // the state that enters the chunk (Dk, Dv); the errors (64, Dv)
     // scratch, by slot and head
     float* dec;      // e^{G_i} and e^{G_last - G_i}: (2, 64)
-    __bf16* inv;     // the chunk's inverse: (planes, 64, 64)
-    __bf16* att;     // the decayed products of q and k: (planes, 64, 64)
-    void *kt, *qt;   // keys and queries, transposed: (Dk padded, 64)
+    float* inv;      // the chunk's inverse: kTri
+    float* att;      // the decayed products of q and k: kTri
+    void *kt, *qt;   // keys and queries, transposed, tokens in places: (Dk padded, 64)
     float *dS1, *dU; // backward: gradients of the state that leaves the chunk, and of U
 };
 
 inline int delta_check(int64_t T, int32_t nseq, int32_t Hk, int32_t Hv, int32_t Dk, int32_t Dv, int32_t dtype) {
     if (T < 0 || T >= (int64_t(1) << 31) || nseq < 1 || Hk < 1 || Hv < 1 || Dk < 1 || Dv < 1) return SSMP_ERR_SHAPE;
-    if (Hv % Hk || Hv > 65535 || Dv > 65536 || nseq > (1 << 24)) return SSMP_ERR_SHAPE;
+    if (Hv % Hk || Hv > 65535 || nseq > (1 << 24)) return SSMP_ERR_SHAPE;
+    if ((int64_t)Hv * Dv > kMaxRow || (int64_t)Hk * Dk > kMaxRow) return SSMP_ERR_SHAPE;
     if (T * Hv * (int64_t)(Dv > Dk ? Dv : Dk) >= (int64_t(1) << 40)) return SSMP_ERR_SHAPE;
-    if ((int64_t)nseq * Hv * ((Dv + kCols - 1) / kCols) >= (int64_t(1) << 31)) return SSMP_ERR_SHAPE;
+    if ((int64_t)(nseq + 7) * Hv * ((Dv + kCols - 1) / kCols) >= (int64_t(1) << 31)) return SSMP_ERR_SHAPE;
+    if ((T / kC + nseq + 7) * Hv >= (int64_t(1) << 31)) return SSMP_ERR_SHAPE;
     if (dtype != SSMP_F32 && dtype != SSMP_BF16) return SSMP_ERR_UNSUPPORTED;
     if (Dk % 8 || Dv % 8 || Dk > kMaxDk) return SSMP_ERR_UNSUPPORTED;
     return SSMP_OK;

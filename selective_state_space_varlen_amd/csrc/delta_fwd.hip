@@ -14,176 +14,124 @@
 
 namespace ssmp {
 
-// One workgroup per (sequence, value head, 32 columns of the state). Wave w
-// holds the state's rows w DKP / 4 .. and the chunk's tokens 16 w .. in its
-// results; left operands come from global memory in operand order, each read
-// by one wave alone, right operands pass through LDS as bf16 planes.
-template <typename T, int DKP>
-__global__ __launch_bounds__(256) void k_delta_chain(DeltaArgs a) {
+// planes of P and of U where they form the output: its own rounding to bf16
+// hides what two planes (16 bits) leave out
+template <typename T>
+constexpr int kOutP = std::is_same<T, float>::value ? 3 : 2;
+
+// One workgroup per (sequence, value head, 64 columns of the state), 16
+// columns a wave. Columns do not meet in the chain, and a wave's results are
+// its next right operands in the registers they are in (kplace), so the waves
+// share nothing but the left operands, which the workgroup holds in LDS while
+// the next chunk's are under way in registers: two barriers a chunk.
+// SAVE: keep S and E for the backward.
+template <typename T, int DKP, bool SAVE>
+__global__ __launch_bounds__(256, NWG<T>) void k_delta_chain(DeltaArgs a) {
     constexpr int NX = kExact<T>, NO = kOutP<T>;
-    constexpr int MT = DKP / 64;  // 16-row tiles of the state a wave holds
-    constexpr int LS = DKP + 8, LT = kC + 8;
-    constexpr int PS = kCols * LS, PT = kCols * LT;
-    __shared__ alignas(16) __bf16 St[3 * PS];   // the state, [column][row]
-    __shared__ alignas(16) __bf16 Xt[3 * PT];   // X, [column][token]
-    __shared__ alignas(16) __bf16 Ut[NO * PT];  // U
-    __shared__ alignas(16) __bf16 Wt[3 * PT];   // e^{G_last - G} U
-    const int ncb = (a.Dv + kCols - 1) / kCols;
-    const int cb = blockIdx.x % ncb, hv = (blockIdx.x / ncb) % a.Hv, seq = blockIdx.x / (ncb * a.Hv);
-    const int hk = hv / (a.Hv / a.Hk);
-    const int tid = threadIdx.x, wave = tid >> 6, l = tid & 63, l16 = l & 15, l4 = l >> 4;
+    constexpr int MT = DKP / 16;  // 16-row tiles of the state
+    using Loads = ChainLoads<T, DKP, 2, 1, NO>;
+    __shared__ alignas(16) typename Loads::Tiles lds;
+    const int ncb = (a.Dv + kCols - 1) / kCols, group = a.Hv / a.Hk;
+    const Spread sp = spread(blockIdx.x, ncb * group);
+    if (sp.group >= (int64_t)a.nseq * a.Hk) return;
+    const int seq = (int)(sp.group / a.Hk), hk = (int)(sp.group % a.Hk);
+    const int hv = hk * group + sp.member / ncb, cb = sp.member % ncb;
+    const int wave = wave_id(), l = lane_id(), l16 = l & 15, l4 = l >> 4;
+    const int col = cb * kCols + wave * 16 + l16;
+    const bool busy = cb * kCols + wave * 16 < a.Dv;
     const Seq q = seq_at(a.cu, seq, a.T);
     const int chunks = (q.len + kC - 1) / kC;
-    f32x4 S[MT][2];
-    const auto state_row = [&](int m, int r) { return wave * (DKP / 4) + m * 16 + l4 * 4 + r; };
-    const auto state_col = [&](int n) { return cb * kCols + n * 16 + l16; };
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int d = state_row(m, r), e = state_col(n);
-                S[m][n][r] = a.h0 && d < a.Dk && e < a.Dv
-                                 ? a.h0[(((size_t)seq * a.Hv + hv) * a.Dk + d) * a.Dv + e] : 0.0f;
-            }
+    const Column cs = column_of<float>(1, a.Dv, col), cv = column_of<T>(a.Hv, a.Dv, col);
+    const size_t state = ((size_t)seq * a.Hv + hv) * a.Dk * a.Dv;
+    f32x4 S[MT];
+    load_matrix(a.h0 ? a.h0 + state : nullptr, a.Dk, a.Dv, cs, S);
+    Loads next;
+    uint32_t v[16];
+    if (chunks > 0) {
+        const int n = q.len < kC ? q.len : kC;
+        next.load(a, q.slot0, q.start, n, hk, hv);
+        load_column<T>(a.v, q.start, n, a.Hv, hv, a.Dv, cv, v);
+    }
     for (int ch = 0; ch < chunks; ++ch) {
         const int64_t slot = q.slot0 + ch, start = q.start + (int64_t)ch * kC;
         const int cn = q.len - ch * kC < kC ? q.len - ch * kC : kC;
         const size_t sh = (size_t)slot * a.Hv + hv;
-        const float* const dec = a.dec + sh * 2 * kC;
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int n = 0; n < 2; ++n) {
-                float v[4];
-#pragma unroll
-                for (int r = 0; r < 4; ++r) v[r] = S[m][n][r];
-                lds_put4<3>(St, PS, LS, n * 16 + l16, state_row(m, 0), v);
-                if (a.S0) {
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int d = state_row(m, r), e = state_col(n);
-                        if (d < a.Dk && e < a.Dv) a.S0[(sh * a.Dk + d) * a.Dv + e] = v[r];
-                    }
-                }
-            }
+        __syncthreads();  // the last chunk's operands have been read
+        next.put(lds);
         __syncthreads();
-        // K S and Q S for this wave's 16 tokens
-        f32x4 x[2] = {}, o[2] = {};
-        const int i0 = wave * 16 + l16;
-        const size_t row = ((size_t)(start + i0) * a.Hk + hk) * a.Dk;
+        const int left = q.len - (ch + 1) * kC, nn = left < kC ? left : kC;
+        if (nn > 0) next.load(a, slot + 1, start + kC, nn, hk, hv);
+        if (!busy) continue;
+        if constexpr (SAVE) store_matrix(a.S0 + sh * a.Dk * a.Dv, a.Dk, a.Dv, cs, S);
+        f32x4 x[4] = {}, o[4] = {};  // K S and Q S
 #pragma unroll
         for (int s = 0; s < DKP / 32; ++s) {
-            const int k0 = s * 32 + l4 * 8;
-            const bool on = i0 < cn && k0 < a.Dk;
-            const auto ka = load_frag(static_cast<const T*>(a.k) + row + k0, on);
-            const auto qa = load_frag(static_cast<const T*>(a.q) + row + k0, on);
+            __builtin_amdgcn_sched_barrier(0);
+            const auto sb = split_tiles<3>(S[2 * s], S[2 * s + 1]);
 #pragma unroll
-            for (int n = 0; n < 2; ++n) {
-                const auto sb = plane_frag<3>(St, PS, LS, n * 16 + l16, k0);
-                mma<3>(x[n], ka, sb);
-                mma<NO>(o[n], qa, sb);
+            for (int m = 0; m < 4; ++m) {
+                mma<3>(x[m], lds.row_frag(0, m * 16 + l16, s * 4 + l4), sb);
+                mma<NO>(o[m], lds.row_frag(1, m * 16 + l16, s * 4 + l4), sb);
             }
         }
-        float eg[4], el[4], bt[4];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int i = wave * 16 + l4 * 4 + r;
-            eg[r] = dec[i];
-            el[r] = dec[kC + i];
-            bt[r] = i < cn ? a.beta[(size_t)(start + i) * a.Hv + hv] : 0.0f;
-        }
-        const float ec = dec[kC - 1];
-#pragma unroll
-        for (int n = 0; n < 2; ++n) {
-            float v[4];
+        for (int m = 0; m < 4; ++m) {
+            const f32x4 eg = *reinterpret_cast<const f32x4*>(lds.eg + m * 16 + l4 * 4);
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const int i = wave * 16 + l4 * 4 + r, e = state_col(n);
-                const float vv = i < cn && e < a.Dv
-                                     ? Elt<T>::ld(static_cast<const T*>(a.v), ((size_t)(start + i) * a.Hv + hv) * a.Dv + e)
-                                     : 0.0f;
-                v[r] = fmaf(-eg[r], x[n][r], vv);
-                o[n][r] *= eg[r];
+                x[m][r] = fmaf(-eg[r], x[m][r], Elt<T>::cvt(v[m * 4 + r]));
+                o[m][r] *= eg[r];
             }
-            lds_put4<3>(Xt, PT, LT, n * 16 + l16, wave * 16 + l4 * 4, v);
         }
-        __syncthreads();
+        if (nn > 0) load_column<T>(a.v, start + kC, nn, a.Hv, hv, a.Dv, cv, v);
         // E = inverse X
-        f32x4 E[2] = {};
-        const __bf16* const inv = a.inv + sh * 3 * kC * kC;
+        f32x4 E[4] = {};
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            const int k0 = s * 32 + l4 * 8;
-            const auto ia = plane_frag<3>(inv, kC * kC, kC, i0, k0);
+            __builtin_amdgcn_sched_barrier(0);
+            const auto xb = split_tiles<3>(x[2 * s], x[2 * s + 1]);
 #pragma unroll
-            for (int n = 0; n < 2; ++n) mma<3>(E[n], ia, plane_frag<3>(Xt, PT, LT, n * 16 + l16, k0));
+            for (int m = 2 * s; m < 4; ++m)
+                mma<3>(E[m], tri_frag<3>(lds.inv, s * 32 + m * 16 + l16, l4), xb);
         }
+        if constexpr (SAVE) store_matrix(a.E + sh * kC * a.Dv, kC, a.Dv, cs, E);
+        f32x4 w[4];
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
-            float u[4], w[4];
+        for (int m = 0; m < 4; ++m) {
+            const f32x4 be = *reinterpret_cast<const f32x4*>(lds.beta + m * 16 + l4 * 4);
+            const f32x4 el = *reinterpret_cast<const f32x4*>(lds.el + m * 16 + l4 * 4);
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                u[r] = bt[r] * E[n][r];
-                w[r] = el[r] * u[r];
-                const int i = wave * 16 + l4 * 4 + r, e = state_col(n);
-                if (a.E && e < a.Dv) a.E[(sh * kC + i) * a.Dv + e] = E[n][r];
+                E[m][r] *= be[r];  // U
+                w[m][r] = el[r] * E[m][r];
             }
-            lds_put4<NO>(Ut, PT, LT, n * 16 + l16, wave * 16 + l4 * 4, u);
-            lds_put4<3>(Wt, PT, LT, n * 16 + l16, wave * 16 + l4 * 4, w);
         }
-        __syncthreads();
-        // S = e^{G_last} S + K^T W
-        const T* const kt = static_cast<const T*>(a.kt) + ((size_t)slot * a.Hk + hk) * DKP * kC;
+        const float ec = lds.eg[kC - 1];
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int n = 0; n < 2; ++n) S[m][n] *= ec;
+        for (int m = 0; m < MT; ++m) S[m] *= ec;
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            const int k0 = s * 32 + l4 * 8;
-            const auto pa = plane_frag<NO>(a.att + sh * NO * kC * kC, kC * kC, kC, i0, k0);
+            __builtin_amdgcn_sched_barrier(0);
+            const auto ub = split_tiles<NO>(E[2 * s], E[2 * s + 1]);
+            const auto wb = split_tiles<3>(w[2 * s], w[2 * s + 1]);
 #pragma unroll
-            for (int n = 0; n < 2; ++n) {
-                const auto wb = plane_frag<3>(Wt, PT, LT, n * 16 + l16, k0);
+            for (int m = 2 * s; m < 4; ++m) mma<NO>(o[m], tri_frag<NO>(lds.att, s * 32 + m * 16 + l16, l4), ub);
 #pragma unroll
-                for (int m = 0; m < MT; ++m)
-                    mma<3>(S[m][n], load_frag(kt + (wave * (DKP / 4) + m * 16 + l16) * kC + k0, true), wb);
-                mma<NO>(o[n], pa, plane_frag<NO>(Ut, PT, LT, n * 16 + l16, k0));
-            }
+            for (int m = 0; m < MT; ++m) mma<3>(S[m], lds.col_frag(0, m * 16 + l16, s * 4 + l4), wb);
         }
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int i = wave * 16 + l4 * 4 + r, e = state_col(n);
-                if (i < cn && e < a.Dv)
-                    Elt<T>::st(static_cast<T*>(a.out), ((size_t)(start + i) * a.Hv + hv) * a.Dv + e, a.scale * o[n][r]);
-            }
+        store_column<T>(a.out, start, cn, a.Hv, hv, a.Dv, cv, o, a.scale);
     }
-    if (a.hT) {
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int n = 0; n < 2; ++n)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int d = state_row(m, r), e = state_col(n);
-                    if (d < a.Dk && e < a.Dv) a.hT[(((size_t)seq * a.Hv + hv) * a.Dk + d) * a.Dv + e] = S[m][n][r];
-                }
-    }
+    if (a.hT && busy) store_matrix(a.hT + state, a.Dk, a.Dv, cs, S);
 }
 
 template <typename T, int DKP>
 int launch_delta_fwd(const DeltaArgs& a, hipStream_t s) {
-    const int64_t slots = delta_slots(a.T, a.nseq);
-    if (a.T > 0) {
-        k_delta_prepare<T, DKP, false><<<dim3((unsigned)slots, a.Hk), 256, 0, s>>>(a);
-        SSMP_LAUNCH_CHECK();
-    }
-    const unsigned blocks = (unsigned)((int64_t)a.nseq * a.Hv * ((a.Dv + kCols - 1) / kCols));
-    k_delta_chain<T, DKP><<<blocks, 256, 0, s>>>(a);
+    if (a.T > 0)
+        if (const int st = launch_delta_prepare<T, DKP, false>(a, s)) return st;
+    const int ncb = (a.Dv + kCols - 1) / kCols;
+    const unsigned blocks = (unsigned)spread_blocks((int64_t)a.nseq * a.Hk, ncb * (a.Hv / a.Hk));
+    if (a.S0) k_delta_chain<T, DKP, true><<<blocks, 256, 0, s>>>(a);
+    else k_delta_chain<T, DKP, false><<<blocks, 256, 0, s>>>(a);
     SSMP_LAUNCH_CHECK();
     return SSMP_OK;
 }
@@ -193,12 +141,11 @@ struct DeltaFwdLayout {
 };
 inline DeltaFwdLayout delta_fwd_layout(int64_t T, int32_t nseq, int32_t Hk, int32_t Hv, int32_t Dk, int32_t dtype) {
     const size_t n = (size_t)delta_slots(T, nseq), elt = dtype == SSMP_F32 ? 4 : 2;
-    const size_t np = dtype == SSMP_F32 ? kOutP<float> : kOutP<uint16_t>;
     DeltaFwdLayout L;
     L.dec = 0;
     L.inv = L.dec + round256(n * Hv * 2 * kC * 4);
-    L.att = L.inv + round256(n * Hv * 3 * kC * kC * 2);
-    L.kt = L.att + round256(n * Hv * np * kC * kC * 2);
+    L.att = L.inv + round256(n * Hv * kTri * 4);
+    L.kt = L.att + round256(n * Hv * kTri * 4);
     L.total = L.kt + round256(n * Hk * delta_dkp(Dk) * kC * elt);
     return L;
 }
@@ -256,8 +203,8 @@ extern "C" int gated_delta_pack_fwd(const void* q, const void* k, const void* v,
     a.scale = scale;
     if (T > 0) {
         a.dec = reinterpret_cast<float*>(ws + L.dec);
-        a.inv = reinterpret_cast<__bf16*>(ws + L.inv);
-        a.att = reinterpret_cast<__bf16*>(ws + L.att);
+        a.inv = reinterpret_cast<float*>(ws + L.inv);
+        a.att = reinterpret_cast<float*>(ws + L.att);
         a.kt = ws + L.kt;
         if (saved) {
             a.S0 = static_cast<float*>(saved);
