@@ -22,12 +22,13 @@
 namespace ssmp {
 
 // As k_delta_chain, from the last chunk to the first.
-template <typename T, int DKP>
-__global__ __launch_bounds__(256, NWG<T>) void k_delta_chain_bwd(DeltaArgs a) {
+template <typename T, int DKP, int NW>
+__global__ __launch_bounds__(NW * 64) void k_delta_chain_bwd(DeltaArgs a) {
     constexpr int NX = kExact<T>;
     constexpr int MT = DKP / 16;
-    using Loads = ChainLoads<T, DKP, 1, 2, 3>;
+    using Loads = ChainLoads<T, DKP, 3, NW * 64>;
     __shared__ alignas(16) typename Loads::Tiles lds;
+    constexpr int kCols = NW * kWaveCols;
     const int ncb = (a.Dv + kCols - 1) / kCols, group = a.Hv / a.Hk;
     const Spread sp = spread(blockIdx.x, ncb * group);
     if (sp.group >= (int64_t)a.nseq * a.Hk) return;
@@ -71,7 +72,7 @@ __global__ __launch_bounds__(256, NWG<T>) void k_delta_chain_bwd(DeltaArgs a) {
             __builtin_amdgcn_sched_barrier(0);
             const auto sb = split_tiles<3>(S[2 * s], S[2 * s + 1]);
 #pragma unroll
-            for (int m = 0; m < 4; ++m) mma<3>(x[m], lds.row_frag(0, m * 16 + l16, s * 4 + l4), sb);
+            for (int m = 0; m < 4; ++m) mma<3>(x[m], lds.k.frag(m * 16 + l16, s * 4 + l4), sb);
         }
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
@@ -116,31 +117,12 @@ __global__ __launch_bounds__(256, NWG<T>) void k_delta_chain_bwd(DeltaArgs a) {
             const auto ub = split_tiles<3>(u[2 * s], u[2 * s + 1]);
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
-                mma<3>(S[m], lds.col_frag(1, m * 16 + l16, s * 4 + l4), ob);
-                mma<3>(S[m], lds.col_frag(0, m * 16 + l16, s * 4 + l4), ub);
+                mma<3>(S[m], lds.q.token_frag(s, m), ob);
+                mma<3>(S[m], lds.k.token_frag(s, m), ub);
             }
         }
     }
     if (a.dh0 && busy) store_matrix(a.dh0 + state, a.Dk, a.Dv, cs, S);
-}
-
-// dq and dk of one column, from the tiles of 64 tokens
-template <typename T, typename F>
-__device__ __forceinline__ void store_qk_t(const DeltaArgs& a, const Chunk& c, int hk, int d, const f32x4 (&dq)[4], F dk) {
-    const int l4 = lane_id() >> 4;
-#pragma unroll
-    for (int m = 0; m < 4; ++m) {
-        const f32x4 k = dk(m);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int i = m * 16 + l4 * 4 + r;
-            if (i < c.n && d < a.Dk) {
-                const size_t o = ((size_t)(c.start + i) * a.Hk + hk) * a.Dk + d;
-                Elt<T>::st(static_cast<T*>(a.dq), o, dq[m][r]);
-                Elt<T>::st(static_cast<T*>(a.dk), o, k[r]);
-            }
-        }
-    }
 }
 
 // One workgroup per (slot, key head), over the value heads of its group, whose
@@ -159,6 +141,7 @@ __global__ __launch_bounds__(DKP * 4) void k_delta_grads(DeltaArgs a) {
     // planes of dOut, dE and U (64 columns at a time, [token][column]), then of
     // a or -b and its transpose
     __shared__ alignas(16) __bf16 lds[(NX + 6) * PT];
+    __shared__ alignas(16) RowTile<T, DKP> kt, qt;
     __shared__ double G[kC];
     __shared__ alignas(16) float decay[2][kC];
     __shared__ float red[kWaves][kC], ends[kWaves];
@@ -172,13 +155,19 @@ __global__ __launch_bounds__(DKP * 4) void k_delta_grads(DeltaArgs a) {
     __bf16* const Up = Ep + 3 * PT;
     __bf16* const M = lds;
     __bf16* const Mt = lds + 3 * PT;
-    const size_t tr = ((size_t)slot * a.Hk + hk) * DKP * kC;
+    for (int u = tid; u < kC * DKP / 8; u += kThreads) {
+        const int i = u / (DKP / 8), k8 = u % (DKP / 8);
+        const size_t first = ((size_t)c.start * a.Hk + hk) * a.Dk;
+        const uint32_t o = k8 * 8 < a.Dk ? (uint32_t)(i * a.Hk * a.Dk + k8 * 8) * (uint32_t)sizeof(T) : kNowhere;
+        Unit<T> x, y;
+        x.load(rows_rsrc(static_cast<const T*>(a.k) + first, c.n, a.Hk * a.Dk, a.Dk), o);
+        y.load(rows_rsrc(static_cast<const T*>(a.q) + first, c.n, a.Hk * a.Dk, a.Dk), o);
+        kt.put(i, k8, x);
+        qt.put(i, k8, y);
+    }
     const int d = wave * 16 + l16;                       // this lane's column of dq and dk
     const int tj = wave / (4 / TT), ti0 = (wave % (4 / TT)) * TT;  // tiles (tj, ti0 + x) of a^T: rows j, columns i
-    f32x4 tq[GROUP ? 4 : 1], tk[GROUP ? 4 : 1];
-    if constexpr (GROUP)
-#pragma unroll
-        for (int m = 0; m < 4; ++m) tq[m] = tk[m] = f32x4{0, 0, 0, 0};
+    f32x4 tq[4] = {}, tk[4] = {};
     for (int hv = hk * group; hv < (hk + 1) * group; ++hv) {
         const size_t sh = (size_t)slot * a.Hv + hv;
         Unit<T> fo[SG];
@@ -254,15 +243,18 @@ __global__ __launch_bounds__(DKP * 4) void k_delta_grads(DeltaArgs a) {
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
                 const int k0 = s * 32 + l4 * 8;
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) sd = fmaf(s0[s].w[e >> 2][e & 3], s1[s].w[e >> 2][e & 3], sd);
                 const auto sb = unit_planes(s0[s]), db1 = unit_planes(s1[s]);
 #pragma unroll
                 for (int m = 0; m < 4; ++m) {
+                    __builtin_amdgcn_sched_barrier(0);
                     mma<3>(dq[m], plane_frag<NX>(Op, PT, LT, m * 16 + l16, k0), sb);
                     mma<3>(dr[m], plane_frag<3>(Ep, PT, LT, m * 16 + l16, k0), sb);
                     mma<3>(dw[m], plane_frag<3>(Up, PT, LT, m * 16 + l16, k0), db1);
                 }
+                __builtin_amdgcn_sched_barrier(0);
                 const auto uw = plane_frag<3>(Up, PT, LT, tj * 16 + l16, k0);
 #pragma unroll
                 for (int x = 0; x < TT; ++x) {
@@ -284,13 +276,14 @@ __global__ __launch_bounds__(DKP * 4) void k_delta_grads(DeltaArgs a) {
             s += __shfl_xor(s, 4);
             if ((u & 7) == 0 && t < c.n) a.dbeta[(size_t)(c.start + t) * a.Hv + hv] = s;
         }
+        __builtin_amdgcn_sched_barrier(0);
         float end = decay[0][kC - 1] * sd;
         float kv[4][4], qv[4][4];  // this lane's column of K and Q: tokens 16 m + 4 l4 + r
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
             const int i = m * 16 + l4 * 4;
-            load4(static_cast<const T*>(a.kt) + tr + d * kC + kplace(i), kv[m]);
-            load4(static_cast<const T*>(a.qt) + tr + d * kC + kplace(i), qv[m]);
+            kt.values4(m, wave, kv[m]);
+            qt.values4(m, wave, qv[m]);
             const f32x4 eg = *reinterpret_cast<const f32x4*>(&decay[0][i]);
             const f32x4 el = *reinterpret_cast<const f32x4*>(&decay[1][i]);
 #pragma unroll
@@ -310,12 +303,19 @@ __global__ __launch_bounds__(DKP * 4) void k_delta_grads(DeltaArgs a) {
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const bool on = pass ? i > j + r : i >= j + r;
-                    const float w = on ? expf((float)(G[i] - G[j + r])) : 0.0f;
+                    const float w = on ? decay_of(G[i] - G[j + r]) : 0.0f;
                     v[r] = on ? (pass ? -w * bt[x][r] : w * a.scale * at[x][r]) : 0.0f;
-                    __bf16 p[3];
-                    split<3>(v[r], p);
+                }
 #pragma unroll
-                    for (int y = 0; y < 3; ++y) Mt[y * PT + (j + r) * LT + kplace(i)] = p[y];
+                for (int r = 0; r < 4; r += 2) {
+                    uint32_t p[3];
+                    split2<3>(v[r], v[r + 1], p);
+#pragma unroll
+                    for (int y = 0; y < 3; ++y) {
+                        uint16_t* const to = reinterpret_cast<uint16_t*>(Mt) + y * PT + (j + r) * LT + kplace(i);
+                        to[0] = (uint16_t)p[y];
+                        to[LT] = (uint16_t)(p[y] >> 16);
+                    }
                 }
                 lds_put4<3>(M, PT, LT, i, kplace(j), v);
             }
@@ -323,9 +323,8 @@ __global__ __launch_bounds__(DKP * 4) void k_delta_grads(DeltaArgs a) {
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
                 const int k0 = s * 32 + l4 * 8;
-                const size_t o = tr + d * kC + k0;
-                const auto kb = load_frag(static_cast<const T*>(a.kt) + o, true);
-                const auto qb = load_frag(static_cast<const T*>(a.qt) + o, true);
+                __builtin_amdgcn_sched_barrier(0);
+                const auto kb = kt.token_frag(s, wave), qb = qt.token_frag(s, wave);
 #pragma unroll
                 for (int m = 0; m < 4; ++m) {
                     if (m >= 2 * s) mma<3>(pass ? dr[m] : dq[m], plane_frag<3>(M, PT, LT, m * 16 + l16, k0), kb);
@@ -368,9 +367,17 @@ __global__ __launch_bounds__(DKP * 4) void k_delta_grads(DeltaArgs a) {
             }
             if (l < c.n) a.dg[(size_t)(c.start + l) * a.Hv + hv] = (float)s;
         }
-        if constexpr (!GROUP) store_qk_t<T>(a, c, hk, d, dq, [&](int m) { return dr[m] + dw[m]; });
+        if constexpr (!GROUP) {
+#pragma unroll
+            for (int m = 0; m < 4; ++m) dr[m] += dw[m];
+            store_column<T>(a.dq, c.start, c.n, a.Hk, hk, a.Dk, column_of<T>(a.Hk, a.Dk, d), dq, 1.0f);
+            store_column<T>(a.dk, c.start, c.n, a.Hk, hk, a.Dk, column_of<T>(a.Hk, a.Dk, d), dr, 1.0f);
+        }
     }
-    if constexpr (GROUP) store_qk_t<T>(a, c, hk, d, tq, [&](int m) { return tk[m]; });
+    if constexpr (GROUP) {
+        store_column<T>(a.dq, c.start, c.n, a.Hk, hk, a.Dk, column_of<T>(a.Hk, a.Dk, d), tq, 1.0f);
+        store_column<T>(a.dk, c.start, c.n, a.Hk, hk, a.Dk, column_of<T>(a.Hk, a.Dk, d), tk, 1.0f);
+    }
 }
 
 template <typename T, int DKP>
@@ -378,9 +385,10 @@ int launch_delta_bwd(const DeltaArgs& a, hipStream_t s) {
     if (a.T > 0)
         if (const int st = launch_delta_prepare<T, DKP, true>(a, s)) return st;
     if (a.T > 0 || a.dh0) {
-        const int ncb = (a.Dv + kCols - 1) / kCols;
-        const unsigned blocks = (unsigned)spread_blocks((int64_t)a.nseq * a.Hk, ncb * (a.Hv / a.Hk));
-        k_delta_chain_bwd<T, DKP><<<blocks, 256, 0, s>>>(a);
+        if (const int nw = chain_waves(a); nw == 8)
+            k_delta_chain_bwd<T, DKP, 8><<<chain_blocks(a, nw), nw * 64, 0, s>>>(a);
+        else
+            k_delta_chain_bwd<T, DKP, 4><<<chain_blocks(a, nw), nw * 64, 0, s>>>(a);
         SSMP_LAUNCH_CHECK();
     }
     if (a.T > 0) {
@@ -393,18 +401,15 @@ int launch_delta_bwd(const DeltaArgs& a, hipStream_t s) {
 }
 
 struct DeltaBwdLayout {
-    size_t dec, inv, att, kt, qt, dS1, dU, total;
+    size_t dec, inv, att, dS1, dU, total;
 };
-inline DeltaBwdLayout delta_bwd_layout(int64_t T, int32_t nseq, int32_t Hk, int32_t Hv, int32_t Dk, int32_t Dv,
-                                       int32_t dtype) {
-    const size_t n = (size_t)delta_slots(T, nseq), elt = dtype == SSMP_F32 ? 4 : 2;
+inline DeltaBwdLayout delta_bwd_layout(int64_t T, int32_t nseq, int32_t Hv, int32_t Dk, int32_t Dv) {
+    const size_t n = (size_t)delta_slots(T, nseq);
     DeltaBwdLayout L;
     L.dec = 0;
     L.inv = L.dec + round256(n * Hv * 2 * kC * 4);
     L.att = L.inv + round256(n * Hv * kTri * 4);
-    L.kt = L.att + round256(n * Hv * kTri * 4);
-    L.qt = L.kt + round256(n * Hk * delta_dkp(Dk) * kC * elt);
-    L.dS1 = L.qt + round256(n * Hk * delta_dkp(Dk) * kC * elt);
+    L.dS1 = L.att + round256(n * Hv * kTri * 4);
     L.dU = L.dS1 + round256(n * Hv * Dk * Dv * 4);
     L.total = L.dU + round256(n * Hv * kC * Dv * 4);
     return L;
@@ -416,7 +421,7 @@ extern "C" size_t gated_delta_pack_bwd_scratch_bytes(int64_t T, int32_t nseq, in
                                                      int32_t Dv, int32_t dtype) {
     using namespace ssmp;
     if (delta_check(T, nseq, Hk, Hv, Dk, Dv, dtype) || T == 0) return 0;
-    return delta_bwd_layout(T, nseq, Hk, Hv, Dk, Dv, dtype).total;
+    return delta_bwd_layout(T, nseq, Hv, Dk, Dv).total;
 }
 
 extern "C" int gated_delta_pack_bwd(const void* q, const void* k, const float* g, const float* beta,
@@ -435,7 +440,7 @@ extern "C" int gated_delta_pack_bwd(const void* q, const void* k, const float* g
     if (T > 0 && (!scratch || scratch_bytes < gated_delta_pack_bwd_scratch_bytes(T, nseq, Hk, Hv, Dk, Dv, dtype)))
         return SSMP_ERR_WORKSPACE;
     if (T == 0 && !dinitial_state) return SSMP_OK;
-    const DeltaBwdLayout L = delta_bwd_layout(T, nseq, Hk, Hv, Dk, Dv, dtype);
+    const DeltaBwdLayout L = delta_bwd_layout(T, nseq, Hv, Dk, Dv);
     char* const ws = static_cast<char*>(scratch);
     DeltaArgs a = {};
     a.q = q;
@@ -465,8 +470,6 @@ extern "C" int gated_delta_pack_bwd(const void* q, const void* k, const float* g
         a.dec = reinterpret_cast<float*>(ws + L.dec);
         a.inv = reinterpret_cast<float*>(ws + L.inv);
         a.att = reinterpret_cast<float*>(ws + L.att);
-        a.kt = ws + L.kt;
-        a.qt = ws + L.qt;
         a.dS1 = reinterpret_cast<float*>(ws + L.dS1);
         a.dU = reinterpret_cast<float*>(ws + L.dU);
     }

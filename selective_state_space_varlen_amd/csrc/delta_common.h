@@ -109,25 +109,50 @@ __device__ __forceinline__ void mma(f32x4& d, const Frag<NA>& a, const Frag<NB>&
             if (s - i >= 0 && s - i < NB) d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.p[i], b.p[s - i], d, 0, 0, 0);
 }
 
-// v as bf16 planes: v = p[0] + p[1] + p[2] up to fp32's last bit
+// Two values as bf16 planes, packed: v = p[0] + p[1] + ... Three planes take
+// the leading 8 bits that are left each, which holds all 24 of an fp32. (Cutting
+// off takes two thirds of the time of rounding: 34 against 52 cycles a pair on
+// one SIMD, and a chain spends more cycles on splitting than on its products.)
+// Two planes round each, so that what they leave out, 2^-17 of v at most, has
+// no sign of its own to add up in a sum.
 template <int NP>
-__device__ __forceinline__ void split(float v, __bf16 (&p)[NP]) {
+__device__ __forceinline__ void split2(float v0, float v1, uint32_t (&p)[NP]) {
+    if constexpr (NP == 3) {
 #pragma unroll
-    for (int i = 0; i < NP; ++i) {
-        p[i] = (__bf16)v;
-        if (i + 1 < NP) v -= (float)p[i];
+        for (int i = 0; i < NP; ++i) {
+            const uint32_t a = __builtin_bit_cast(uint32_t, v0), b = __builtin_bit_cast(uint32_t, v1);
+            p[i] = __builtin_amdgcn_perm(b, a, 0x07060302u);
+            if (i + 1 < NP) {
+                v0 -= __builtin_bit_cast(float, a & 0xffff0000u);
+                v1 -= __builtin_bit_cast(float, b & 0xffff0000u);
+            }
+        }
+    } else {
+        typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+        typedef float f32x2 __attribute__((ext_vector_type(2)));
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            p[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{v0, v1}), bf16x2));
+            if (i + 1 < NP) {
+                v0 -= __builtin_bit_cast(float, p[i] << 16);
+                v1 -= __builtin_bit_cast(float, p[i] & 0xffff0000u);
+            }
+        }
     }
 }
 template <int NP>
 __device__ __forceinline__ Frag<NP> split8(const float (&v)[8]) {
+    u32x4 w[NP];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        uint32_t p[NP];
+        split2<NP>(v[2 * e], v[2 * e + 1], p);
+#pragma unroll
+        for (int i = 0; i < NP; ++i) w[i][e] = p[i];
+    }
     Frag<NP> f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        __bf16 p[NP];
-        split<NP>(v[e], p);
-#pragma unroll
-        for (int i = 0; i < NP; ++i) f.p[i][e] = p[i];
-    }
+    for (int i = 0; i < NP; ++i) f.p[i] = __builtin_bit_cast(bf16x8, w[i]);
     return f;
 }
 
@@ -172,29 +197,12 @@ __device__ __forceinline__ Frag<NP> plane_frag(const __bf16* base, int plane, in
 // four values along k (a lane's rows of a result) into the planes
 template <int NP>
 __device__ __forceinline__ void lds_put4(__bf16* base, int plane, int ld, int row, int k, const float (&v)[4]) {
-    __bf16 p[4][NP];
+    uint32_t p[2][NP];
+    split2<NP>(v[0], v[1], p[0]);
+    split2<NP>(v[2], v[3], p[1]);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) split<NP>(v[e], p[e]);
-#pragma unroll
-    for (int i = 0; i < NP; ++i) {
-        typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
-        const bf16x4 w = {p[0][i], p[1][i], p[2][i], p[3][i]};
-        *reinterpret_cast<bf16x4*>(base + i * plane + row * ld + k) = w;
-    }
-}
-
-// four contiguous elements
-__device__ __forceinline__ void load4(const uint16_t* p, float (&v)[4]) {
-    const u32x2 w = *reinterpret_cast<const u32x2*>(p);
-    v[0] = bf16_to_f32(w[0]);
-    v[1] = bf16_hi_to_f32(w[0]);
-    v[2] = bf16_to_f32(w[1]);
-    v[3] = bf16_hi_to_f32(w[1]);
-}
-__device__ __forceinline__ void load4(const float* p, float (&v)[4]) {
-    const f32x4 w = *reinterpret_cast<const f32x4*>(p);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = w[e];
+    for (int i = 0; i < NP; ++i)
+        *reinterpret_cast<u32x2*>(base + i * plane + row * ld + k) = u32x2{p[0][i], p[1][i]};
 }
 
 // Results as operands. The order of a product's k is free as long as both
@@ -294,6 +302,73 @@ __device__ __forceinline__ Frag<3> tile_frag(const float* p) {
     return split8<3>(v);
 }
 
+// Rows of keys or queries in LDS as [token][d], d in places, and their two
+// readings as operands: along d, and along the tokens of a block of 32 for the
+// 16 columns d = 16 m .. + 15. The second is a transposing read of 8 bytes for
+// bf16 (in a group of 16 lanes, lane j points at token j / 4, four columns
+// from 4 (j % 4), and receives column j of the four tokens), single elements
+// for fp32. So keys need no transposed copy.
+template <typename T, int DKP>
+struct RowTile {
+    using L = Tile<T, DKP>;
+    T x[kC * DKP];
+
+    __device__ __forceinline__ Frag<kExact<T>> frag(int token, int unit) const { return tile_frag(x + L::at(token, unit)); }
+    // tokens 16 t + 4 (l / 16) .. + 3 of column 16 m + l % 16
+    __device__ __forceinline__ void column4(int t, int m, uint32_t (&v)[kExact<T> == 1 ? 2 : 4]) const {
+        const int l = lane_id(), l16 = l & 15, l4 = l >> 4;
+        if constexpr (kExact<T> == 1) {
+            const int token = t * 16 + l4 * 4 + (l16 >> 2);
+            const T* p = x + L::at(token, (m >> 1) * 4 + (l16 & 3)) + (m & 1) * 4;
+            typedef short s16x4 __attribute__((ext_vector_type(4)));
+            const s16x4 r = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)p);
+            const u32x2 w = __builtin_bit_cast(u32x2, r);
+            v[0] = w[0];
+            v[1] = w[1];
+        } else {
+            const int p = kplace(m * 16 + l16);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = __builtin_bit_cast(uint32_t, x[L::at(t * 16 + l4 * 4 + e, p >> 3) + (p & 7)]);
+        }
+    }
+    __device__ __forceinline__ void values4(int t, int m, float (&f)[4]) const {
+        if constexpr (kExact<T> == 1) {
+            uint32_t v[2];
+            column4(t, m, v);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                f[2 * e] = bf16_to_f32(v[e]);
+                f[2 * e + 1] = bf16_hi_to_f32(v[e]);
+            }
+        } else {
+            uint32_t v[4];
+            column4(t, m, v);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) f[e] = __builtin_bit_cast(float, v[e]);
+        }
+    }
+    // tokens of block s of 32 as k, in places
+    __device__ __forceinline__ Frag<kExact<T>> token_frag(int s, int m) const {
+        if constexpr (kExact<T> == 1) {
+            uint32_t a[2], b[2];
+            column4(2 * s, m, a);
+            column4(2 * s + 1, m, b);
+            return {{__builtin_bit_cast(bf16x8, u32x4{a[0], a[1], b[0], b[1]})}};
+        } else {
+            float a[4], b[4];
+            values4(2 * s, m, a);
+            values4(2 * s + 1, m, b);
+            return split8<3>({a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]});
+        }
+    }
+    // a unit of 8 elements of token i from column 8 k8 on
+    __device__ __forceinline__ void put(int i, int k8, const Unit<T>& u) {
+        const int p0 = kplace(k8 * 8), p1 = kplace(k8 * 8 + 4);
+        u.put_half(x + L::at(i, p0 >> 3) + (p0 & 4), 0);
+        u.put_half(x + L::at(i, p1 >> 3) + (p1 & 4), 1);
+    }
+};
+
 // The triangular matrices of a chunk (the inverse, the decayed products) in
 // memory: fp32, in places, the blocks of 32 columns that hold anything:
 // lower: columns 0-31 of all 64 rows, then 32-63 of rows 32-63;
@@ -307,16 +382,9 @@ __device__ __forceinline__ int tri_row(int row, int col) {
 // the same in LDS: NP planes of 96 rows of 32 places
 template <int NP>
 __device__ __forceinline__ void tri_put4(__bf16* base, int idx4, const f32x4& v) {
-    typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
     const int row = idx4 >> 3, q = idx4 & 7;
-    __bf16 p[4][NP];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) split<NP>(v[e], p[e]);
-#pragma unroll
-    for (int i = 0; i < NP; ++i) {
-        const bf16x4 w = {p[0][i], p[1][i], p[2][i], p[3][i]};
-        *reinterpret_cast<bf16x4*>(base + i * kTri + Tile<uint16_t, 32>::at(row, q >> 1) + (q & 1) * 4) = w;
-    }
+    const float x[4] = {v[0], v[1], v[2], v[3]};
+    lds_put4<NP>(base, kTri, 0, 0, Tile<uint16_t, 32>::at(row, q >> 1) + (q & 1) * 4, x);
 }
 template <int NP>
 __device__ __forceinline__ Frag<NP> tri_frag(const __bf16* base, int row, int unit) {
@@ -342,17 +410,20 @@ __device__ __forceinline__ Spread spread(int64_t block, int members) {
 inline int64_t spread_blocks(int64_t groups, int members) { return (groups + 7) / 8 * 8 * members; }
 
 // ---------------------------------------------------------------------------
-// Decays of a chunk: G = running sum of g in 64 bits (32-bit sums would lose
+// Decays of a chunk: G = running sum of g / log 2 in 64 bits (32-bit sums would lose
 // the small steps behind a large one), lane l holding token l. g below
 // kGMin is taken as kGMin: e^g is zero all the same, and a full reset
 // (g = -infinity) does not turn G's differences into NaN.
 constexpr double kGMin = -4096.0;
+// e^(sum of g over some tokens) from G's difference: rounded to 32 bits only
+// here, where an exponent of size |d| errs by |d| 2^-24 of a result 2^d
+__device__ __forceinline__ float decay_of(double d) { return exp2_fast((float)d); }
 __device__ __forceinline__ double chunk_decay_sum(const float* __restrict__ g, int64_t start, int n, int H, int h) {
     const int lane = lane_id();
     double v = 0.0;
     if (lane < n) {
         v = (double)g[(size_t)(start + lane) * H + h];
-        v = v < kGMin ? kGMin : v;
+        v = (v < kGMin ? kGMin : v) * 1.4426950408889634074;
     }
 #pragma unroll
     for (int m = 1; m < kC; m <<= 1) {
@@ -392,11 +463,9 @@ __device__ __forceinline__ void put_tile16(float* x, const f32x4& v) {
 }
 __device__ __forceinline__ void chunk_inverse(const float* A, float* X) {
     const int tid = threadIdx.x, wave = wave_id(), l = lane_id();
-    // zero the blocks above the diagonal's
-    for (int i = tid; i < kC * kC; i += 256) {
-        const int r = i >> 6, c = i & 63;
-        if ((c >> 4) > (r >> 4)) X[r * kLdA + c] = 0.0f;
-    }
+    // zero the blocks (0, 1) and (2, 3), the only ones above the diagonal's that are read
+#pragma unroll
+    for (int i = tid; i < 512; i += 256) X[((i >> 8) * 32 + ((i >> 4) & 15)) * kLdA + (i >> 8) * 32 + 16 + (i & 15)] = 0.0f;
     if (wave == 0) {
         const int at = (l >> 4) * 16, c = l & 15;
         float x[16];
@@ -440,7 +509,7 @@ __device__ __forceinline__ void chunk_inverse(const float* A, float* X) {
 // ---------------------------------------------------------------------------
 // Sizes and buffers
 constexpr int kMaxDk = 128;
-constexpr int kCols = 64;  // state columns a workgroup of the chunk chains takes: 16 a wave
+constexpr int kWaveCols = 16;  // state columns a wave of the chains takes
 
 inline int delta_dkp(int Dk) { return Dk <= 64 ? 64 : 128; }
 inline size_t round256(size_t n) { return (n + 255) / 256 * 256; }
@@ -462,7 +531,6 @@ struct DeltaArgs {
     float* dec;      // e^{G_i} and e^{G_last - G_i}: (2, 64)
     float* inv;      // the chunk's inverse: kTri
     float* att;      // the decayed products of q and k: kTri
-    void *kt, *qt;   // keys and queries, transposed, tokens in places: (Dk padded, 64)
     float *dS1, *dU; // backward: gradients of the state that leaves the chunk, and of U
 };
 
@@ -471,7 +539,7 @@ inline int delta_check(int64_t T, int32_t nseq, int32_t Hk, int32_t Hv, int32_t 
     if (Hv % Hk || Hv > 65535 || nseq > (1 << 24)) return SSMP_ERR_SHAPE;
     if ((int64_t)Hv * Dv > kMaxRow || (int64_t)Hk * Dk > kMaxRow) return SSMP_ERR_SHAPE;
     if (T * Hv * (int64_t)(Dv > Dk ? Dv : Dk) >= (int64_t(1) << 40)) return SSMP_ERR_SHAPE;
-    if ((int64_t)(nseq + 7) * Hv * ((Dv + kCols - 1) / kCols) >= (int64_t(1) << 31)) return SSMP_ERR_SHAPE;
+    if ((int64_t)(nseq + 7) * Hv * ((Dv + 63) / 64) >= (int64_t(1) << 31)) return SSMP_ERR_SHAPE;
     if ((T / kC + nseq + 7) * Hv >= (int64_t(1) << 31)) return SSMP_ERR_SHAPE;
     if (dtype != SSMP_F32 && dtype != SSMP_BF16) return SSMP_ERR_UNSUPPORTED;
     if (Dk % 8 || Dv % 8 || Dk > kMaxDk) return SSMP_ERR_UNSUPPORTED;

@@ -7,7 +7,7 @@
 //   (I + L diag(beta)) E = X,  X = V - diag(e^G) K S,  L = D . K K^T below the diagonal,
 //   out = scale (diag(e^G) Q S + P U),                 P = D . Q K^T on and below it,
 //   S'  = e^{G_last} S + (diag(e^{G_last - G}) K)^T U.
-// What does not depend on the state (the inverse, P, K^T, the decays) is made
+// What does not depend on the state (the inverse, P, the decays) is made
 // for all chunks at once by k_delta_prepare; k_delta_chain then goes along
 // each sequence's chunks with the state in registers.
 #include "delta_prepare.h"
@@ -19,18 +19,19 @@ namespace ssmp {
 template <typename T>
 constexpr int kOutP = std::is_same<T, float>::value ? 3 : 2;
 
-// One workgroup per (sequence, value head, 64 columns of the state), 16
+// One workgroup per (sequence, value head, 64 or 128 columns of the state), 16
 // columns a wave. Columns do not meet in the chain, and a wave's results are
 // its next right operands in the registers they are in (kplace), so the waves
 // share nothing but the left operands, which the workgroup holds in LDS while
 // the next chunk's are under way in registers: two barriers a chunk.
 // SAVE: keep S and E for the backward.
-template <typename T, int DKP, bool SAVE>
-__global__ __launch_bounds__(256, NWG<T>) void k_delta_chain(DeltaArgs a) {
+template <typename T, int DKP, int NW, bool SAVE>
+__global__ __launch_bounds__(NW * 64) void k_delta_chain(DeltaArgs a) {
     constexpr int NX = kExact<T>, NO = kOutP<T>;
     constexpr int MT = DKP / 16;  // 16-row tiles of the state
-    using Loads = ChainLoads<T, DKP, 2, 1, NO>;
+    using Loads = ChainLoads<T, DKP, NO, NW * 64>;
     __shared__ alignas(16) typename Loads::Tiles lds;
+    constexpr int kCols = NW * kWaveCols;
     const int ncb = (a.Dv + kCols - 1) / kCols, group = a.Hv / a.Hk;
     const Spread sp = spread(blockIdx.x, ncb * group);
     if (sp.group >= (int64_t)a.nseq * a.Hk) return;
@@ -70,8 +71,8 @@ __global__ __launch_bounds__(256, NWG<T>) void k_delta_chain(DeltaArgs a) {
             const auto sb = split_tiles<3>(S[2 * s], S[2 * s + 1]);
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
-                mma<3>(x[m], lds.row_frag(0, m * 16 + l16, s * 4 + l4), sb);
-                mma<NO>(o[m], lds.row_frag(1, m * 16 + l16, s * 4 + l4), sb);
+                mma<3>(x[m], lds.k.frag(m * 16 + l16, s * 4 + l4), sb);
+                mma<NO>(o[m], lds.q.frag(m * 16 + l16, s * 4 + l4), sb);
             }
         }
 #pragma unroll
@@ -117,7 +118,7 @@ __global__ __launch_bounds__(256, NWG<T>) void k_delta_chain(DeltaArgs a) {
 #pragma unroll
             for (int m = 2 * s; m < 4; ++m) mma<NO>(o[m], tri_frag<NO>(lds.att, s * 32 + m * 16 + l16, l4), ub);
 #pragma unroll
-            for (int m = 0; m < MT; ++m) mma<3>(S[m], lds.col_frag(0, m * 16 + l16, s * 4 + l4), wb);
+            for (int m = 0; m < MT; ++m) mma<3>(S[m], lds.k.token_frag(s, m), wb);
         }
         store_column<T>(a.out, start, cn, a.Hv, hv, a.Dv, cv, o, a.scale);
     }
@@ -128,25 +129,29 @@ template <typename T, int DKP>
 int launch_delta_fwd(const DeltaArgs& a, hipStream_t s) {
     if (a.T > 0)
         if (const int st = launch_delta_prepare<T, DKP, false>(a, s)) return st;
-    const int ncb = (a.Dv + kCols - 1) / kCols;
-    const unsigned blocks = (unsigned)spread_blocks((int64_t)a.nseq * a.Hk, ncb * (a.Hv / a.Hk));
-    if (a.S0) k_delta_chain<T, DKP, true><<<blocks, 256, 0, s>>>(a);
-    else k_delta_chain<T, DKP, false><<<blocks, 256, 0, s>>>(a);
+    const int nw = chain_waves(a);
+    const unsigned blocks = chain_blocks(a, nw);
+    if (a.S0) {
+        if (nw == 8) k_delta_chain<T, DKP, 8, true><<<blocks, nw * 64, 0, s>>>(a);
+        else k_delta_chain<T, DKP, 4, true><<<blocks, nw * 64, 0, s>>>(a);
+    } else {
+        if (nw == 8) k_delta_chain<T, DKP, 8, false><<<blocks, nw * 64, 0, s>>>(a);
+        else k_delta_chain<T, DKP, 4, false><<<blocks, nw * 64, 0, s>>>(a);
+    }
     SSMP_LAUNCH_CHECK();
     return SSMP_OK;
 }
 
 struct DeltaFwdLayout {
-    size_t dec, inv, att, kt, total;
+    size_t dec, inv, att, total;
 };
-inline DeltaFwdLayout delta_fwd_layout(int64_t T, int32_t nseq, int32_t Hk, int32_t Hv, int32_t Dk, int32_t dtype) {
-    const size_t n = (size_t)delta_slots(T, nseq), elt = dtype == SSMP_F32 ? 4 : 2;
+inline DeltaFwdLayout delta_fwd_layout(int64_t T, int32_t nseq, int32_t Hv) {
+    const size_t n = (size_t)delta_slots(T, nseq);
     DeltaFwdLayout L;
     L.dec = 0;
     L.inv = L.dec + round256(n * Hv * 2 * kC * 4);
     L.att = L.inv + round256(n * Hv * kTri * 4);
-    L.kt = L.att + round256(n * Hv * kTri * 4);
-    L.total = L.kt + round256(n * Hk * delta_dkp(Dk) * kC * elt);
+    L.total = L.att + round256(n * Hv * kTri * 4);
     return L;
 }
 
@@ -164,7 +169,7 @@ extern "C" size_t gated_delta_pack_fwd_scratch_bytes(int64_t T, int32_t nseq, in
                                                      int32_t Dv, int32_t dtype) {
     using namespace ssmp;
     if (delta_check(T, nseq, Hk, Hv, Dk, Dv, dtype) || T == 0) return 0;
-    return delta_fwd_layout(T, nseq, Hk, Hv, Dk, dtype).total;
+    return delta_fwd_layout(T, nseq, Hv).total;
 }
 
 extern "C" int gated_delta_pack_fwd(const void* q, const void* k, const void* v, const float* g, const float* beta,
@@ -182,7 +187,7 @@ extern "C" int gated_delta_pack_fwd(const void* q, const void* k, const void* v,
     if (T > 0 && saved && saved_bytes < gated_delta_pack_saved_bytes(T, nseq, Hk, Hv, Dk, Dv))
         return SSMP_ERR_WORKSPACE;
     if (T == 0 && !final_state) return SSMP_OK;
-    const DeltaFwdLayout L = delta_fwd_layout(T, nseq, Hk, Hv, Dk, dtype);
+    const DeltaFwdLayout L = delta_fwd_layout(T, nseq, Hv);
     char* const ws = static_cast<char*>(scratch);
     DeltaArgs a = {};
     a.q = q;
@@ -205,7 +210,6 @@ extern "C" int gated_delta_pack_fwd(const void* q, const void* k, const void* v,
         a.dec = reinterpret_cast<float*>(ws + L.dec);
         a.inv = reinterpret_cast<float*>(ws + L.inv);
         a.att = reinterpret_cast<float*>(ws + L.att);
-        a.kt = ws + L.kt;
         if (saved) {
             a.S0 = static_cast<float*>(saved);
             a.E = reinterpret_cast<float*>(static_cast<char*>(saved) +

@@ -7,8 +7,7 @@
 namespace ssmp {
 
 // One workgroup per (slot, value head); the heads of a group run on one XCD,
-// whose L2 then holds their keys and queries, and the first of them also
-// writes these transposed.
+// whose L2 then holds their keys and queries.
 //   forward:  (I + L diag(beta))^-1 and P,           both lower triangular
 //   backward: (I + diag(beta) L)^-T and scale P^T,   both upper triangular
 template <typename T, int DKP, bool BWD>
@@ -48,8 +47,8 @@ __global__ __launch_bounds__(256) void k_delta_prepare(DeltaArgs a) {
         G[l] = s;
         beta[l] = l < c.n ? a.beta[(size_t)(c.start + l) * a.Hv + hv] : 0.0f;
         const double last = __shfl(s, kC - 1);
-        a.dec[sh * 2 * kC + l] = expf((float)s);
-        a.dec[sh * 2 * kC + kC + l] = expf((float)(last - s));
+        a.dec[sh * 2 * kC + l] = decay_of(s);
+        a.dec[sh * 2 * kC + kC + l] = decay_of(last - s);
     }
     __syncthreads();
     // Wave w has rows 16 w .. of both products. kk: K K^T. qk: forward K Q^T
@@ -74,35 +73,20 @@ __global__ __launch_bounds__(256) void k_delta_prepare(DeltaArgs a) {
                 if (n >= wave) mma<NX>(qk[n], ka, tile_frag(Ql + Rows::at(j, u)));
         }
     }
-    if (sp.member == 0) {
-        // keys (and for the backward queries) as [d][token], 8 places a lane
-        for (int w = 0; w < (BWD ? 2 : 1); ++w) {
-            const T* const src = w ? Ql : Kl;
-            T* const dst = static_cast<T*>(w ? a.qt : a.kt) + ((size_t)slot * a.Hk + hk) * DKP * kC;
-            for (int u = tid; u < DKP * 8; u += 256) {
-                const int d = u >> 3, p = u & 7, i = (p >> 2) * 32 + (p & 3) * 4;
-                T v[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int t = i + (e < 4 ? e : 12 + e);
-                    v[e] = src[Rows::at(t, d >> 3) + (d & 7)];
-                }
-                put8(dst + d * kC + p * 8, v);
-            }
-        }
-    }
     __syncthreads();
     float* const att = a.att + sh * kTri;
 #pragma unroll
     for (int n = 0; n < 4; ++n) {
-        f32x4 p;
+        f32x4 p = {0, 0, 0, 0};
+        if (!BWD || n <= wave) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int i = wave * 16 + l4 * 4 + r, j = n * 16 + l16;  // row and column of the tiles
-            const float d = expf((float)(i > j ? G[i] - G[j] : G[j] - G[i]));
-            A[i * kLdA + j] = i > j ? (BWD ? beta[i] : beta[j]) * d * kk[n][r] : 0.0f;
-            if constexpr (BWD) p[r] = i >= j ? d * qk[n][r] * a.scale : 0.0f;
-            else p[r] = j >= i ? d * qk[n][r] : 0.0f;
+            for (int r = 0; r < 4; ++r) {
+                const int i = wave * 16 + l4 * 4 + r, j = n * 16 + l16;  // row and column of the tiles
+                const float d = decay_of(i > j ? G[i] - G[j] : G[j] - G[i]);
+                if (n <= wave) A[i * kLdA + j] = i > j ? (BWD ? beta[i] : beta[j]) * d * kk[n][r] : 0.0f;
+                if constexpr (BWD) p[r] = i >= j ? d * qk[n][r] * a.scale : 0.0f;
+                else p[r] = j >= i ? d * qk[n][r] : 0.0f;
+            }
         }
         const int row = n * 16 + l16, k = wave * 16 + l4 * 4;
         // what lies in neither block of the other triangle is not stored
@@ -133,62 +117,48 @@ int launch_delta_prepare(const DeltaArgs& a, hipStream_t s) {
 }
 
 // ---------------------------------------------------------------------------
-// The operands of one chunk that a chain holds in LDS, for its four waves, and
-// the registers in which the next chunk's are under way meanwhile.
-//   rows:  keys (forward: and queries), [token][d in places]
-//   cols:  keys (backward: and queries) transposed, [d][token in places]
-//   tris:  the inverse (3 planes) and the products (NP planes)
-// 78 KB for bf16 heads of 128, so that two workgroups share a CU.
-template <typename T, int DKP, int NROWS, int NCOLS, int NP>
+// The operands of one chunk that a chain holds in LDS for all its waves, and
+// the registers in which the next chunk's are under way meanwhile: keys and
+// queries, the inverse (3 planes) and the products (NP planes). 62 to 68 KB
+// for bf16 heads of 128.
+template <typename T, int DKP, int NP>
 struct ChainTiles {
-    static constexpr int kRow = kC * DKP, kCol = DKP * kC;
-    using Rows = Tile<T, DKP>;
-    using Cols = Tile<T, kC>;
-    T rows[NROWS][kRow];
-    T cols[NCOLS][kCol];
+    RowTile<T, DKP> k, q;
     __bf16 inv[3 * kTri];
     __bf16 att[NP * kTri];
     float eg[kC], el[kC], beta[kC];
-
-    __device__ __forceinline__ Frag<kExact<T>> row_frag(int w, int row, int unit) const {
-        return tile_frag(rows[w] + Rows::at(row, unit));
-    }
-    __device__ __forceinline__ Frag<kExact<T>> col_frag(int w, int row, int unit) const {
-        return tile_frag(cols[w] + Cols::at(row, unit));
-    }
 };
 
-template <typename T, int DKP, int NROWS, int NCOLS, int NP>
+template <typename T, int DKP, int NP, int THREADS>
 struct ChainLoads {
-    using Tiles = ChainTiles<T, DKP, NROWS, NCOLS, NP>;
-    static constexpr int kN = DKP * kC / 8 / 256;  // units of 8 elements a thread
-    Unit<T> rows[NROWS][kN], cols[NCOLS][kN];
-    f32x4 inv[kTri / 4 / 256], att[kTri / 4 / 256];
+    using Tiles = ChainTiles<T, DKP, NP>;
+    static constexpr int kN = DKP * kC / 8 / THREADS;                         // units of 8 elements a thread
+    static constexpr int kM = (kTri / 4 + THREADS - 1) / THREADS;             // units of 4 of a triangle
+    static __device__ __forceinline__ bool tri_on(int x) { return (x + 1) * THREADS <= kTri / 4 || threadIdx.x + x * THREADS < kTri / 4; }
+    Unit<T> k[kN], q[kN];
+    f32x4 inv[kM], att[kM];
     float dec;
 
     __device__ __forceinline__ void load(const DeltaArgs& a, int64_t slot, int64_t start, int n, int hk, int hv) {
         const int tid = threadIdx.x;
         const size_t sh = (size_t)slot * a.Hv + hv;
-        const size_t first = ((size_t)start * a.Hk + hk) * a.Dk, tr = ((size_t)slot * a.Hk + hk) * DKP * kC;
+        const size_t first = ((size_t)start * a.Hk + hk) * a.Dk;
         const int stride = a.Hk * a.Dk;
-        const auto k = rows_rsrc(static_cast<const T*>(a.k) + first, n, stride, a.Dk);
-        const auto q = rows_rsrc(static_cast<const T*>(a.q) + first, n, stride, a.Dk);
-        const auto kt = bytes_rsrc(static_cast<const T*>(a.kt) + tr, DKP * kC * sizeof(T));
-        const auto qt = bytes_rsrc(static_cast<const T*>(a.qt) + tr, DKP * kC * sizeof(T));
+        const auto kr = rows_rsrc(static_cast<const T*>(a.k) + first, n, stride, a.Dk);
+        const auto qr = rows_rsrc(static_cast<const T*>(a.q) + first, n, stride, a.Dk);
 #pragma unroll
         for (int x = 0; x < kN; ++x) {
-            const int u = tid + x * 256, i = u / (DKP / 8), k8 = u % (DKP / 8);
+            const int u = tid + x * THREADS, i = u / (DKP / 8), k8 = u % (DKP / 8);
             const uint32_t o = k8 * 8 < a.Dk ? (uint32_t)(i * stride + k8 * 8) * (uint32_t)sizeof(T) : kNowhere;
-            rows[0][x].load(k, o);
-            if constexpr (NROWS > 1) rows[1][x].load(q, o);
-            cols[0][x].load(kt, (uint32_t)u * 8u * (uint32_t)sizeof(T));
-            if constexpr (NCOLS > 1) cols[1][x].load(qt, (uint32_t)u * 8u * (uint32_t)sizeof(T));
+            k[x].load(kr, o);
+            q[x].load(qr, o);
         }
 #pragma unroll
-        for (int x = 0; x < kTri / 4 / 256; ++x) {
-            inv[x] = *reinterpret_cast<const f32x4*>(at_bytes(a.inv + sh * kTri, (uint32_t)(tid + x * 256) * 16u));
-            att[x] = *reinterpret_cast<const f32x4*>(at_bytes(a.att + sh * kTri, (uint32_t)(tid + x * 256) * 16u));
-        }
+        for (int x = 0; x < kM; ++x)
+            if (tri_on(x)) {
+                inv[x] = *reinterpret_cast<const f32x4*>(at_bytes(a.inv + sh * kTri, (uint32_t)(tid + x * THREADS) * 16u));
+                att[x] = *reinterpret_cast<const f32x4*>(at_bytes(a.att + sh * kTri, (uint32_t)(tid + x * THREADS) * 16u));
+            }
         dec = 0.0f;
         if (tid < 2 * kC) dec = a.dec[sh * 2 * kC + tid];
         else if (tid < 2 * kC + n) dec = a.beta[(size_t)(start + tid - 2 * kC) * a.Hv + hv];
@@ -197,35 +167,33 @@ struct ChainLoads {
         const int tid = threadIdx.x;
 #pragma unroll
         for (int x = 0; x < kN; ++x) {
-            const int u = tid + x * 256, i = u / (DKP / 8), k8 = u % (DKP / 8);
-            // d = 8 k8 .. + 3 and + 4 .. + 7 go to two places
-            const int p0 = kplace(k8 * 8), p1 = kplace(k8 * 8 + 4);
-#pragma unroll
-            for (int w = 0; w < NROWS; ++w) {
-                rows[w][x].put_half(t.rows[w] + Tiles::Rows::at(i, p0 >> 3) + (p0 & 4), 0);
-                rows[w][x].put_half(t.rows[w] + Tiles::Rows::at(i, p1 >> 3) + (p1 & 4), 1);
-            }
-#pragma unroll
-            for (int w = 0; w < NCOLS; ++w) {
-                T* const p = t.cols[w] + Tiles::Cols::at(u >> 3, u & 7);
-                cols[w][x].put_half(p, 0);
-                cols[w][x].put_half(p + 4, 1);
-            }
+            const int u = tid + x * THREADS, i = u / (DKP / 8), k8 = u % (DKP / 8);
+            t.k.put(i, k8, k[x]);
+            t.q.put(i, k8, q[x]);
         }
 #pragma unroll
-        for (int x = 0; x < kTri / 4 / 256; ++x) {
-            tri_put4<3>(t.inv, tid + x * 256, inv[x]);
-            tri_put4<NP>(t.att, tid + x * 256, att[x]);
-        }
+        for (int x = 0; x < kM; ++x)
+            if (tri_on(x)) {
+                tri_put4<3>(t.inv, tid + x * THREADS, inv[x]);
+                tri_put4<NP>(t.att, tid + x * THREADS, att[x]);
+            }
         if (tid < kC) t.eg[tid] = dec;
         else if (tid < 2 * kC) t.el[tid - kC] = dec;
         else if (tid < 3 * kC) t.beta[tid - 2 * kC] = dec;
     }
 };
 
-// workgroups of a chain that share a CU (as waves per SIMD, for the register budget)
-template <typename T>
-constexpr int NWG = std::is_same<T, float>::value ? 1 : 2;
+// Waves of a chain's workgroup. Eight (128 columns) read a chunk's operands
+// once for a whole head; with fewer heads than CUs, two workgroups of four
+// bring more of the chip to work and each chunk's chain ends sooner.
+constexpr int kCUs = 256;
+inline int chain_waves(const DeltaArgs& a) {
+    return a.Dv > 64 && (int64_t)a.nseq * a.Hv * ((a.Dv + 127) / 128) >= kCUs ? 8 : 4;
+}
+inline unsigned chain_blocks(const DeltaArgs& a, int waves) {
+    const int ncb = (a.Dv + waves * kWaveCols - 1) / (waves * kWaveCols);
+    return (unsigned)spread_blocks((int64_t)a.nseq * a.Hk, ncb * (a.Hv / a.Hk));
+}
 
 // A lane's elements of a (tokens, Dv) tensor of one head, as a result of 4
 // tiles holds them: tokens 16 m + 4 (l / 16) + r of its column (kNowhere where
