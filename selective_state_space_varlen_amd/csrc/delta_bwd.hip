@@ -16,7 +16,8 @@
 //   dg_t = sum of dG_i, i >= t in the chunk.
 // k_delta_prepare makes what no gradient enters, k_delta_chain_bwd walks each
 // sequence's chunks back with dS in registers, and k_delta_grads forms the
-// chunks' gradients, all at once, from S, E, dS' and dU.
+// chunks' gradients, all at once, from S, E, dS' and dU (k_delta_dg the last
+// sums of dg).
 #include "delta_prepare.h"
 
 namespace ssmp {
@@ -117,105 +118,116 @@ __global__ __launch_bounds__(NW * 64) void k_delta_chain_bwd(DeltaArgs a) {
             const auto ub = split_tiles<3>(u[2 * s], u[2 * s + 1]);
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
-                mma<3>(S[m], lds.q.token_frag(s, m), ob);
-                mma<3>(S[m], lds.k.token_frag(s, m), ub);
+                mma<3>(S[m], lds.q.token_frag(l, s, m), ob);
+                mma<3>(S[m], lds.k.token_frag(l, s, m), ub);
             }
         }
     }
     if (a.dh0 && busy) store_matrix(a.dh0 + state, a.Dk, a.Dv, cs, S);
 }
 
-// One workgroup per (slot, key head), over the value heads of its group, whose
-// dq and dk it adds in registers (GROUP; a head that has its keys to itself
-// needs no second set). Wave w of DKP / 16 holds columns 16 w .. of dq and dk
-// for all 64 tokens, so its rows of S and dS' come straight from memory, and
-// some of the tiles of a^T and b^T. The next 64 columns of dOut, E and dU are
-// under way in registers while the present ones are multiplied.
-template <typename T, int DKP, bool GROUP>
-__global__ __launch_bounds__(DKP * 4) void k_delta_grads(DeltaArgs a) {
+// One workgroup per (slot, key head, 64 columns of dq and dk), over the value
+// heads of the group, whose dq and dk it adds in registers. Wave w holds
+// columns 16 w .. for all 64 tokens, so its rows of S and dS' come straight
+// from memory, and row tile w of a^T and b^T. 74 KB of LDS for bf16, so that
+// two workgroups share a CU and one's loads pass behind the other's products.
+// The rows of q.dq + k.(dkread - dkwrite) over these columns go to a.rows, for
+// k_delta_dg to add up.
+constexpr int kDh = 64;
+template <typename T>
+__global__ __launch_bounds__(256, kExact<T> == 1 ? 2 : 1) void k_delta_grads(DeltaArgs a) {
     constexpr int NX = kExact<T>;
-    constexpr int kThreads = DKP * 4, kWaves = DKP / 16;
-    constexpr int SG = 512 / kThreads;    // 8-column units a thread stages
-    constexpr int TT = 16 / kWaves;       // tiles of a^T a wave holds: row tile w / (4 / TT)
-    constexpr int LT = kC + 8, PT = kC * LT;
+    using Plane = Tile<uint16_t, kC>;
+    constexpr int PT = kC * kC;
     // planes of dOut, dE and U (64 columns at a time, [token][column]), then of
     // a or -b and its transpose
     __shared__ alignas(16) __bf16 lds[(NX + 6) * PT];
-    __shared__ alignas(16) RowTile<T, DKP> kt, qt;
+    __shared__ alignas(16) RowTile<T, kDh> kt, qt;
     __shared__ double G[kC];
     __shared__ alignas(16) float decay[2][kC];
-    __shared__ float red[kWaves][kC], ends[kWaves];
-    const int64_t slot = blockIdx.x;
-    const int hk = blockIdx.y, group = a.Hv / a.Hk;
+    __shared__ float red[4][kC], ends[16];
+    const int halves = (a.Dk + kDh - 1) / kDh;
+    const Spread sp = spread(blockIdx.x, halves);
+    if (sp.group >= delta_slots(a.T, a.nseq) * a.Hk) return;
+    const int64_t slot = sp.group / a.Hk;
+    const int hk = (int)(sp.group % a.Hk), half = sp.member, group = a.Hv / a.Hk;
     Chunk c;
     if (!chunk_at(a.cu, a.nseq, a.T, slot, c)) return;
-    const int tid = threadIdx.x, wave = wave_id(), l = lane_id(), l16 = l & 15, l4 = l >> 4;
+    const int wave = wave_id();
     __bf16* const Op = lds;
     __bf16* const Ep = lds + NX * PT;
     __bf16* const Up = Ep + 3 * PT;
     __bf16* const M = lds;
     __bf16* const Mt = lds + 3 * PT;
-    for (int u = tid; u < kC * DKP / 8; u += kThreads) {
-        const int i = u / (DKP / 8), k8 = u % (DKP / 8);
+    {
+        const int stride = a.Hk * a.Dk, d0 = half * kDh;
         const size_t first = ((size_t)c.start * a.Hk + hk) * a.Dk;
-        const uint32_t o = k8 * 8 < a.Dk ? (uint32_t)(i * a.Hk * a.Dk + k8 * 8) * (uint32_t)sizeof(T) : kNowhere;
-        Unit<T> x, y;
-        x.load(rows_rsrc(static_cast<const T*>(a.k) + first, c.n, a.Hk * a.Dk, a.Dk), o);
-        y.load(rows_rsrc(static_cast<const T*>(a.q) + first, c.n, a.Hk * a.Dk, a.Dk), o);
-        kt.put(i, k8, x);
-        qt.put(i, k8, y);
+        const auto kr = rows_rsrc(static_cast<const T*>(a.k) + first, c.n, stride, a.Dk);
+        const auto qr = rows_rsrc(static_cast<const T*>(a.q) + first, c.n, stride, a.Dk);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const int u = threadIdx.x + x * 256, i = u >> 3, k8 = u & 7;
+            const uint32_t o =
+                d0 + k8 * 8 < a.Dk ? (uint32_t)(i * stride + d0 + k8 * 8) * (uint32_t)sizeof(T) : kNowhere;
+            Unit<T> ku, qu;
+            ku.load(kr, o);
+            qu.load(qr, o);
+            kt.put(i, k8, ku);
+            qt.put(i, k8, qu);
+        }
     }
-    const int d = wave * 16 + l16;                       // this lane's column of dq and dk
-    const int tj = wave / (4 / TT), ti0 = (wave % (4 / TT)) * TT;  // tiles (tj, ti0 + x) of a^T: rows j, columns i
+    const int d0 = half * kDh + wave * 16;  // this wave's first column of dq and dk
     f32x4 tq[4] = {}, tk[4] = {};
     for (int hv = hk * group; hv < (hk + 1) * group; ++hv) {
         const size_t sh = (size_t)slot * a.Hv + hv;
-        Unit<T> fo[SG];
-        Unit<float> fE[SG], fU[SG];
-        float beta[SG], db[SG];
-        const auto stage_load = [&](int v0) {
-#pragma unroll
-            for (int x = 0; x < SG; ++x) {
-                const int u = tid + x * kThreads, t = u >> 3, e = (u & 7) * 8;
-                const bool on = v0 + e < a.Dv;
-                const size_t ws = (sh * kC + t) * a.Dv + v0 + e;
-                fo[x].load(static_cast<const T*>(a.dout) + ((size_t)(c.start + t) * a.Hv + hv) * a.Dv + v0 + e,
-                           on && t < c.n);
-                fE[x].load(a.E + ws, on);
-                fU[x].load(a.dU + ws, on);
-            }
-        };
-        stage_load(0);
-#pragma unroll
-        for (int x = 0; x < SG; ++x) {
-            const int t = (tid + x * kThreads) >> 3;
-            beta[x] = t < c.n ? a.beta[(size_t)(c.start + t) * a.Hv + hv] : 0.0f;
-            db[x] = 0.0f;
+        __syncthreads();  // the last head's G and decays have been read
+        const int tid0 = fresh(threadIdx.x);
+        {
+            const float* const dec = a.dec + sh * kDec;
+            if (wave < 2) reinterpret_cast<float*>(G)[tid0] = *at_bytes(dec, (uint32_t)tid0 * 4u);
+            else (&decay[0][0])[tid0 - 2 * kC] = *at_bytes(dec, (uint32_t)tid0 * 4u);
         }
-        __syncthreads();  // the last head's sums have been read
-        if (wave == 0) {
-            G[l] = chunk_decay_sum(a.g, c.start, c.n, a.Hv, hv);
-            decay[0][l] = a.dec[sh * 2 * kC + l];
-            decay[1][l] = a.dec[sh * 2 * kC + kC + l];
-        }
+        const auto brows = rows_rsrc(a.beta + (size_t)c.start * a.Hv + hv, c.n, a.Hv, 1);
+        float beta[2], db[2] = {};
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+            beta[x] = Elt<float>::cvt(Elt<float>::raw_rsrc(brows, (uint32_t)(((tid0 + x * 256) >> 3) * a.Hv) * 4u));
         f32x4 dq[4] = {}, dr[4] = {}, dw[4] = {};  // dq, dk read, dk write
-        f32x4 at[TT] = {}, bt[TT] = {};
+        f32x4 at[4] = {}, bt[4] = {};              // row tile `wave` of a^T and b^T
         float sd = 0.0f;                           // <dS', S>
+        const auto orows = rows_rsrc(static_cast<const T*>(a.dout) + ((size_t)c.start * a.Hv + hv) * a.Dv, c.n,
+                                     a.Hv * a.Dv, a.Dv);
+        const auto vrows = rows_rsrc(static_cast<const T*>(a.dv) + ((size_t)c.start * a.Hv + hv) * a.Dv, c.n,
+                                     a.Hv * a.Dv, a.Dv);
+        const auto erows = rows_rsrc(a.E + sh * kC * a.Dv, kC, a.Dv, a.Dv);
+        const auto urows = rows_rsrc(a.dU + sh * kC * a.Dv, kC, a.Dv, a.Dv);
+        const auto srows = rows_rsrc(a.S0 + sh * a.Dk * a.Dv, a.Dk, a.Dv, a.Dv);
+        const auto grows = rows_rsrc(a.dS1 + sh * a.Dk * a.Dv, a.Dk, a.Dv, a.Dv);
         for (int v0 = 0; v0 < a.Dv; v0 += 64) {
-            Unit<float> s0[2], s1[2];              // this lane's row of S and dS'
+            const int tid = fresh(threadIdx.x), l = tid & 63, l16 = l & 15, l4 = l >> 4;
+            Unit<T> fo[2];
+            Unit<float> fE[2], fU[2], s0[2], s1[2];
 #pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                const int k0 = s * 32 + l4 * 8;
-                const bool on = d < a.Dk && v0 + k0 < a.Dv;
-                const size_t o = (sh * a.Dk + d) * a.Dv + v0 + k0;
-                s0[s].load(a.S0 + o, on);
-                s1[s].load(a.dS1 + o, on);
+            for (int x = 0; x < 2; ++x) {
+                const int u = tid + x * 256, t = u >> 3, e = v0 + (u & 7) * 8;
+                const bool on = e < a.Dv;
+                fo[x].load(orows, on ? (uint32_t)(t * a.Hv * a.Dv + e) * (uint32_t)sizeof(T) : kNowhere);
+                fE[x].load(erows, on ? (uint32_t)(t * a.Dv + e) * 4u : kNowhere);
+                fU[x].load(urows, on ? (uint32_t)(t * a.Dv + e) * 4u : kNowhere);
             }
 #pragma unroll
-            for (int x = 0; x < SG; ++x) {
-                const int u = tid + x * kThreads, t = u >> 3, e = (u & 7) * 8;
+            for (int s = 0; s < 2; ++s) {  // this lane's row of S and dS'
+                const int e = v0 + s * 32 + l4 * 8;
+                const uint32_t o = e < a.Dv ? (uint32_t)((d0 + l16) * a.Dv + e) * 4u : kNowhere;
+                s0[s].load(srows, o);
+                s1[s].load(grows, o);
+            }
+            if (v0) __syncthreads();  // the last block's planes have been read
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const int u = tid + x * 256, t = u >> 3, e = v0 + (u & 7) * 8;
+                __builtin_amdgcn_sched_barrier(0);
                 float E[8], dU[8];
-                T dv[8];
 #pragma unroll
                 for (int p = 0; p < 8; ++p) {
                     E[p] = fE[x].w[p >> 2][p & 3];
@@ -223,13 +235,15 @@ __global__ __launch_bounds__(DKP * 4) void k_delta_grads(DeltaArgs a) {
                     db[x] = fmaf(dU[p], E[p], db[x]);
                     E[p] *= beta[x];
                     dU[p] *= beta[x];
-                    Elt<T>::st(dv, p, dU[p]);
                 }
-                if (v0 + e < a.Dv && t < c.n)
-                    put8(static_cast<T*>(a.dv) + ((size_t)(c.start + t) * a.Hv + hv) * a.Dv + v0 + e, dv);
+                if (half == 0) {
+                    Unit<T> dv;
+                    dv.pack(dU);
+                    dv.store(vrows, e < a.Dv ? (uint32_t)(t * a.Hv * a.Dv + e) * (uint32_t)sizeof(T) : kNowhere);
+                }
                 const auto po = unit_planes(fo[x]);
                 const auto pe = split8<3>(dU), pu = split8<3>(E);
-                const int o = t * LT + e;
+                const int o = Plane::at(t, u & 7);
 #pragma unroll
                 for (int p = 0; p < NX; ++p) *reinterpret_cast<bf16x8*>(Op + p * PT + o) = po.p[p];
 #pragma unroll
@@ -239,96 +253,98 @@ __global__ __launch_bounds__(DKP * 4) void k_delta_grads(DeltaArgs a) {
                 }
             }
             __syncthreads();
-            if (v0 + 64 < a.Dv) stage_load(v0 + 64);
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
-                const int k0 = s * 32 + l4 * 8;
+                const int u = s * 4 + l4;
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) sd = fmaf(s0[s].w[e >> 2][e & 3], s1[s].w[e >> 2][e & 3], sd);
-                const auto sb = unit_planes(s0[s]), db1 = unit_planes(s1[s]);
+                const auto sb = unit_planes(s0[s]), gb = unit_planes(s1[s]);
+                const auto uw = tile_planes<3>(Up, PT, Plane::at(wave * 16 + l16, u));
 #pragma unroll
                 for (int m = 0; m < 4; ++m) {
-                    __builtin_amdgcn_sched_barrier(0);
-                    mma<3>(dq[m], plane_frag<NX>(Op, PT, LT, m * 16 + l16, k0), sb);
-                    mma<3>(dr[m], plane_frag<3>(Ep, PT, LT, m * 16 + l16, k0), sb);
-                    mma<3>(dw[m], plane_frag<3>(Up, PT, LT, m * 16 + l16, k0), db1);
-                }
-                __builtin_amdgcn_sched_barrier(0);
-                const auto uw = plane_frag<3>(Up, PT, LT, tj * 16 + l16, k0);
-#pragma unroll
-                for (int x = 0; x < TT; ++x) {
-                    const int i = ti0 + x;
-                    if (i >= tj) {  // below the diagonal of a and b
-                        mma<3>(at[x], uw, plane_frag<NX>(Op, PT, LT, i * 16 + l16, k0));
-                        mma<3>(bt[x], uw, plane_frag<3>(Ep, PT, LT, i * 16 + l16, k0));
+                    const int o = Plane::at(m * 16 + l16, u);
+                    const auto po = tile_planes<NX>(Op, PT, o);
+                    const auto pe = tile_planes<3>(Ep, PT, o);
+                    mma<3>(dq[m], po, sb);
+                    mma<3>(dr[m], pe, sb);
+                    mma<3>(dw[m], tile_planes<3>(Up, PT, o), gb);
+                    if (m >= wave) {  // below the diagonal of a and b
+                        mma<3>(at[m], uw, po);
+                        mma<3>(bt[m], uw, pe);
                     }
+                    __builtin_amdgcn_sched_barrier(0);
                 }
             }
-            __syncthreads();
         }
+        __syncthreads();
+        const int tid = fresh(threadIdx.x), l = tid & 63, l16 = l & 15, l4 = l >> 4;
+        if (half == 0) {
 #pragma unroll
-        for (int x = 0; x < SG; ++x) {
-            const int u = tid + x * kThreads, t = u >> 3;
-            float s = db[x];
-            s += __shfl_xor(s, 1);
-            s += __shfl_xor(s, 2);
-            s += __shfl_xor(s, 4);
-            if ((u & 7) == 0 && t < c.n) a.dbeta[(size_t)(c.start + t) * a.Hv + hv] = s;
+            for (int x = 0; x < 2; ++x) {
+                const int u = tid + x * 256, t = u >> 3;
+                const float s = sum8(db[x]);
+                Elt<float>::st_rsrc(rows_rsrc(a.dbeta + (size_t)c.start * a.Hv + hv, c.n, a.Hv, 1),
+                                    (u & 7) == 0 ? (uint32_t)(t * a.Hv) * 4u : kNowhere, s);
+            }
         }
-        __builtin_amdgcn_sched_barrier(0);
         float end = decay[0][kC - 1] * sd;
-        float kv[4][4], qv[4][4];  // this lane's column of K and Q: tokens 16 m + 4 l4 + r
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
-            const int i = m * 16 + l4 * 4;
-            kt.values4(m, wave, kv[m]);
-            qt.values4(m, wave, qv[m]);
-            const f32x4 eg = *reinterpret_cast<const f32x4*>(&decay[0][i]);
-            const f32x4 el = *reinterpret_cast<const f32x4*>(&decay[1][i]);
+            __builtin_amdgcn_sched_barrier(0);
+            float kv[4];
+            kt.values4(l, m, wave, kv);
+            const f32x4 eg = *reinterpret_cast<const f32x4*>(&decay[0][m * 16 + l4 * 4]);
+            const f32x4 el = *reinterpret_cast<const f32x4*>(&decay[1][m * 16 + l4 * 4]);
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 dq[m][r] *= eg[r] * a.scale;
                 dr[m][r] *= -eg[r];
                 dw[m][r] *= el[r];
-                end = fmaf(kv[m][r], dw[m][r], end);
+                end = fmaf(kv[r], dw[m][r], end);
             }
         }
 #pragma unroll
         for (int pass = 0; pass < 2; ++pass) {  // a, then -b
 #pragma unroll
-            for (int x = 0; x < TT; ++x) {
-                const int i = (ti0 + x) * 16 + l16, j = tj * 16 + l4 * 4;
-                float v[4];
+            for (int n = 0; n < 4; ++n) {
+                __builtin_amdgcn_sched_barrier(0);
+                const int i = n * 16 + (int)fresh(l16), j = wave * 16 + (int)fresh(l4) * 4;
+                float v[4] = {};
+                if (n >= wave) {
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const bool on = pass ? i > j + r : i >= j + r;
-                    const float w = on ? decay_of(G[i] - G[j + r]) : 0.0f;
-                    v[r] = on ? (pass ? -w * bt[x][r] : w * a.scale * at[x][r]) : 0.0f;
+                    for (int r = 0; r < 4; ++r) {
+                        const bool on = pass ? i > j + r : i >= j + r;
+                        const float w = on ? decay_of(G[i] - G[j + r]) : 0.0f;
+                        v[r] = on ? (pass ? -w * bt[n][r] : w * a.scale * at[n][r]) : 0.0f;
+                    }
                 }
+                const int pj = kplace(j), pi = kplace(i);
+                lds_put4<3>(M, PT, Plane::at(i, pj >> 3) + (pj & 7), v);
 #pragma unroll
                 for (int r = 0; r < 4; r += 2) {
                     uint32_t p[3];
                     split2<3>(v[r], v[r + 1], p);
 #pragma unroll
                     for (int y = 0; y < 3; ++y) {
-                        uint16_t* const to = reinterpret_cast<uint16_t*>(Mt) + y * PT + (j + r) * LT + kplace(i);
-                        to[0] = (uint16_t)p[y];
-                        to[LT] = (uint16_t)(p[y] >> 16);
+                        uint16_t* const to = reinterpret_cast<uint16_t*>(Mt) + y * PT;
+                        to[Plane::at(j + r, pi >> 3) + (pi & 7)] = (uint16_t)p[y];
+                        to[Plane::at(j + r + 1, pi >> 3) + (pi & 7)] = (uint16_t)(p[y] >> 16);
                     }
                 }
-                lds_put4<3>(M, PT, LT, i, kplace(j), v);
             }
             __syncthreads();
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
-                const int k0 = s * 32 + l4 * 8;
+                const int u = s * 4 + l4;
                 __builtin_amdgcn_sched_barrier(0);
-                const auto kb = kt.token_frag(s, wave), qb = qt.token_frag(s, wave);
+                const auto kb = kt.token_frag(l, s, wave), qb = qt.token_frag(l, s, wave);
 #pragma unroll
                 for (int m = 0; m < 4; ++m) {
-                    if (m >= 2 * s) mma<3>(pass ? dr[m] : dq[m], plane_frag<3>(M, PT, LT, m * 16 + l16, k0), kb);
-                    if (m < 2 + 2 * s) mma<3>(dw[m], plane_frag<3>(Mt, PT, LT, m * 16 + l16, k0), pass ? kb : qb);
+                    const int o = Plane::at(m * 16 + l16, u);
+                    if (m >= 2 * s) mma<3>(pass ? dr[m] : dq[m], tile_planes<3>(M, PT, o), kb);
+                    if (m < 2 + 2 * s) mma<3>(dw[m], tile_planes<3>(Mt, PT, o), pass ? kb : qb);
+                    __builtin_amdgcn_sched_barrier(0);
                 }
             }
             __syncthreads();
@@ -336,48 +352,50 @@ __global__ __launch_bounds__(DKP * 4) void k_delta_grads(DeltaArgs a) {
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
             const int i = m * 16 + l4 * 4;
+            __builtin_amdgcn_sched_barrier(0);
+            float kv[4], qv[4];
+            kt.values4(l, m, wave, kv);
+            qt.values4(l, m, wave, qv);
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                float s = fmaf(qv[m][r], dq[m][r], kv[m][r] * (dr[m][r] - dw[m][r]));
-#pragma unroll
-                for (int x = 1; x < 16; x <<= 1) s += __shfl_xor(s, x);
+                const float s = sum16(fmaf(qv[r], dq[m][r], kv[r] * (dr[m][r] - dw[m][r])));
                 if (l16 == 0) red[wave][i + r] = s;
             }
-            if constexpr (GROUP) {
-                tq[m] += dq[m];
-                tk[m] += dr[m] + dw[m];
-            }
+            tq[m] += dq[m];
+            tk[m] += dr[m] + dw[m];
         }
-#pragma unroll
-        for (int x = 1; x < 64; x <<= 1) end += __shfl_xor(end, x);
-        if (l == 0) ends[wave] = end;
+        end = sum16(end);
+        if (l16 == 0) ends[wave * 4 + l4] = end;
         __syncthreads();
         if (wave == 0) {
-            double s = 0.0, e = 0.0;
-#pragma unroll
-            for (int w = 0; w < kWaves; ++w) {
-                s += (double)red[w][l];
-                e += (double)ends[w];
-            }
+            float s = (red[0][l] + red[1][l]) + (red[2][l] + red[3][l]);
+            const float e = sum16(ends[l16]);
             if (l == kC - 1) s += e;
-#pragma unroll
-            for (int x = 1; x < kC; x <<= 1) {
-                const double o = __shfl_down(s, x);
-                if (l + x < kC) s += o;
-            }
-            if (l < c.n) a.dg[(size_t)(c.start + l) * a.Hv + hv] = (float)s;
-        }
-        if constexpr (!GROUP) {
-#pragma unroll
-            for (int m = 0; m < 4; ++m) dr[m] += dw[m];
-            store_column<T>(a.dq, c.start, c.n, a.Hk, hk, a.Dk, column_of<T>(a.Hk, a.Dk, d), dq, 1.0f);
-            store_column<T>(a.dk, c.start, c.n, a.Hk, hk, a.Dk, column_of<T>(a.Hk, a.Dk, d), dr, 1.0f);
+            *at_bytes(a.rows + (sh * halves + half) * kC, (uint32_t)l * 4u) = s;
         }
     }
-    if constexpr (GROUP) {
-        store_column<T>(a.dq, c.start, c.n, a.Hk, hk, a.Dk, column_of<T>(a.Hk, a.Dk, d), tq, 1.0f);
-        store_column<T>(a.dk, c.start, c.n, a.Hk, hk, a.Dk, column_of<T>(a.Hk, a.Dk, d), tk, 1.0f);
+    const Column cd = column_of<T>(a.Hk, a.Dk, d0 + (lane_id() & 15));
+    store_column<T>(a.dq, c.start, c.n, a.Hk, hk, a.Dk, cd, tq, 1.0f);
+    store_column<T>(a.dk, c.start, c.n, a.Hk, hk, a.Dk, cd, tk, 1.0f);
+}
+
+// dg of a chunk: the sums of a.rows from each token to the chunk's end, in 64
+// bits. One wave per (slot, value head).
+template <int kUnused = 0>
+__global__ __launch_bounds__(256) void k_delta_dg(DeltaArgs a) {
+    const int64_t sh = (int64_t)blockIdx.x * 4 + wave_id();
+    if (sh >= delta_slots(a.T, a.nseq) * a.Hv) return;
+    const int hv = (int)(sh % a.Hv), halves = (a.Dk + kDh - 1) / kDh, l = lane_id();
+    Chunk c;
+    if (!chunk_at(a.cu, a.nseq, a.T, sh / a.Hv, c)) return;
+    double s = 0.0;
+    for (int h = 0; h < halves; ++h) s += (double)a.rows[(sh * halves + h) * kC + l];
+#pragma unroll
+    for (int x = 1; x < kC; x <<= 1) {
+        const double o = __shfl_down(s, x);
+        if (l + x < kC) s += o;
     }
+    if (l < c.n) a.dg[(size_t)(c.start + l) * a.Hv + hv] = (float)s;
 }
 
 template <typename T, int DKP>
@@ -392,26 +410,29 @@ int launch_delta_bwd(const DeltaArgs& a, hipStream_t s) {
         SSMP_LAUNCH_CHECK();
     }
     if (a.T > 0) {
-        const dim3 grid((unsigned)delta_slots(a.T, a.nseq), a.Hk);
-        if (a.Hv > a.Hk) k_delta_grads<T, DKP, true><<<grid, DKP * 4, 0, s>>>(a);
-        else k_delta_grads<T, DKP, false><<<grid, DKP * 4, 0, s>>>(a);
+        const int64_t slots = delta_slots(a.T, a.nseq);
+        const unsigned blocks = (unsigned)spread_blocks(slots * a.Hk, (a.Dk + kDh - 1) / kDh);
+        k_delta_grads<T><<<blocks, 256, 0, s>>>(a);
+        SSMP_LAUNCH_CHECK();
+        k_delta_dg<><<<(unsigned)((slots * a.Hv + 3) / 4), 256, 0, s>>>(a);
         SSMP_LAUNCH_CHECK();
     }
     return SSMP_OK;
 }
 
 struct DeltaBwdLayout {
-    size_t dec, inv, att, dS1, dU, total;
+    size_t dec, inv, att, dS1, dU, rows, total;
 };
 inline DeltaBwdLayout delta_bwd_layout(int64_t T, int32_t nseq, int32_t Hv, int32_t Dk, int32_t Dv) {
     const size_t n = (size_t)delta_slots(T, nseq);
     DeltaBwdLayout L;
     L.dec = 0;
-    L.inv = L.dec + round256(n * Hv * 2 * kC * 4);
+    L.inv = L.dec + round256(n * Hv * kDec * 4);
     L.att = L.inv + round256(n * Hv * kTri * 4);
     L.dS1 = L.att + round256(n * Hv * kTri * 4);
     L.dU = L.dS1 + round256(n * Hv * Dk * Dv * 4);
-    L.total = L.dU + round256(n * Hv * kC * Dv * 4);
+    L.rows = L.dU + round256(n * Hv * kC * Dv * 4);
+    L.total = L.rows + round256(n * Hv * ((Dk + kDh - 1) / kDh) * kC * 4);
     return L;
 }
 
@@ -472,6 +493,7 @@ extern "C" int gated_delta_pack_bwd(const void* q, const void* k, const float* g
         a.att = reinterpret_cast<float*>(ws + L.att);
         a.dS1 = reinterpret_cast<float*>(ws + L.dS1);
         a.dU = reinterpret_cast<float*>(ws + L.dU);
+        a.rows = reinterpret_cast<float*>(ws + L.rows);
     }
     hipStream_t s = static_cast<hipStream_t>(stream);
     const bool wide = Dk > 64;

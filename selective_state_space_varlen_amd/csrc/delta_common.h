@@ -12,9 +12,27 @@ inline bool aligned16(P... p) {
     return ((reinterpret_cast<uintptr_t>(p) % 16 == 0) && ...);
 }
 
+// A value again, in a way that the compiler does not see through: it would
+// else form the addresses of a loop's every access ahead of the loop and keep
+// them, dozens of registers that these kernels do not have.
+__device__ __forceinline__ uint32_t fresh(uint32_t v) {
+    asm volatile("" : "+v"(v));
+    return v;
+}
+
 // The wave's number in its workgroup, as a scalar: branches on it are the
 // wave's own, as matrix instructions, which heed no lane mask, need them to be.
 __device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)); }
+
+// Sums over the 8 or 16 lanes that share l / 8 or l / 16, in every lane:
+// neighbours, pairs, then the mirrored half (no address registers, unlike a
+// shuffle through LDS).
+template <int CTRL>
+__device__ __forceinline__ float dpp_add(float v) {
+    return v + __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 0xF, 0xF, true));
+}
+__device__ __forceinline__ float sum8(float v) { return dpp_add<0x141>(dpp_add<0x4E>(dpp_add<0xB1>(v))); }
+__device__ __forceinline__ float sum16(float v) { return dpp_add<0x140>(sum8(v)); }
 
 // ---------------------------------------------------------------------------
 // Chunks. A chunk is up to 64 tokens of one sequence, counted from its first
@@ -160,12 +178,6 @@ __device__ __forceinline__ Frag<NP> split8(const float (&v)[8]) {
 template <typename T>
 constexpr int kExact = std::is_same<T, float>::value ? 3 : 1;
 
-// 8 contiguous elements at p as an operand (zeros where off)
-__device__ __forceinline__ Frag<1> load_frag(const uint16_t* p, bool on) {
-    u32x4 w = {0, 0, 0, 0};
-    if (on) w = *reinterpret_cast<const u32x4*>(p);
-    return {{__builtin_bit_cast(bf16x8, w)}};
-}
 __device__ __forceinline__ void load8(const float* p, bool on, float (&v)[8]) {
     f32x4 a = {0, 0, 0, 0}, b = {0, 0, 0, 0};
     if (on) {
@@ -178,31 +190,25 @@ __device__ __forceinline__ void load8(const float* p, bool on, float (&v)[8]) {
         v[4 + e] = b[e];
     }
 }
-__device__ __forceinline__ Frag<3> load_frag(const float* p, bool on) {
-    float v[8];
-    load8(p, on, v);
-    return split8<3>(v);
-}
 
-// Planes: [plane][row][ld] bf16; in LDS ld = k length + 8 so that the 16
-// rows of a 16-byte read fall into different banks.
+// NP planes of `plane` elements each, at one place
 template <int NP>
-__device__ __forceinline__ Frag<NP> plane_frag(const __bf16* base, int plane, int ld, int row, int k) {
+__device__ __forceinline__ Frag<NP> tile_planes(const __bf16* base, int plane, int at) {
     Frag<NP> f;
 #pragma unroll
     for (int i = 0; i < NP; ++i)
-        f.p[i] = __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4*>(base + i * plane + row * ld + k));
+        f.p[i] = __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4*>(base + i * plane + at));
     return f;
 }
 // four values along k (a lane's rows of a result) into the planes
 template <int NP>
-__device__ __forceinline__ void lds_put4(__bf16* base, int plane, int ld, int row, int k, const float (&v)[4]) {
+__device__ __forceinline__ void lds_put4(__bf16* base, int plane, int at, const float (&v)[4]) {
     uint32_t p[2][NP];
     split2<NP>(v[0], v[1], p[0]);
     split2<NP>(v[2], v[3], p[1]);
 #pragma unroll
     for (int i = 0; i < NP; ++i)
-        *reinterpret_cast<u32x2*>(base + i * plane + row * ld + k) = u32x2{p[0][i], p[1][i]};
+        *reinterpret_cast<u32x2*>(base + i * plane + at) = u32x2{p[0][i], p[1][i]};
 }
 
 // Results as operands. The order of a product's k is free as long as both
@@ -245,6 +251,14 @@ struct Unit<uint16_t> {
     __device__ __forceinline__ void put_half(uint16_t* p, int h) const {
         *reinterpret_cast<u32x2*>(p) = h ? u32x2{w[2], w[3]} : u32x2{w[0], w[1]};
     }
+    __device__ __forceinline__ void pack(const float (&v)[8]) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            w[e] = (uint32_t)f32_to_bf16(v[2 * e]) | ((uint32_t)f32_to_bf16(v[2 * e + 1]) << 16);
+    }
+    __device__ __forceinline__ void store(__amdgpu_buffer_rsrc_t r, uint32_t o) const {
+        __builtin_amdgcn_raw_buffer_store_b128(w, r, (int)o, 0, 0);
+    }
 };
 template <>
 struct Unit<float> {
@@ -261,6 +275,14 @@ struct Unit<float> {
         }
     }
     __device__ __forceinline__ void put_half(float* p, int h) const { *reinterpret_cast<f32x4*>(p) = w[h]; }
+    __device__ __forceinline__ void pack(const float (&v)[8]) {
+        w[0] = f32x4{v[0], v[1], v[2], v[3]};
+        w[1] = f32x4{v[4], v[5], v[6], v[7]};
+    }
+    __device__ __forceinline__ void store(__amdgpu_buffer_rsrc_t r, uint32_t o) const {
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, w[0]), r, (int)o, 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, w[1]), r, (int)(o + 16), 0, 0);
+    }
 };
 __device__ __forceinline__ Frag<1> unit_planes(const Unit<uint16_t>& u) { return {{__builtin_bit_cast(bf16x8, u.w)}}; }
 __device__ __forceinline__ Frag<3> unit_planes(const Unit<float>& u) { return split_tiles<3>(u.w[0], u.w[1]); }
@@ -271,17 +293,6 @@ __device__ __forceinline__ void copy8(T* to, const T* from, bool on) {
     u.put_half(to, 0);
     u.put_half(to + 4, 1);
 }
-__device__ __forceinline__ void put8(uint16_t* p, const uint16_t (&v)[8]) {
-    u32x4 w;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) w[e] = (uint32_t)v[2 * e] | ((uint32_t)v[2 * e + 1] << 16);
-    *reinterpret_cast<u32x4*>(p) = w;
-}
-__device__ __forceinline__ void put8(float* p, const float (&v)[8]) {
-    reinterpret_cast<f32x4*>(p)[0] = f32x4{v[0], v[1], v[2], v[3]};
-    reinterpret_cast<f32x4*>(p)[1] = f32x4{v[4], v[5], v[6], v[7]};
-}
-
 // Left operands in LDS: rows of W elements of E in 16-byte units (32 for fp32:
 // what one lane reads), without padding; unit u of row r lies at u ^ swz(r),
 // so that the 16 rows a read touches fall into different banks.
@@ -314,9 +325,9 @@ struct RowTile {
     T x[kC * DKP];
 
     __device__ __forceinline__ Frag<kExact<T>> frag(int token, int unit) const { return tile_frag(x + L::at(token, unit)); }
-    // tokens 16 t + 4 (l / 16) .. + 3 of column 16 m + l % 16
-    __device__ __forceinline__ void column4(int t, int m, uint32_t (&v)[kExact<T> == 1 ? 2 : 4]) const {
-        const int l = lane_id(), l16 = l & 15, l4 = l >> 4;
+    // lane l: tokens 16 t + 4 (l / 16) .. + 3 of column 16 m + l % 16
+    __device__ __forceinline__ void column4(int l, int t, int m, uint32_t (&v)[kExact<T> == 1 ? 2 : 4]) const {
+        const int l16 = l & 15, l4 = l >> 4;
         if constexpr (kExact<T> == 1) {
             const int token = t * 16 + l4 * 4 + (l16 >> 2);
             const T* p = x + L::at(token, (m >> 1) * 4 + (l16 & 3)) + (m & 1) * 4;
@@ -331,10 +342,10 @@ struct RowTile {
             for (int e = 0; e < 4; ++e) v[e] = __builtin_bit_cast(uint32_t, x[L::at(t * 16 + l4 * 4 + e, p >> 3) + (p & 7)]);
         }
     }
-    __device__ __forceinline__ void values4(int t, int m, float (&f)[4]) const {
+    __device__ __forceinline__ void values4(int l, int t, int m, float (&f)[4]) const {
         if constexpr (kExact<T> == 1) {
             uint32_t v[2];
-            column4(t, m, v);
+            column4(l, t, m, v);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 f[2 * e] = bf16_to_f32(v[e]);
@@ -342,22 +353,22 @@ struct RowTile {
             }
         } else {
             uint32_t v[4];
-            column4(t, m, v);
+            column4(l, t, m, v);
 #pragma unroll
             for (int e = 0; e < 4; ++e) f[e] = __builtin_bit_cast(float, v[e]);
         }
     }
     // tokens of block s of 32 as k, in places
-    __device__ __forceinline__ Frag<kExact<T>> token_frag(int s, int m) const {
+    __device__ __forceinline__ Frag<kExact<T>> token_frag(int l, int s, int m) const {
         if constexpr (kExact<T> == 1) {
             uint32_t a[2], b[2];
-            column4(2 * s, m, a);
-            column4(2 * s + 1, m, b);
+            column4(l, 2 * s, m, a);
+            column4(l, 2 * s + 1, m, b);
             return {{__builtin_bit_cast(bf16x8, u32x4{a[0], a[1], b[0], b[1]})}};
         } else {
             float a[4], b[4];
-            values4(2 * s, m, a);
-            values4(2 * s + 1, m, b);
+            values4(l, 2 * s, m, a);
+            values4(l, 2 * s + 1, m, b);
             return split8<3>({a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]});
         }
     }
@@ -384,16 +395,11 @@ template <int NP>
 __device__ __forceinline__ void tri_put4(__bf16* base, int idx4, const f32x4& v) {
     const int row = idx4 >> 3, q = idx4 & 7;
     const float x[4] = {v[0], v[1], v[2], v[3]};
-    lds_put4<NP>(base, kTri, 0, 0, Tile<uint16_t, 32>::at(row, q >> 1) + (q & 1) * 4, x);
+    lds_put4<NP>(base, kTri, Tile<uint16_t, 32>::at(row, q >> 1) + (q & 1) * 4, x);
 }
 template <int NP>
 __device__ __forceinline__ Frag<NP> tri_frag(const __bf16* base, int row, int unit) {
-    Frag<NP> f;
-#pragma unroll
-    for (int i = 0; i < NP; ++i)
-        f.p[i] = __builtin_bit_cast(
-            bf16x8, *reinterpret_cast<const u32x4*>(base + i * kTri + Tile<uint16_t, 32>::at(row, unit)));
-    return f;
+    return tile_planes<NP>(base, kTri, Tile<uint16_t, 32>::at(row, unit));
 }
 
 // The workgroups that share keys and queries (the column blocks of a head,
@@ -514,6 +520,7 @@ constexpr int kWaveCols = 16;  // state columns a wave of the chains takes
 inline int delta_dkp(int Dk) { return Dk <= 64 ? 64 : 128; }
 inline size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
+constexpr int kDec = 4 * kC;
 struct DeltaArgs {
     const void *q, *k, *v, *dout;
     const float *g, *beta;
@@ -528,10 +535,11 @@ struct DeltaArgs {
     // kept from the forward to the backward, by slot and value head
     float *S0, *E;   // the state that enters the chunk (Dk, Dv); the errors (64, Dv)
     // scratch, by slot and head
-    float* dec;      // e^{G_i} and e^{G_last - G_i}: (2, 64)
+    float* dec;      // G (64 doubles), e^{G_i}, e^{G_last - G_i}: kDec
     float* inv;      // the chunk's inverse: kTri
     float* att;      // the decayed products of q and k: kTri
     float *dS1, *dU; // backward: gradients of the state that leaves the chunk, and of U
+    float* rows;     // backward: per 64 columns of dq and dk, what k_delta_dg adds up: 64
 };
 
 inline int delta_check(int64_t T, int32_t nseq, int32_t Hk, int32_t Hv, int32_t Dk, int32_t Dv, int32_t dtype) {

@@ -118,7 +118,7 @@ __global__ __launch_bounds__(NW * 64) void k_delta_chain(DeltaArgs a) {
 #pragma unroll
             for (int m = 2 * s; m < 4; ++m) mma<NO>(o[m], tri_frag<NO>(lds.att, s * 32 + m * 16 + l16, l4), ub);
 #pragma unroll
-            for (int m = 0; m < MT; ++m) mma<3>(S[m], lds.k.token_frag(s, m), wb);
+            for (int m = 0; m < MT; ++m) mma<3>(S[m], lds.k.token_frag(l, s, m), wb);
         }
         store_column<T>(a.out, start, cn, a.Hv, hv, a.Dv, cv, o, a.scale);
     }
@@ -149,7 +149,7 @@ inline DeltaFwdLayout delta_fwd_layout(int64_t T, int32_t nseq, int32_t Hv) {
     const size_t n = (size_t)delta_slots(T, nseq);
     DeltaFwdLayout L;
     L.dec = 0;
-    L.inv = L.dec + round256(n * Hv * 2 * kC * 4);
+    L.inv = L.dec + round256(n * Hv * kDec * 4);
     L.att = L.inv + round256(n * Hv * kTri * 4);
     L.total = L.att + round256(n * Hv * kTri * 4);
     return L;

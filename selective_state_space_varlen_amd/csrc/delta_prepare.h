@@ -47,8 +47,9 @@ __global__ __launch_bounds__(256) void k_delta_prepare(DeltaArgs a) {
         G[l] = s;
         beta[l] = l < c.n ? a.beta[(size_t)(c.start + l) * a.Hv + hv] : 0.0f;
         const double last = __shfl(s, kC - 1);
-        a.dec[sh * 2 * kC + l] = decay_of(s);
-        a.dec[sh * 2 * kC + kC + l] = decay_of(last - s);
+        reinterpret_cast<double*>(a.dec + sh * kDec)[l] = s;
+        a.dec[sh * kDec + 2 * kC + l] = decay_of(s);
+        a.dec[sh * kDec + 3 * kC + l] = decay_of(last - s);
     }
     __syncthreads();
     // Wave w has rows 16 w .. of both products. kk: K K^T. qk: forward K Q^T
@@ -160,7 +161,7 @@ struct ChainLoads {
                 att[x] = *reinterpret_cast<const f32x4*>(at_bytes(a.att + sh * kTri, (uint32_t)(tid + x * THREADS) * 16u));
             }
         dec = 0.0f;
-        if (tid < 2 * kC) dec = a.dec[sh * 2 * kC + tid];
+        if (tid < 2 * kC) dec = a.dec[sh * kDec + 2 * kC + tid];
         else if (tid < 2 * kC + n) dec = a.beta[(size_t)(start + tid - 2 * kC) * a.Hv + hv];
     }
     __device__ __forceinline__ void put(Tiles& t) const {
@@ -206,13 +207,6 @@ template <typename T>
 __device__ __forceinline__ Column column_of(int H, int Dv, int col) {
     const int stride = H * Dv * (int)sizeof(T), l4 = lane_id() >> 4;
     return {col < Dv ? (uint32_t)(l4 * 4 * stride + col * (int)sizeof(T)) : kNowhere, stride};
-}
-// The offset again, in a way that the compiler does not see through: it would
-// else form the offsets of all rows ahead of the loop over the chunks and keep
-// them, 64 registers that the chain does not have.
-__device__ __forceinline__ uint32_t fresh(uint32_t o) {
-    asm volatile("" : "+v"(o));
-    return o;
 }
 template <typename T>
 __device__ __forceinline__ void load_column(const void* p, int64_t start, int n, int H, int h, int Dv, const Column& c,
