@@ -37,7 +37,6 @@ __global__ __launch_bounds__(NW * 64) void k_delta_chain_bwd(DeltaArgs a) {
     const int hv = hk * group + sp.member / ncb, cb = sp.member % ncb;
     const int wave = wave_id(), l = lane_id(), l16 = l & 15, l4 = l >> 4;
     const int col = cb * kCols + wave * 16 + l16;
-    const bool busy = cb * kCols + wave * 16 < a.Dv;
     const Seq q = seq_at(a.cu, seq, a.T);
     const int chunks = (q.len + kC - 1) / kC;
     const Column cs = column_of<float>(1, a.Dv, col), cv = column_of<T>(a.Hv, a.Dv, col);
@@ -46,9 +45,9 @@ __global__ __launch_bounds__(NW * 64) void k_delta_chain_bwd(DeltaArgs a) {
     load_matrix(a.dhT ? a.dhT + state : nullptr, a.Dk, a.Dv, cs, S);
     Loads next;
     uint32_t onext[16];
-    if (chunks > 0) {
+    {
         const int64_t start = q.start + (int64_t)(chunks - 1) * kC;
-        const int n = q.len - (chunks - 1) * kC;
+        const int n = chunks > 0 ? q.len - (chunks - 1) * kC : 0;  // an empty sequence has no last chunk
         next.load(a, q.slot0 + chunks - 1, start, n, hk, hv);
         load_column<T>(a.dout, start, n, a.Hv, hv, a.Dv, cv, onext);
     }
@@ -61,69 +60,92 @@ __global__ __launch_bounds__(NW * 64) void k_delta_chain_bwd(DeltaArgs a) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) o[i >> 2][i & 3] = Elt<T>::cvt(onext[i]);
         __syncthreads();
-        if (ch > 0) {
-            next.load(a, slot - 1, start - kC, kC, hk, hv);
-            load_column<T>(a.dout, start - kC, kC, a.Hv, hv, a.Dv, cv, onext);
-        }
-        if (!busy) continue;
+        const int nn = ch > 0 ? kC : 0;
+        next.load(a, slot - 1, start - kC, nn, hk, hv);
+        load_column<T>(a.dout, start - kC, nn, a.Hv, hv, a.Dv, cv, onext);
         store_matrix(a.dS1 + sh * a.Dk * a.Dv, a.Dk, a.Dv, cs, S);
         f32x4 x[4] = {}, y[4] = {};  // K dS', scale P^T dOut
+        Frag<3> sb = split_tiles<3>(S[0], S[1]);
 #pragma unroll
         for (int s = 0; s < DKP / 32; ++s) {
             __builtin_amdgcn_sched_barrier(0);
-            const auto sb = split_tiles<3>(S[2 * s], S[2 * s + 1]);
+            Frag<NX> ka[4];
 #pragma unroll
-            for (int m = 0; m < 4; ++m) mma<3>(x[m], lds.k.frag(m * 16 + l16, s * 4 + l4), sb);
+            for (int m = 0; m < 4; ++m) ka[m] = lds.k.frag(m * 16 + l16, s * 4 + l4);
+            Frag<3> nb;
+            if (s + 1 < DKP / 32) nb = split_tiles<3>(S[2 * s + 2], S[2 * s + 3]);
+            mma_tiles<3, 0, 4>(x, ka, sb);
+            if constexpr (NX == 1) step_order<4, 12, 4>();
+            sb = nb;
         }
+        const float ec = lds.eg[kC - 1];
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
+        for (int s = 0; s < 2; ++s) {  // in its shadow the state's gradient decays
             __builtin_amdgcn_sched_barrier(0);
             const auto ob = split_tiles<NX>(o[2 * s], o[2 * s + 1]);
+            Frag<3> pa[4];
 #pragma unroll
-            for (int m = 0; m < 2 + 2 * s; ++m)
-                mma<3>(y[m], tri_frag<3>(lds.att, (s ? 0 : 64) + m * 16 + l16, l4), ob);
+            for (int m = 0; m < 2 + 2 * s; ++m) pa[m] = tri_frag<3>(lds.att, (s ? 0 : 64) + m * 16 + l16, l4);
+            if (s == 0) mma_tiles<3, 0, 2>(y, pa, ob);
+            else mma_tiles<3, 0, 4>(y, pa, ob);
+#pragma unroll
+            for (int m = s * MT / 2; m < (s + 1) * MT / 2; ++m) S[m] *= ec;
         }
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
             const f32x4 el = *reinterpret_cast<const f32x4*>(lds.el + m * 16 + l4 * 4);
             y[m] += el * x[m];
         }
         f32x4 u[4] = {};
+        {
+            Frag<3> ia[4];
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
+            for (int m = 0; m < 4; ++m) ia[m] = tri_frag<3>(lds.inv, m * 16 + l16, l4);
+            const auto yb = split_tiles<3>(y[2], y[3]);
             __builtin_amdgcn_sched_barrier(0);
-            const auto yb = split_tiles<3>(y[2 * s], y[2 * s + 1]);
+            const auto yc = split_tiles<3>(y[0], y[1]);
+            mma_tiles<3, 0, 4>(u, ia, yb);
+            step_order<0, 24, 2>();
+            __builtin_amdgcn_sched_barrier(0);
+            Frag<3> ib[2];
 #pragma unroll
-            for (int m = 0; m < 2 + 2 * s; ++m)
-                mma<3>(u[m], tri_frag<3>(lds.inv, (s ? 0 : 64) + m * 16 + l16, l4), yb);
+            for (int m = 0; m < 2; ++m) ib[m] = tri_frag<3>(lds.inv, 64 + m * 16 + l16, l4);
+            mma_tiles<3, 0, 2>(u, ib, yc);
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                const f32x4 eg = *reinterpret_cast<const f32x4*>(lds.eg + m * 16 + l4 * 4);
+                o[m] *= eg * a.scale;  // e^G scale dOut
+            }
+            step_order<10, 12, 3>();
         }
+        __builtin_amdgcn_sched_barrier(0);
         store_matrix(a.dU + sh * kC * a.Dv, kC, a.Dv, cs, u);
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
             const f32x4 be = *reinterpret_cast<const f32x4*>(lds.beta + m * 16 + l4 * 4);
             const f32x4 eg = *reinterpret_cast<const f32x4*>(lds.eg + m * 16 + l4 * 4);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                u[m][r] *= -eg[r] * be[r];         // -e^G dE
-                o[m][r] *= eg[r] * a.scale;        // e^G scale dOut
-            }
+            u[m] *= -eg * be;  // -e^G dE
         }
-        const float ec = lds.eg[kC - 1];
+        // dS += (e^G Q)^T scale dOut - (e^G K)^T dE
+        Frag<3> rb = split_tiles<3>(o[0], o[1]);
 #pragma unroll
-        for (int m = 0; m < MT; ++m) S[m] *= ec;
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
+        for (int t = 0; t < 4; ++t) {  // queries, keys of the first 32 tokens, then of the others
+            const int s = t >> 1;
             __builtin_amdgcn_sched_barrier(0);
-            const auto ob = split_tiles<3>(o[2 * s], o[2 * s + 1]);
-            const auto ub = split_tiles<3>(u[2 * s], u[2 * s + 1]);
+            Frag<NX> ra[MT];
 #pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                mma<3>(S[m], lds.q.token_frag(l, s, m), ob);
-                mma<3>(S[m], lds.k.token_frag(l, s, m), ub);
-            }
+            for (int m = 0; m < MT; ++m) ra[m] = t & 1 ? lds.k.token_frag(l, s, m) : lds.q.token_frag(l, s, m);
+            Frag<3> rn;
+            if (t == 0) rn = split_tiles<3>(u[0], u[1]);
+            if (t == 1) rn = split_tiles<3>(o[2], o[3]);
+            if (t == 2) rn = split_tiles<3>(u[2], u[3]);
+            mma_tiles<3, 0, MT>(S, ra, rb);
+            if constexpr (NX == 1) step_order<2 * MT, 3 * MT, 2>();
+            rb = rn;
         }
     }
-    if (a.dh0 && busy) store_matrix(a.dh0 + state, a.Dk, a.Dv, cs, S);
+    if (a.dh0) store_matrix(a.dh0 + state, a.Dk, a.Dv, cs, S);
 }
 
 // One workgroup per (slot, key head, 64 columns of dq and dk), over the value

@@ -127,6 +127,33 @@ __device__ __forceinline__ void mma(f32x4& d, const Frag<NA>& a, const Frag<NB>&
             if (s - i >= 0 && s - i < NB) d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.p[i], b.p[s - i], d, 0, 0, 0);
 }
 
+// d[m] += a[m] b for tiles FROM .. TO - 1, one plane product after the other
+// over all tiles: a matrix instruction waits for the last one on its tile.
+template <int LIM, int FROM, int TO, int NA, int NB, int N, int NF>
+__device__ __forceinline__ void mma_tiles(f32x4 (&d)[N], const Frag<NA> (&a)[NF], const Frag<NB>& b) {
+#pragma unroll
+    for (int s = LIM - 1; s >= 0; --s)
+#pragma unroll
+        for (int i = 0; i < NA; ++i)
+            if (s - i >= 0 && s - i < NB)
+#pragma unroll
+                for (int m = FROM; m < TO; ++m)
+                    d[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[m - FROM].p[i], b.p[s - i], d[m], 0, 0, 0);
+}
+
+// The order of one step of a chain: its LDS reads, then per matrix
+// instruction V of the other operations (the next step's splitting), which
+// run in its shadow.
+template <int READS, int MFMAS, int V>
+__device__ __forceinline__ void step_order() {
+    __builtin_amdgcn_sched_group_barrier(0x100, READS, 0);
+#pragma unroll
+    for (int i = 0; i < MFMAS; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x002, V, 0);
+    }
+}
+
 // Two values as bf16 planes, packed: v = p[0] + p[1] + ... Three planes take
 // the leading 8 bits that are left each, which holds all 24 of an fp32. (Cutting
 // off takes two thirds of the time of rounding: 34 against 52 cycles a pair on
@@ -258,6 +285,13 @@ struct Unit<uint16_t> {
     }
     __device__ __forceinline__ void store(__amdgpu_buffer_rsrc_t r, uint32_t o) const {
         __builtin_amdgcn_raw_buffer_store_b128(w, r, (int)o, 0, 0);
+    }
+};
+template <>
+struct Unit<float4> {  // four of fp32
+    f32x4 w;
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t o) {
+        w = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)o, 0, 0));
     }
 };
 template <>

@@ -39,7 +39,6 @@ __global__ __launch_bounds__(NW * 64) void k_delta_chain(DeltaArgs a) {
     const int hv = hk * group + sp.member / ncb, cb = sp.member % ncb;
     const int wave = wave_id(), l = lane_id(), l16 = l & 15, l4 = l >> 4;
     const int col = cb * kCols + wave * 16 + l16;
-    const bool busy = cb * kCols + wave * 16 < a.Dv;
     const Seq q = seq_at(a.cu, seq, a.T);
     const int chunks = (q.len + kC - 1) / kC;
     const Column cs = column_of<float>(1, a.Dv, col), cv = column_of<T>(a.Hv, a.Dv, col);
@@ -48,7 +47,7 @@ __global__ __launch_bounds__(NW * 64) void k_delta_chain(DeltaArgs a) {
     load_matrix(a.h0 ? a.h0 + state : nullptr, a.Dk, a.Dv, cs, S);
     Loads next;
     uint32_t v[16];
-    if (chunks > 0) {
+    {
         const int n = q.len < kC ? q.len : kC;
         next.load(a, q.slot0, q.start, n, hk, hv);
         load_column<T>(a.v, q.start, n, a.Hv, hv, a.Dv, cv, v);
@@ -61,20 +60,27 @@ __global__ __launch_bounds__(NW * 64) void k_delta_chain(DeltaArgs a) {
         next.put(lds);
         __syncthreads();
         const int left = q.len - (ch + 1) * kC, nn = left < kC ? left : kC;
-        if (nn > 0) next.load(a, slot + 1, start + kC, nn, hk, hv);
-        if (!busy) continue;
+        next.load(a, slot + 1, start + kC, nn, hk, hv);
         if constexpr (SAVE) store_matrix(a.S0 + sh * a.Dk * a.Dv, a.Dk, a.Dv, cs, S);
         f32x4 x[4] = {}, o[4] = {};  // K S and Q S
+        Frag<3> sb = split_tiles<3>(S[0], S[1]);
 #pragma unroll
         for (int s = 0; s < DKP / 32; ++s) {
             __builtin_amdgcn_sched_barrier(0);
-            const auto sb = split_tiles<3>(S[2 * s], S[2 * s + 1]);
+            Frag<NX> ka[4], qa[4];
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
-                mma<3>(x[m], lds.k.frag(m * 16 + l16, s * 4 + l4), sb);
-                mma<NO>(o[m], lds.q.frag(m * 16 + l16, s * 4 + l4), sb);
+                ka[m] = lds.k.frag(m * 16 + l16, s * 4 + l4);
+                qa[m] = lds.q.frag(m * 16 + l16, s * 4 + l4);
             }
+            Frag<3> nb;
+            if (s + 1 < DKP / 32) nb = split_tiles<3>(S[2 * s + 2], S[2 * s + 3]);
+            mma_tiles<3, 0, 4>(x, ka, sb);
+            mma_tiles<NO, 0, 4>(o, qa, sb);
+            if constexpr (NX == 1) step_order<8, 20, 3>();
+            sb = nb;
         }
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
             const f32x4 eg = *reinterpret_cast<const f32x4*>(lds.eg + m * 16 + l4 * 4);
@@ -84,17 +90,29 @@ __global__ __launch_bounds__(NW * 64) void k_delta_chain(DeltaArgs a) {
                 o[m][r] *= eg[r];
             }
         }
-        if (nn > 0) load_column<T>(a.v, start + kC, nn, a.Hv, hv, a.Dv, cv, v);
-        // E = inverse X
+        load_column<T>(a.v, start + kC, nn, a.Hv, hv, a.Dv, cv, v);
+        // E = inverse X; in its shadow the state decays
         f32x4 E[4] = {};
+        const float ec = lds.eg[kC - 1];
+        {
+            Frag<3> ia[4];
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
+            for (int m = 0; m < 4; ++m) ia[m] = tri_frag<3>(lds.inv, m * 16 + l16, l4);
+            const auto xb = split_tiles<3>(x[0], x[1]);
             __builtin_amdgcn_sched_barrier(0);
-            const auto xb = split_tiles<3>(x[2 * s], x[2 * s + 1]);
+            const auto xc = split_tiles<3>(x[2], x[3]);
+            mma_tiles<3, 0, 4>(E, ia, xb);
+            step_order<0, 24, 2>();
+            __builtin_amdgcn_sched_barrier(0);
+            Frag<3> ib[2];
 #pragma unroll
-            for (int m = 2 * s; m < 4; ++m)
-                mma<3>(E[m], tri_frag<3>(lds.inv, s * 32 + m * 16 + l16, l4), xb);
+            for (int m = 0; m < 2; ++m) ib[m] = tri_frag<3>(lds.inv, 64 + m * 16 + l16, l4);
+            mma_tiles<3, 2, 4>(E, ib, xc);
+#pragma unroll
+            for (int m = 0; m < MT; ++m) S[m] *= ec;
+            step_order<6, 12, 3>();
         }
+        __builtin_amdgcn_sched_barrier(0);
         if constexpr (SAVE) store_matrix(a.E + sh * kC * a.Dv, kC, a.Dv, cs, E);
         f32x4 w[4];
 #pragma unroll
@@ -107,22 +125,35 @@ __global__ __launch_bounds__(NW * 64) void k_delta_chain(DeltaArgs a) {
                 w[m][r] = el[r] * E[m][r];
             }
         }
-        const float ec = lds.eg[kC - 1];
-#pragma unroll
-        for (int m = 0; m < MT; ++m) S[m] *= ec;
+        // S += K^T W, out += P U
+        Frag<3> wb = split_tiles<3>(w[0], w[1]);
+        Frag<NO> ub = split_tiles<NO>(E[0], E[1]);
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
             __builtin_amdgcn_sched_barrier(0);
-            const auto ub = split_tiles<NO>(E[2 * s], E[2 * s + 1]);
-            const auto wb = split_tiles<3>(w[2 * s], w[2 * s + 1]);
+            Frag<NX> ka[MT];
 #pragma unroll
-            for (int m = 2 * s; m < 4; ++m) mma<NO>(o[m], tri_frag<NO>(lds.att, s * 32 + m * 16 + l16, l4), ub);
+            for (int m = 0; m < MT; ++m) ka[m] = lds.k.token_frag(l, s, m);
+            Frag<3> wn;
+            Frag<NO> un;
+            if (s == 0) {
+                wn = split_tiles<3>(w[2], w[3]);
+                un = split_tiles<NO>(E[2], E[3]);
+            }
+            mma_tiles<3, 0, MT>(S, ka, wb);
+            if constexpr (NX == 1) step_order<2 * MT, 3 * MT, 3>();
+            __builtin_amdgcn_sched_barrier(0);
+            Frag<NO> pa[4];
 #pragma unroll
-            for (int m = 0; m < MT; ++m) mma<3>(S[m], lds.k.token_frag(l, s, m), wb);
+            for (int m = 2 * s; m < 4; ++m) pa[m - 2 * s] = tri_frag<NO>(lds.att, s * 32 + m * 16 + l16, l4);
+            if (s == 0) mma_tiles<NO, 0, 4>(o, pa, ub);
+            else mma_tiles<NO, 2, 4>(o, pa, ub);
+            wb = wn;
+            ub = un;
         }
         store_column<T>(a.out, start, cn, a.Hv, hv, a.Dv, cv, o, a.scale);
     }
-    if (a.hT && busy) store_matrix(a.hT + state, a.Dk, a.Dv, cs, S);
+    if (a.hT) store_matrix(a.hT + state, a.Dk, a.Dv, cs, S);
 }
 
 template <typename T, int DKP>

@@ -135,18 +135,22 @@ struct ChainLoads {
     using Tiles = ChainTiles<T, DKP, NP>;
     static constexpr int kN = DKP * kC / 8 / THREADS;                         // units of 8 elements a thread
     static constexpr int kM = (kTri / 4 + THREADS - 1) / THREADS;             // units of 4 of a triangle
-    static __device__ __forceinline__ bool tri_on(int x) { return (x + 1) * THREADS <= kTri / 4 || threadIdx.x + x * THREADS < kTri / 4; }
+    static __device__ __forceinline__ bool tri_on(int x) {
+        return (x + 1) * THREADS <= kTri / 4 || threadIdx.x + x * THREADS < kTri / 4;
+    }
     Unit<T> k[kN], q[kN];
-    f32x4 inv[kM], att[kM];
-    float dec;
+    Unit<float4> inv[kM], att[kM];
+    uint32_t dec, beta;
 
+    // The chunk of n tokens at `start` (n <= 0: none, all zeros). The loads are
+    // the same in every wave and on every path, so that a wait for an older
+    // load can count the ones behind it and need not wait for these too.
     __device__ __forceinline__ void load(const DeltaArgs& a, int64_t slot, int64_t start, int n, int hk, int hv) {
         const int tid = threadIdx.x;
-        const size_t sh = (size_t)slot * a.Hv + hv;
-        const size_t first = ((size_t)start * a.Hk + hk) * a.Dk;
+        const size_t sh = n > 0 ? (size_t)slot * a.Hv + hv : 0, from = n > 0 ? (size_t)start : 0;
         const int stride = a.Hk * a.Dk;
-        const auto kr = rows_rsrc(static_cast<const T*>(a.k) + first, n, stride, a.Dk);
-        const auto qr = rows_rsrc(static_cast<const T*>(a.q) + first, n, stride, a.Dk);
+        const auto kr = rows_rsrc(static_cast<const T*>(a.k) + (from * a.Hk + hk) * a.Dk, n, stride, a.Dk);
+        const auto qr = rows_rsrc(static_cast<const T*>(a.q) + (from * a.Hk + hk) * a.Dk, n, stride, a.Dk);
 #pragma unroll
         for (int x = 0; x < kN; ++x) {
             const int u = tid + x * THREADS, i = u / (DKP / 8), k8 = u % (DKP / 8);
@@ -154,15 +158,17 @@ struct ChainLoads {
             k[x].load(kr, o);
             q[x].load(qr, o);
         }
+        const auto ir = bytes_rsrc(a.inv + sh * kTri, n > 0 ? kTri * 4 : 0);
+        const auto ar = bytes_rsrc(a.att + sh * kTri, n > 0 ? kTri * 4 : 0);
 #pragma unroll
-        for (int x = 0; x < kM; ++x)
-            if (tri_on(x)) {
-                inv[x] = *reinterpret_cast<const f32x4*>(at_bytes(a.inv + sh * kTri, (uint32_t)(tid + x * THREADS) * 16u));
-                att[x] = *reinterpret_cast<const f32x4*>(at_bytes(a.att + sh * kTri, (uint32_t)(tid + x * THREADS) * 16u));
-            }
-        dec = 0.0f;
-        if (tid < 2 * kC) dec = a.dec[sh * kDec + 2 * kC + tid];
-        else if (tid < 2 * kC + n) dec = a.beta[(size_t)(start + tid - 2 * kC) * a.Hv + hv];
+        for (int x = 0; x < kM; ++x) {
+            inv[x].load(ir, (uint32_t)(tid + x * THREADS) * 16u);
+            att[x].load(ar, (uint32_t)(tid + x * THREADS) * 16u);
+        }
+        const auto dr = bytes_rsrc(a.dec + sh * kDec + 2 * kC, n > 0 ? 2 * kC * 4 : 0);
+        const auto br = rows_rsrc(a.beta + from * a.Hv + hv, n, a.Hv, 1);
+        dec = Elt<float>::raw_rsrc(dr, (uint32_t)tid * 4u);
+        beta = Elt<float>::raw_rsrc(br, tid < 2 * kC ? kNowhere : (uint32_t)((tid - 2 * kC) * a.Hv) * 4u);
     }
     __device__ __forceinline__ void put(Tiles& t) const {
         const int tid = threadIdx.x;
@@ -175,12 +181,12 @@ struct ChainLoads {
 #pragma unroll
         for (int x = 0; x < kM; ++x)
             if (tri_on(x)) {
-                tri_put4<3>(t.inv, tid + x * THREADS, inv[x]);
-                tri_put4<NP>(t.att, tid + x * THREADS, att[x]);
+                tri_put4<3>(t.inv, tid + x * THREADS, inv[x].w);
+                tri_put4<NP>(t.att, tid + x * THREADS, att[x].w);
             }
-        if (tid < kC) t.eg[tid] = dec;
-        else if (tid < 2 * kC) t.el[tid - kC] = dec;
-        else if (tid < 3 * kC) t.beta[tid - 2 * kC] = dec;
+        if (tid < kC) t.eg[tid] = Elt<float>::cvt(dec);
+        else if (tid < 2 * kC) t.el[tid - kC] = Elt<float>::cvt(dec);
+        else if (tid < 3 * kC) t.beta[tid - 2 * kC] = Elt<float>::cvt(beta);
     }
 };
 
@@ -211,7 +217,7 @@ __device__ __forceinline__ Column column_of(int H, int Dv, int col) {
 template <typename T>
 __device__ __forceinline__ void load_column(const void* p, int64_t start, int n, int H, int h, int Dv, const Column& c,
                                             uint32_t (&v)[16]) {
-    const auto r = rows_rsrc(static_cast<const T*>(p) + ((size_t)start * H + h) * Dv, n, H * Dv, Dv);
+    const auto r = rows_rsrc(static_cast<const T*>(p) + ((n > 0 ? (size_t)start : 0) * H + h) * Dv, n, H * Dv, Dv);
     const uint32_t o = fresh(c.o);
 #pragma unroll
     for (int i = 0; i < 16; ++i) v[i] = Elt<T>::raw_rsrc(r, o + (uint32_t)((i >> 2) * 16 + (i & 3)) * (uint32_t)c.stride);
