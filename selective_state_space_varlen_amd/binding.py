@@ -575,11 +575,43 @@ def selective_scan_pack_fwd_noalloc(u, delta, A, B, C, Dskip, z, pos, out: Optio
 
 # ---------------------------------------------------------------------------
 # Head norms and the gated delta rule
+# torch.cuda.current_stream(i).cuda_stream without the Stream object, which
+# costs 4 us: a third of a single-token call
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda i: torch.cuda.current_stream(i).cuda_stream)
+
+
 def _call_on(dev, name: str, *args):
-    """_call with the tensors' device current: their stream takes no launch
-    from another one."""
-    with torch.cuda.device(dev):
-        _call(name, *args)
+    """Calls `name` on dev's current stream (the last argument) with dev
+    current: its stream takes no launch from another device."""
+    fn = getattr(_lib if _lib is not None else load(), name)
+    i = dev.index
+    if torch.cuda.current_device() == i:
+        st = fn(*args, _raw_stream(i))
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, _raw_stream(i))
+    if st != 0:
+        raise SsmpError(name, st)
+
+
+def _arg(t: Optional[torch.Tensor], name: str, shape, dtype, dev) -> Optional[int]:
+    """The address of a tensor that is as it has to be (None: no tensor);
+    _check names what is wrong with one that is not."""
+    if t is None:
+        return None
+    if not (t.shape == shape and t.dtype is dtype and t.device == dev and t.is_contiguous()) or dev.type != "cuda":
+        _check(t, name, shape, dtype, dev)
+    return t.data_ptr()
+
+
+def _buffer(t: Optional[torch.Tensor], name: str, nbytes: int, dev):
+    """(tensor, address, size) of a byte buffer, made here where none is given."""
+    if t is None:
+        t = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dev)
+    else:
+        _check(t, name, device=dev)
+    return t, t.data_ptr(), _nbytes(t)
 
 
 def _heads(t: torch.Tensor, name: str):
@@ -588,19 +620,22 @@ def _heads(t: torch.Tensor, name: str):
     return t.shape
 
 
-def _qk_norm_args(q, k, wq, wk, pos, inv_freq, interleaved):
-    """Checks of what the forward and the backward share; (T, Hq, Hk, D, rot)."""
+def _qk_norm_args(q, k, wq, wk, pos, inv_freq):
+    """Checks of what the forward and the backward share: sizes (T, Hq, Hk, D,
+    rot), the addresses of the shared inputs, and the dtype and its code."""
     T, Hq, D = _heads(q, "q")
     Hk = _heads(k, "k")[1]
-    dev = q.device
-    _check(q, "q"); _check(k, "k", (T, Hk, D), q.dtype, dev)
-    _check(wq, "wq", (D,), torch.float32, dev); _check(wk, "wk", (D,), torch.float32, dev)
+    dev, dt = q.device, q.dtype
+    code = _dtype_code(q)
     rot = 0 if inv_freq is None else 2 * inv_freq.numel()
+    ptrs = [_arg(q, "q", (T, Hq, D), dt, dev), _arg(k, "k", (T, Hk, D), dt, dev),
+            _arg(wq, "wq", (D,), torch.float32, dev), _arg(wk, "wk", (D,), torch.float32, dev), None, None]
     if rot:
         if pos is None:
             raise ValueError("the rotation (inv_freq) needs pos")
-        _check(inv_freq, "inv_freq", (rot // 2,), torch.float32, dev); _check(pos, "pos", (T,), torch.int32, dev)
-    return T, Hq, Hk, D, rot
+        ptrs[4] = _arg(pos, "pos", (T,), torch.int32, dev)
+        ptrs[5] = _arg(inv_freq, "inv_freq", (rot // 2,), torch.float32, dev)
+    return (T, Hq, Hk, D, rot), ptrs, dt, code
 
 
 def qk_norm_pack_fwd(q: torch.Tensor, k: torch.Tensor, wq: Optional[torch.Tensor] = None,
@@ -610,11 +645,11 @@ def qk_norm_pack_fwd(q: torch.Tensor, k: torch.Tensor, wq: Optional[torch.Tensor
     """Norms of the heads of q (T, Hq, D) and k (T, Hk, D), times the weights
     (D,), the first 2 * len(inv_freq) components turned by pos * inv_freq.
     Returns (yq, yk); `out` may supply them (q and k themselves included)."""
-    T, Hq, Hk, D, rot = _qk_norm_args(q, k, wq, wk, pos, inv_freq, interleaved)
+    sizes, ptrs, dt, code = _qk_norm_args(q, k, wq, wk, pos, inv_freq)
+    dev = q.device
     yq, yk = (torch.empty_like(q), torch.empty_like(k)) if out is None else out
-    _check(yq, "yq", q.shape, q.dtype, q.device); _check(yk, "yk", k.shape, q.dtype, q.device)
-    _call_on(q.device, "qk_norm_pack_fwd", _ptr(q), _ptr(k), _ptr(wq), _ptr(wk), _ptr(pos), _ptr(inv_freq), _ptr(yq),
-             _ptr(yk), T, Hq, Hk, D, rot, _dtype_code(q), int(norm), float(eps), int(bool(interleaved)), _stream(q))
+    _call_on(dev, "qk_norm_pack_fwd", *ptrs, _arg(yq, "yq", q.shape, dt, dev), _arg(yk, "yk", k.shape, dt, dev),
+             *sizes, code, int(norm), float(eps), int(bool(interleaved)))
     return yq, yk
 
 
@@ -628,35 +663,37 @@ def qk_norm_pack_bwd(q: torch.Tensor, k: torch.Tensor, dyq: torch.Tensor, dyk: t
                      norm: int = SSMP_NORM_L2, eps: float = 1e-6, interleaved: bool = False,
                      workspace: Optional[torch.Tensor] = None, out: Optional[dict] = None) -> dict:
     """Gradients of sum(dyq * yq) + sum(dyk * yk): {"dq", "dk", "dwq", "dwk"}
-    (the last two None without weights). q and k are the forward's inputs."""
-    T, Hq, Hk, D, rot = _qk_norm_args(q, k, wq, wk, pos, inv_freq, interleaved)
-    dev = q.device
-    _check(dyq, "dyq", q.shape, q.dtype, dev); _check(dyk, "dyk", k.shape, q.dtype, dev)
+    (the last two None without weights). q and k are the forward's inputs.
+    `out` may supply them (dq and dk may be dyq and dyk)."""
+    sizes, ptrs, dt, code = _qk_norm_args(q, k, wq, wk, pos, inv_freq)
+    T, Hq, Hk, D, _ = sizes
+    dev, f32 = q.device, torch.float32
+    ptrs += [_arg(dyq, "dyq", q.shape, dt, dev), _arg(dyk, "dyk", k.shape, dt, dev)]
     if out is None:
-        new = lambda w: None if w is None else torch.empty_like(w)  # noqa: E731
-        out = {"dq": torch.empty_like(q), "dk": torch.empty_like(k), "dwq": new(wq), "dwk": new(wk)}
+        out = {"dq": torch.empty_like(q), "dk": torch.empty_like(k), "dwq": None if wq is None else torch.empty_like(wq),
+               "dwk": None if wk is None else torch.empty_like(wk)}
     dq, dk, dwq, dwk = (out[n] for n in ("dq", "dk", "dwq", "dwk"))
-    _check(dq, "dq", q.shape, q.dtype, dev); _check(dk, "dk", k.shape, q.dtype, dev)
-    _check(dwq, "dwq", (D,), torch.float32, dev); _check(dwk, "dwk", (D,), torch.float32, dev)
-    if workspace is None and (dwq is not None or dwk is not None):
-        workspace = torch.empty(max(qk_norm_pack_bwd_workspace_bytes(T, Hq, Hk, D), 1), dtype=torch.uint8, device=dev)
-    _check(workspace, "workspace", device=dev)
-    _call_on(dev, "qk_norm_pack_bwd", _ptr(q), _ptr(k), _ptr(wq), _ptr(wk), _ptr(pos), _ptr(inv_freq), _ptr(dyq),
-             _ptr(dyk), _ptr(dq), _ptr(dk), _ptr(dwq), _ptr(dwk), _ptr(workspace), _nbytes(workspace), T, Hq, Hk, D,
-             rot, _dtype_code(q), int(norm), float(eps), int(bool(interleaved)), _stream(q))
+    ws = (workspace, None, 0)
+    if workspace is not None or dwq is not None or dwk is not None:
+        nbytes = qk_norm_pack_bwd_workspace_bytes(T, Hq, Hk, D) if workspace is None else 0
+        ws = _buffer(workspace, "workspace", nbytes, dev)
+    _call_on(dev, "qk_norm_pack_bwd", *ptrs, _arg(dq, "dq", q.shape, dt, dev), _arg(dk, "dk", k.shape, dt, dev),
+             _arg(dwq, "dwq", (D,), f32, dev), _arg(dwk, "dwk", (D,), f32, dev), ws[1], ws[2], *sizes, code,
+             int(norm), float(eps), int(bool(interleaved)))
     return {"dq": dq, "dk": dk, "dwq": dwq, "dwk": dwk}
 
 
-def _delta_sizes(q, k, heads_v, g, beta):
-    """Checks of what the delta-rule calls share; (tokens, Hk, Hv, Dk, Dv).
-    heads_v: the tensor that has v's shape, with its name."""
-    t, name = heads_v
+def _delta_args(q, k, v, name, g, beta):
+    """Checks of what the delta-rule calls share: sizes (tokens, Hk, Hv, Dk,
+    Dv), the addresses of q, k, v (or what has its shape, `name`), g and beta,
+    and the dtype's code."""
     T, Hk, Dk = _heads(q, "q")
-    _, Hv, Dv = _heads(t, name)
-    dev = q.device
-    _check(q, "q"); _check(k, "k", (T, Hk, Dk), q.dtype, dev); _check(t, name, (T, Hv, Dv), q.dtype, dev)
-    _check(g, "g", (T, Hv), torch.float32, dev); _check(beta, "beta", (T, Hv), torch.float32, dev)
-    return T, Hk, Hv, Dk, Dv
+    _, Hv, Dv = _heads(v, name)
+    dev, dt = q.device, q.dtype
+    code = _dtype_code(q)
+    return (T, Hk, Hv, Dk, Dv), (_arg(q, "q", (T, Hk, Dk), dt, dev), _arg(k, "k", (T, Hk, Dk), dt, dev),
+                                 _arg(v, name, (T, Hv, Dv), dt, dev), _arg(g, "g", (T, Hv), torch.float32, dev),
+                                 _arg(beta, "beta", (T, Hv), torch.float32, dev)), code
 
 
 def gated_delta_pack_saved_bytes(T: int, nseq: int, Hk: int, Hv: int, Dk: int, Dv: int) -> int:
@@ -685,24 +722,24 @@ def gated_delta_pack_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: t
     (nseq, Hv, Dk, Dv). scale defaults to Dk ** -0.5. Returns (out, saved or
     None, final_state or None); save=True (or a `saved` buffer) keeps what the
     backward reads. The scratch is free again once the call's work on the
-    current stream is done."""
-    T, Hk, Hv, Dk, Dv = _delta_sizes(q, k, (v, "v"), g, beta)
-    dev = q.device
+    current stream is done. Rows behind cu_seqlens[-1] are left as they were."""
+    sizes, (pq, pk, pv, pg, pb), code = _delta_args(q, k, v, "v", g, beta)
+    T, Hk, Hv, Dk, Dv = sizes
+    dev, f32 = q.device, torch.float32
     nseq = _nseq(cu_seqlens, dev)
-    fs = _out_or_new(final_state, (nseq, Hv, Dk, Dv), torch.float32, dev)
-    for name, t in (("initial_state", initial_state), ("final_state", fs)):
-        _check(t, name, (nseq, Hv, Dk, Dv), torch.float32, dev)
-    if saved is None and save:
-        saved = torch.empty(max(gated_delta_pack_saved_bytes(T, nseq, Hk, Hv, Dk, Dv), 1), dtype=torch.uint8,
-                            device=dev)
-    _check(saved, "saved", device=dev)
-    scratch = _scratch(scratch, gated_delta_pack_fwd_scratch_bytes(T, nseq, Hk, Hv, Dk, Dv, q.dtype), dev)
+    state = (nseq, Hv, Dk, Dv)
+    fs = _out_or_new(final_state, state, f32, dev)
+    kept = (saved, None, 0)
+    if save or saved is not None:
+        kept = _buffer(saved, "saved", gated_delta_pack_saved_bytes(T, nseq, Hk, Hv, Dk, Dv) if saved is None else 0, dev)
+    ws = _buffer(scratch, "scratch",
+                 gated_delta_pack_fwd_scratch_bytes(T, nseq, Hk, Hv, Dk, Dv, q.dtype) if scratch is None else 0, dev)
     o = torch.empty_like(v) if out is None else out
-    _check(o, "out", (T, Hv, Dv), q.dtype, dev)
-    _call_on(dev, "gated_delta_pack_fwd", _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(cu_seqlens), nseq,
-             _ptr(o), T, Hk, Hv, Dk, Dv, _dtype_code(q), float(Dk ** -0.5 if scale is None else scale),
-             _ptr(initial_state), _ptr(fs), _ptr(saved), _nbytes(saved), _ptr(scratch), _nbytes(scratch), _stream(q))
-    return o, saved, fs
+    _call_on(dev, "gated_delta_pack_fwd", pq, pk, pv, pg, pb, cu_seqlens.data_ptr(), nseq,
+             _arg(o, "out", (T, Hv, Dv), q.dtype, dev), *sizes, code, float(Dk ** -0.5 if scale is None else scale),
+             _arg(initial_state, "initial_state", state, f32, dev), _arg(fs, "final_state", state, f32, dev),
+             kept[1], kept[2], ws[1], ws[2])
+    return o, kept[0], fs
 
 
 def gated_delta_pack_bwd(q: torch.Tensor, k: torch.Tensor, g: torch.Tensor, beta: torch.Tensor,
@@ -714,25 +751,24 @@ def gated_delta_pack_bwd(q: torch.Tensor, k: torch.Tensor, g: torch.Tensor, beta
     what the forward saved: {"dq", "dk", "dv", "dg", "dbeta",
     "dinitial_state"} (the last None unless asked for: True, or an output
     tensor). `out` may supply the first five."""
-    T, Hk, Hv, Dk, Dv = _delta_sizes(q, k, (dout, "dout"), g, beta)
-    dev = q.device
+    sizes, (pq, pk, pdo, pg, pb), code = _delta_args(q, k, dout, "dout", g, beta)
+    T, Hk, Hv, Dk, Dv = sizes
+    dev, dt, f32 = q.device, q.dtype, torch.float32
     nseq = _nseq(cu_seqlens, dev)
-    di = _out_or_new(dinitial_state, (nseq, Hv, Dk, Dv), torch.float32, dev)
-    for name, t in (("dfinal_state", dfinal_state), ("dinitial_state", di)):
-        _check(t, name, (nseq, Hv, Dk, Dv), torch.float32, dev)
+    state = (nseq, Hv, Dk, Dv)
+    di = _out_or_new(dinitial_state, state, f32, dev)
     _check(saved, "saved", device=dev)
-    scratch = _scratch(scratch, gated_delta_pack_bwd_scratch_bytes(T, nseq, Hk, Hv, Dk, Dv, q.dtype), dev)
+    ws = _buffer(scratch, "scratch",
+                 gated_delta_pack_bwd_scratch_bytes(T, nseq, Hk, Hv, Dk, Dv, dt) if scratch is None else 0, dev)
     if out is None:
         out = {"dq": torch.empty_like(q), "dk": torch.empty_like(k), "dv": torch.empty_like(dout),
                "dg": torch.empty_like(g), "dbeta": torch.empty_like(beta)}
     dq, dk, dv, dg, dbeta = (out[n] for n in ("dq", "dk", "dv", "dg", "dbeta"))
-    _check(dq, "dq", q.shape, q.dtype, dev); _check(dk, "dk", q.shape, q.dtype, dev)
-    _check(dv, "dv", dout.shape, q.dtype, dev); _check(dg, "dg", g.shape, torch.float32, dev)
-    _check(dbeta, "dbeta", g.shape, torch.float32, dev)
-    _call_on(dev, "gated_delta_pack_bwd", _ptr(q), _ptr(k), _ptr(g), _ptr(beta), _ptr(cu_seqlens), nseq, _ptr(dout),
-             T, Hk, Hv, Dk, Dv, _dtype_code(q), float(Dk ** -0.5 if scale is None else scale), _ptr(dfinal_state),
-             _ptr(di), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dg), _ptr(dbeta), _ptr(saved), _nbytes(saved),
-             _ptr(scratch), _nbytes(scratch), _stream(q))
+    _call_on(dev, "gated_delta_pack_bwd", pq, pk, pg, pb, cu_seqlens.data_ptr(), nseq, pdo, *sizes, code,
+             float(Dk ** -0.5 if scale is None else scale), _arg(dfinal_state, "dfinal_state", state, f32, dev),
+             _arg(di, "dinitial_state", state, f32, dev), _arg(dq, "dq", q.shape, dt, dev),
+             _arg(dk, "dk", q.shape, dt, dev), _arg(dv, "dv", dout.shape, dt, dev), _arg(dg, "dg", g.shape, f32, dev),
+             _arg(dbeta, "dbeta", g.shape, f32, dev), saved.data_ptr(), _nbytes(saved), ws[1], ws[2])
     return {"dq": dq, "dk": dk, "dv": dv, "dg": dg, "dbeta": dbeta, "dinitial_state": di}
 
 
@@ -741,18 +777,18 @@ def gated_delta_pack_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: 
                           out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """One token for each row: q, k (B, Hk, Dk), v (B, Hv, Dv), g, beta
     (B, Hv); state fp32 (nslots, Hv, Dk, Dv) is updated in place at slots
-    (int32 (B); None: row b uses slot b). Returns out (B, Hv, Dv); a row whose
-    slot lies outside the pool keeps what `out` held (zeros, if it is made here)."""
-    B, Hk, Hv, Dk, Dv = _delta_sizes(q, k, (v, "v"), g, beta)
+    (int32 (B); None: row b uses slot b). Returns out (B, Hv, Dv). A row whose
+    slot lies outside the pool is skipped: its out is left as it was, which for
+    an `out` made here is unset memory."""
+    sizes, ptrs, code = _delta_args(q, k, v, "v", g, beta)
+    B, Hk, Hv, Dk, Dv = sizes
     dev = q.device
     if state.dim() != 4:
         raise ValueError(f"state has shape {tuple(state.shape)}, expected (slots, heads, Dk, Dv)")
-    _check(state, "state", (state.shape[0], Hv, Dk, Dv), torch.float32, dev)
-    _check(slots, "slots", (B,), torch.int32, dev)
+    n = state.shape[0]
     if out is None:
-        out = torch.empty_like(v) if slots is None else torch.zeros_like(v)
-    _check(out, "out", (B, Hv, Dv), q.dtype, dev)
-    _call_on(dev, "gated_delta_pack_step", _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(state), _ptr(slots),
-             _ptr(out), B, state.shape[0], Hk, Hv, Dk, Dv, _dtype_code(q),
-             float(Dk ** -0.5 if scale is None else scale), _stream(q))
+        out = torch.empty_like(v)
+    _call_on(dev, "gated_delta_pack_step", *ptrs, _arg(state, "state", (n, Hv, Dk, Dv), torch.float32, dev),
+             _arg(slots, "slots", (B,), torch.int32, dev), _arg(out, "out", (B, Hv, Dv), q.dtype, dev), B, n, Hk, Hv,
+             Dk, Dv, code, float(Dk ** -0.5 if scale is None else scale))
     return out
