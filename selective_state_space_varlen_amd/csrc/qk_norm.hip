@@ -35,20 +35,40 @@ struct NormArgs {
     int32_t hsplit;       // waves that share a token's heads
 };
 
-__device__ __forceinline__ void norm_load(const float* p, float (&v)[kNormVec]) {
-    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-}
-__device__ __forceinline__ void norm_load(const uint16_t* p, float (&v)[kNormVec]) {
-    const uint4 a = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[2 * i] = bf16_to_f32(w[i]);
-        v[2 * i + 1] = bf16_hi_to_f32(w[i]);
+// a lane's components as they lie in memory, so that the next row's are under
+// way while the present ones are worked on
+template <typename T>
+struct NormRow;
+template <>
+struct NormRow<float> {
+    f32x4 w[2];
+    __device__ __forceinline__ void load(const float* p, bool on) {
+        w[0] = w[1] = f32x4{0, 0, 0, 0};
+        if (on) {
+            w[0] = reinterpret_cast<const f32x4*>(p)[0];
+            w[1] = reinterpret_cast<const f32x4*>(p)[1];
+        }
     }
-}
+    __device__ __forceinline__ void values(float (&v)[kNormVec]) const {
+#pragma unroll
+        for (int e = 0; e < kNormVec; ++e) v[e] = w[e >> 2][e & 3];
+    }
+};
+template <>
+struct NormRow<uint16_t> {
+    u32x4 w;
+    __device__ __forceinline__ void load(const uint16_t* p, bool on) {
+        w = u32x4{0, 0, 0, 0};
+        if (on) w = *reinterpret_cast<const u32x4*>(p);
+    }
+    __device__ __forceinline__ void values(float (&v)[kNormVec]) const {
+#pragma unroll
+        for (int e = 0; e < kNormVec / 2; ++e) {
+            v[2 * e] = bf16_to_f32(w[e]);
+            v[2 * e + 1] = bf16_hi_to_f32(w[e]);
+        }
+    }
+};
 __device__ __forceinline__ void norm_store(float* p, const float (&v)[kNormVec]) {
     reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
     reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
@@ -62,39 +82,59 @@ __device__ __forceinline__ void norm_store(uint16_t* p, const float (&v)[kNormVe
 
 template <int LPR>
 __device__ __forceinline__ float row_sum(float v) {
+    if constexpr (LPR >= 2) v = dpp_add<0xB1>(v);
+    if constexpr (LPR >= 4) v = dpp_add<0x4E>(v);
+    if constexpr (LPR >= 8) v = dpp_add<0x141>(v);
+    if constexpr (LPR >= 16) v = dpp_add<0x140>(v);
 #pragma unroll
-    for (int m = 1; m < LPR; m <<= 1) v += __shfl_xor(v, m);
+    for (int m = 16; m < LPR; m <<= 1) v += __shfl_xor(v, m);
     return v;
+}
+
+// Where a wave's rows of a token lie: the heads of q, then those of k.
+struct NormAt {
+    size_t at;
+    bool isk, on;
+};
+__device__ __forceinline__ NormAt norm_at(const NormArgs& a, int64_t t, int h, int col) {
+    const bool isk = h >= a.H[0];
+    const size_t row = isk ? (size_t)t * a.H[1] + (h - a.H[0]) : (size_t)t * a.H[0] + h;
+    return {row * a.D + col, isk, col < a.D && h < a.H[0] + a.H[1]};
 }
 
 // The turn of a lane's components at one position: y_e = x_e c_e + p_e s_e with
 // p_e the other member of e's pair and the sign in s_e. The angle in turns is
 // formed in 64 bits (a 32-bit one is off by radians at positions near 1e7)
-// and reduced to half a turn either way before it is rounded to 32.
+// and reduced to half a turn either way before it is rounded to 32. The wave's
+// lanes form one angle each (rot / 2 of them in all) and pass them on through
+// LDS: formed where they are used, they would take longer than the heads do
+// (16384 tokens of 40 heads of 128, half turned: 118 us against 84).
 struct Turn {
     float c[kNormVec], s[kNormVec];
     int partner;  // lane that holds the other members (half-split pairs)
     bool on;      // this lane holds turned components
 };
-__device__ __forceinline__ void make_turn(Turn& t, const NormArgs& a, int32_t pos, int lane, int col) {
+__device__ __forceinline__ void make_turn(Turn& t, const NormArgs& a, int32_t pos, int lane, int col, float2* cs) {
     const int half = a.rot >> 1;
+    wave_sync();  // the last token's have been read
+    for (int i = lane; i < half; i += kWave) {
+        const double turns = (double)pos * (double)a.inv_freq[i] * 0.15915494309189533577;
+        float sn, co;
+        sincospif((float)(2.0 * (turns - rint(turns))), &sn, &co);
+        cs[i] = make_float2(co, sn);
+    }
+    wave_sync();
     t.on = col < a.rot;
     t.partner = lane;
     if (!a.interleaved && t.on) t.partner = col < half ? lane + half / kNormVec : lane - half / kNormVec;
 #pragma unroll
     for (int e = 0; e < kNormVec; ++e) {
-        t.c[e] = 1.0f;
-        t.s[e] = 0.0f;
         const int d = col + e;
-        if (d < a.rot) {
-            const int i = a.interleaved ? d >> 1 : (d < half ? d : d - half);
-            const bool first = a.interleaved ? (d & 1) == 0 : d < half;
-            const double turns = (double)pos * (double)a.inv_freq[i] * 0.15915494309189533577;
-            float sn, cs;
-            sincospif((float)(2.0 * (turns - rint(turns))), &sn, &cs);
-            t.c[e] = cs;
-            t.s[e] = first ? -sn : sn;
-        }
+        const int i = a.interleaved ? d >> 1 : (d < half ? d : d - half);
+        const bool first = a.interleaved ? (e & 1) == 0 : d < half;
+        const float2 v = d < a.rot ? cs[i] : make_float2(1.0f, 0.0f);
+        t.c[e] = v.x;
+        t.s[e] = first ? -v.y : v.y;
     }
 }
 template <bool BACK>
@@ -114,10 +154,11 @@ __device__ __forceinline__ void apply_turn(const Turn& t, int interleaved, float
     }
 }
 
-// One wave per (token, share of its heads); the heads of q, then those of k.
+// One wave per (token, share of its heads).
 template <typename T, int LPR, bool ROT>
 __global__ __launch_bounds__(kNormWaves* kWave) void k_qk_norm_fwd(NormArgs a) {
     constexpr int RPW = kWave / LPR;  // rows a wave holds at a time
+    __shared__ float2 cs[ROT ? kNormWaves : 1][ROT ? kNormMaxD / 2 : 1];
     const int lane = lane_id();
     const int64_t task = (int64_t)blockIdx.x * kNormWaves + (threadIdx.x >> 6);
     if (task >= a.T * a.hsplit) return;
@@ -125,28 +166,35 @@ __global__ __launch_bounds__(kNormWaves* kWave) void k_qk_norm_fwd(NormArgs a) {
     const int share = (int)(task % a.hsplit);
     const int col = (lane & (LPR - 1)) * kNormVec;
     const bool in = col < a.D;
-    const int heads = a.H[0] + a.H[1];
+    const int heads = a.H[0] + a.H[1], step = a.hsplit * RPW;
+    int h = share * RPW + lane / LPR;
+    NormAt p = norm_at(a, t, h, col);
+    NormRow<T> row;
+    row.load(static_cast<const T*>(a.x[p.isk]) + p.at, p.on);
     float w[2][kNormVec];
 #pragma unroll
     for (int n = 0; n < 2; ++n)
 #pragma unroll
         for (int e = 0; e < kNormVec; ++e) w[n][e] = a.w[n] && in ? a.w[n][col + e] : 1.0f;
     Turn turn;
-    if constexpr (ROT) make_turn(turn, a, a.pos[t], lane, col);
-    for (int h0 = share * RPW; h0 < heads; h0 += a.hsplit * RPW) {
-        const int h = h0 + lane / LPR;
-        const bool isk = h >= a.H[0], on = in && h < heads;
-        const size_t at = isk ? ((size_t)t * a.H[1] + (h - a.H[0])) * a.D + col : ((size_t)t * a.H[0] + h) * a.D + col;
-        float v[kNormVec] = {};
-        if (on) norm_load(static_cast<const T*>(a.x[isk]) + at, v);
+    if constexpr (ROT) make_turn(turn, a, a.pos[t], lane, col, cs[threadIdx.x >> 6]);
+    for (int h0 = share * RPW; h0 < heads; h0 += step) {
+        h += step;
+        const NormAt pn = norm_at(a, t, h, col);
+        NormRow<T> next;
+        next.load(static_cast<const T*>(a.x[pn.isk]) + pn.at, pn.on);
+        float v[kNormVec];
+        row.values(v);
         float ss = 0.0f;
 #pragma unroll
         for (int e = 0; e < kNormVec; ++e) ss = fmaf(v[e], v[e], ss);
         const float r = rsqrtf(fmaf(row_sum<LPR>(ss), a.inv_n, a.eps));
 #pragma unroll
-        for (int e = 0; e < kNormVec; ++e) v[e] = v[e] * r * (isk ? w[1][e] : w[0][e]);
+        for (int e = 0; e < kNormVec; ++e) v[e] = v[e] * r * (p.isk ? w[1][e] : w[0][e]);
         if constexpr (ROT) apply_turn<false>(turn, a.interleaved, v);
-        if (on) norm_store(static_cast<T*>(a.y[isk]) + at, v);
+        if (p.on) norm_store(static_cast<T*>(a.y[p.isk]) + p.at, v);
+        p = pn;
+        row = next;
     }
 }
 
@@ -155,10 +203,11 @@ __global__ __launch_bounds__(kNormWaves* kWave) void k_qk_norm_fwd(NormArgs a) {
 template <typename T, int LPR, bool ROT, bool DW>
 __global__ __launch_bounds__(kNormWaves* kWave) void k_qk_norm_bwd(NormArgs a) {
     constexpr int RPW = kWave / LPR;
+    __shared__ float2 cs[ROT ? kNormWaves : 1][ROT ? kNormMaxD / 2 : 1];
     const int lane = lane_id(), wave = threadIdx.x >> 6;
     const int col = (lane & (LPR - 1)) * kNormVec;
     const bool in = col < a.D;
-    const int heads = a.H[0] + a.H[1];
+    const int heads = a.H[0] + a.H[1], step = a.hsplit * RPW;
     float w[2][kNormVec], dw[2][kNormVec];
 #pragma unroll
     for (int n = 0; n < 2; ++n)
@@ -171,18 +220,23 @@ __global__ __launch_bounds__(kNormWaves* kWave) void k_qk_norm_bwd(NormArgs a) {
     for (int64_t task = (int64_t)blockIdx.x * kNormWaves + wave; task < tasks; task += (int64_t)gridDim.x * kNormWaves) {
         const int64_t t = task / a.hsplit;
         const int share = (int)(task % a.hsplit);
+        int h = share * RPW + lane / LPR;
+        NormAt p = norm_at(a, t, h, col);
+        NormRow<T> xr, gr;
+        xr.load(static_cast<const T*>(a.x[p.isk]) + p.at, p.on);
+        gr.load(static_cast<const T*>(a.dy[p.isk]) + p.at, p.on);
         Turn turn;
-        if constexpr (ROT) make_turn(turn, a, a.pos[t], lane, col);
-        for (int h0 = share * RPW; h0 < heads; h0 += a.hsplit * RPW) {
-            const int h = h0 + lane / LPR;
-            const bool isk = h >= a.H[0], on = in && h < heads;
-            const size_t at =
-                isk ? ((size_t)t * a.H[1] + (h - a.H[0])) * a.D + col : ((size_t)t * a.H[0] + h) * a.D + col;
-            float v[kNormVec] = {}, g[kNormVec] = {};
-            if (on) {
-                norm_load(static_cast<const T*>(a.x[isk]) + at, v);
-                norm_load(static_cast<const T*>(a.dy[isk]) + at, g);
-            }
+        if constexpr (ROT) make_turn(turn, a, a.pos[t], lane, col, cs[wave]);
+        for (int h0 = share * RPW; h0 < heads; h0 += step) {
+            h += step;
+            const NormAt pn = norm_at(a, t, h, col);
+            NormRow<T> xn, gn;
+            xn.load(static_cast<const T*>(a.x[pn.isk]) + pn.at, pn.on);
+            gn.load(static_cast<const T*>(a.dy[pn.isk]) + pn.at, pn.on);
+            const bool isk = p.isk, on = p.on;
+            float v[kNormVec], g[kNormVec];
+            xr.values(v);
+            gr.values(g);
             float ss = 0.0f;
 #pragma unroll
             for (int e = 0; e < kNormVec; ++e) ss = fmaf(v[e], v[e], ss);
@@ -203,7 +257,10 @@ __global__ __launch_bounds__(kNormWaves* kWave) void k_qk_norm_bwd(NormArgs a) {
             m = row_sum<LPR>(m) * a.inv_n;
 #pragma unroll
             for (int e = 0; e < kNormVec; ++e) v[e] = r * fmaf(-v[e], m, g[e]);
-            if (on) norm_store(static_cast<T*>(a.y[isk]) + at, v);
+            if (on) norm_store(static_cast<T*>(a.y[isk]) + p.at, v);
+            p = pn;
+            xr = xn;
+            gr = gn;
         }
     }
     if constexpr (DW) {
