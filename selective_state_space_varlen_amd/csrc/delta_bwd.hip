@@ -33,7 +33,9 @@ __global__ __launch_bounds__(NW * 64) void k_delta_chain_bwd(DeltaArgs a) {
     const int ncb = (a.Dv + kCols - 1) / kCols, group = a.Hv / a.Hk;
     const Spread sp = spread(blockIdx.x, ncb * group);
     if (sp.group >= (int64_t)a.nseq * a.Hk) return;
-    const int seq = (int)(sp.group / a.Hk), hk = (int)(sp.group % a.Hk);
+    const int hk = (int)(sp.group % a.Hk);
+    int seq = (int)(sp.group / a.Hk);
+    if (a.order) seq = a.order[seq];
     const int hv = hk * group + sp.member / ncb, cb = sp.member % ncb;
     const int wave = wave_id(), l = lane_id(), l16 = l & 15, l4 = l >> 4;
     const int col = cb * kCols + wave * 16 + l16;
@@ -443,7 +445,7 @@ int launch_delta_bwd(const DeltaArgs& a, hipStream_t s) {
 }
 
 struct DeltaBwdLayout {
-    size_t dec, inv, att, dS1, dU, rows, total;
+    size_t dec, inv, att, order, dS1, dU, rows, total;
 };
 inline DeltaBwdLayout delta_bwd_layout(int64_t T, int32_t nseq, int32_t Hv, int32_t Dk, int32_t Dv) {
     const size_t n = (size_t)delta_slots(T, nseq);
@@ -451,7 +453,8 @@ inline DeltaBwdLayout delta_bwd_layout(int64_t T, int32_t nseq, int32_t Hv, int3
     L.dec = 0;
     L.inv = L.dec + round256(n * Hv * kDec * 4);
     L.att = L.inv + round256(n * Hv * kTri * 4);
-    L.dS1 = L.att + round256(n * Hv * kTri * 4);
+    L.order = L.att + round256(n * Hv * kTri * 4);
+    L.dS1 = L.order + round256((size_t)nseq * 4);
     L.dU = L.dS1 + round256(n * Hv * Dk * Dv * 4);
     L.rows = L.dU + round256(n * Hv * kC * Dv * 4);
     L.total = L.rows + round256(n * Hv * ((Dk + kDh - 1) / kDh) * kC * 4);
@@ -516,6 +519,7 @@ extern "C" int gated_delta_pack_bwd(const void* q, const void* k, const float* g
         a.dS1 = reinterpret_cast<float*>(ws + L.dS1);
         a.dU = reinterpret_cast<float*>(ws + L.dU);
         a.rows = reinterpret_cast<float*>(ws + L.rows);
+        if (chain_ordered(a)) a.order = reinterpret_cast<int32_t*>(ws + L.order);
     }
     hipStream_t s = static_cast<hipStream_t>(stream);
     const bool wide = Dk > 64;

@@ -59,39 +59,42 @@ __device__ __forceinline__ Seq seq_at(const int32_t* __restrict__ cu, int s, int
 }
 
 // The chunk in a slot: false where the slot holds none. Called by whole waves;
-// 64 boundaries are looked at in one step, so 2 steps find a sequence among 4096.
+// 64 boundaries are looked at in one step, so one trip to memory finds a
+// sequence among 64, two among 4096.
 struct Chunk {
     int64_t start;  // its first token
     int32_t n;      // tokens
-    bool last;      // of its sequence
-    int32_t seq;
 };
 __device__ __forceinline__ bool chunk_at(const int32_t* __restrict__ cu, int32_t nseq, int64_t T, int64_t slot,
                                          Chunk& c) {
+    const int top = (int)T, lane = lane_id();
     int lo = 0, hi = nseq;
-    const int lane = lane_id();
-    while (hi - lo > 1) {
+    while (true) {
         const int step = (hi - lo + 63) / 64, i = lo + lane * step;
-        bool below = false;
-        if (i < hi) {
-            int64_t a = cu[i];
-            a = a < 0 ? 0 : (a > T ? T : a);
-            below = a / kC + i <= slot;
-        }
-        int n = __popcll(__ballot(below));
+        int a = cu[i < nseq ? i : nseq];
+        a = a < 0 ? 0 : (a > top ? top : a);
+        int n = __popcll(__ballot(i < hi && (int64_t)(a / kC) + i <= slot));
         n = n < 1 ? 1 : n;
-        lo += (n - 1) * step;
-        hi = lo + step < hi ? lo + step : hi;
+        if (step > 1) {
+            lo += (n - 1) * step;
+            hi = lo + step < hi ? lo + step : hi;
+            continue;
+        }
+        lo += n - 1;  // the sequence
+        const int first = __builtin_amdgcn_readlane(a, n - 1);
+        int end;
+        if (n < 64) {
+            end = __builtin_amdgcn_readlane(a, n);
+        } else {
+            end = cu[lo + 1];
+            end = end < 0 ? 0 : (end > top ? top : end);
+        }
+        const int64_t at = (slot - (first / kC + lo)) * kC;
+        if (at < 0 || at >= end - first) return false;
+        c.start = first + at;
+        c.n = end - first - at < kC ? (int32_t)(end - first - at) : kC;
+        return true;
     }
-    lo = __builtin_amdgcn_readfirstlane(lo);
-    const Seq q = seq_at(cu, lo, T);
-    const int64_t at = (slot - q.slot0) * kC;
-    if (at < 0 || at >= q.len) return false;
-    c.start = q.start + at;
-    c.n = q.len - at < kC ? (int32_t)(q.len - at) : kC;
-    c.last = at + kC >= q.len;
-    c.seq = lo;
-    return true;
 }
 
 // ---------------------------------------------------------------------------
@@ -573,6 +576,7 @@ struct DeltaArgs {
     float* inv;      // the chunk's inverse: kTri
     float* att;      // the decayed products of q and k: kTri
     float *dS1, *dU; // backward: gradients of the state that leaves the chunk, and of U
+    int32_t* order;  // the sequences by length (null: as they come)
     float* rows;     // backward: per 64 columns of dq and dk, what k_delta_dg adds up: 64
 };
 

@@ -35,7 +35,9 @@ __global__ __launch_bounds__(NW * 64) void k_delta_chain(DeltaArgs a) {
     const int ncb = (a.Dv + kCols - 1) / kCols, group = a.Hv / a.Hk;
     const Spread sp = spread(blockIdx.x, ncb * group);
     if (sp.group >= (int64_t)a.nseq * a.Hk) return;
-    const int seq = (int)(sp.group / a.Hk), hk = (int)(sp.group % a.Hk);
+    const int hk = (int)(sp.group % a.Hk);
+    int seq = (int)(sp.group / a.Hk);
+    if (a.order) seq = a.order[seq];
     const int hv = hk * group + sp.member / ncb, cb = sp.member % ncb;
     const int wave = wave_id(), l = lane_id(), l16 = l & 15, l4 = l >> 4;
     const int col = cb * kCols + wave * 16 + l16;
@@ -174,7 +176,7 @@ int launch_delta_fwd(const DeltaArgs& a, hipStream_t s) {
 }
 
 struct DeltaFwdLayout {
-    size_t dec, inv, att, total;
+    size_t dec, inv, att, order, total;
 };
 inline DeltaFwdLayout delta_fwd_layout(int64_t T, int32_t nseq, int32_t Hv) {
     const size_t n = (size_t)delta_slots(T, nseq);
@@ -182,7 +184,8 @@ inline DeltaFwdLayout delta_fwd_layout(int64_t T, int32_t nseq, int32_t Hv) {
     L.dec = 0;
     L.inv = L.dec + round256(n * Hv * kDec * 4);
     L.att = L.inv + round256(n * Hv * kTri * 4);
-    L.total = L.att + round256(n * Hv * kTri * 4);
+    L.order = L.att + round256(n * Hv * kTri * 4);
+    L.total = L.order + round256((size_t)nseq * 4);
     return L;
 }
 
@@ -241,6 +244,7 @@ extern "C" int gated_delta_pack_fwd(const void* q, const void* k, const void* v,
         a.dec = reinterpret_cast<float*>(ws + L.dec);
         a.inv = reinterpret_cast<float*>(ws + L.inv);
         a.att = reinterpret_cast<float*>(ws + L.att);
+        if (chain_ordered(a)) a.order = reinterpret_cast<int32_t*>(ws + L.order);
         if (saved) {
             a.S0 = static_cast<float*>(saved);
             a.E = reinterpret_cast<float*>(static_cast<char*>(saved) +

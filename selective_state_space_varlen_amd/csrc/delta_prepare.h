@@ -6,12 +6,43 @@
 
 namespace ssmp {
 
+// The sequences by chunks, most first, for the chains: a chain takes as long as
+// its sequence, and a long one that starts last is waited for alone. Sorted by
+// counting in one workgroup beside those that prepare the chunks; the order
+// among equals is left to chance and changes no result. h: 2048 ints of LDS.
+constexpr int kOrderMax = 4096;  // sequences; more need no order, they are short beside the whole
+__device__ __forceinline__ void order_sequences(const DeltaArgs& a, int* h) {
+    constexpr int kBins = 1024;
+    const int tid = threadIdx.x;
+    const auto bin = [&](int s) {
+        const int n = (seq_at(a.cu, s, a.T).len + kC - 1) / kC;
+        return kBins - 1 - (n < kBins ? n : kBins - 1);
+    };
+    for (int i = tid; i < kBins; i += 256) h[i] = 0;
+    __syncthreads();
+    for (int s = tid; s < a.nseq; s += 256) atomicAdd(&h[bin(s)], 1);
+    __syncthreads();
+    int own = 0;  // of four bins
+    for (int i = 0; i < 4; ++i) own += h[tid * 4 + i];
+    h[kBins + tid] = own;
+    __syncthreads();
+    int before = 0;
+    for (int i = 0; i < tid; ++i) before += h[kBins + i];
+    for (int i = 0; i < 4; ++i) {
+        const int n = h[tid * 4 + i];
+        h[tid * 4 + i] = before;
+        before += n;
+    }
+    __syncthreads();
+    for (int s = tid; s < a.nseq; s += 256) a.order[atomicAdd(&h[bin(s)], 1)] = s;
+}
+
 // One workgroup per (slot, value head); the heads of a group run on one XCD,
 // whose L2 then holds their keys and queries.
 //   forward:  (I + L diag(beta))^-1 and P,           both lower triangular
 //   backward: (I + diag(beta) L)^-T and scale P^T,   both upper triangular
 template <typename T, int DKP, bool BWD>
-__global__ __launch_bounds__(256) void k_delta_prepare(DeltaArgs a) {
+__global__ __launch_bounds__(256, kExact<T> == 1 ? 4 : 1) void k_delta_prepare(DeltaArgs a) {
     constexpr int NX = kExact<T>;
     using Rows = Tile<T, DKP>;
     constexpr int kKeys = kC * DKP * (int)sizeof(T), kMats = kC * kLdA * 4;
@@ -23,6 +54,7 @@ __global__ __launch_bounds__(256) void k_delta_prepare(DeltaArgs a) {
     T* const Ql = Kl + kC * DKP;
     float* const A = reinterpret_cast<float*>(lds);
     float* const X = A + kC * kLdA;
+    if (a.order && blockIdx.x == gridDim.x - 1) return order_sequences(a, reinterpret_cast<int*>(lds));
     const int members = a.Hv / a.Hk;
     const Spread sp = spread(blockIdx.x, members);
     const int64_t slots = delta_slots(a.T, a.nseq);
@@ -52,47 +84,54 @@ __global__ __launch_bounds__(256) void k_delta_prepare(DeltaArgs a) {
         a.dec[sh * kDec + 3 * kC + l] = decay_of(last - s);
     }
     __syncthreads();
-    // Wave w has rows 16 w .. of both products. kk: K K^T. qk: forward K Q^T
-    // (rows j, columns i), backward Q K^T (rows i, columns j): a lane then
-    // holds four contiguous k of one row of what is stored.
-    f32x4 kk[4] = {}, qk[4] = {};
+    // The products' 16 x 16 tiles that hold anything are five for each wave:
+    //   forward:  K K^T rows w, columns 0 .. w; K Q^T rows w, columns w .. 3
+    //   backward: Q K^T rows w, columns 0 .. w; K K^T rows 3 - w, columns 0 .. 3 - w
+    // (K Q^T, as a lane then holds four contiguous keys of one query's row; in
+    // the backward four queries of one key.) Which is which is a matter of
+    // addresses, so that no tile hangs on a branch.
+    const auto first = [&](int t) { return t <= wave; };  // of the two products
+    const auto tile_row = [&](int t) { return BWD && !first(t) ? 3 - wave : wave; };
+    const auto tile_col = [&](int t) { return first(t) ? t : (BWD ? t - wave - 1 : t - 1); };
+    f32x4 acc[5] = {};
 #pragma unroll
     for (int s = 0; s < DKP / 32; ++s) {
-        const int i = wave * 16 + l16, u = s * 4 + l4;
-        const auto ka = tile_frag(Kl + Rows::at(i, u));
-        const auto qa = tile_frag(Ql + Rows::at(i, u));
+        const int u = s * 4 + l4;
+        Frag<NX> fa[2], fb[5];
+        fa[0] = tile_frag((BWD ? Ql : Kl) + Rows::at(wave * 16 + l16, u));
+        fa[1] = BWD ? tile_frag(Kl + Rows::at((3 - wave) * 16 + l16, u)) : fa[0];
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
-            const int j = n * 16 + l16;
-            const bool below = n <= wave;  // tiles with some i >= j, rows i
-            if (below || !BWD) {
-                const auto kb = tile_frag(Kl + Rows::at(j, u));
-                if (below) mma<NX>(kk[n], ka, kb);
-                if constexpr (BWD) mma<NX>(qk[n], qa, kb);
-            }
-            if constexpr (!BWD)
-                if (n >= wave) mma<NX>(qk[n], ka, tile_frag(Ql + Rows::at(j, u)));
-        }
+        for (int t = 0; t < 5; ++t)
+            fb[t] = tile_frag((BWD || first(t) ? Kl : Ql) + Rows::at(tile_col(t) * 16 + l16, u));
+#pragma unroll
+        for (int t = 0; t < 5; ++t) mma<NX>(acc[t], first(t) ? fa[0] : fa[1], fb[t]);
     }
     __syncthreads();
     float* const att = a.att + sh * kTri;
 #pragma unroll
-    for (int n = 0; n < 4; ++n) {
-        f32x4 p = {0, 0, 0, 0};
-        if (!BWD || n <= wave) {
+    for (int t = 0; t < 5; ++t) {
+        const int i0 = tile_row(t) * 16 + l4 * 4, j = tile_col(t) * 16 + l16;
+        if (first(t) != BWD) {  // K K^T: rows are later tokens
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const int i = wave * 16 + l4 * 4 + r, j = n * 16 + l16;  // row and column of the tiles
-                const float d = decay_of(i > j ? G[i] - G[j] : G[j] - G[i]);
-                if (n <= wave) A[i * kLdA + j] = i > j ? (BWD ? beta[i] : beta[j]) * d * kk[n][r] : 0.0f;
-                if constexpr (BWD) p[r] = i >= j ? d * qk[n][r] * a.scale : 0.0f;
-                else p[r] = j >= i ? d * qk[n][r] : 0.0f;
+                const int i = i0 + r;
+                A[i * kLdA + j] = i > j ? (BWD ? beta[i] : beta[j]) * decay_of(G[i] - G[j]) * acc[t][r] : 0.0f;
             }
+        } else {
+            f32x4 p;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int i = i0 + r;
+                if constexpr (BWD) p[r] = i >= j ? decay_of(G[i] - G[j]) * acc[t][r] * a.scale : 0.0f;
+                else p[r] = j >= i ? decay_of(G[j] - G[i]) * acc[t][r] : 0.0f;
+            }
+            *reinterpret_cast<f32x4*>(att + tri_row<BWD>(j, i0) * 32 + (kplace(i0) & 31)) = p;
         }
-        const int row = n * 16 + l16, k = wave * 16 + l4 * 4;
-        // what lies in neither block of the other triangle is not stored
-        if (BWD ? (k >= 32 || row < 32) : (k < 32 || row >= 32))
-            *reinterpret_cast<f32x4*>(att + tri_row<BWD>(row, k) * 32 + (kplace(k) & 31)) = p;
+    }
+    // the two empty tiles in the stored blocks
+    if ((wave & 1) != BWD) {
+        const int row = (BWD ? wave + 1 : wave - 1) * 16 + l16, k = wave * 16 + l4 * 4;
+        *reinterpret_cast<f32x4*>(att + tri_row<BWD>(row, k) * 32 + (kplace(k) & 31)) = f32x4{0, 0, 0, 0};
     }
     __syncthreads();
     chunk_inverse(A, X);
@@ -111,7 +150,7 @@ __global__ __launch_bounds__(256) void k_delta_prepare(DeltaArgs a) {
 
 template <typename T, int DKP, bool BWD>
 int launch_delta_prepare(const DeltaArgs& a, hipStream_t s) {
-    const int64_t blocks = spread_blocks(delta_slots(a.T, a.nseq) * a.Hk, a.Hv / a.Hk);
+    const int64_t blocks = spread_blocks(delta_slots(a.T, a.nseq) * a.Hk, a.Hv / a.Hk) + (a.order ? 1 : 0);
     k_delta_prepare<T, DKP, BWD><<<(unsigned)blocks, 256, 0, s>>>(a);
     SSMP_LAUNCH_CHECK();
     return SSMP_OK;
@@ -196,6 +235,12 @@ struct ChainLoads {
 constexpr int kCUs = 256;
 inline int chain_waves(const DeltaArgs& a) {
     return a.Dv > 64 && (int64_t)a.nseq * a.Hv * ((a.Dv + 127) / 128) >= kCUs ? 8 : 4;
+}
+// Whether the chains are started by length: where they are more than the CUs
+// take at once.
+inline bool chain_ordered(const DeltaArgs& a) {
+    return a.nseq > 1 && a.nseq <= kOrderMax &&
+           (int64_t)a.nseq * a.Hv * ((a.Dv + 127) / 128) > kCUs;
 }
 inline unsigned chain_blocks(const DeltaArgs& a, int waves) {
     const int ncb = (a.Dv + waves * kWaveCols - 1) / (waves * kWaveCols);

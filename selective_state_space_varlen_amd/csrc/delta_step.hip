@@ -28,6 +28,17 @@ struct StepArgs {
     float scale;
 };
 
+// The state passes once each way and would push everything else out of the
+// caches: without temporal hint 246 us for 256 sequences of 32 heads of
+// 128 x 128, with it 211 (5.1 TB/s); the same 4.7 us for one sequence.
+__device__ __forceinline__ float4 state_load(const float* p) {
+    const f32x4 v = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(p));
+    return make_float4(v[0], v[1], v[2], v[3]);
+}
+__device__ __forceinline__ void state_store(float* p, float4 v) {
+    __builtin_nontemporal_store(f32x4{v.x, v.y, v.z, v.w}, reinterpret_cast<f32x4*>(p));
+}
+
 // RPG: rows of the state a thread holds (Dk <= 32 RPG). Rows of the batch that
 // name the same slot are applied in their order, by the workgroups of the
 // first of them (the others end at once), so a slot may be named twice.
@@ -48,7 +59,7 @@ __global__ __launch_bounds__(kStepThreads) void k_delta_step(StepArgs a) {
 #pragma unroll
     for (int j = 0; j < RPG; ++j) {
         const int d = rg + j * kStepRowGroups;
-        s[j] = in && d < a.Dk ? *reinterpret_cast<const float4*>(S + (size_t)d * a.Dv + col) : make_float4(0, 0, 0, 0);
+        s[j] = in && d < a.Dk ? state_load(S + (size_t)d * a.Dv + col) : make_float4(0, 0, 0, 0);
     }
     if (a.slots) {
         int earlier = 0;
@@ -119,7 +130,7 @@ __global__ __launch_bounds__(kStepThreads) void k_delta_step(StepArgs a) {
 #pragma unroll
     for (int j = 0; j < RPG; ++j) {
         const int d = rg + j * kStepRowGroups;
-        if (in && d < a.Dk) *reinterpret_cast<float4*>(S + (size_t)d * a.Dv + col) = s[j];
+        if (in && d < a.Dk) state_store(S + (size_t)d * a.Dv + col, s[j]);
     }
 }
 
