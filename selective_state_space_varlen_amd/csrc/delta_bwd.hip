@@ -12,8 +12,11 @@
 //   dk write =  diag(e^{G_last - G}) U dS'^T + a^T Q - b^T K
 // and, since e^{G_i} scales what token i reads and e^{-G_i} what it writes,
 //   dG_i = q_i.dq_i + k_i.dkread_i - k_i.dkwrite_i,  the last token's also + <dS', S'>,
-//   <dS', S'> = e^{G_last} <dS', S> + sum_j e^{G_last - G_j} k_j.(dS' U_j),
 //   dg_t = sum of dG_i, i >= t in the chunk.
+// U_i is written through k_i alone, so k_i.dkwrite_i = U_i.dU_i = beta_i dbeta_i;
+// and the sum of U_i.Y_i, taken from Y's two forms, gives
+//   <dS', S'> = e^{G_last} <dS', S> + sum_i beta_i dbeta_i - (q.dq + k.dkread of a K and -b K, summed),
+// so that dkwrite enters nothing but dk.
 // k_delta_prepare makes what no gradient enters, k_delta_chain_bwd walks each
 // sequence's chunks back with dS in registers, and k_delta_grads forms the
 // chunks' gradients, all at once, from S, E, dS' and dU (k_delta_dg the last
@@ -155,12 +158,13 @@ __global__ __launch_bounds__(NW * 64) void k_delta_chain_bwd(DeltaArgs a) {
 // columns 16 w .. for all 64 tokens, so its rows of S and dS' come straight
 // from memory, and row tile w of a^T and b^T. 74 KB of LDS for bf16, so that
 // two workgroups share a CU and one's loads pass behind the other's products.
-// The rows of q.dq + k.(dkread - dkwrite) over these columns go to a.rows, for
-// k_delta_dg to add up.
+// The rows of q.dq + k.dkread over these columns go to a.rows, with what the
+// columns give of <dS', S'> (below) on the last, for k_delta_dg to add up.
 constexpr int kDh = 64;
 template <typename T>
 __global__ __launch_bounds__(256, kExact<T> == 1 ? 2 : 1) void k_delta_grads(DeltaArgs a) {
     constexpr int NX = kExact<T>;
+    constexpr int NK = kOutP<T>;  // planes of what enters dk alone: its rounding hides the third
     using Plane = Tile<uint16_t, kC>;
     constexpr int PT = kC * kC;
     // planes of dOut, dE and U (64 columns at a time, [token][column]), then of
@@ -283,20 +287,26 @@ __global__ __launch_bounds__(256, kExact<T> == 1 ? 2 : 1) void k_delta_grads(Del
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) sd = fmaf(s0[s].w[e >> 2][e & 3], s1[s].w[e >> 2][e & 3], sd);
-                const auto sb = unit_planes(s0[s]), gb = unit_planes(s1[s]);
+                const auto sb = unit_planes(s0[s]);
+                const auto gb = split_tiles<NK>(s1[s].w[0], s1[s].w[1]);
                 const auto uw = tile_planes<3>(Up, PT, Plane::at(wave * 16 + l16, u));
 #pragma unroll
                 for (int m = 0; m < 4; ++m) {
                     const int o = Plane::at(m * 16 + l16, u);
                     const auto po = tile_planes<NX>(Op, PT, o);
                     const auto pe = tile_planes<3>(Ep, PT, o);
-                    mma<3>(dq[m], po, sb);
-                    mma<3>(dr[m], pe, sb);
-                    mma<3>(dw[m], tile_planes<3>(Up, PT, o), gb);
-                    if (m >= wave) {  // below the diagonal of a and b
-                        mma<3>(at[m], uw, po);
-                        mma<3>(bt[m], uw, pe);
-                    }
+                    const auto pu = tile_planes<NK>(Up, PT, o);
+                    const bool below = m >= wave;  // the diagonal of a and b
+                    static_for<6>([&](auto t) {
+                        mma_term<3, t>(dr[m], pe, sb);
+                        mma_term<3, t>(dq[m], po, sb);
+                        mma_term<NK, t>(dw[m], pu, gb);
+                    });
+                    if (below)
+                        static_for<6>([&](auto t) {
+                            mma_term<3, t>(bt[m], uw, pe);
+                            mma_term<3, t>(at[m], uw, po);
+                        });
                     __builtin_amdgcn_sched_barrier(0);
                 }
             }
@@ -316,17 +326,18 @@ __global__ __launch_bounds__(256, kExact<T> == 1 ? 2 : 1) void k_delta_grads(Del
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
             __builtin_amdgcn_sched_barrier(0);
-            float kv[4];
+            float kv[4], qv[4];
             kt.values4(l, m, wave, kv);
+            qt.values4(l, m, wave, qv);
             const f32x4 eg = *reinterpret_cast<const f32x4*>(&decay[0][m * 16 + l4 * 4]);
             const f32x4 el = *reinterpret_cast<const f32x4*>(&decay[1][m * 16 + l4 * 4]);
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 dq[m][r] *= eg[r] * a.scale;
                 dr[m][r] *= -eg[r];
-                dw[m][r] *= el[r];
-                end = fmaf(kv[r], dw[m][r], end);
+                end += fmaf(qv[r], dq[m][r], kv[r] * dr[m][r]);
             }
+            tk[m] += el * dw[m];
         }
 #pragma unroll
         for (int pass = 0; pass < 2; ++pass) {  // a, then -b
@@ -350,7 +361,7 @@ __global__ __launch_bounds__(256, kExact<T> == 1 ? 2 : 1) void k_delta_grads(Del
                     uint32_t p[3];
                     split2<3>(v[r], v[r + 1], p);
 #pragma unroll
-                    for (int y = 0; y < 3; ++y) {
+                    for (int y = 0; y < NK; ++y) {
                         uint16_t* const to = reinterpret_cast<uint16_t*>(Mt) + y * PT;
                         to[Plane::at(j + r, pi >> 3) + (pi & 7)] = (uint16_t)p[y];
                         to[Plane::at(j + r + 1, pi >> 3) + (pi & 7)] = (uint16_t)(p[y] >> 16);
@@ -367,7 +378,7 @@ __global__ __launch_bounds__(256, kExact<T> == 1 ? 2 : 1) void k_delta_grads(Del
                 for (int m = 0; m < 4; ++m) {
                     const int o = Plane::at(m * 16 + l16, u);
                     if (m >= 2 * s) mma<3>(pass ? dr[m] : dq[m], tile_planes<3>(M, PT, o), kb);
-                    if (m < 2 + 2 * s) mma<3>(dw[m], tile_planes<3>(Mt, PT, o), pass ? kb : qb);
+                    if (m < 2 + 2 * s) mma<NK>(tk[m], tile_planes<NK>(Mt, PT, o), pass ? kb : qb);
                     __builtin_amdgcn_sched_barrier(0);
                 }
             }
@@ -382,11 +393,13 @@ __global__ __launch_bounds__(256, kExact<T> == 1 ? 2 : 1) void k_delta_grads(Del
             qt.values4(l, m, wave, qv);
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const float s = sum16(fmaf(qv[r], dq[m][r], kv[r] * (dr[m][r] - dw[m][r])));
-                if (l16 == 0) red[wave][i + r] = s;
+                const float s = fmaf(qv[r], dq[m][r], kv[r] * dr[m][r]);
+                end -= s;
+                const float row = sum16(s);
+                if (l16 == 0) red[wave][i + r] = row;
             }
             tq[m] += dq[m];
-            tk[m] += dr[m] + dw[m];
+            tk[m] += dr[m];
         }
         end = sum16(end);
         if (l16 == 0) ends[wave * 4 + l4] = end;
@@ -414,12 +427,19 @@ __global__ __launch_bounds__(256) void k_delta_dg(DeltaArgs a) {
     if (!chunk_at(a.cu, a.nseq, a.T, sh / a.Hv, c)) return;
     double s = 0.0;
     for (int h = 0; h < halves; ++h) s += (double)a.rows[(sh * halves + h) * kC + l];
+    // what token i writes counts against it, and once for the whole chunk
+    const size_t at = (size_t)(c.start + l) * a.Hv + hv;
+    const double w = l < c.n ? (double)a.beta[at] * (double)a.dbeta[at] : 0.0;
+    double all = w;
+#pragma unroll
+    for (int x = 1; x < kC; x <<= 1) all += __shfl_xor(all, x);
+    s += (l == kC - 1 ? all : 0.0) - w;
 #pragma unroll
     for (int x = 1; x < kC; x <<= 1) {
         const double o = __shfl_down(s, x);
         if (l + x < kC) s += o;
     }
-    if (l < c.n) a.dg[(size_t)(c.start + l) * a.Hv + hv] = (float)s;
+    if (l < c.n) a.dg[at] = (float)s;
 }
 
 template <typename T, int DKP>

@@ -130,6 +130,21 @@ __device__ __forceinline__ void mma(f32x4& d, const Frag<NA>& a, const Frag<NB>&
             if (s - i >= 0 && s - i < NB) d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.p[i], b.p[s - i], d, 0, 0, 0);
 }
 
+// One of the plane products of mma, the TERM-th in its order, if there are as
+// many: for products on several results to take turns.
+template <int LIM, int TERM, int NA, int NB>
+__device__ __forceinline__ void mma_term(f32x4& d, const Frag<NA>& a, const Frag<NB>& b) {
+    int t = 0;
+#pragma unroll
+    for (int s = LIM - 1; s >= 0; --s)
+#pragma unroll
+        for (int i = 0; i < NA; ++i)
+            if (s - i >= 0 && s - i < NB) {
+                if (t == TERM) d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.p[i], b.p[s - i], d, 0, 0, 0);
+                ++t;
+            }
+}
+
 // d[m] += a[m] b for tiles FROM .. TO - 1, one plane product after the other
 // over all tiles: a matrix instruction waits for the last one on its tile.
 template <int LIM, int FROM, int TO, int NA, int NB, int N, int NF>
@@ -207,6 +222,11 @@ __device__ __forceinline__ Frag<NP> split8(const float (&v)[8]) {
 // planes that hold an input of this type exactly
 template <typename T>
 constexpr int kExact = std::is_same<T, float>::value ? 3 : 1;
+
+// planes of what enters a result of this type alone: bf16's own rounding hides
+// what two planes (16 bits) leave out
+template <typename T>
+constexpr int kOutP = std::is_same<T, float>::value ? 3 : 2;
 
 __device__ __forceinline__ void load8(const float* p, bool on, float (&v)[8]) {
     f32x4 a = {0, 0, 0, 0}, b = {0, 0, 0, 0};
@@ -323,13 +343,6 @@ struct Unit<float> {
 };
 __device__ __forceinline__ Frag<1> unit_planes(const Unit<uint16_t>& u) { return {{__builtin_bit_cast(bf16x8, u.w)}}; }
 __device__ __forceinline__ Frag<3> unit_planes(const Unit<float>& u) { return split_tiles<3>(u.w[0], u.w[1]); }
-template <typename T>
-__device__ __forceinline__ void copy8(T* to, const T* from, bool on) {
-    Unit<T> u;
-    u.load(from, on);
-    u.put_half(to, 0);
-    u.put_half(to + 4, 1);
-}
 // Left operands in LDS: rows of W elements of E in 16-byte units (32 for fp32:
 // what one lane reads), without padding; unit u of row r lies at u ^ swz(r),
 // so that the 16 rows a read touches fall into different banks.
@@ -461,19 +474,31 @@ constexpr double kGMin = -4096.0;
 // e^(sum of g over some tokens) from G's difference: rounded to 32 bits only
 // here, where an exponent of size |d| errs by |d| 2^-24 of a result 2^d
 __device__ __forceinline__ float decay_of(double d) { return exp2_fast((float)d); }
-__device__ __forceinline__ double chunk_decay_sum(const float* __restrict__ g, int64_t start, int n, int H, int h) {
+template <int CTRL>
+__device__ __forceinline__ double dpp_add_f64(double v) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)b, CTRL, 0xF, 0xF, true);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)(b >> 32), CTRL, 0xF, 0xF, true);
+    return v + __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+__device__ __forceinline__ double read_lane(double v, int l) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)b, l);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), l);
+    return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+// G from g of this lane's token (zero behind the chunk's end): sums within
+// the rows of 16 lanes, then those of the rows before
+__device__ __forceinline__ double chunk_decay_sum(float g) {
     const int lane = lane_id();
-    double v = 0.0;
-    if (lane < n) {
-        v = (double)g[(size_t)(start + lane) * H + h];
-        v = (v < kGMin ? kGMin : v) * 1.4426950408889634074;
-    }
-#pragma unroll
-    for (int m = 1; m < kC; m <<= 1) {
-        const double o = __shfl_up(v, m);
-        if (lane >= m) v += o;
-    }
-    return v;
+    double v = (double)g;
+    v = (v < kGMin ? kGMin : v) * 1.4426950408889634074;
+    v = dpp_add_f64<0x111>(v);
+    v = dpp_add_f64<0x112>(v);
+    v = dpp_add_f64<0x114>(v);
+    v = dpp_add_f64<0x118>(v);
+    const double a = read_lane(v, 15), b = a + read_lane(v, 31), c = b + read_lane(v, 47);
+    return v + (lane < 16 ? 0.0 : lane < 32 ? a : lane < 48 ? b : c);
 }
 
 // The inverse of I + A for strictly lower triangular A (64 x 64, fp32 in LDS

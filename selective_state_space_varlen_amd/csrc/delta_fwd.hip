@@ -14,11 +14,6 @@
 
 namespace ssmp {
 
-// planes of P and of U where they form the output: its own rounding to bf16
-// hides what two planes (16 bits) leave out
-template <typename T>
-constexpr int kOutP = std::is_same<T, float>::value ? 3 : 2;
-
 // One workgroup per (sequence, value head, 64 or 128 columns of the state), 16
 // columns a wave. Columns do not meet in the chain, and a wave's results are
 // its next right operands in the registers they are in (kplace), so the waves

@@ -64,24 +64,41 @@ __global__ __launch_bounds__(256, kExact<T> == 1 ? 4 : 1) void k_delta_prepare(D
     Chunk c;
     if (!chunk_at(a.cu, a.nseq, a.T, slot, c)) return;
     const int tid = threadIdx.x, wave = wave_id(), l = lane_id(), l16 = l & 15, l4 = l >> 4;
-    constexpr int kUnits = DKP / 8;
-#pragma unroll
-    for (int u = tid; u < kC * kUnits; u += 256) {
-        const int i = u / kUnits, k8 = u % kUnits;
-        const bool on = i < c.n && k8 * 8 < a.Dk;
-        const size_t o = ((size_t)(c.start + i) * a.Hk + hk) * a.Dk + k8 * 8;
-        copy8(Kl + Rows::at(i, k8), static_cast<const T*>(a.k) + o, on);
-        copy8(Ql + Rows::at(i, k8), static_cast<const T*>(a.q) + o, on);
-    }
     const size_t sh = (size_t)slot * a.Hv + hv;
+    constexpr int kUnits = DKP / 8, kN = kC * kUnits / 256;
+    // every load is under way before the first is waited for
+    const auto brows = rows_rsrc(a.beta + (size_t)c.start * a.Hv + hv, c.n, a.Hv, 1);
+    const auto grows = rows_rsrc(a.g + (size_t)c.start * a.Hv + hv, c.n, a.Hv, 1);
+    const uint32_t gl = Elt<float>::raw_rsrc(grows, (uint32_t)(l * a.Hv) * 4u);
+    const uint32_t bl = Elt<float>::raw_rsrc(brows, (uint32_t)(l * a.Hv) * 4u);
+    const size_t from = ((size_t)c.start * a.Hk + hk) * a.Dk;
+    const int stride = a.Hk * a.Dk;
+    const auto krows = rows_rsrc(static_cast<const T*>(a.k) + from, c.n, stride, a.Dk);
+    const auto qrows = rows_rsrc(static_cast<const T*>(a.q) + from, c.n, stride, a.Dk);
+    Unit<T> ku[kN], qu[kN];
+#pragma unroll
+    for (int x = 0; x < kN; ++x) {
+        const int u = tid + x * 256, i = u / kUnits, k8 = u % kUnits;
+        const uint32_t o = k8 * 8 < a.Dk ? (uint32_t)(i * stride + k8 * 8) * (uint32_t)sizeof(T) : kNowhere;
+        ku[x].load(krows, o);
+        qu[x].load(qrows, o);
+    }
     if (wave == 0) {
-        const double s = chunk_decay_sum(a.g, c.start, c.n, a.Hv, hv);
+        const double s = chunk_decay_sum(Elt<float>::cvt(gl));
         G[l] = s;
-        beta[l] = l < c.n ? a.beta[(size_t)(c.start + l) * a.Hv + hv] : 0.0f;
-        const double last = __shfl(s, kC - 1);
+        beta[l] = Elt<float>::cvt(bl);
+        const double last = read_lane(s, kC - 1);
         reinterpret_cast<double*>(a.dec + sh * kDec)[l] = s;
         a.dec[sh * kDec + 2 * kC + l] = decay_of(s);
         a.dec[sh * kDec + 3 * kC + l] = decay_of(last - s);
+    }
+#pragma unroll
+    for (int x = 0; x < kN; ++x) {
+        const int u = tid + x * 256, at = Rows::at(u / kUnits, u % kUnits);
+        ku[x].put_half(Kl + at, 0);
+        ku[x].put_half(Kl + at + 4, 1);
+        qu[x].put_half(Ql + at, 0);
+        qu[x].put_half(Ql + at + 4, 1);
     }
     __syncthreads();
     // The products' 16 x 16 tiles that hold anything are five for each wave:
