@@ -156,22 +156,56 @@ __global__ __launch_bounds__(NW * 64) void k_delta_chain_bwd(DeltaArgs a) {
 // One workgroup per (slot, key head, 64 columns of dq and dk), over the value
 // heads of the group, whose dq and dk it adds in registers. Wave w holds
 // columns 16 w .. for all 64 tokens, so its rows of S and dS' come straight
-// from memory, and row tile w of a^T and b^T. 74 KB of LDS for bf16, so that
-// two workgroups share a CU and one's loads pass behind the other's products.
+// from memory, and row tile w of a^T and b^T. It goes over dOut, dE, U, S and
+// dS' 32 columns at a time, the next ones (of the next head too) under way in
+// registers meanwhile: without that the kernel waits for memory two thirds of
+// its time. Two workgroups share a CU.
 // The rows of q.dq + k.dkread over these columns go to a.rows, with what the
-// columns give of <dS', S'> (below) on the last, for k_delta_dg to add up.
+// columns give of <dS', S'> on the last, for k_delta_dg to add up.
 constexpr int kDh = 64;
+constexpr int kDv = 32;
+
+// what a thread has under way of 32 columns of one head
+template <typename T>
+struct GradLoads {
+    Unit<T> o;             // token tid / 4, 8 columns: dOut,
+    Unit<float> E, dU;     // E and dU
+    Unit<float> s0, s1;    // row of S and dS' of this lane, 8 columns
+    uint32_t beta, dec;    // of its token; and place tid of the chunk's decays
+
+    // (the same loads whether there is such a head or not: n = 0 makes zeros)
+    __device__ __forceinline__ void load(const DeltaArgs& a, int64_t slot, const Chunk& c, int hv, int v0, int d0, int n) {
+        const int tid = fresh(threadIdx.x), l = tid & 63, t = tid >> 2;
+        const size_t sh = (size_t)slot * a.Hv + (n > 0 ? hv : 0);
+        const size_t at = (size_t)c.start * a.Hv + (n > 0 ? hv : 0);
+        const int e = v0 + (tid & 3) * 8, es = v0 + (l >> 4) * 8;
+        const auto rows = [&](const float* p, int r) { return rows_rsrc(p, n > 0 ? r : 0, a.Dv, a.Dv); };
+        o.load(rows_rsrc(static_cast<const T*>(a.dout) + at * a.Dv, n, a.Hv * a.Dv, a.Dv),
+               e < a.Dv ? (uint32_t)(t * a.Hv * a.Dv + e) * (uint32_t)sizeof(T) : kNowhere);
+        const uint32_t oe = e < a.Dv ? (uint32_t)(t * a.Dv + e) * 4u : kNowhere;
+        E.load(rows(a.E + sh * kC * a.Dv, kC), oe);
+        dU.load(rows(a.dU + sh * kC * a.Dv, kC), oe);
+        const uint32_t os = es < a.Dv ? (uint32_t)((d0 + (l & 15)) * a.Dv + es) * 4u : kNowhere;
+        s0.load(rows(a.S0 + sh * a.Dk * a.Dv, a.Dk), os);
+        s1.load(rows(a.dS1 + sh * a.Dk * a.Dv, a.Dk), os);
+        beta = Elt<float>::raw_rsrc(rows_rsrc(a.beta + at, n, a.Hv, 1), (uint32_t)(t * a.Hv) * 4u);
+        dec = Elt<float>::raw_rsrc(bytes_rsrc(a.dec + sh * kDec, n > 0 ? kDec * 4 : 0), (uint32_t)tid * 4u);
+    }
+};
+
 template <typename T>
 __global__ __launch_bounds__(256, kExact<T> == 1 ? 2 : 1) void k_delta_grads(DeltaArgs a) {
     constexpr int NX = kExact<T>;
     constexpr int NK = kOutP<T>;  // planes of what enters dk alone: its rounding hides the third
-    using Plane = Tile<uint16_t, kC>;
-    constexpr int PT = kC * kC;
-    // planes of dOut, dE and U (64 columns at a time, [token][column]), then of
-    // a or -b and its transpose
-    __shared__ alignas(16) __bf16 lds[(NX + 6) * PT];
+    using Plane = Tile<uint16_t, kDv>;
+    using Square = Tile<uint16_t, kC>;
+    constexpr int PT = kC * kDv, MT = kC * kC;
+    constexpr int kPlanes = (NX + 6) * PT, kSquares = (3 + NK) * MT;
+    // planes of dOut, dE and U ([token][column]); after a head's columns, of a
+    // or -b ([i][j]) and its transpose
+    __shared__ alignas(16) __bf16 lds[kPlanes > kSquares ? kPlanes : kSquares];
     __shared__ alignas(16) RowTile<T, kDh> kt, qt;
-    __shared__ double G[kC];
+    __shared__ alignas(16) double G[kC];
     __shared__ alignas(16) float decay[2][kC];
     __shared__ float red[4][kC], ends[16];
     const int halves = (a.Dk + kDh - 1) / kDh;
@@ -186,92 +220,62 @@ __global__ __launch_bounds__(256, kExact<T> == 1 ? 2 : 1) void k_delta_grads(Del
     __bf16* const Ep = lds + NX * PT;
     __bf16* const Up = Ep + 3 * PT;
     __bf16* const M = lds;
-    __bf16* const Mt = lds + 3 * PT;
+    __bf16* const Mt = lds + 3 * MT;
+    const int d0 = half * kDh + wave * 16;  // this wave's first column of dq and dk
+    GradLoads<T> next;
+    next.load(a, slot, c, hk * group, 0, d0, c.n);
     {
-        const int stride = a.Hk * a.Dk, d0 = half * kDh;
+        const int stride = a.Hk * a.Dk, dh = half * kDh;
         const size_t first = ((size_t)c.start * a.Hk + hk) * a.Dk;
         const auto kr = rows_rsrc(static_cast<const T*>(a.k) + first, c.n, stride, a.Dk);
         const auto qr = rows_rsrc(static_cast<const T*>(a.q) + first, c.n, stride, a.Dk);
+        Unit<T> ku[2], qu[2];
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
             const int u = threadIdx.x + x * 256, i = u >> 3, k8 = u & 7;
             const uint32_t o =
-                d0 + k8 * 8 < a.Dk ? (uint32_t)(i * stride + d0 + k8 * 8) * (uint32_t)sizeof(T) : kNowhere;
-            Unit<T> ku, qu;
-            ku.load(kr, o);
-            qu.load(qr, o);
-            kt.put(i, k8, ku);
-            qt.put(i, k8, qu);
+                dh + k8 * 8 < a.Dk ? (uint32_t)(i * stride + dh + k8 * 8) * (uint32_t)sizeof(T) : kNowhere;
+            ku[x].load(kr, o);
+            qu[x].load(qr, o);
+        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const int u = threadIdx.x + x * 256;
+            kt.put(u >> 3, u & 7, ku[x]);
+            qt.put(u >> 3, u & 7, qu[x]);
         }
     }
-    const int d0 = half * kDh + wave * 16;  // this wave's first column of dq and dk
     f32x4 tq[4] = {}, tk[4] = {};
     for (int hv = hk * group; hv < (hk + 1) * group; ++hv) {
         const size_t sh = (size_t)slot * a.Hv + hv;
-        __syncthreads();  // the last head's G and decays have been read
-        const int tid0 = fresh(threadIdx.x);
-        {
-            const float* const dec = a.dec + sh * kDec;
-            if (wave < 2) reinterpret_cast<float*>(G)[tid0] = *at_bytes(dec, (uint32_t)tid0 * 4u);
-            else (&decay[0][0])[tid0 - 2 * kC] = *at_bytes(dec, (uint32_t)tid0 * 4u);
-        }
-        const auto brows = rows_rsrc(a.beta + (size_t)c.start * a.Hv + hv, c.n, a.Hv, 1);
-        float beta[2], db[2] = {};
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-            beta[x] = Elt<float>::cvt(Elt<float>::raw_rsrc(brows, (uint32_t)(((tid0 + x * 256) >> 3) * a.Hv) * 4u));
         f32x4 dq[4] = {}, dr[4] = {}, dw[4] = {};  // dq, dk read, dk write
         f32x4 at[4] = {}, bt[4] = {};              // row tile `wave` of a^T and b^T
-        float sd = 0.0f;                           // <dS', S>
-        const auto orows = rows_rsrc(static_cast<const T*>(a.dout) + ((size_t)c.start * a.Hv + hv) * a.Dv, c.n,
-                                     a.Hv * a.Dv, a.Dv);
-        const auto vrows = rows_rsrc(static_cast<const T*>(a.dv) + ((size_t)c.start * a.Hv + hv) * a.Dv, c.n,
-                                     a.Hv * a.Dv, a.Dv);
-        const auto erows = rows_rsrc(a.E + sh * kC * a.Dv, kC, a.Dv, a.Dv);
-        const auto urows = rows_rsrc(a.dU + sh * kC * a.Dv, kC, a.Dv, a.Dv);
-        const auto srows = rows_rsrc(a.S0 + sh * a.Dk * a.Dv, a.Dk, a.Dv, a.Dv);
-        const auto grows = rows_rsrc(a.dS1 + sh * a.Dk * a.Dv, a.Dk, a.Dv, a.Dv);
-        for (int v0 = 0; v0 < a.Dv; v0 += 64) {
+        float sd = 0.0f, db = 0.0f;                // <dS', S>; this thread's part of dbeta
+        for (int v0 = 0; v0 < a.Dv; v0 += kDv) {
+            __syncthreads();  // what lies in lds, and the last head's decays, have been read
             const int tid = fresh(threadIdx.x), l = tid & 63, l16 = l & 15, l4 = l >> 4;
-            Unit<T> fo[2];
-            Unit<float> fE[2], fU[2], s0[2], s1[2];
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const int u = tid + x * 256, t = u >> 3, e = v0 + (u & 7) * 8;
-                const bool on = e < a.Dv;
-                fo[x].load(orows, on ? (uint32_t)(t * a.Hv * a.Dv + e) * (uint32_t)sizeof(T) : kNowhere);
-                fE[x].load(erows, on ? (uint32_t)(t * a.Dv + e) * 4u : kNowhere);
-                fU[x].load(urows, on ? (uint32_t)(t * a.Dv + e) * 4u : kNowhere);
-            }
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {  // this lane's row of S and dS'
-                const int e = v0 + s * 32 + l4 * 8;
-                const uint32_t o = e < a.Dv ? (uint32_t)((d0 + l16) * a.Dv + e) * 4u : kNowhere;
-                s0[s].load(srows, o);
-                s1[s].load(grows, o);
-            }
-            if (v0) __syncthreads();  // the last block's planes have been read
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const int u = tid + x * 256, t = u >> 3, e = v0 + (u & 7) * 8;
-                __builtin_amdgcn_sched_barrier(0);
+            {
+                if (wave < 2) reinterpret_cast<uint32_t*>(G)[tid] = next.dec;
+                else reinterpret_cast<uint32_t*>(&decay[0][0])[tid - 2 * kC] = next.dec;
+                const int t = tid >> 2, e = v0 + (tid & 3) * 8;
+                const float beta = Elt<float>::cvt(next.beta);
                 float E[8], dU[8];
 #pragma unroll
                 for (int p = 0; p < 8; ++p) {
-                    E[p] = fE[x].w[p >> 2][p & 3];
-                    dU[p] = fU[x].w[p >> 2][p & 3];
-                    db[x] = fmaf(dU[p], E[p], db[x]);
-                    E[p] *= beta[x];
-                    dU[p] *= beta[x];
+                    E[p] = next.E.w[p >> 2][p & 3];
+                    dU[p] = next.dU.w[p >> 2][p & 3];
+                    db = fmaf(dU[p], E[p], db);
+                    E[p] *= beta;
+                    dU[p] *= beta;
                 }
-                if (half == 0) {
-                    Unit<T> dv;
-                    dv.pack(dU);
-                    dv.store(vrows, e < a.Dv ? (uint32_t)(t * a.Hv * a.Dv + e) * (uint32_t)sizeof(T) : kNowhere);
-                }
-                const auto po = unit_planes(fo[x]);
+                Unit<T> dv;
+                dv.pack(dU);
+                dv.store(rows_rsrc(static_cast<const T*>(a.dv) + ((size_t)c.start * a.Hv + hv) * a.Dv,
+                                   half == 0 ? c.n : 0, a.Hv * a.Dv, a.Dv),
+                         e < a.Dv ? (uint32_t)(t * a.Hv * a.Dv + e) * (uint32_t)sizeof(T) : kNowhere);
+                const auto po = unit_planes(next.o);
                 const auto pe = split8<3>(dU), pu = split8<3>(E);
-                const int o = Plane::at(t, u & 7);
+                const int o = Plane::at(t, tid & 3);
 #pragma unroll
                 for (int p = 0; p < NX; ++p) *reinterpret_cast<bf16x8*>(Op + p * PT + o) = po.p[p];
 #pragma unroll
@@ -280,47 +284,42 @@ __global__ __launch_bounds__(256, kExact<T> == 1 ? 2 : 1) void k_delta_grads(Del
                     *reinterpret_cast<bf16x8*>(Up + p * PT + o) = pu.p[p];
                 }
             }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sd = fmaf(next.s0.w[e >> 2][e & 3], next.s1.w[e >> 2][e & 3], sd);
+            const auto sb = unit_planes(next.s0);
+            const auto gb = split_tiles<NK>(next.s1.w[0], next.s1.w[1]);
+            {
+                const bool more = v0 + kDv < a.Dv;
+                next.load(a, slot, c, more ? hv : hv + 1, more ? v0 + kDv : 0, d0,
+                          more || hv + 1 < (hk + 1) * group ? c.n : 0);
+            }
             __syncthreads();
+            const auto uw = tile_planes<3>(Up, PT, Plane::at(wave * 16 + l16, l4));
 #pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                const int u = s * 4 + l4;
-                __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) sd = fmaf(s0[s].w[e >> 2][e & 3], s1[s].w[e >> 2][e & 3], sd);
-                const auto sb = unit_planes(s0[s]);
-                const auto gb = split_tiles<NK>(s1[s].w[0], s1[s].w[1]);
-                const auto uw = tile_planes<3>(Up, PT, Plane::at(wave * 16 + l16, u));
-#pragma unroll
-                for (int m = 0; m < 4; ++m) {
-                    const int o = Plane::at(m * 16 + l16, u);
-                    const auto po = tile_planes<NX>(Op, PT, o);
-                    const auto pe = tile_planes<3>(Ep, PT, o);
-                    const auto pu = tile_planes<NK>(Up, PT, o);
-                    const bool below = m >= wave;  // the diagonal of a and b
+            for (int m = 0; m < 4; ++m) {
+                const int o = Plane::at(m * 16 + l16, l4);
+                const auto po = tile_planes<NX>(Op, PT, o);
+                const auto pe = tile_planes<3>(Ep, PT, o);
+                const auto pu = tile_planes<NK>(Up, PT, o);
+                static_for<6>([&](auto t) {
+                    mma_term<3, t>(dr[m], pe, sb);
+                    mma_term<3, t>(dq[m], po, sb);
+                    mma_term<NK, t>(dw[m], pu, gb);
+                });
+                if (m >= wave)  // below the diagonal of a and b
                     static_for<6>([&](auto t) {
-                        mma_term<3, t>(dr[m], pe, sb);
-                        mma_term<3, t>(dq[m], po, sb);
-                        mma_term<NK, t>(dw[m], pu, gb);
+                        mma_term<3, t>(bt[m], uw, pe);
+                        mma_term<3, t>(at[m], uw, po);
                     });
-                    if (below)
-                        static_for<6>([&](auto t) {
-                            mma_term<3, t>(bt[m], uw, pe);
-                            mma_term<3, t>(at[m], uw, po);
-                        });
-                    __builtin_amdgcn_sched_barrier(0);
-                }
+                __builtin_amdgcn_sched_barrier(0);
             }
         }
         __syncthreads();
         const int tid = fresh(threadIdx.x), l = tid & 63, l16 = l & 15, l4 = l >> 4;
-        if (half == 0) {
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const int u = tid + x * 256, t = u >> 3;
-                const float s = sum8(db[x]);
-                Elt<float>::st_rsrc(rows_rsrc(a.dbeta + (size_t)c.start * a.Hv + hv, c.n, a.Hv, 1),
-                                    (u & 7) == 0 ? (uint32_t)(t * a.Hv) * 4u : kNowhere, s);
-            }
+        {
+            const float s = dpp_add<0x4E>(dpp_add<0xB1>(db));
+            Elt<float>::st_rsrc(rows_rsrc(a.dbeta + (size_t)c.start * a.Hv + hv, half == 0 ? c.n : 0, a.Hv, 1),
+                                (tid & 3) == 0 ? (uint32_t)((tid >> 2) * a.Hv) * 4u : kNowhere, s);
         }
         float end = decay[0][kC - 1] * sd;
 #pragma unroll
@@ -355,16 +354,16 @@ __global__ __launch_bounds__(256, kExact<T> == 1 ? 2 : 1) void k_delta_grads(Del
                     }
                 }
                 const int pj = kplace(j), pi = kplace(i);
-                lds_put4<3>(M, PT, Plane::at(i, pj >> 3) + (pj & 7), v);
+                lds_put4<3>(M, MT, Square::at(i, pj >> 3) + (pj & 7), v);
 #pragma unroll
                 for (int r = 0; r < 4; r += 2) {
                     uint32_t p[3];
                     split2<3>(v[r], v[r + 1], p);
 #pragma unroll
                     for (int y = 0; y < NK; ++y) {
-                        uint16_t* const to = reinterpret_cast<uint16_t*>(Mt) + y * PT;
-                        to[Plane::at(j + r, pi >> 3) + (pi & 7)] = (uint16_t)p[y];
-                        to[Plane::at(j + r + 1, pi >> 3) + (pi & 7)] = (uint16_t)(p[y] >> 16);
+                        uint16_t* const to = reinterpret_cast<uint16_t*>(Mt) + y * MT;
+                        to[Square::at(j + r, pi >> 3) + (pi & 7)] = (uint16_t)p[y];
+                        to[Square::at(j + r + 1, pi >> 3) + (pi & 7)] = (uint16_t)(p[y] >> 16);
                     }
                 }
             }
@@ -376,13 +375,13 @@ __global__ __launch_bounds__(256, kExact<T> == 1 ? 2 : 1) void k_delta_grads(Del
                 const auto kb = kt.token_frag(l, s, wave), qb = qt.token_frag(l, s, wave);
 #pragma unroll
                 for (int m = 0; m < 4; ++m) {
-                    const int o = Plane::at(m * 16 + l16, u);
-                    if (m >= 2 * s) mma<3>(pass ? dr[m] : dq[m], tile_planes<3>(M, PT, o), kb);
-                    if (m < 2 + 2 * s) mma<NK>(tk[m], tile_planes<NK>(Mt, PT, o), pass ? kb : qb);
+                    const int o = Square::at(m * 16 + l16, u);
+                    if (m >= 2 * s) mma<3>(pass ? dr[m] : dq[m], tile_planes<3>(M, MT, o), kb);
+                    if (m < 2 + 2 * s) mma<NK>(tk[m], tile_planes<NK>(Mt, MT, o), pass ? kb : qb);
                     __builtin_amdgcn_sched_barrier(0);
                 }
             }
-            __syncthreads();
+            if (pass == 0) __syncthreads();
         }
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
