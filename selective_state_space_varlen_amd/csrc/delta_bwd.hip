@@ -47,7 +47,7 @@ __global__ __launch_bounds__(NW * 64) void k_delta_chain_bwd(DeltaArgs a) {
     const Column cs = column_of<float>(1, a.Dv, col), cv = column_of<T>(a.Hv, a.Dv, col);
     const size_t state = ((size_t)seq * a.Hv + hv) * a.Dk * a.Dv;
     f32x4 S[MT];
-    load_matrix(a.dhT ? a.dhT + state : nullptr, a.Dk, a.Dv, cs, S);
+    load_state(a.dhT ? a.dhT + state : nullptr, a.Dk, a.Dv, cs, S);
     Loads next;
     uint32_t onext[16];
     {
@@ -68,7 +68,7 @@ __global__ __launch_bounds__(NW * 64) void k_delta_chain_bwd(DeltaArgs a) {
         const int nn = ch > 0 ? kC : 0;
         next.load(a, slot - 1, start - kC, nn, hk, hv);
         load_column<T>(a.dout, start - kC, nn, a.Hv, hv, a.Dv, cv, onext);
-        store_matrix(a.dS1 + sh * a.Dk * a.Dv, a.Dk, a.Dv, cs, S);
+        store_kept(a.dS1 + sh * DKP * kept_cols(a.Dv), a.Dv, col, S);
         f32x4 x[4] = {}, y[4] = {};  // K dS', scale P^T dOut
         Frag<3> sb = split_tiles<3>(S[0], S[1]);
 #pragma unroll
@@ -125,7 +125,7 @@ __global__ __launch_bounds__(NW * 64) void k_delta_chain_bwd(DeltaArgs a) {
             step_order<10, 12, 3>();
         }
         __builtin_amdgcn_sched_barrier(0);
-        store_matrix(a.dU + sh * kC * a.Dv, kC, a.Dv, cs, u);
+        store_kept(a.dU + sh * kC * kept_cols(a.Dv), a.Dv, col, u);
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
             const f32x4 be = *reinterpret_cast<const f32x4*>(lds.beta + m * 16 + l4 * 4);
@@ -150,44 +150,52 @@ __global__ __launch_bounds__(NW * 64) void k_delta_chain_bwd(DeltaArgs a) {
             rb = rn;
         }
     }
-    if (a.dh0) store_matrix(a.dh0 + state, a.Dk, a.Dv, cs, S);
+    if (a.dh0) store_state(a.dh0 + state, a.Dk, a.Dv, cs, S);
 }
 
 // One workgroup per (slot, key head, 64 columns of dq and dk), over the value
 // heads of the group, whose dq and dk it adds in registers. Wave w holds
 // columns 16 w .. for all 64 tokens, so its rows of S and dS' come straight
-// from memory, and row tile w of a^T and b^T. It goes over dOut, dE, U, S and
-// dS' 32 columns at a time, the next ones (of the next head too) under way in
-// registers meanwhile: without that the kernel waits for memory two thirds of
-// its time. Two workgroups share a CU.
+// from memory, and its share of the ten tiles of a^T and b^T. It goes over
+// dOut, dE, U, S and dS' 32 columns at a time, the next ones (of the next head
+// too) under way in registers meanwhile. Two workgroups share a CU and fill
+// each other's waits at barriers: one of eight waves with all columns of a
+// head, which stages each chunk once instead of twice, takes 1660 us where
+// these take 1410 (32768 tokens, 32 heads of 128 x 128).
 // The rows of q.dq + k.dkread over these columns go to a.rows, with what the
 // columns give of <dS', S'> on the last, for k_delta_dg to add up.
 constexpr int kDh = 64;
-constexpr int kDv = 32;
 
-// what a thread has under way of 32 columns of one head
-template <typename T>
+// what a thread has under way of KC columns of one head
+template <typename T, int KC>
 struct GradLoads {
-    Unit<T> o;             // token tid / 4, 8 columns: dOut,
-    Unit<float> E, dU;     // E and dU
-    Unit<float> s0, s1;    // row of S and dS' of this lane, 8 columns
-    uint32_t beta, dec;    // of its token; and place tid of the chunk's decays
+    Unit<T> o;                         // token tid / (KC / 8), 8 columns: dOut,
+    Unit<float> E, dU;                 // E and dU
+    Unit<float> s0[KC / 32], s1[KC / 32];  // row of S and dS' of this lane, 8 columns of each 32
+    uint32_t beta, dec;                // of its token; and place tid of the chunk's decays
 
     // (the same loads whether there is such a head or not: n = 0 makes zeros)
     __device__ __forceinline__ void load(const DeltaArgs& a, int64_t slot, const Chunk& c, int hv, int v0, int d0, int n) {
-        const int tid = fresh(threadIdx.x), l = tid & 63, t = tid >> 2;
+        const int tid = fresh(threadIdx.x), l = tid & 63, t = tid / (KC / 8);
         const size_t sh = (size_t)slot * a.Hv + (n > 0 ? hv : 0);
         const size_t at = (size_t)c.start * a.Hv + (n > 0 ? hv : 0);
-        const int e = v0 + (tid & 3) * 8, es = v0 + (l >> 4) * 8;
-        const auto rows = [&](const float* p, int r) { return rows_rsrc(p, n > 0 ? r : 0, a.Dv, a.Dv); };
+        const int e = v0 + (tid % (KC / 8)) * 8;
+        const int dkp = delta_dkp(a.Dk), kept = kept_cols(a.Dv);
         o.load(rows_rsrc(static_cast<const T*>(a.dout) + at * a.Dv, n, a.Hv * a.Dv, a.Dv),
                e < a.Dv ? (uint32_t)(t * a.Hv * a.Dv + e) * (uint32_t)sizeof(T) : kNowhere);
-        const uint32_t oe = e < a.Dv ? (uint32_t)(t * a.Dv + e) * 4u : kNowhere;
-        E.load(rows(a.E + sh * kC * a.Dv, kC), oe);
-        dU.load(rows(a.dU + sh * kC * a.Dv, kC), oe);
-        const uint32_t os = es < a.Dv ? (uint32_t)((d0 + (l & 15)) * a.Dv + es) * 4u : kNowhere;
-        s0.load(rows(a.S0 + sh * a.Dk * a.Dv, a.Dk), os);
-        s1.load(rows(a.dS1 + sh * a.Dk * a.Dv, a.Dk), os);
+        const auto rows = [&](const float* p, int r) {
+            return bytes_rsrc(p + sh * r * kept, n > 0 ? (uint32_t)(r * kept) * 4u : 0u);
+        };
+        const uint32_t oe = e < a.Dv ? (uint32_t)kept_at(kC, t, e) * 4u : kNowhere;
+        E.load(rows(a.E, kC), oe);
+        dU.load(rows(a.dU, kC), oe);
+#pragma unroll
+        for (int s = 0; s < KC / 32; ++s) {
+            const int es = v0 + s * 32 + (l >> 4) * 8;
+            const uint32_t os = es < a.Dv ? (uint32_t)kept_at(dkp, d0 + (l & 15), es) * 4u : kNowhere;
+            s0[s].load(rows(a.S0, dkp), os);
+            s1[s].load(rows(a.dS1, dkp), os);
+        }
         beta = Elt<float>::raw_rsrc(rows_rsrc(a.beta + at, n, a.Hv, 1), (uint32_t)(t * a.Hv) * 4u);
         dec = Elt<float>::raw_rsrc(bytes_rsrc(a.dec + sh * kDec, n > 0 ? kDec * 4 : 0), (uint32_t)tid * 4u);
     }
@@ -195,19 +203,22 @@ struct GradLoads {
 
 template <typename T>
 __global__ __launch_bounds__(256, kExact<T> == 1 ? 2 : 1) void k_delta_grads(DeltaArgs a) {
+    constexpr int NW = 4;
     constexpr int NX = kExact<T>;
     constexpr int NK = kOutP<T>;  // planes of what enters dk alone: its rounding hides the third
-    using Plane = Tile<uint16_t, kDv>;
+    constexpr int KC = NW * 8;    // columns at a time
+    constexpr int TT = (10 + NW - 1) / NW;  // tiles of a^T a wave has: w, w + NW, ...
+    using Plane = Tile<uint16_t, KC>;
     using Square = Tile<uint16_t, kC>;
-    constexpr int PT = kC * kDv, MT = kC * kC;
+    constexpr int PT = kC * KC, MT = kC * kC;
     constexpr int kPlanes = (NX + 6) * PT, kSquares = (3 + NK) * MT;
     // planes of dOut, dE and U ([token][column]); after a head's columns, of a
     // or -b ([i][j]) and its transpose
     __shared__ alignas(16) __bf16 lds[kPlanes > kSquares ? kPlanes : kSquares];
-    __shared__ alignas(16) RowTile<T, kDh> kt, qt;
+    __shared__ alignas(16) RowTile<T, NW * 16> kt, qt;
     __shared__ alignas(16) double G[kC];
     __shared__ alignas(16) float decay[2][kC];
-    __shared__ float red[4][kC], ends[16];
+    __shared__ float red[NW][kC], ends[NW * 4];
     const int halves = (a.Dk + kDh - 1) / kDh;
     const Spread sp = spread(blockIdx.x, halves);
     if (sp.group >= delta_slots(a.T, a.nseq) * a.Hk) return;
@@ -222,7 +233,12 @@ __global__ __launch_bounds__(256, kExact<T> == 1 ? 2 : 1) void k_delta_grads(Del
     __bf16* const M = lds;
     __bf16* const Mt = lds + 3 * MT;
     const int d0 = half * kDh + wave * 16;  // this wave's first column of dq and dk
-    GradLoads<T> next;
+    // tile x of this wave: rows j of tile tj, columns i of tile ti >= tj, in the
+    // order (0,0) (0,1) (0,2) (0,3) (1,1) ... (3,3); four bits each. The two
+    // waves that have two make the last one again rather than branch.
+    const auto tj = [&](int x) { return (int)((0x333221110000ull >> (4 * (wave + x * NW))) & 15); };
+    const auto ti = [&](int x) { return (int)((0x333323213210ull >> (4 * (wave + x * NW))) & 15); };
+    GradLoads<T, KC> next;
     next.load(a, slot, c, hk * group, 0, d0, c.n);
     {
         const int stride = a.Hk * a.Dk, dh = half * kDh;
@@ -232,7 +248,7 @@ __global__ __launch_bounds__(256, kExact<T> == 1 ? 2 : 1) void k_delta_grads(Del
         Unit<T> ku[2], qu[2];
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-            const int u = threadIdx.x + x * 256, i = u >> 3, k8 = u & 7;
+            const int u = threadIdx.x + x * NW * 64, i = u / (NW * 2), k8 = u % (NW * 2);
             const uint32_t o =
                 dh + k8 * 8 < a.Dk ? (uint32_t)(i * stride + dh + k8 * 8) * (uint32_t)sizeof(T) : kNowhere;
             ku[x].load(kr, o);
@@ -240,24 +256,23 @@ __global__ __launch_bounds__(256, kExact<T> == 1 ? 2 : 1) void k_delta_grads(Del
         }
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-            const int u = threadIdx.x + x * 256;
-            kt.put(u >> 3, u & 7, ku[x]);
-            qt.put(u >> 3, u & 7, qu[x]);
+            const int u = threadIdx.x + x * NW * 64;
+            kt.put(u / (NW * 2), u % (NW * 2), ku[x]);
+            qt.put(u / (NW * 2), u % (NW * 2), qu[x]);
         }
     }
     f32x4 tq[4] = {}, tk[4] = {};
     for (int hv = hk * group; hv < (hk + 1) * group; ++hv) {
-        const size_t sh = (size_t)slot * a.Hv + hv;
         f32x4 dq[4] = {}, dr[4] = {}, dw[4] = {};  // dq, dk read, dk write
-        f32x4 at[4] = {}, bt[4] = {};              // row tile `wave` of a^T and b^T
+        f32x4 at[TT] = {}, bt[TT] = {};
         float sd = 0.0f, db = 0.0f;                // <dS', S>; this thread's part of dbeta
-        for (int v0 = 0; v0 < a.Dv; v0 += kDv) {
+        for (int v0 = 0; v0 < a.Dv; v0 += KC) {
             __syncthreads();  // what lies in lds, and the last head's decays, have been read
             const int tid = fresh(threadIdx.x), l = tid & 63, l16 = l & 15, l4 = l >> 4;
             {
                 if (wave < 2) reinterpret_cast<uint32_t*>(G)[tid] = next.dec;
                 else reinterpret_cast<uint32_t*>(&decay[0][0])[tid - 2 * kC] = next.dec;
-                const int t = tid >> 2, e = v0 + (tid & 3) * 8;
+                const int t = tid / (KC / 8), u = tid % (KC / 8), e = v0 + u * 8;
                 const float beta = Elt<float>::cvt(next.beta);
                 float E[8], dU[8];
 #pragma unroll
@@ -275,7 +290,7 @@ __global__ __launch_bounds__(256, kExact<T> == 1 ? 2 : 1) void k_delta_grads(Del
                          e < a.Dv ? (uint32_t)(t * a.Hv * a.Dv + e) * (uint32_t)sizeof(T) : kNowhere);
                 const auto po = unit_planes(next.o);
                 const auto pe = split8<3>(dU), pu = split8<3>(E);
-                const int o = Plane::at(t, tid & 3);
+                const int o = Plane::at(t, u);
 #pragma unroll
                 for (int p = 0; p < NX; ++p) *reinterpret_cast<bf16x8*>(Op + p * PT + o) = po.p[p];
 #pragma unroll
@@ -284,42 +299,67 @@ __global__ __launch_bounds__(256, kExact<T> == 1 ? 2 : 1) void k_delta_grads(Del
                     *reinterpret_cast<bf16x8*>(Up + p * PT + o) = pu.p[p];
                 }
             }
+            Frag<3> sb[KC / 32];
+            Frag<NK> gb[KC / 32];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) sd = fmaf(next.s0.w[e >> 2][e & 3], next.s1.w[e >> 2][e & 3], sd);
-            const auto sb = unit_planes(next.s0);
-            const auto gb = split_tiles<NK>(next.s1.w[0], next.s1.w[1]);
+            for (int s = 0; s < KC / 32; ++s) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) sd = fmaf(next.s0[s].w[e >> 2][e & 3], next.s1[s].w[e >> 2][e & 3], sd);
+                sb[s] = unit_planes(next.s0[s]);
+                gb[s] = split_tiles<NK>(next.s1[s].w[0], next.s1[s].w[1]);
+            }
             {
-                const bool more = v0 + kDv < a.Dv;
-                next.load(a, slot, c, more ? hv : hv + 1, more ? v0 + kDv : 0, d0,
+                const bool more = v0 + KC < a.Dv;
+                next.load(a, slot, c, more ? hv : hv + 1, more ? v0 + KC : 0, d0,
                           more || hv + 1 < (hk + 1) * group ? c.n : 0);
             }
             __syncthreads();
-            const auto uw = tile_planes<3>(Up, PT, Plane::at(wave * 16 + l16, l4));
 #pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                const int o = Plane::at(m * 16 + l16, l4);
-                const auto po = tile_planes<NX>(Op, PT, o);
-                const auto pe = tile_planes<3>(Ep, PT, o);
-                const auto pu = tile_planes<NK>(Up, PT, o);
-                static_for<6>([&](auto t) {
-                    mma_term<3, t>(dr[m], pe, sb);
-                    mma_term<3, t>(dq[m], po, sb);
-                    mma_term<NK, t>(dw[m], pu, gb);
-                });
-                if (m >= wave)  // below the diagonal of a and b
+            for (int s = 0; s < KC / 32; ++s) {
+                const int u = s * 4 + l4;
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    const int o = Plane::at(m * 16 + l16, u);
+                    const auto po = tile_planes<NX>(Op, PT, o);
+                    const auto pe = tile_planes<3>(Ep, PT, o);
+                    const auto pu = tile_planes<NK>(Up, PT, o);
                     static_for<6>([&](auto t) {
-                        mma_term<3, t>(bt[m], uw, pe);
-                        mma_term<3, t>(at[m], uw, po);
+                        mma_term<3, t>(dr[m], pe, sb[s]);
+                        mma_term<3, t>(dq[m], po, sb[s]);
+                        mma_term<NK, t>(dw[m], pu, gb[s]);
                     });
-                __builtin_amdgcn_sched_barrier(0);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+#pragma unroll
+                for (int x = 0; x < TT; ++x) {
+                    const auto uj = tile_planes<3>(Up, PT, Plane::at(tj(x) * 16 + l16, u));
+                    const int o = Plane::at(ti(x) * 16 + l16, u);
+                    const auto po = tile_planes<NX>(Op, PT, o);
+                    const auto pe = tile_planes<3>(Ep, PT, o);
+                    static_for<6>([&](auto t) {
+                        mma_term<3, t>(bt[x], uj, pe);
+                        mma_term<3, t>(at[x], uj, po);
+                    });
+                    __builtin_amdgcn_sched_barrier(0);
+                }
             }
         }
         __syncthreads();
         const int tid = fresh(threadIdx.x), l = tid & 63, l16 = l & 15, l4 = l >> 4;
         {
+            const int t = tid / (KC / 8);
             const float s = dpp_add<0x4E>(dpp_add<0xB1>(db));
+            const bool first = tid % (KC / 8) == 0;
             Elt<float>::st_rsrc(rows_rsrc(a.dbeta + (size_t)c.start * a.Hv + hv, half == 0 ? c.n : 0, a.Hv, 1),
-                                (tid & 3) == 0 ? (uint32_t)((tid >> 2) * a.Hv) * 4u : kNowhere, s);
+                                first ? (uint32_t)(t * a.Hv) * 4u : kNowhere, s);
+        }
+        // the empty tiles (0, 1), (2, 3) of a and (1, 0), (3, 2) of its transpose
+        for (int x = tid; x < 4 * 16 * 4; x += NW * 64) {
+            const int w = x >> 6, r = (x >> 2) & 15, k4 = (x & 3) * 4;
+            const int row = (w & 1) * 32 + (w >> 1) * 16 + r, k = kplace((w & 1) * 32 + (1 - (w >> 1)) * 16 + k4);
+            const float zero[4] = {};
+            if (w < 2) lds_put4<3>(M, MT, Square::at(row, k >> 3) + (k & 7), zero);
+            else lds_put4<NK>(Mt, MT, Square::at(row, k >> 3) + (k & 7), zero);
         }
         float end = decay[0][kC - 1] * sd;
 #pragma unroll
@@ -338,20 +378,24 @@ __global__ __launch_bounds__(256, kExact<T> == 1 ? 2 : 1) void k_delta_grads(Del
             }
             tk[m] += el * dw[m];
         }
+        float dx[TT][4];  // the decays of this wave's tiles
+#pragma unroll
+        for (int x = 0; x < TT; ++x) {
+            const double gi = G[ti(x) * 16 + l16];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) dx[x][r] = decay_of(gi - G[tj(x) * 16 + l4 * 4 + r]);
+        }
 #pragma unroll
         for (int pass = 0; pass < 2; ++pass) {  // a, then -b
 #pragma unroll
-            for (int n = 0; n < 4; ++n) {
-                __builtin_amdgcn_sched_barrier(0);
-                const int i = n * 16 + (int)fresh(l16), j = wave * 16 + (int)fresh(l4) * 4;
-                float v[4] = {};
-                if (n >= wave) {
+            for (int x = 0; x < TT; ++x) {
+                const int i = ti(x) * 16 + (int)fresh(l16), j = tj(x) * 16 + (int)fresh(l4) * 4;
+                float v[4];
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const bool on = pass ? i > j + r : i >= j + r;
-                        const float w = on ? decay_of(G[i] - G[j + r]) : 0.0f;
-                        v[r] = on ? (pass ? -w * bt[n][r] : w * a.scale * at[n][r]) : 0.0f;
-                    }
+                for (int r = 0; r < 4; ++r) {
+                    // (where it is not wanted the decay may be infinite: chosen, not multiplied, away)
+                    const float w = dx[x][r] * (pass ? -bt[x][r] : a.scale * at[x][r]);
+                    v[r] = (pass ? i > j + r : i >= j + r) ? w : 0.0f;
                 }
                 const int pj = kplace(j), pi = kplace(i);
                 lds_put4<3>(M, MT, Square::at(i, pj >> 3) + (pj & 7), v);
@@ -407,7 +451,7 @@ __global__ __launch_bounds__(256, kExact<T> == 1 ? 2 : 1) void k_delta_grads(Del
             float s = (red[0][l] + red[1][l]) + (red[2][l] + red[3][l]);
             const float e = sum16(ends[l16]);
             if (l == kC - 1) s += e;
-            *at_bytes(a.rows + (sh * halves + half) * kC, (uint32_t)l * 4u) = s;
+            *at_bytes(a.rows + ((size_t)(slot * a.Hv + hv) * halves + half) * kC, (uint32_t)l * 4u) = s;
         }
     }
     const Column cd = column_of<T>(a.Hk, a.Dk, d0 + (lane_id() & 15));
@@ -474,8 +518,8 @@ inline DeltaBwdLayout delta_bwd_layout(int64_t T, int32_t nseq, int32_t Hv, int3
     L.att = L.inv + round256(n * Hv * kTri * 4);
     L.order = L.att + round256(n * Hv * kTri * 4);
     L.dS1 = L.order + round256((size_t)nseq * 4);
-    L.dU = L.dS1 + round256(n * Hv * Dk * Dv * 4);
-    L.rows = L.dU + round256(n * Hv * kC * Dv * 4);
+    L.dU = L.dS1 + kept_bytes(T, nseq, Hv, delta_dkp(Dk), Dv);
+    L.rows = L.dU + kept_bytes(T, nseq, Hv, kC, Dv);
     L.total = L.rows + round256(n * Hv * ((Dk + kDh - 1) / kDh) * kC * 4);
     return L;
 }
@@ -531,7 +575,7 @@ extern "C" int gated_delta_pack_bwd(const void* q, const void* k, const float* g
     if (T > 0) {
         char* const kept = static_cast<char*>(const_cast<void*>(saved));
         a.S0 = reinterpret_cast<float*>(kept);
-        a.E = reinterpret_cast<float*>(kept + round256((size_t)delta_slots(T, nseq) * Hv * Dk * Dv * 4));
+        a.E = reinterpret_cast<float*>(kept + kept_bytes(T, nseq, Hv, delta_dkp(Dk), Dv));
         a.dec = reinterpret_cast<float*>(ws + L.dec);
         a.inv = reinterpret_cast<float*>(ws + L.inv);
         a.att = reinterpret_cast<float*>(ws + L.att);

@@ -579,10 +579,20 @@ __device__ __forceinline__ void chunk_inverse(const float* A, float* X) {
 constexpr int kMaxDk = 128;
 constexpr int kWaveCols = 16;  // state columns a wave of the chains takes
 
-inline int delta_dkp(int Dk) { return Dk <= 64 ? 64 : 128; }
+__host__ __device__ inline int delta_dkp(int Dk) { return Dk <= 64 ? 64 : 128; }
 inline size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
 constexpr int kDec = 4 * kC;
+
+// What goes from the chains to the gradients, S, E, dS' and dU of each chunk:
+// fp32 in blocks of 32 columns, [block][row][32], as k_delta_grads reads them:
+// in rows of all columns it would read 128 bytes of each 512 at a time, and
+// memory gave 3.0 TB/s of its 5.2.
+constexpr int kKeptCols = 32;
+__host__ __device__ inline int kept_cols(int Dv) { return (Dv + kKeptCols - 1) / kKeptCols * kKeptCols; }
+__device__ __forceinline__ int kept_at(int rows, int row, int col) {
+    return ((col / kKeptCols) * rows + row) * kKeptCols + col % kKeptCols;
+}
 struct DeltaArgs {
     const void *q, *k, *v, *dout;
     const float *g, *beta;
@@ -595,15 +605,19 @@ struct DeltaArgs {
     int32_t nseq, Hk, Hv, Dk, Dv;
     float scale;
     // kept from the forward to the backward, by slot and value head
-    float *S0, *E;   // the state that enters the chunk (Dk, Dv); the errors (64, Dv)
+    float *S0, *E;   // the state that enters the chunk (rows: Dk padded), the errors (64 rows)
     // scratch, by slot and head
     float* dec;      // G (64 doubles), e^{G_i}, e^{G_last - G_i}: kDec
     float* inv;      // the chunk's inverse: kTri
     float* att;      // the decayed products of q and k: kTri
     float *dS1, *dU; // backward: gradients of the state that leaves the chunk, and of U
-    int32_t* order;  // the sequences by length (null: as they come)
     float* rows;     // backward: per 64 columns of dq and dk, what k_delta_dg adds up: 64
+    int32_t* order;  // the sequences by length (null: as they come)
 };
+
+inline size_t kept_bytes(int64_t T, int32_t nseq, int32_t Hv, int rows, int32_t Dv) {
+    return round256((size_t)delta_slots(T, nseq) * Hv * rows * kept_cols(Dv) * sizeof(float));
+}
 
 inline int delta_check(int64_t T, int32_t nseq, int32_t Hk, int32_t Hv, int32_t Dk, int32_t Dv, int32_t dtype) {
     if (T < 0 || T >= (int64_t(1) << 31) || nseq < 1 || Hk < 1 || Hv < 1 || Dk < 1 || Dv < 1) return SSMP_ERR_SHAPE;

@@ -41,7 +41,7 @@ __global__ __launch_bounds__(NW * 64) void k_delta_chain(DeltaArgs a) {
     const Column cs = column_of<float>(1, a.Dv, col), cv = column_of<T>(a.Hv, a.Dv, col);
     const size_t state = ((size_t)seq * a.Hv + hv) * a.Dk * a.Dv;
     f32x4 S[MT];
-    load_matrix(a.h0 ? a.h0 + state : nullptr, a.Dk, a.Dv, cs, S);
+    load_state(a.h0 ? a.h0 + state : nullptr, a.Dk, a.Dv, cs, S);
     Loads next;
     uint32_t v[16];
     {
@@ -58,7 +58,7 @@ __global__ __launch_bounds__(NW * 64) void k_delta_chain(DeltaArgs a) {
         __syncthreads();
         const int left = q.len - (ch + 1) * kC, nn = left < kC ? left : kC;
         next.load(a, slot + 1, start + kC, nn, hk, hv);
-        if constexpr (SAVE) store_matrix(a.S0 + sh * a.Dk * a.Dv, a.Dk, a.Dv, cs, S);
+        if constexpr (SAVE) store_kept(a.S0 + sh * DKP * kept_cols(a.Dv), a.Dv, col, S);
         f32x4 x[4] = {}, o[4] = {};  // K S and Q S
         Frag<3> sb = split_tiles<3>(S[0], S[1]);
 #pragma unroll
@@ -110,7 +110,7 @@ __global__ __launch_bounds__(NW * 64) void k_delta_chain(DeltaArgs a) {
             step_order<6, 12, 3>();
         }
         __builtin_amdgcn_sched_barrier(0);
-        if constexpr (SAVE) store_matrix(a.E + sh * kC * a.Dv, kC, a.Dv, cs, E);
+        if constexpr (SAVE) store_kept(a.E + sh * kC * kept_cols(a.Dv), a.Dv, col, E);
         f32x4 w[4];
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
@@ -150,7 +150,7 @@ __global__ __launch_bounds__(NW * 64) void k_delta_chain(DeltaArgs a) {
         }
         store_column<T>(a.out, start, cn, a.Hv, hv, a.Dv, cv, o, a.scale);
     }
-    if (a.hT) store_matrix(a.hT + state, a.Dk, a.Dv, cs, S);
+    if (a.hT) store_state(a.hT + state, a.Dk, a.Dv, cs, S);
 }
 
 template <typename T, int DKP>
@@ -190,8 +190,7 @@ extern "C" size_t gated_delta_pack_saved_bytes(int64_t T, int32_t nseq, int32_t 
                                                int32_t Dv) {
     using namespace ssmp;
     if (delta_check(T, nseq, Hk, Hv, Dk, Dv, SSMP_F32) || T == 0) return 0;
-    const size_t n = (size_t)delta_slots(T, nseq) * Hv;
-    return round256(n * Dk * Dv * 4) + round256(n * kC * Dv * 4);
+    return kept_bytes(T, nseq, Hv, delta_dkp(Dk), Dv) + kept_bytes(T, nseq, Hv, kC, Dv);
 }
 
 extern "C" size_t gated_delta_pack_fwd_scratch_bytes(int64_t T, int32_t nseq, int32_t Hk, int32_t Hv, int32_t Dk,
@@ -243,7 +242,7 @@ extern "C" int gated_delta_pack_fwd(const void* q, const void* k, const void* v,
         if (saved) {
             a.S0 = static_cast<float*>(saved);
             a.E = reinterpret_cast<float*>(static_cast<char*>(saved) +
-                                           round256((size_t)delta_slots(T, nseq) * Hv * Dk * Dv * 4));
+                                           kept_bytes(T, nseq, Hv, delta_dkp(Dk), Dv));
         }
     }
     hipStream_t s = static_cast<hipStream_t>(stream);

@@ -293,9 +293,9 @@ __device__ __forceinline__ void store_column(void* p, int64_t start, int n, int 
     for (int i = 0; i < 16; ++i)
         Elt<T>::st_rsrc(r, o + (uint32_t)((i >> 2) * 16 + (i & 3)) * (uint32_t)c.stride, scale * v[i >> 2][i & 3]);
 }
-// the same of a dense fp32 matrix of `rows` rows (a state; E or dU of a chunk)
+// the same of a caller's state (rows, Dv)
 template <int MT>
-__device__ __forceinline__ void store_matrix(float* p, int rows, int Dv, const Column& c, const f32x4 (&v)[MT]) {
+__device__ __forceinline__ void store_state(float* p, int rows, int Dv, const Column& c, const f32x4 (&v)[MT]) {
     const auto r = rows_rsrc(p, rows, Dv, Dv);
     const uint32_t o = fresh(c.o);
 #pragma unroll
@@ -303,12 +303,21 @@ __device__ __forceinline__ void store_matrix(float* p, int rows, int Dv, const C
         Elt<float>::st_rsrc(r, o + (uint32_t)((i >> 2) * 16 + (i & 3)) * (uint32_t)c.stride, v[i >> 2][i & 3]);
 }
 template <int MT>
-__device__ __forceinline__ void load_matrix(const float* p, int rows, int Dv, const Column& c, f32x4 (&v)[MT]) {
+__device__ __forceinline__ void load_state(const float* p, int rows, int Dv, const Column& c, f32x4 (&v)[MT]) {
     const auto r = rows_rsrc(p, p ? rows : 0, Dv, Dv);
 #pragma unroll
     for (int i = 0; i < MT * 4; ++i)
         v[i >> 2][i & 3] = Elt<float>::cvt(
             Elt<float>::raw_rsrc(r, c.o + (uint32_t)((i >> 2) * 16 + (i & 3)) * (uint32_t)c.stride));
+}
+// and of a kept matrix (kept_at)
+template <int MT>
+__device__ __forceinline__ void store_kept(float* p, int Dv, int col, const f32x4 (&v)[MT]) {
+    const auto r = bytes_rsrc(p, (uint32_t)(kept_cols(Dv) * MT * 16) * 4u);
+    const uint32_t o = fresh(col < Dv ? (uint32_t)kept_at(MT * 16, (lane_id() >> 4) * 4, col) * 4u : kNowhere);
+#pragma unroll
+    for (int i = 0; i < MT * 4; ++i)
+        Elt<float>::st_rsrc(r, o + (uint32_t)((i >> 2) * 16 + (i & 3)) * (kKeptCols * 4u), v[i >> 2][i & 3]);
 }
 
 }  // namespace ssmp
