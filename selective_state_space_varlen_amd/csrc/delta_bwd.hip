@@ -417,13 +417,18 @@ __global__ __launch_bounds__(256, kExact<T> == 1 ? 2 : 1) void k_delta_grads(Del
                 const int u = s * 4 + l4;
                 __builtin_amdgcn_sched_barrier(0);
                 const auto kb = kt.token_frag(l, s, wave), qb = qt.token_frag(l, s, wave);
+                // rows 32 s .. of a, rows .. 32 s + 31 of its transpose
+                Frag<3> fm[4];
+                Frag<NK> ft[4];
 #pragma unroll
-                for (int m = 0; m < 4; ++m) {
-                    const int o = Square::at(m * 16 + l16, u);
-                    if (m >= 2 * s) mma<3>(pass ? dr[m] : dq[m], tile_planes<3>(M, MT, o), kb);
-                    if (m < 2 + 2 * s) mma<NK>(tk[m], tile_planes<NK>(Mt, MT, o), pass ? kb : qb);
-                    __builtin_amdgcn_sched_barrier(0);
-                }
+                for (int m = 2 * s; m < 4; ++m) fm[m - 2 * s] = tile_planes<3>(M, MT, Square::at(m * 16 + l16, u));
+                if (s == 0) mma_tiles<3, 0, 4>(pass ? dr : dq, fm, kb);
+                else mma_tiles<3, 2, 4>(pass ? dr : dq, fm, kb);
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int m = 0; m < 2 + 2 * s; ++m) ft[m] = tile_planes<NK>(Mt, MT, Square::at(m * 16 + l16, u));
+                if (s == 0) mma_tiles<NK, 0, 2>(tk, ft, pass ? kb : qb);
+                else mma_tiles<NK, 0, 4>(tk, ft, pass ? kb : qb);
             }
             if (pass == 0) __syncthreads();
         }
