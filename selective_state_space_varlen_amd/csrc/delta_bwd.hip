@@ -31,7 +31,8 @@ __global__ __launch_bounds__(NW * 64) void k_delta_chain_bwd(DeltaArgs a) {
     constexpr int NX = kExact<T>;
     constexpr int MT = DKP / 16;
     using Loads = ChainLoads<T, DKP, 3, NW * 64>;
-    __shared__ alignas(16) typename Loads::Tiles lds;
+    constexpr int SETS = kSets<typename Loads::Tiles, DKP, NW>;
+    __shared__ alignas(16) typename Loads::Tiles sets[SETS];
     constexpr int kCols = NW * kWaveCols;
     const int ncb = (a.Dv + kCols - 1) / kCols, group = a.Hv / a.Hk;
     const Spread sp = spread(blockIdx.x, ncb * group);
@@ -50,24 +51,31 @@ __global__ __launch_bounds__(NW * 64) void k_delta_chain_bwd(DeltaArgs a) {
     load_state(a.dhT ? a.dhT + state : nullptr, a.Dk, a.Dv, cs, S);
     Loads next;
     uint32_t onext[16];
-    {
-        const int64_t start = q.start + (int64_t)(chunks - 1) * kC;
-        const int n = chunks > 0 ? q.len - (chunks - 1) * kC : 0;  // an empty sequence has no last chunk
-        next.load(a, q.slot0 + chunks - 1, start, n, hk, hv);
-        load_column<T>(a.dout, start, n, a.Hv, hv, a.Dv, cv, onext);
-    }
+    // an empty sequence has no last chunk
+    const int last = chunks > 0 ? chunks - 1 : 0;
+    const auto tokens = [&](int ch) { return ch < 0 ? 0 : min(q.len - ch * kC, kC); };
+    ChainAt<T> at(a, q.slot0 + last, q.start + (int64_t)last * kC, hk, hv);
+    const T* dp = static_cast<const T*>(a.dout) + (((size_t)q.start + (size_t)last * kC) * a.Hv + hv) * a.Dv;
+    const int64_t dstep = (int64_t)kC * a.Hv * a.Dv;
+    next.load_rows(a, at, tokens(last));
+    next.load_rest(a, at, tokens(last));
+    load_column<T>(dp, tokens(last), a.Hv, a.Dv, cv, onext);
+    next.put_rows(sets[0]);
+    next.put_rest(sets[0]);
+    at.step(a, -1);
+    next.load_rows(a, at, tokens(last - 1));
+    next.load_rest(a, at, tokens(last - 1));
+    __syncthreads();
     for (int ch = chunks - 1; ch >= 0; --ch) {
-        const int64_t slot = q.slot0 + ch, start = q.start + (int64_t)ch * kC;
-        const size_t sh = (size_t)slot * a.Hv + hv;
-        __syncthreads();  // the last chunk's operands have been read
-        next.put(lds);
+        const size_t sh = (size_t)(q.slot0 + ch) * a.Hv + hv;
+        const int set = SETS == 2 ? (last - ch) & 1 : 0;
+        const typename Loads::Tiles& lds = sets[set];
+        typename Loads::Tiles& other = sets[SETS == 2 ? set ^ 1 : 0];
         f32x4 o[4];
 #pragma unroll
         for (int i = 0; i < 16; ++i) o[i >> 2][i & 3] = Elt<T>::cvt(onext[i]);
-        __syncthreads();
-        const int nn = ch > 0 ? kC : 0;
-        next.load(a, slot - 1, start - kC, nn, hk, hv);
-        load_column<T>(a.dout, start - kC, nn, a.Hv, hv, a.Dv, cv, onext);
+        dp -= dstep;
+        load_column<T>(dp, tokens(ch - 1), a.Hv, a.Dv, cv, onext);
         store_kept(a.dS1 + sh * DKP * kept_cols(a.Dv), a.Dv, col, S);
         f32x4 x[4] = {}, y[4] = {};  // K dS', scale P^T dOut
         Frag<3> sb = split_tiles<3>(S[0], S[1]);
@@ -145,10 +153,23 @@ __global__ __launch_bounds__(NW * 64) void k_delta_chain_bwd(DeltaArgs a) {
             if (t == 0) rn = split_tiles<3>(u[0], u[1]);
             if (t == 1) rn = split_tiles<3>(o[2], o[3]);
             if (t == 2) rn = split_tiles<3>(u[2], u[3]);
+            if constexpr (SETS == 2) {  // the next chunk's operands
+                if (t == 1) next.put_rows(other);
+                if (t == 2) next.put_rest(other);
+            }
             mma_tiles<3, 0, MT>(S, ra, rb);
             if constexpr (NX == 1) step_order<2 * MT, 3 * MT, 2>();
             rb = rn;
         }
+        if constexpr (SETS == 1) {
+            __syncthreads();  // this chunk's operands have been read
+            next.put_rows(other);
+            next.put_rest(other);
+        }
+        at.step(a, -1);
+        next.load_rows(a, at, tokens(ch - 2));
+        next.load_rest(a, at, tokens(ch - 2));
+        __syncthreads();
     }
     if (a.dh0) store_state(a.dh0 + state, a.Dk, a.Dv, cs, S);
 }
@@ -460,8 +481,9 @@ __global__ __launch_bounds__(256, kExact<T> == 1 ? 2 : 1) void k_delta_grads(Del
         }
     }
     const Column cd = column_of<T>(a.Hk, a.Dk, d0 + (lane_id() & 15));
-    store_column<T>(a.dq, c.start, c.n, a.Hk, hk, a.Dk, cd, tq, 1.0f);
-    store_column<T>(a.dk, c.start, c.n, a.Hk, hk, a.Dk, cd, tk, 1.0f);
+    const size_t first = ((size_t)c.start * a.Hk + hk) * a.Dk;
+    store_column<T>(static_cast<T*>(a.dq) + first, c.n, a.Hk, a.Dk, cd, tq, 1.0f);
+    store_column<T>(static_cast<T*>(a.dk) + first, c.n, a.Hk, a.Dk, cd, tk, 1.0f);
 }
 
 // dg of a chunk: the sums of a.rows from each token to the chunk's end, in 64

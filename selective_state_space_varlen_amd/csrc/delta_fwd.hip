@@ -17,15 +17,16 @@ namespace ssmp {
 // One workgroup per (sequence, value head, 64 or 128 columns of the state), 16
 // columns a wave. Columns do not meet in the chain, and a wave's results are
 // its next right operands in the registers they are in (kplace), so the waves
-// share nothing but the left operands, which the workgroup holds in LDS while
-// the next chunk's are under way in registers: two barriers a chunk.
+// share nothing but the left operands: of one chunk in LDS, the next one's on
+// their way there, and those of the one after it under way in registers.
 // SAVE: keep S and E for the backward.
 template <typename T, int DKP, int NW, bool SAVE>
 __global__ __launch_bounds__(NW * 64) void k_delta_chain(DeltaArgs a) {
     constexpr int NX = kExact<T>, NO = kOutP<T>;
     constexpr int MT = DKP / 16;  // 16-row tiles of the state
     using Loads = ChainLoads<T, DKP, NO, NW * 64>;
-    __shared__ alignas(16) typename Loads::Tiles lds;
+    constexpr int SETS = kSets<typename Loads::Tiles, DKP, NW>;
+    __shared__ alignas(16) typename Loads::Tiles sets[SETS];
     constexpr int kCols = NW * kWaveCols;
     const int ncb = (a.Dv + kCols - 1) / kCols, group = a.Hv / a.Hk;
     const Spread sp = spread(blockIdx.x, ncb * group);
@@ -44,20 +45,26 @@ __global__ __launch_bounds__(NW * 64) void k_delta_chain(DeltaArgs a) {
     load_state(a.h0 ? a.h0 + state : nullptr, a.Dk, a.Dv, cs, S);
     Loads next;
     uint32_t v[16];
-    {
-        const int n = q.len < kC ? q.len : kC;
-        next.load(a, q.slot0, q.start, n, hk, hv);
-        load_column<T>(a.v, q.start, n, a.Hv, hv, a.Dv, cv, v);
-    }
+    ChainAt<T> at(a, q.slot0, q.start, hk, hv);
+    const size_t vrow = ((size_t)q.start * a.Hv + hv) * a.Dv;
+    const T* vp = static_cast<const T*>(a.v) + vrow;
+    T* op = static_cast<T*>(a.out) + vrow;
+    const int64_t vstep = (int64_t)kC * a.Hv * a.Dv;
+    // tokens of the i-th chunk from here on, none behind the last
+    const auto tokens = [&](int ch) { return min(q.len - ch * kC, kC); };
+    next.load_rows(a, at, tokens(0));
+    next.load_rest(a, at, tokens(0));
+    load_column<T>(vp, tokens(0), a.Hv, a.Dv, cv, v);
+    next.put_rows(sets[0]);
+    next.put_rest(sets[0]);
+    at.step(a, 1);
+    next.load_rows(a, at, tokens(1));
+    next.load_rest(a, at, tokens(1));
+    __syncthreads();
     for (int ch = 0; ch < chunks; ++ch) {
-        const int64_t slot = q.slot0 + ch, start = q.start + (int64_t)ch * kC;
-        const int cn = q.len - ch * kC < kC ? q.len - ch * kC : kC;
-        const size_t sh = (size_t)slot * a.Hv + hv;
-        __syncthreads();  // the last chunk's operands have been read
-        next.put(lds);
-        __syncthreads();
-        const int left = q.len - (ch + 1) * kC, nn = left < kC ? left : kC;
-        next.load(a, slot + 1, start + kC, nn, hk, hv);
+        const size_t sh = (size_t)(q.slot0 + ch) * a.Hv + hv;
+        const typename Loads::Tiles& lds = sets[SETS == 2 ? ch & 1 : 0];
+        typename Loads::Tiles& other = sets[SETS == 2 ? (ch & 1) ^ 1 : 0];
         if constexpr (SAVE) store_kept(a.S0 + sh * DKP * kept_cols(a.Dv), a.Dv, col, S);
         f32x4 x[4] = {}, o[4] = {};  // K S and Q S
         Frag<3> sb = split_tiles<3>(S[0], S[1]);
@@ -87,7 +94,8 @@ __global__ __launch_bounds__(NW * 64) void k_delta_chain(DeltaArgs a) {
                 o[m][r] *= eg[r];
             }
         }
-        load_column<T>(a.v, start + kC, nn, a.Hv, hv, a.Dv, cv, v);
+        vp += vstep;
+        load_column<T>(vp, tokens(ch + 1), a.Hv, a.Dv, cv, v);
         // E = inverse X; in its shadow the state decays
         f32x4 E[4] = {};
         const float ec = lds.eg[kC - 1];
@@ -137,6 +145,10 @@ __global__ __launch_bounds__(NW * 64) void k_delta_chain(DeltaArgs a) {
                 wn = split_tiles<3>(w[2], w[3]);
                 un = split_tiles<NO>(E[2], E[3]);
             }
+            if constexpr (SETS == 2) {  // the next chunk's operands
+                if (s == 0) next.put_rows(other);
+                else next.put_rest(other);
+            }
             mma_tiles<3, 0, MT>(S, ka, wb);
             if constexpr (NX == 1) step_order<2 * MT, 3 * MT, 3>();
             __builtin_amdgcn_sched_barrier(0);
@@ -148,7 +160,17 @@ __global__ __launch_bounds__(NW * 64) void k_delta_chain(DeltaArgs a) {
             wb = wn;
             ub = un;
         }
-        store_column<T>(a.out, start, cn, a.Hv, hv, a.Dv, cv, o, a.scale);
+        if constexpr (SETS == 1) {
+            __syncthreads();  // this chunk's operands have been read
+            next.put_rows(other);
+            next.put_rest(other);
+        }
+        at.step(a, 1);
+        next.load_rows(a, at, tokens(ch + 2));
+        store_column<T>(op, tokens(ch), a.Hv, a.Dv, cv, o, a.scale);
+        op += vstep;
+        next.load_rest(a, at, tokens(ch + 2));
+        __syncthreads();
     }
     if (a.hT) store_state(a.hT + state, a.Dk, a.Dv, cs, S);
 }

@@ -186,6 +186,32 @@ struct ChainTiles {
     float eg[kC], el[kC], beta[kC];
 };
 
+// Where the operands of a chain's chunks lie; they go on by the same step
+// from chunk to chunk, which costs a scalar addition each.
+template <typename T>
+struct ChainAt {
+    const T *k, *q;
+    const float *inv, *att, *dec, *beta;
+
+    __device__ __forceinline__ ChainAt(const DeltaArgs& a, int64_t slot, int64_t start, int hk, int hv) {
+        const size_t sh = (size_t)slot * a.Hv + hv, row = ((size_t)start * a.Hk + hk) * a.Dk;
+        k = static_cast<const T*>(a.k) + row;
+        q = static_cast<const T*>(a.q) + row;
+        inv = a.inv + sh * kTri;
+        att = a.att + sh * kTri;
+        dec = a.dec + sh * kDec + 2 * kC;
+        beta = a.beta + (size_t)start * a.Hv + hv;
+    }
+    __device__ __forceinline__ void step(const DeltaArgs& a, int chunks) {
+        k += (int64_t)chunks * kC * a.Hk * a.Dk;
+        q += (int64_t)chunks * kC * a.Hk * a.Dk;
+        inv += (int64_t)chunks * a.Hv * kTri;
+        att += (int64_t)chunks * a.Hv * kTri;
+        dec += (int64_t)chunks * a.Hv * kDec;
+        beta += (int64_t)chunks * kC * a.Hv;
+    }
+};
+
 template <typename T, int DKP, int NP, int THREADS>
 struct ChainLoads {
     using Tiles = ChainTiles<T, DKP, NP>;
@@ -198,42 +224,42 @@ struct ChainLoads {
     Unit<float4> inv[kM], att[kM];
     uint32_t dec, beta;
 
-    // The chunk of n tokens at `start` (n <= 0: none, all zeros). The loads are
+    // The chunk of n tokens at `p` (n <= 0: none, all zeros). The loads are
     // the same in every wave and on every path, so that a wait for an older
     // load can count the ones behind it and need not wait for these too.
-    __device__ __forceinline__ void load(const DeltaArgs& a, int64_t slot, int64_t start, int n, int hk, int hv) {
-        const int tid = threadIdx.x;
-        const size_t sh = n > 0 ? (size_t)slot * a.Hv + hv : 0, from = n > 0 ? (size_t)start : 0;
+    __device__ __forceinline__ void load_rows(const DeltaArgs& a, const ChainAt<T>& p, int n) {
         const int stride = a.Hk * a.Dk;
-        const auto kr = rows_rsrc(static_cast<const T*>(a.k) + (from * a.Hk + hk) * a.Dk, n, stride, a.Dk);
-        const auto qr = rows_rsrc(static_cast<const T*>(a.q) + (from * a.Hk + hk) * a.Dk, n, stride, a.Dk);
+        const auto kr = rows_rsrc(p.k, n, stride, a.Dk), qr = rows_rsrc(p.q, n, stride, a.Dk);
 #pragma unroll
         for (int x = 0; x < kN; ++x) {
-            const int u = tid + x * THREADS, i = u / (DKP / 8), k8 = u % (DKP / 8);
+            const int u = threadIdx.x + x * THREADS, i = u / (DKP / 8), k8 = u % (DKP / 8);
             const uint32_t o = k8 * 8 < a.Dk ? (uint32_t)(i * stride + k8 * 8) * (uint32_t)sizeof(T) : kNowhere;
             k[x].load(kr, o);
             q[x].load(qr, o);
         }
-        const auto ir = bytes_rsrc(a.inv + sh * kTri, n > 0 ? kTri * 4 : 0);
-        const auto ar = bytes_rsrc(a.att + sh * kTri, n > 0 ? kTri * 4 : 0);
+    }
+    __device__ __forceinline__ void load_rest(const DeltaArgs& a, const ChainAt<T>& p, int n) {
+        const int tid = threadIdx.x;
+        const auto ir = bytes_rsrc(p.inv, n > 0 ? kTri * 4 : 0), ar = bytes_rsrc(p.att, n > 0 ? kTri * 4 : 0);
 #pragma unroll
         for (int x = 0; x < kM; ++x) {
             inv[x].load(ir, (uint32_t)(tid + x * THREADS) * 16u);
             att[x].load(ar, (uint32_t)(tid + x * THREADS) * 16u);
         }
-        const auto dr = bytes_rsrc(a.dec + sh * kDec + 2 * kC, n > 0 ? 2 * kC * 4 : 0);
-        const auto br = rows_rsrc(a.beta + from * a.Hv + hv, n, a.Hv, 1);
-        dec = Elt<float>::raw_rsrc(dr, (uint32_t)tid * 4u);
-        beta = Elt<float>::raw_rsrc(br, tid < 2 * kC ? kNowhere : (uint32_t)((tid - 2 * kC) * a.Hv) * 4u);
+        dec = Elt<float>::raw_rsrc(bytes_rsrc(p.dec, n > 0 ? 2 * kC * 4 : 0), (uint32_t)tid * 4u);
+        beta = Elt<float>::raw_rsrc(rows_rsrc(p.beta, n, a.Hv, 1),
+                                    tid < 2 * kC ? kNowhere : (uint32_t)((tid - 2 * kC) * a.Hv) * 4u);
     }
-    __device__ __forceinline__ void put(Tiles& t) const {
-        const int tid = threadIdx.x;
+    __device__ __forceinline__ void put_rows(Tiles& t) const {
 #pragma unroll
         for (int x = 0; x < kN; ++x) {
-            const int u = tid + x * THREADS, i = u / (DKP / 8), k8 = u % (DKP / 8);
+            const int u = threadIdx.x + x * THREADS, i = u / (DKP / 8), k8 = u % (DKP / 8);
             t.k.put(i, k8, k[x]);
             t.q.put(i, k8, q[x]);
         }
+    }
+    __device__ __forceinline__ void put_rest(Tiles& t) const {
+        const int tid = threadIdx.x;
 #pragma unroll
         for (int x = 0; x < kM; ++x)
             if (tri_on(x)) {
@@ -245,6 +271,15 @@ struct ChainLoads {
         else if (tid < 3 * kC) t.beta[tid - 2 * kC] = Elt<float>::cvt(beta);
     }
 };
+
+// Sets of a chain's operands in LDS: two where they fit and cost no workgroup
+// beside it, so that the next chunk's are put while this one's are read and a
+// chunk has one barrier. Against one set, at heads of 128 in bf16: 710 us
+// against 740 (keeping, 8 waves, 32768 tokens x 32 heads), 733 against 750
+// backward; 411 against 435 backward with 4 waves (16384 tokens x 12 heads).
+// What a start costs more: 43 us against 41 at 513 tokens.
+template <typename Tiles, int DKP, int NW>
+constexpr int kSets = 2 * sizeof(Tiles) <= 160 * 1024 && (DKP > 64 || NW == 8) ? 2 : 1;
 
 // Waves of a chain's workgroup. Eight (128 columns) read a chunk's operands
 // once for a whole head; with fewer heads than CUs, two workgroups of four
@@ -277,17 +312,16 @@ __device__ __forceinline__ Column column_of(int H, int Dv, int col) {
     return {col < Dv ? (uint32_t)(l4 * 4 * stride + col * (int)sizeof(T)) : kNowhere, stride};
 }
 template <typename T>
-__device__ __forceinline__ void load_column(const void* p, int64_t start, int n, int H, int h, int Dv, const Column& c,
-                                            uint32_t (&v)[16]) {
-    const auto r = rows_rsrc(static_cast<const T*>(p) + ((n > 0 ? (size_t)start : 0) * H + h) * Dv, n, H * Dv, Dv);
+__device__ __forceinline__ void load_column(const T* first, int n, int H, int Dv, const Column& c, uint32_t (&v)[16]) {
+    const auto r = rows_rsrc(first, n, H * Dv, Dv);
     const uint32_t o = fresh(c.o);
 #pragma unroll
     for (int i = 0; i < 16; ++i) v[i] = Elt<T>::raw_rsrc(r, o + (uint32_t)((i >> 2) * 16 + (i & 3)) * (uint32_t)c.stride);
 }
 template <typename T>
-__device__ __forceinline__ void store_column(void* p, int64_t start, int n, int H, int h, int Dv, const Column& c,
-                                             const f32x4 (&v)[4], float scale) {
-    const auto r = rows_rsrc(static_cast<T*>(p) + ((size_t)start * H + h) * Dv, n, H * Dv, Dv);
+__device__ __forceinline__ void store_column(T* first, int n, int H, int Dv, const Column& c, const f32x4 (&v)[4],
+                                             float scale) {
+    const auto r = rows_rsrc(first, n, H * Dv, Dv);
     const uint32_t o = fresh(c.o);
 #pragma unroll
     for (int i = 0; i < 16; ++i)
