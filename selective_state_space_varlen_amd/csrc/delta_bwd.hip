@@ -513,14 +513,23 @@ __global__ __launch_bounds__(256) void k_delta_dg(DeltaArgs a) {
 }
 
 template <typename T, int DKP>
-int launch_delta_bwd(const DeltaArgs& a, hipStream_t s) {
+void launch_delta_chain_bwd(const DeltaArgs& a, int waves, hipStream_t s) {
+    if constexpr (kWide<T, DKP>)
+        if (waves == 8) {
+            k_delta_chain_bwd<T, DKP, 8><<<chain_blocks(a, 8), 512, 0, s>>>(a);
+            return;
+        }
+    k_delta_chain_bwd<T, DKP, 4><<<chain_blocks(a, 4), 256, 0, s>>>(a);
+}
+
+template <typename T, int DKP>
+int launch_delta_bwd(DeltaArgs a, hipStream_t s) {
+    const int waves = chain_waves<T, DKP>(a);
+    if (!chain_ordered(a, waves)) a.order = nullptr;
     if (a.T > 0)
         if (const int st = launch_delta_prepare<T, DKP, true>(a, s)) return st;
     if (a.T > 0 || a.dh0) {
-        if (const int nw = chain_waves(a); nw == 8)
-            k_delta_chain_bwd<T, DKP, 8><<<chain_blocks(a, nw), nw * 64, 0, s>>>(a);
-        else
-            k_delta_chain_bwd<T, DKP, 4><<<chain_blocks(a, nw), nw * 64, 0, s>>>(a);
+        launch_delta_chain_bwd<T, DKP>(a, waves, s);
         SSMP_LAUNCH_CHECK();
     }
     if (a.T > 0) {
@@ -609,7 +618,7 @@ extern "C" int gated_delta_pack_bwd(const void* q, const void* k, const float* g
         a.dS1 = reinterpret_cast<float*>(ws + L.dS1);
         a.dU = reinterpret_cast<float*>(ws + L.dU);
         a.rows = reinterpret_cast<float*>(ws + L.rows);
-        if (chain_ordered(a)) a.order = reinterpret_cast<int32_t*>(ws + L.order);
+        a.order = reinterpret_cast<int32_t*>(ws + L.order);
     }
     hipStream_t s = static_cast<hipStream_t>(stream);
     const bool wide = Dk > 64;

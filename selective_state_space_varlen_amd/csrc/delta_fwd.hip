@@ -175,19 +175,24 @@ __global__ __launch_bounds__(NW * 64) void k_delta_chain(DeltaArgs a) {
     if (a.hT) store_state(a.hT + state, a.Dk, a.Dv, cs, S);
 }
 
+template <typename T, int DKP, bool SAVE>
+void launch_delta_chain(const DeltaArgs& a, int waves, hipStream_t s) {
+    if constexpr (kWide<T, DKP>)
+        if (waves == 8) {
+            k_delta_chain<T, DKP, 8, SAVE><<<chain_blocks(a, 8), 512, 0, s>>>(a);
+            return;
+        }
+    k_delta_chain<T, DKP, 4, SAVE><<<chain_blocks(a, 4), 256, 0, s>>>(a);
+}
+
 template <typename T, int DKP>
-int launch_delta_fwd(const DeltaArgs& a, hipStream_t s) {
+int launch_delta_fwd(DeltaArgs a, hipStream_t s) {
+    const int waves = chain_waves<T, DKP>(a);
+    if (!chain_ordered(a, waves)) a.order = nullptr;
     if (a.T > 0)
         if (const int st = launch_delta_prepare<T, DKP, false>(a, s)) return st;
-    const int nw = chain_waves(a);
-    const unsigned blocks = chain_blocks(a, nw);
-    if (a.S0) {
-        if (nw == 8) k_delta_chain<T, DKP, 8, true><<<blocks, nw * 64, 0, s>>>(a);
-        else k_delta_chain<T, DKP, 4, true><<<blocks, nw * 64, 0, s>>>(a);
-    } else {
-        if (nw == 8) k_delta_chain<T, DKP, 8, false><<<blocks, nw * 64, 0, s>>>(a);
-        else k_delta_chain<T, DKP, 4, false><<<blocks, nw * 64, 0, s>>>(a);
-    }
+    if (a.S0) launch_delta_chain<T, DKP, true>(a, waves, s);
+    else launch_delta_chain<T, DKP, false>(a, waves, s);
     SSMP_LAUNCH_CHECK();
     return SSMP_OK;
 }
@@ -260,7 +265,7 @@ extern "C" int gated_delta_pack_fwd(const void* q, const void* k, const void* v,
         a.dec = reinterpret_cast<float*>(ws + L.dec);
         a.inv = reinterpret_cast<float*>(ws + L.inv);
         a.att = reinterpret_cast<float*>(ws + L.att);
-        if (chain_ordered(a)) a.order = reinterpret_cast<int32_t*>(ws + L.order);
+        a.order = reinterpret_cast<int32_t*>(ws + L.order);
         if (saved) {
             a.S0 = static_cast<float*>(saved);
             a.E = reinterpret_cast<float*>(static_cast<char*>(saved) +

@@ -282,17 +282,29 @@ template <typename Tiles, int DKP, int NW>
 constexpr int kSets = 2 * sizeof(Tiles) <= 160 * 1024 && (DKP > 64 || NW == 8) ? 2 : 1;
 
 // Waves of a chain's workgroup. Eight (128 columns) read a chunk's operands
-// once for a whole head; with fewer heads than CUs, two workgroups of four
-// bring more of the chip to work and each chunk's chain ends sooner.
+// once for a whole head and give each SIMD two waves, one of which works while
+// the other waits; while every workgroup of four finds a CU of its own, each
+// chunk of a chain ends sooner there. Keeping forward / backward in bf16, heads
+// of 128 (us, 32768 tokens): 128 chains 651 / 618 with eight and 525 / 507 with
+// four; 192 chains (24576 tokens) 378 / 354 and 477 / 461; 512 chains 764 / 738
+// and 1012 / 974. fp32 keys over 64 keep four: eight waves have half the
+// registers each and spill (512 chains of 512 tokens, 685 / 613 against 486 /
+// 508; keys of 64 fit, 214 / 237 against 306 / 321).
 constexpr int kCUs = 256;
-inline int chain_waves(const DeltaArgs& a) {
-    return a.Dv > 64 && (int64_t)a.nseq * a.Hv * ((a.Dv + 127) / 128) >= kCUs ? 8 : 4;
+template <typename T, int DKP>
+constexpr bool kWide = kExact<T> == 1 || DKP <= 64;
+inline int64_t chain_groups(const DeltaArgs& a, int waves) {
+    return (int64_t)a.nseq * a.Hv * ((a.Dv + waves * kWaveCols - 1) / (waves * kWaveCols));
+}
+template <typename T, int DKP>
+int chain_waves(const DeltaArgs& a) {
+    return kWide<T, DKP> && a.Dv > 4 * kWaveCols && chain_groups(a, 4) > kCUs ? 8 : 4;
 }
 // Whether the chains are started by length: where they are more than the CUs
-// take at once.
-inline bool chain_ordered(const DeltaArgs& a) {
-    return a.nseq > 1 && a.nseq <= kOrderMax &&
-           (int64_t)a.nseq * a.Hv * ((a.Dv + 127) / 128) > kCUs;
+// take at once (31 sequences of 64 to 2048 tokens x 32 heads: 720 us against
+// 820 keeping, 751 against 847 backward).
+inline bool chain_ordered(const DeltaArgs& a, int waves) {
+    return a.nseq > 1 && a.nseq <= kOrderMax && chain_groups(a, waves) > kCUs;
 }
 inline unsigned chain_blocks(const DeltaArgs& a, int waves) {
     const int ncb = (a.Dv + waves * kWaveCols - 1) / (waves * kWaveCols);

@@ -9,6 +9,18 @@ another, the rms is below sqrt(L (Dk + 64)) 2^-24 of the largest value, and
 four times that is allowed (`tol32`). Gradients are the same recurrence
 backwards. A result stored in bf16 is off by at most half a step more, 2^-8
 of its value (finfo(bf16).eps / 2).
+
+`out` and `dk` of bf16 inputs add products in which a 32-bit operand stands as
+two bf16 parts. A part holds 8 significant bits. Cut, the first leaves less
+than 2^-7 of the value and the second less than 2^-7 of that: 2^-14 of the
+value at most, and an rms of 2^-14 / 3 < 2^-15.5 where the lower bits are
+uniform (each remainder is r u with u uniform in (0, 1), whose rms is
+1 / sqrt 3). Rounded to nearest, each is half of that, so both operands of a
+product and the product of their second parts, which is left out, add
+sqrt 3 2^-17.5 < 2^-16.5. Together the rms is below 2^-15 of a term, hence of
+the root of the sum of the squared terms, which is below the largest value
+as above; four times that, 2^-13, is allowed (`tol_parts`): 1 / 32 of the
+type's own half step.
 """
 from __future__ import annotations
 
@@ -21,6 +33,10 @@ F64 = torch.float64
 
 def tol32(L: int, Dk: int) -> float:
     return 4.0 * math.sqrt(max(L, 1) * (Dk + 64)) * 2.0 ** -24
+
+
+def tol_parts(name: str, dtype) -> float:
+    return 2.0 ** -13 if name in ("out", "dk") and dtype != torch.float32 else 0.0
 
 
 def half_step(dtype) -> float:

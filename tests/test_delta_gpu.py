@@ -59,7 +59,7 @@ def compare(got, ref, d, lens, carry, Dk):
     r = d["v"].shape[1] // d["q"].shape[1]
     for n in ("out", "dq", "dk", "dv", "dbeta"):
         # dq and dk add r heads
-        dc.check(got[n][:T], ref[n], tol * (r if n in ("dq", "dk") else 1), n)
+        dc.check(got[n][:T], ref[n], (tol + dc.tol_parts(n, got[n].dtype)) * (r if n in ("dq", "dk") else 1), n)
     # dg sums what reads and writes a state, dq.q and dk.k, with both signs
     terms = sum(float((ref[a].abs() * d[b][:T].to(dc.F64).abs()).sum(-1).max()) if T else 0.0
                 for a, b in (("dq", "q"), ("dk", "k")))
