@@ -390,7 +390,8 @@ enum ssmp_norm {
  * Supports D a multiple of 8 up to 512, rot a multiple of 16 (of 2 when
  * interleaved) up to D. Activation pointers must be multiples of 16 bytes.
  * A row of zeros with eps = 0 gives NaN, as the formula does.
- * Errors: SSMP_ERR_SHAPE, SSMP_ERR_UNSUPPORTED, SSMP_ERR_NULL, SSMP_ERR_ALIGN,
+ * Errors: SSMP_ERR_SHAPE (also T >= 2^26, more than 65536 heads, 2^40 elements
+ * or more), SSMP_ERR_UNSUPPORTED, SSMP_ERR_NULL, SSMP_ERR_ALIGN,
  * SSMP_ERR_WORKSPACE.
  */
 int qk_norm_pack_fwd(const void *q, const void *k, const float *wq, const float *wk, const int32_t *pos,
@@ -433,7 +434,9 @@ int qk_norm_pack_bwd(const void *q, const void *k, const float *wq, const float 
  * Supports Dk a multiple of 8 up to 128, Dv a multiple of 8, Hv a multiple
  * of Hk. Pointers other than g, beta, cu_seqlens must be multiples of 16 bytes.
  * Buffers must not overlap.
- * Errors: SSMP_ERR_SHAPE, SSMP_ERR_UNSUPPORTED, SSMP_ERR_NULL, SSMP_ERR_ALIGN,
+ * Errors: SSMP_ERR_SHAPE (also Hv > 65535, Hk * Dk or Hv * Dv > 2^20, nseq >
+ * 2^24, T * Hv * max(Dk, Dv) >= 2^40, or more than 2^23 pairs of a chunk, or of
+ * a sequence and 128 columns, with a value head), SSMP_ERR_UNSUPPORTED, SSMP_ERR_NULL, SSMP_ERR_ALIGN,
  * SSMP_ERR_WORKSPACE. The size queries return 0 for arguments out of range.
  */
 size_t gated_delta_pack_saved_bytes(int64_t T, int32_t nseq, int32_t Hk, int32_t Hv, int32_t Dk, int32_t Dv);
@@ -476,7 +479,8 @@ int gated_delta_pack_bwd(const void *q, const void *k, const float *g, const flo
  *          whose slot is outside [0, nslots) is skipped: its out is left as
  *          it was.
  * Supports Dk a multiple of 8 up to 128, Dv a multiple of 8. Allocates and
- * needs nothing. Errors: SSMP_ERR_SHAPE (also B > nslots without slots),
+ * needs nothing. Errors: SSMP_ERR_SHAPE (also B > nslots without slots, Hv or
+ * Dv > 65536, B * Hv * ceil(Dv / 32) >= 2^24),
  * SSMP_ERR_UNSUPPORTED, SSMP_ERR_NULL, SSMP_ERR_ALIGN.
  */
 int gated_delta_pack_step(const void *q, const void *k, const void *v, const float *g, const float *beta,

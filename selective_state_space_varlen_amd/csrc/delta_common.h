@@ -34,6 +34,9 @@ __device__ __forceinline__ float dpp_add(float v) {
 __device__ __forceinline__ float sum8(float v) { return dpp_add<0x141>(dpp_add<0x4E>(dpp_add<0xB1>(v))); }
 __device__ __forceinline__ float sum16(float v) { return dpp_add<0x140>(sum8(v)); }
 
+// A launch takes fewer than 2^32 threads: this many workgroups of 256 at most.
+constexpr int64_t kMaxBlocks = int64_t(1) << 24;
+
 // ---------------------------------------------------------------------------
 // Chunks. A chunk is up to 64 tokens of one sequence, counted from its first
 // token. Sequence s has its chunks in the slots floor(cu[s] / 64) + s + c,
@@ -176,7 +179,7 @@ __device__ __forceinline__ void step_order() {
 // the leading 8 bits that are left each, which holds all 24 of an fp32. (Cutting
 // off takes two thirds of the time of rounding: 34 against 52 cycles a pair on
 // one SIMD, and a chain spends more cycles on splitting than on its products.)
-// Two planes round each, so that what they leave out, 2^-17 of v at most, has
+// Two planes round each, so that what they leave out, 2^-16 of v at most, has
 // no sign of its own to add up in a sum.
 template <int NP>
 __device__ __forceinline__ void split2(float v0, float v1, uint32_t (&p)[NP]) {
@@ -223,8 +226,9 @@ __device__ __forceinline__ Frag<NP> split8(const float (&v)[8]) {
 template <typename T>
 constexpr int kExact = std::is_same<T, float>::value ? 3 : 1;
 
-// planes of what enters a result of this type alone: bf16's own rounding hides
-// what two planes (16 bits) leave out
+// planes of what enters a result of this type alone: bf16's own rounding, 2^-8
+// of the result, hides what two planes leave out, 2^-14 of a term at most (the
+// first two of a cut value's three; 2^-16 of one that is split in two)
 template <typename T>
 constexpr int kOutP = std::is_same<T, float>::value ? 3 : 2;
 
@@ -586,8 +590,8 @@ constexpr int kDec = 4 * kC;
 
 // What goes from the chains to the gradients, S, E, dS' and dU of each chunk:
 // fp32 in blocks of 32 columns, [block][row][32], as k_delta_grads reads them:
-// in rows of all columns it would read 128 bytes of each 512 at a time, and
-// memory gave 3.0 TB/s of its 5.2.
+// in rows of all columns it would read 128 bytes of each 512 at a time (1500 us
+// where it takes 1415, 32768 tokens x 32 heads of 128 x 128).
 constexpr int kKeptCols = 32;
 __host__ __device__ inline int kept_cols(int Dv) { return (Dv + kKeptCols - 1) / kKeptCols * kKeptCols; }
 __device__ __forceinline__ int kept_at(int rows, int row, int col) {
@@ -624,8 +628,9 @@ inline int delta_check(int64_t T, int32_t nseq, int32_t Hk, int32_t Hv, int32_t 
     if (Hv % Hk || Hv > 65535 || nseq > (1 << 24)) return SSMP_ERR_SHAPE;
     if ((int64_t)Hv * Dv > kMaxRow || (int64_t)Hk * Dk > kMaxRow) return SSMP_ERR_SHAPE;
     if (T * Hv * (int64_t)(Dv > Dk ? Dv : Dk) >= (int64_t(1) << 40)) return SSMP_ERR_SHAPE;
-    if ((int64_t)(nseq + 7) * Hv * ((Dv + 63) / 64) >= (int64_t(1) << 31)) return SSMP_ERR_SHAPE;
-    if ((T / kC + nseq + 7) * Hv >= (int64_t(1) << 31)) return SSMP_ERR_SHAPE;
+    // the chains' and the chunks' workgroups (of chunks two a head: 64 columns of dq and dk)
+    if ((int64_t)(nseq + 7) * Hv * ((Dv + 127) / 128 * 2) >= kMaxBlocks) return SSMP_ERR_SHAPE;
+    if ((T / kC + nseq + 7) * Hv * 2 >= kMaxBlocks) return SSMP_ERR_SHAPE;
     if (dtype != SSMP_F32 && dtype != SSMP_BF16) return SSMP_ERR_UNSUPPORTED;
     if (Dk % 8 || Dv % 8 || Dk > kMaxDk) return SSMP_ERR_UNSUPPORTED;
     return SSMP_OK;

@@ -10,7 +10,7 @@ namespace ssmp {
 // its sequence, and a long one that starts last is waited for alone. Sorted by
 // counting in one workgroup beside those that prepare the chunks; the order
 // among equals is left to chance and changes no result. h: 2048 ints of LDS.
-constexpr int kOrderMax = 4096;  // sequences; more need no order, they are short beside the whole
+constexpr int kOrderMax = 4096;  // sequences one workgroup sorts beside the others; more start as they lie
 __device__ __forceinline__ void order_sequences(const DeltaArgs& a, int* h) {
     constexpr int kBins = 1024;
     const int tid = threadIdx.x;
@@ -41,6 +41,9 @@ __device__ __forceinline__ void order_sequences(const DeltaArgs& a, int* h) {
 // whose L2 then holds their keys and queries.
 //   forward:  (I + L diag(beta))^-1 and P,           both lower triangular
 //   backward: (I + diag(beta) L)^-T and scale P^T,   both upper triangular
+// The inverse is one dependent sequence of small products, which four
+// workgroups a CU hide from each other: 198 us forward, 216 us backward for
+// 32768 tokens x 32 heads of 128 in bf16, 0.76 GB at 3.8 TB/s.
 template <typename T, int DKP, bool BWD>
 __global__ __launch_bounds__(256, kExact<T> == 1 ? 4 : 1) void k_delta_prepare(DeltaArgs a) {
     constexpr int NX = kExact<T>;

@@ -154,7 +154,7 @@ extern "C" int gated_delta_pack_step(const void* q, const void* k, const void* v
     using namespace ssmp;
     if (B < 0 || nslots < 0 || Hk < 1 || Hv < 1 || Dk < 1 || Dv < 1 || Hv % Hk) return SSMP_ERR_SHAPE;
     if (!slots && B > nslots) return SSMP_ERR_SHAPE;
-    if (Hv > 65536 || Dv > 65536 || (int64_t)B * Hv * ((Dv + kStepCols - 1) / kStepCols) >= (int64_t(1) << 31))
+    if (Hv > 65536 || Dv > 65536 || (int64_t)B * Hv * ((Dv + kStepCols - 1) / kStepCols) >= kMaxBlocks)
         return SSMP_ERR_SHAPE;
     if (dtype != SSMP_F32 && dtype != SSMP_BF16) return SSMP_ERR_UNSUPPORTED;
     if (Dk % 8 || Dv % 8 || Dk > kStepMaxDk) return SSMP_ERR_UNSUPPORTED;

@@ -10,7 +10,8 @@
 // Bound by HBM: each row is read and written once. A row lies across 1 to 64
 // lanes, 8 components in each, so that a wave reads 1 KiB (bf16) at a time;
 // a wave takes the heads of one token together, which turn by the same
-// angles, and forms its lanes' cosines and sines once.
+// angles, and forms its lanes' cosines and sines once. 32768 tokens of 32 heads
+// of 128 in bf16: 97 us forward and 155 us backward, 5.5 and 5.2 TB/s.
 #include "delta_common.h"
 
 namespace ssmp {
@@ -108,7 +109,7 @@ __device__ __forceinline__ NormAt norm_at(const NormArgs& a, int64_t t, int h, i
 // and reduced to half a turn either way before it is rounded to 32. The wave's
 // lanes form one angle each (rot / 2 of them in all) and pass them on through
 // LDS: formed where they are used, they would take longer than the heads do
-// (16384 tokens of 40 heads of 128, half turned: 118 us against 84).
+// (16384 tokens of 40 heads of 128, half turned: 118 us against 87).
 struct Turn {
     float c[kNormVec], s[kNormVec];
     int partner;  // lane that holds the other members (half-split pairs)
@@ -346,7 +347,7 @@ void launch_norm_d(const NormArgs& a, bool bwd, bool dw, int64_t blocks, hipStre
 }
 
 inline bool norm_sizes_ok(int64_t T, int32_t Hq, int32_t Hk, int32_t D) {
-    return T >= 0 && T < (int64_t(1) << 31) && Hq >= 0 && Hk >= 0 && Hq <= 65536 && Hk <= 65536 && Hq + Hk >= 1 &&
+    return T >= 0 && T < kMaxBlocks * kNormWaves && Hq >= 0 && Hk >= 0 && Hq <= 65536 && Hk <= 65536 && Hq + Hk >= 1 &&
            D >= 1 && T * ((int64_t)Hq + Hk) * D < (int64_t(1) << 40);
 }
 inline int norm_check(int64_t T, int32_t Hq, int32_t Hk, int32_t D, int32_t rot, int32_t dtype, int32_t norm,

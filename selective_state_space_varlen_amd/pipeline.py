@@ -106,7 +106,10 @@ def delta_forward(x: tuple, w: tuple, b: Optional[tuple], g: torch.Tensor, beta:
     (nseq, Hv, Dk, Dv) fp32, 'conv': three contexts (nseq, W-1, .)} (either may
     be None: zeros); with final_states=True, or with initial states, the result
     also holds 'final_states' in the same form. pos then still counts inside
-    the pack; a rotation (inv_freq) that goes on is given its own pos."""
+    the pack; a rotation (inv_freq) that goes on is given its own pos.
+
+    cu_seqlens ends at T: the convs and norms go over every row, and sum their
+    weights' gradients over every row."""
     T = x[0].shape[0]
     starts, _, _ = _b.varlen_pack_indices(cu_seqlens, T, heads=False, dev_err=False)
     carry = initial_states is not None or final_states

@@ -72,6 +72,17 @@ def test_rule_refusals(lib):
     assert rule_fwd(lib, T=0, q=NULL, out=NULL, scratch=NULL, nscratch=0) == OK  # nothing to do
 
 
+def test_more_threads_than_a_launch_takes_are_refused(lib):
+    assert norm_fwd(lib, T=1 << 26) == E_SHAPE
+    assert rule_fwd(lib, T=1 << 30, Hk=1, Hv=1, Dk=8, Dv=8) == E_SHAPE       # chunks
+    assert rule_fwd(lib, T=100, nseq=1 << 23, Hk=1, Hv=1, Dk=8, Dv=8) == E_SHAPE  # chunks, of which each sequence has a slot
+    assert rule_fwd(lib, T=100, nseq=1 << 14, Hv=2, Dv=1 << 19) == E_SHAPE   # chains
+    assert lib.gated_delta_pack_step(FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, 1 << 19, 8, 1, 32, 64, 32, 1, 0.1,
+                                     NULL) == E_SHAPE
+    assert lib.qk_norm_pack_bwd_workspace_bytes(1 << 26, 2, 1, 64) == 0
+    assert lib.gated_delta_pack_saved_bytes(1 << 30, 2, 1, 1, 8, 8) == 0
+
+
 def test_rule_sizes(lib):
     T, n, Hk, Hv, Dk, Dv = 1000, 3, 1, 2, 64, 40
     slots = T // 64 + n
