@@ -26,8 +26,7 @@
 namespace ssmp {
 
 // As k_delta_chain, from the last chunk to the first, with the same bound: 730
-// us for 32768 tokens x 32 heads of 128 x 128 in bf16, longest sequence 2048;
-// 4.0 us a chunk where each workgroup has a CU of its own.
+// us for 32768 tokens x 32 heads of 128 x 128 in bf16.
 template <typename T, int DKP, int NW>
 __global__ __launch_bounds__(NW * 64) void k_delta_chain_bwd(DeltaArgs a) {
     constexpr int NX = kExact<T>;

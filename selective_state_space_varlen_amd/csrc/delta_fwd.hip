@@ -21,10 +21,11 @@ namespace ssmp {
 // their way there, and those of the one after it under way in registers.
 // SAVE: keep S and E for the backward.
 // Bound by what a SIMD can issue: a wave's chunk (heads of 128, bf16) is 182
-// matrix instructions of 16 cycles and twice their time in splitting fp32
-// values into planes, reading LDS and storing, of 8000 cycles in all. 4.0 us a
-// chunk where each workgroup has a CU of its own (43 us for one prompt of 513
-// tokens); 490 to 550 us for 32768 tokens x 32 heads, 710 keeping S and E.
+// matrix instructions of 16 cycles, and the rest of its 10000 cycles in
+// splitting fp32 values into planes, reading LDS, storing, and the latency of
+// each upon the last. One prompt of 513 tokens x 32 heads takes 43 us, 4.3 a
+// chunk (6.1 with every CU at work, when the clock is lower, and 8.2 keeping S
+// and E); 32768 tokens x 32 heads 490 to 550 us, 710 keeping.
 template <typename T, int DKP, int NW, bool SAVE>
 __global__ __launch_bounds__(NW * 64) void k_delta_chain(DeltaArgs a) {
     constexpr int NX = kExact<T>, NO = kOutP<T>;
