@@ -27,7 +27,8 @@ namespace ssmp {
 
 // As k_delta_chain, from the last chunk to the first, with the same bound: 730
 // us for 32768 tokens x 32 heads of 128 x 128 in bf16.
-template <typename T, int DKP, int NW>
+// SUM: the first walk over the parts of split sequences.
+template <typename T, int DKP, int NW, bool SUM>
 __global__ __launch_bounds__(NW * 64) void k_delta_chain_bwd(DeltaArgs a) {
     constexpr int NX = kExact<T>;
     constexpr int MT = DKP / 16;
@@ -35,21 +36,25 @@ __global__ __launch_bounds__(NW * 64) void k_delta_chain_bwd(DeltaArgs a) {
     constexpr int SETS = kSets<typename Loads::Tiles, DKP, NW>;
     __shared__ alignas(16) typename Loads::Tiles sets[SETS];
     constexpr int kCols = NW * kWaveCols;
-    const int ncb = (a.Dv + kCols - 1) / kCols, group = a.Hv / a.Hk;
+    const int ncb = SUM ? (joint_b(a.Dv) + DKP) / kCols : (a.Dv + kCols - 1) / kCols, group = a.Hv / a.Hk;
     const Spread sp = spread(blockIdx.x, ncb * group);
-    if (sp.group >= (int64_t)a.nseq * a.Hk) return;
+    const bool split = SUM || (NW == 4 && a.split);
+    if (sp.group >= (split ? split_parts(a) : (int64_t)a.nseq) * a.Hk) return;
     const int hk = (int)(sp.group % a.Hk);
-    int seq = (int)(sp.group / a.Hk);
-    if (a.order) seq = a.order[seq];
+    Walk q;
+    if (!walk_at<NW == 4>(a, sp.group / a.Hk, q) || (SUM && q.first)) return;
     const int hv = hk * group + sp.member / ncb, cb = sp.member % ncb;
     const int wave = wave_id(), l = lane_id(), l16 = l & 15, l4 = l >> 4;
     const int col = cb * kCols + wave * 16 + l16;
-    const Seq q = seq_at(a.cu, seq, a.T);
     const int chunks = (q.len + kC - 1) / kC;
     const Column cs = column_of<float>(1, a.Dv, col), cv = column_of<T>(a.Hv, a.Dv, col);
-    const size_t state = ((size_t)seq * a.Hv + hv) * a.Dk * a.Dv;
+    const size_t state = ((size_t)q.seq * a.Hv + hv) * a.Dk * a.Dv;
+    const int width = joint_b(a.Dv) + DKP;
+    float* const joint = a.joint + ((size_t)q.part * a.Hv + hv) * DKP * width;
     f32x4 S[MT];
-    load_state(a.dhT ? a.dhT + state : nullptr, a.Dk, a.Dv, cs, S);
+    if constexpr (SUM) unit_state<DKP>(S, col - joint_b(a.Dv));
+    else if (split) load_state(joint, DKP, width, column_of<float>(1, width, col), S);
+    else load_state(a.dhT ? a.dhT + state : nullptr, a.Dk, a.Dv, cs, S);
     Loads next;
     uint32_t onext[16];
     // an empty sequence has no last chunk
@@ -77,7 +82,7 @@ __global__ __launch_bounds__(NW * 64) void k_delta_chain_bwd(DeltaArgs a) {
         for (int i = 0; i < 16; ++i) o[i >> 2][i & 3] = Elt<T>::cvt(onext[i]);
         dp -= dstep;
         load_column<T>(dp, tokens(ch - 1), a.Hv, a.Dv, cv, onext);
-        store_kept(a.dS1 + sh * DKP * kept_cols(a.Dv), a.Dv, col, S);
+        if constexpr (!SUM) store_kept(a.dS1 + sh * DKP * kept_cols(a.Dv), a.Dv, col, S);
         f32x4 x[4] = {}, y[4] = {};  // K dS', scale P^T dOut
         Frag<3> sb = split_tiles<3>(S[0], S[1]);
 #pragma unroll
@@ -134,7 +139,7 @@ __global__ __launch_bounds__(NW * 64) void k_delta_chain_bwd(DeltaArgs a) {
             step_order<10, 12, 3>();
         }
         __builtin_amdgcn_sched_barrier(0);
-        store_kept(a.dU + sh * kC * kept_cols(a.Dv), a.Dv, col, u);
+        if constexpr (!SUM) store_kept(a.dU + sh * kC * kept_cols(a.Dv), a.Dv, col, u);
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
             const f32x4 be = *reinterpret_cast<const f32x4*>(lds.beta + m * 16 + l4 * 4);
@@ -172,7 +177,8 @@ __global__ __launch_bounds__(NW * 64) void k_delta_chain_bwd(DeltaArgs a) {
         next.load_rest(a, at, tokens(ch - 2));
         __syncthreads();
     }
-    if (a.dh0) store_state(a.dh0 + state, a.Dk, a.Dv, cs, S);
+    if constexpr (SUM) store_state(joint, DKP, width, column_of<float>(1, width, col), S);
+    else if (a.dh0 && q.first) store_state(a.dh0 + state, a.Dk, a.Dv, cs, S);
 }
 
 // One workgroup per (slot, key head, 64 columns of dq and dk), over the value
@@ -520,10 +526,10 @@ template <typename T, int DKP>
 void launch_delta_chain_bwd(const DeltaArgs& a, int waves, hipStream_t s) {
     if constexpr (kWide<T, DKP>)
         if (waves == 8) {
-            k_delta_chain_bwd<T, DKP, 8><<<chain_blocks(a, 8), 512, 0, s>>>(a);
+            k_delta_chain_bwd<T, DKP, 8, false><<<chain_blocks(a, 8), 512, 0, s>>>(a);
             return;
         }
-    k_delta_chain_bwd<T, DKP, 4><<<chain_blocks(a, 4), 256, 0, s>>>(a);
+    k_delta_chain_bwd<T, DKP, 4, false><<<chain_blocks(a, 4), 256, 0, s>>>(a);
 }
 
 template <typename T, int DKP>
@@ -533,6 +539,12 @@ int launch_delta_bwd(DeltaArgs a, hipStream_t s) {
     if (a.T > 0)
         if (const int st = launch_delta_prepare<T, DKP, true>(a, s)) return st;
     if (a.T > 0 || a.dh0) {
+        if (a.split) {
+            k_delta_chain_bwd<T, DKP, 4, true><<<split_blocks(a, DKP), 256, 0, s>>>(a);
+            SSMP_LAUNCH_CHECK();
+            launch_delta_join<DKP, true>(a, a.dhT, a.dh0, s);
+            SSMP_LAUNCH_CHECK();
+        }
         launch_delta_chain_bwd<T, DKP>(a, waves, s);
         SSMP_LAUNCH_CHECK();
     }
@@ -548,7 +560,7 @@ int launch_delta_bwd(DeltaArgs a, hipStream_t s) {
 }
 
 struct DeltaBwdLayout {
-    size_t dec, inv, att, order, dS1, dU, rows, total;
+    size_t dec, inv, att, order, dS1, dU, rows, joint, total;
 };
 inline DeltaBwdLayout delta_bwd_layout(int64_t T, int32_t nseq, int32_t Hv, int32_t Dk, int32_t Dv) {
     const size_t n = (size_t)delta_slots(T, nseq);
@@ -560,7 +572,8 @@ inline DeltaBwdLayout delta_bwd_layout(int64_t T, int32_t nseq, int32_t Hv, int3
     L.dS1 = L.order + round256((size_t)nseq * 4);
     L.dU = L.dS1 + kept_bytes(T, nseq, Hv, delta_dkp(Dk), Dv);
     L.rows = L.dU + kept_bytes(T, nseq, Hv, kC, Dv);
-    L.total = L.rows + round256(n * Hv * ((Dk + kDh - 1) / kDh) * kC * 4);
+    L.joint = L.rows + round256(n * Hv * ((Dk + kDh - 1) / kDh) * kC * 4);
+    L.total = L.joint + joint_bytes(T, nseq, Hv, delta_dkp(Dk), Dv);
     return L;
 }
 
@@ -623,6 +636,8 @@ extern "C" int gated_delta_pack_bwd(const void* q, const void* k, const float* g
         a.dU = reinterpret_cast<float*>(ws + L.dU);
         a.rows = reinterpret_cast<float*>(ws + L.rows);
         a.order = reinterpret_cast<int32_t*>(ws + L.order);
+        a.joint = reinterpret_cast<float*>(ws + L.joint);
+        a.split = split_chunks(T, nseq, Hv, Dv);
     }
     hipStream_t s = static_cast<hipStream_t>(stream);
     const bool wide = Dk > 64;

@@ -63,20 +63,24 @@ __device__ __forceinline__ Seq seq_at(const int32_t* __restrict__ cu, int s, int
 
 // The chunk in a slot: false where the slot holds none. Called by whole waves;
 // 64 boundaries are looked at in one step, so one trip to memory finds a
-// sequence among 64, two among 4096.
+// sequence among 64, two among 4096. (Pieces of another size than kC lie in
+// slots by the same rule.)
 struct Chunk {
-    int64_t start;  // its first token
-    int32_t n;      // tokens
+    int64_t start;   // its first token
+    int32_t n;       // tokens
+    int32_t seq;
+    int64_t index;   // in its sequence
+    bool last;       // of its sequence
 };
 __device__ __forceinline__ bool chunk_at(const int32_t* __restrict__ cu, int32_t nseq, int64_t T, int64_t slot,
-                                         Chunk& c) {
+                                         Chunk& c, int size = kC) {
     const int top = (int)T, lane = lane_id();
     int lo = 0, hi = nseq;
     while (true) {
         const int step = (hi - lo + 63) / 64, i = lo + lane * step;
         int a = cu[i < nseq ? i : nseq];
         a = a < 0 ? 0 : (a > top ? top : a);
-        int n = __popcll(__ballot(i < hi && (int64_t)(a / kC) + i <= slot));
+        int n = __popcll(__ballot(i < hi && (int64_t)(a / size) + i <= slot));
         n = n < 1 ? 1 : n;
         if (step > 1) {
             lo += (n - 1) * step;
@@ -92,10 +96,13 @@ __device__ __forceinline__ bool chunk_at(const int32_t* __restrict__ cu, int32_t
             end = cu[lo + 1];
             end = end < 0 ? 0 : (end > top ? top : end);
         }
-        const int64_t at = (slot - (first / kC + lo)) * kC;
+        c.index = slot - (first / size + lo);
+        const int64_t at = c.index * size;
         if (at < 0 || at >= end - first) return false;
         c.start = first + at;
-        c.n = end - first - at < kC ? (int32_t)(end - first - at) : kC;
+        c.last = end - first - at <= size;
+        c.n = c.last ? (int32_t)(end - first - at) : size;
+        c.seq = lo;
         return true;
     }
 }
@@ -617,6 +624,8 @@ struct DeltaArgs {
     float *dS1, *dU; // backward: gradients of the state that leaves the chunk, and of U
     float* rows;     // backward: per 64 columns of dq and dk, what k_delta_dg adds up: 64
     int32_t* order;  // the sequences by length (null: as they come)
+    float* joint;    // of split sequences, by part and value head: what joins them
+    int32_t split;   // chunks of a part (0: sequences are not split)
 };
 
 inline size_t kept_bytes(int64_t T, int32_t nseq, int32_t Hv, int rows, int32_t Dv) {

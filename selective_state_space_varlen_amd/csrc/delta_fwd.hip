@@ -19,36 +19,43 @@ namespace ssmp {
 // its next right operands in the registers they are in (kplace), so the waves
 // share nothing but the left operands: of one chunk in LDS, the next one's on
 // their way there, and those of the one after it under way in registers.
-// SAVE: keep S and E for the backward.
+// kKeep: keep S and E for the backward. kSum: the first walk over the parts of
+// split sequences (split_chunks), whose last columns are A's.
 // Bound by what a SIMD can issue: a wave's chunk (heads of 128, bf16) is 182
 // matrix instructions of 16 cycles, and the rest of its 10000 cycles in
 // splitting fp32 values into planes, reading LDS, storing, and the latency of
 // each upon the last. One prompt of 513 tokens x 32 heads takes 43 us, 4.3 a
 // chunk (6.1 with every CU at work, when the clock is lower, and 8.2 keeping S
 // and E); 32768 tokens x 32 heads 490 to 550 us, 710 keeping.
-template <typename T, int DKP, int NW, bool SAVE>
+enum ChainMode { kPlain, kKeep, kSum };
+template <typename T, int DKP, int NW, ChainMode MODE>
 __global__ __launch_bounds__(NW * 64) void k_delta_chain(DeltaArgs a) {
     constexpr int NX = kExact<T>, NO = kOutP<T>;
+    constexpr bool SAVE = MODE == kKeep, SUM = MODE == kSum;
     constexpr int MT = DKP / 16;  // 16-row tiles of the state
     using Loads = ChainLoads<T, DKP, NO, NW * 64>;
     constexpr int SETS = kSets<typename Loads::Tiles, DKP, NW>;
     __shared__ alignas(16) typename Loads::Tiles sets[SETS];
     constexpr int kCols = NW * kWaveCols;
-    const int ncb = (a.Dv + kCols - 1) / kCols, group = a.Hv / a.Hk;
+    const int ncb = SUM ? (joint_b(a.Dv) + DKP) / kCols : (a.Dv + kCols - 1) / kCols, group = a.Hv / a.Hk;
     const Spread sp = spread(blockIdx.x, ncb * group);
-    if (sp.group >= (int64_t)a.nseq * a.Hk) return;
+    const bool split = SUM || (NW == 4 && a.split);
+    if (sp.group >= (split ? split_parts(a) : (int64_t)a.nseq) * a.Hk) return;
     const int hk = (int)(sp.group % a.Hk);
-    int seq = (int)(sp.group / a.Hk);
-    if (a.order) seq = a.order[seq];
+    Walk q;
+    if (!walk_at<NW == 4>(a, sp.group / a.Hk, q) || (SUM && q.last)) return;
     const int hv = hk * group + sp.member / ncb, cb = sp.member % ncb;
     const int wave = wave_id(), l = lane_id(), l16 = l & 15, l4 = l >> 4;
     const int col = cb * kCols + wave * 16 + l16;
-    const Seq q = seq_at(a.cu, seq, a.T);
     const int chunks = (q.len + kC - 1) / kC;
     const Column cs = column_of<float>(1, a.Dv, col), cv = column_of<T>(a.Hv, a.Dv, col);
-    const size_t state = ((size_t)seq * a.Hv + hv) * a.Dk * a.Dv;
+    const size_t state = ((size_t)q.seq * a.Hv + hv) * a.Dk * a.Dv;
+    const int width = joint_b(a.Dv) + DKP;
+    float* const joint = a.joint + ((size_t)q.part * a.Hv + hv) * DKP * width;
     f32x4 S[MT];
-    load_state(a.h0 ? a.h0 + state : nullptr, a.Dk, a.Dv, cs, S);
+    if constexpr (SUM) unit_state<DKP>(S, col - joint_b(a.Dv));
+    else if (split) load_state(joint, DKP, width, column_of<float>(1, width, col), S);
+    else load_state(a.h0 ? a.h0 + state : nullptr, a.Dk, a.Dv, cs, S);
     Loads next;
     uint32_t v[16];
     ChainAt<T> at(a, q.slot0, q.start, hk, hv);
@@ -86,8 +93,8 @@ __global__ __launch_bounds__(NW * 64) void k_delta_chain(DeltaArgs a) {
             Frag<3> nb;
             if (s + 1 < DKP / 32) nb = split_tiles<3>(S[2 * s + 2], S[2 * s + 3]);
             mma_tiles<3, 0, 4>(x, ka, sb);
-            mma_tiles<NO, 0, 4>(o, qa, sb);
-            if constexpr (NX == 1) step_order<8, 20, 3>();
+            if constexpr (!SUM) mma_tiles<NO, 0, 4>(o, qa, sb);
+            if constexpr (NX == 1 && !SUM) step_order<8, 20, 3>();
             sb = nb;
         }
         __builtin_amdgcn_sched_barrier(0);
@@ -158,11 +165,13 @@ __global__ __launch_bounds__(NW * 64) void k_delta_chain(DeltaArgs a) {
             mma_tiles<3, 0, MT>(S, ka, wb);
             if constexpr (NX == 1) step_order<2 * MT, 3 * MT, 3>();
             __builtin_amdgcn_sched_barrier(0);
-            Frag<NO> pa[4];
+            if constexpr (!SUM) {
+                Frag<NO> pa[4];
 #pragma unroll
-            for (int m = 2 * s; m < 4; ++m) pa[m - 2 * s] = tri_frag<NO>(lds.att, s * 32 + m * 16 + l16, l4);
-            if (s == 0) mma_tiles<NO, 0, 4>(o, pa, ub);
-            else mma_tiles<NO, 2, 4>(o, pa, ub);
+                for (int m = 2 * s; m < 4; ++m) pa[m - 2 * s] = tri_frag<NO>(lds.att, s * 32 + m * 16 + l16, l4);
+                if (s == 0) mma_tiles<NO, 0, 4>(o, pa, ub);
+                else mma_tiles<NO, 2, 4>(o, pa, ub);
+            }
             wb = wn;
             ub = un;
         }
@@ -173,22 +182,23 @@ __global__ __launch_bounds__(NW * 64) void k_delta_chain(DeltaArgs a) {
         }
         at.step(a, 1);
         next.load_rows(a, at, tokens(ch + 2));
-        store_column<T>(op, tokens(ch), a.Hv, a.Dv, cv, o, a.scale);
+        if constexpr (!SUM) store_column<T>(op, tokens(ch), a.Hv, a.Dv, cv, o, a.scale);
         op += vstep;
         next.load_rest(a, at, tokens(ch + 2));
         __syncthreads();
     }
-    if (a.hT) store_state(a.hT + state, a.Dk, a.Dv, cs, S);
+    if constexpr (SUM) store_state(joint, DKP, width, column_of<float>(1, width, col), S);
+    else if (a.hT && q.last) store_state(a.hT + state, a.Dk, a.Dv, cs, S);
 }
 
-template <typename T, int DKP, bool SAVE>
+template <typename T, int DKP, ChainMode MODE>
 void launch_delta_chain(const DeltaArgs& a, int waves, hipStream_t s) {
     if constexpr (kWide<T, DKP>)
         if (waves == 8) {
-            k_delta_chain<T, DKP, 8, SAVE><<<chain_blocks(a, 8), 512, 0, s>>>(a);
+            k_delta_chain<T, DKP, 8, MODE><<<chain_blocks(a, 8), 512, 0, s>>>(a);
             return;
         }
-    k_delta_chain<T, DKP, 4, SAVE><<<chain_blocks(a, 4), 256, 0, s>>>(a);
+    k_delta_chain<T, DKP, 4, MODE><<<chain_blocks(a, 4), 256, 0, s>>>(a);
 }
 
 template <typename T, int DKP>
@@ -197,23 +207,30 @@ int launch_delta_fwd(DeltaArgs a, hipStream_t s) {
     if (!chain_ordered(a, waves)) a.order = nullptr;
     if (a.T > 0)
         if (const int st = launch_delta_prepare<T, DKP, false>(a, s)) return st;
-    if (a.S0) launch_delta_chain<T, DKP, true>(a, waves, s);
-    else launch_delta_chain<T, DKP, false>(a, waves, s);
+    if (a.split) {
+        k_delta_chain<T, DKP, 4, kSum><<<split_blocks(a, DKP), 256, 0, s>>>(a);
+        SSMP_LAUNCH_CHECK();
+        launch_delta_join<DKP, false>(a, a.h0, a.hT, s);
+        SSMP_LAUNCH_CHECK();
+    }
+    if (a.S0) launch_delta_chain<T, DKP, kKeep>(a, waves, s);
+    else launch_delta_chain<T, DKP, kPlain>(a, waves, s);
     SSMP_LAUNCH_CHECK();
     return SSMP_OK;
 }
 
 struct DeltaFwdLayout {
-    size_t dec, inv, att, order, total;
+    size_t dec, inv, att, order, joint, total;
 };
-inline DeltaFwdLayout delta_fwd_layout(int64_t T, int32_t nseq, int32_t Hv) {
+inline DeltaFwdLayout delta_fwd_layout(int64_t T, int32_t nseq, int32_t Hv, int32_t Dk, int32_t Dv) {
     const size_t n = (size_t)delta_slots(T, nseq);
     DeltaFwdLayout L;
     L.dec = 0;
     L.inv = L.dec + round256(n * Hv * kDec * 4);
     L.att = L.inv + round256(n * Hv * kTri * 4);
     L.order = L.att + round256(n * Hv * kTri * 4);
-    L.total = L.order + round256((size_t)nseq * 4);
+    L.joint = L.order + round256((size_t)nseq * 4);
+    L.total = L.joint + joint_bytes(T, nseq, Hv, delta_dkp(Dk), Dv);
     return L;
 }
 
@@ -230,7 +247,7 @@ extern "C" size_t gated_delta_pack_fwd_scratch_bytes(int64_t T, int32_t nseq, in
                                                      int32_t Dv, int32_t dtype) {
     using namespace ssmp;
     if (delta_check(T, nseq, Hk, Hv, Dk, Dv, dtype) || T == 0) return 0;
-    return delta_fwd_layout(T, nseq, Hv).total;
+    return delta_fwd_layout(T, nseq, Hv, Dk, Dv).total;
 }
 
 extern "C" int gated_delta_pack_fwd(const void* q, const void* k, const void* v, const float* g, const float* beta,
@@ -248,7 +265,7 @@ extern "C" int gated_delta_pack_fwd(const void* q, const void* k, const void* v,
     if (T > 0 && saved && saved_bytes < gated_delta_pack_saved_bytes(T, nseq, Hk, Hv, Dk, Dv))
         return SSMP_ERR_WORKSPACE;
     if (T == 0 && !final_state) return SSMP_OK;
-    const DeltaFwdLayout L = delta_fwd_layout(T, nseq, Hv);
+    const DeltaFwdLayout L = delta_fwd_layout(T, nseq, Hv, Dk, Dv);
     char* const ws = static_cast<char*>(scratch);
     DeltaArgs a = {};
     a.q = q;
@@ -272,6 +289,8 @@ extern "C" int gated_delta_pack_fwd(const void* q, const void* k, const void* v,
         a.inv = reinterpret_cast<float*>(ws + L.inv);
         a.att = reinterpret_cast<float*>(ws + L.att);
         a.order = reinterpret_cast<int32_t*>(ws + L.order);
+        a.joint = reinterpret_cast<float*>(ws + L.joint);
+        a.split = split_chunks(T, nseq, Hv, Dv);
         if (saved) {
             a.S0 = static_cast<float*>(saved);
             a.E = reinterpret_cast<float*>(static_cast<char*>(saved) +

@@ -309,9 +309,64 @@ int chain_waves(const DeltaArgs& a) {
 inline bool chain_ordered(const DeltaArgs& a, int waves) {
     return a.nseq > 1 && a.nseq <= kOrderMax && chain_groups(a, waves) > kCUs;
 }
+// Long sequences in few heads are split into parts, so that more than a few
+// CUs work on them. The state that leaves a part is A S + B with S the one that
+// enters: a first walk over all parts at once forms B, from S = 0, and A, whose
+// columns are those of S = 1 with no values read; k_delta_join goes from part
+// to part; a second walk, from the states it found, does what the walk of
+// whole sequences does. Backwards the same with the gradient of the state.
+// That is (Dv + Dk) / Dv and 1 times the steps of the plain walk, so it takes
+// few chains and long ones. A part has at least the square root of half the
+// chunks (the walks take 2 parts' time, the join a chunk's for each part), and
+// there are no more parts than CUs take at once.
+constexpr int kSplitChains = 32, kSplitChunks = 32;
+inline int split_chunks(int64_t T, int32_t nseq, int32_t Hv, int32_t Dv) {
+    const int64_t chains = (int64_t)nseq * Hv * ((Dv + 63) / 64), chunks = T / kC / nseq;
+    if (chains > kSplitChains || chunks < kSplitChunks) return 0;
+    int64_t p = chunks * chains / (kCUs / 2);
+    if (p < 4) p = 4;
+    while (2 * p * p < chunks) ++p;
+    return (int)p;
+}
+__host__ __device__ inline int64_t split_parts(const DeltaArgs& a) { return a.T / ((int64_t)kC * a.split) + a.nseq; }
+// A part's matrix in `joint`: DKP rows of B's columns (whole waves of them; the
+// state that enters, once it is known), then A's.
+__host__ __device__ inline int joint_b(int Dv) { return (Dv + 63) / 64 * 64; }
+inline size_t joint_bytes(int64_t T, int32_t nseq, int32_t Hv, int dkp, int32_t Dv) {
+    const int split = split_chunks(T, nseq, Hv, Dv);
+    if (!split) return 0;
+    return round256((size_t)(T / ((int64_t)kC * split) + nseq) * Hv * dkp * (joint_b(Dv) + dkp) * sizeof(float));
+}
+
 inline unsigned chain_blocks(const DeltaArgs& a, int waves) {
     const int ncb = (a.Dv + waves * kWaveCols - 1) / (waves * kWaveCols);
-    return (unsigned)spread_blocks((int64_t)a.nseq * a.Hk, ncb * (a.Hv / a.Hk));
+    return (unsigned)spread_blocks((a.split ? split_parts(a) : (int64_t)a.nseq) * a.Hk, ncb * (a.Hv / a.Hk));
+}
+// of the first walk over parts, by workgroups of four waves
+inline unsigned split_blocks(const DeltaArgs& a, int dkp) {
+    return (unsigned)spread_blocks(split_parts(a) * a.Hk, (joint_b(a.Dv) + dkp) / 64 * (a.Hv / a.Hk));
+}
+
+// What a chain walks: a sequence, or a part of one.
+struct Walk {
+    int64_t start, slot0;
+    int32_t len, seq;
+    int64_t part;      // its place in `joint`
+    bool first, last;  // of its sequence
+};
+template <bool SPLIT>
+__device__ __forceinline__ bool walk_at(const DeltaArgs& a, int64_t i, Walk& w) {
+    if (SPLIT && a.split) {
+        Chunk c;
+        if (!chunk_at(a.cu, a.nseq, a.T, i, c, kC * a.split)) return false;
+        const int64_t slot0 = (c.start - c.index * kC * a.split) / kC + c.seq;
+        w = {c.start, slot0 + c.index * a.split, c.n, c.seq, i, c.index == 0, c.last};
+        return true;
+    }
+    const int s = a.order ? a.order[i] : (int)i;
+    const Seq q = seq_at(a.cu, s, a.T);
+    w = {q.start, q.slot0, q.len, s, 0, true, true};
+    return true;
 }
 
 // A lane's elements of a (tokens, Dv) tensor of one head, as a result of 4
@@ -359,6 +414,13 @@ __device__ __forceinline__ void load_state(const float* p, int rows, int Dv, con
         v[i >> 2][i & 3] = Elt<float>::cvt(
             Elt<float>::raw_rsrc(r, c.o + (uint32_t)((i >> 2) * 16 + (i & 3)) * (uint32_t)c.stride));
 }
+// the states of A's columns, and no state in B's (e < 0)
+template <int DKP>
+__device__ __forceinline__ void unit_state(f32x4 (&v)[DKP / 16], int e) {
+#pragma unroll
+    for (int i = 0; i < DKP / 4; ++i)
+        v[i >> 2][i & 3] = (i >> 2) * 16 + (lane_id() >> 4) * 4 + (i & 3) == e ? 1.0f : 0.0f;
+}
 // and of a kept matrix (kept_at)
 template <int MT>
 __device__ __forceinline__ void store_kept(float* p, int Dv, int col, const f32x4 (&v)[MT]) {
@@ -367,6 +429,49 @@ __device__ __forceinline__ void store_kept(float* p, int Dv, int col, const f32x
 #pragma unroll
     for (int i = 0; i < MT * 4; ++i)
         Elt<float>::st_rsrc(r, o + (uint32_t)((i >> 2) * 16 + (i & 3)) * (kKeptCols * 4u), v[i >> 2][i & 3]);
+}
+
+// From part to part of a split sequence: 16 columns of the state a wave. `from`
+// enters the first part (backwards: its gradient leaves the last); where there
+// are no tokens it goes to `to` as it is.
+template <int DKP, bool BWD>
+__global__ __launch_bounds__(64) void k_delta_join(DeltaArgs a, const float* from, float* to) {
+    constexpr int MT = DKP / 16;
+    const int ncb = (a.Dv + 15) / 16, l = lane_id(), l16 = l & 15, l4 = l >> 4;
+    const int col = (int)(blockIdx.x % ncb) * 16 + l16, hv = (int)(blockIdx.x / ncb % a.Hv);
+    const int seq = (int)(blockIdx.x / ncb / a.Hv);
+    const Seq q = seq_at(a.cu, seq, a.T);
+    const int64_t size = (int64_t)kC * a.split, first = q.start / size + seq;
+    const int n = (int)((q.len + size - 1) / size), b = joint_b(a.Dv), width = b + DKP;
+    const size_t state = ((size_t)seq * a.Hv + hv) * a.Dk * a.Dv;
+    const Column cs = column_of<float>(1, a.Dv, col), cj = column_of<float>(1, width, col);
+    f32x4 S[MT];
+    load_state(from ? from + state : nullptr, a.Dk, a.Dv, cs, S);
+    if (n == 0 && to) store_state(to + state, a.Dk, a.Dv, cs, S);
+    for (int i = 0; i < n; ++i) {
+        float* const J = a.joint + ((size_t)(first + (BWD ? n - 1 - i : i)) * a.Hv + hv) * DKP * width;
+        f32x4 next[MT];
+        load_state(i + 1 < n ? J : nullptr, DKP, width, cj, next);
+        store_state(J, DKP, width, cj, S);
+        if (i + 1 == n) break;
+#pragma unroll
+        for (int s = 0; s < DKP / 32; ++s) {
+            const auto sb = split_tiles<3>(S[2 * s], S[2 * s + 1]);
+            Frag<3> fa[MT];
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                const float* const row = J + (size_t)(m * 16 + l16) * width + b + s * 32 + l4 * 4;
+                fa[m] = split_tiles<3>(*reinterpret_cast<const f32x4*>(row), *reinterpret_cast<const f32x4*>(row + 16));
+            }
+            mma_tiles<3, 0, MT>(next, fa, sb);
+        }
+#pragma unroll
+        for (int m = 0; m < MT; ++m) S[m] = next[m];
+    }
+}
+template <int DKP, bool BWD>
+void launch_delta_join(const DeltaArgs& a, const float* from, float* to, hipStream_t s) {
+    k_delta_join<DKP, BWD><<<(unsigned)(a.nseq * a.Hv * ((a.Dv + 15) / 16)), 64, 0, s>>>(a, from, to);
 }
 
 }  // namespace ssmp
