@@ -757,6 +757,8 @@ def gated_delta_pack_bwd(q: torch.Tensor, k: torch.Tensor, g: torch.Tensor, beta
     nseq = _nseq(cu_seqlens, dev)
     state = (nseq, Hv, Dk, Dv)
     di = _out_or_new(dinitial_state, state, f32, dev)
+    if saved is None:
+        raise ValueError("saved is None: the forward keeps what the backward reads with save=True")
     _check(saved, "saved", device=dev)
     ws = _buffer(scratch, "scratch",
                  gated_delta_pack_bwd_scratch_bytes(T, nseq, Hk, Hv, Dk, Dv, dt) if scratch is None else 0, dev)

@@ -125,7 +125,7 @@ def delta_forward(x: tuple, w: tuple, b: Optional[tuple], g: torch.Tensor, beta:
         else:
             y = _b.conv1d_pack_fwd(x[i], w[i], bias, starts, silu=True)
         u.append(y)
-    q, k, v = u[0].view(T, Hk, -1), u[1].view(T, Hk, -1), u[2].view(T, Hv, -1)
+    q, k, v = (u[i].view(T, n, u[i].shape[1] // n) for i, n in enumerate((Hk, Hk, Hv)))
     nk = dict(wq=norm_weights[0], wk=norm_weights[1], pos=starts if pos is None else pos, inv_freq=inv_freq,
               norm=norm, eps=eps)
     qn, kn = _b.qk_norm_pack_fwd(q, k, **nk)

@@ -125,3 +125,30 @@ def test_block_in_two_packs():
         dc.check(Ga["dw"][i] + Gb["dw"][i], gw["dw"][i].cpu(), tol, "dw")
     dc.check(Ga["dg"], gw["dg"].cpu()[first.cpu()], tol, "dg")
     dc.check(Gb["dbeta"], gw["dbeta"].cpu()[second.cpu()], tol, "dbeta")
+
+
+def test_block_without_tokens():
+    """No rows, two sequences: states go through as they are, weights get no gradient."""
+    Hk, Hv, Dk, Dv, W = 1, 2, 32, 24, 4
+    d = make([0, 0], Hk, Hv, Dk, Dv, W, True)
+    m, cu = ssp(), dc.cu_of([0, 0]).cuda()
+    x = tree(d, lambda t: t.cuda())
+    F = m.delta_forward(x["x"], x["w"], x["b"], x["g"], x["beta"], cu, Hk, Hv, initial_states=x["states"])
+    G = m.delta_backward(x["x"], x["w"], x["b"], x["g"], x["beta"], F, x["dout"], dfinal_states=x["dstates"])
+    torch.cuda.synchronize()
+    assert F["out"].shape == (0, Hv, Dv)
+    for a, b in zip(leaves(F["final_states"]), leaves(x["states"])):
+        assert torch.equal(a, b)
+    for a, b in zip(leaves(G["dinitial_states"]), leaves(x["dstates"])):
+        assert torch.equal(a, b)
+    for t in G["dw"] + G["db"]:
+        assert not bool(t.any())
+
+
+def test_a_forward_that_kept_nothing_has_no_backward():
+    Hk, Hv, Dk, Dv = 1, 1, 16, 8
+    d = make([5], Hk, Hv, Dk, Dv, 4, False)
+    x = tree(d, lambda t: t.cuda())
+    F = ssp().delta_forward(x["x"], x["w"], x["b"], x["g"], x["beta"], dc.cu_of([5]).cuda(), Hk, Hv, save=False)
+    with pytest.raises(ValueError, match="save=True"):
+        ssp().delta_backward(x["x"], x["w"], x["b"], x["g"], x["beta"], F, x["dout"])
