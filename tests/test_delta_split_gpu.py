@@ -147,3 +147,54 @@ def test_split_in_pieces_and_captured():
         if n == T:  # v's sign has turned once, or five times; both sides are within tol of the exact values
             dc.check(g_out, -whole.cpu(), 2 * tol, "out")
             dc.check(g_hT, -state.cpu(), 2 * tol, "hT")
+
+
+def test_two_graphs_share_a_scratch():
+    """A split pack and a short one, captured on the same scratch and replayed
+    in turn on one stream: each call leaves nothing there that the next reads."""
+    m = ssp()
+    Hk, Hv, Dk, Dv = 1, 2, 64, 40
+    calls, outs, size = [], [], 0
+    for lens in ([2304], [70, 0, 130]):
+        d = dev(dc.rule_inputs(550 + len(lens), lens, Hk, Hv, Dk, Dv, BF, True))
+        T, n = sum(lens), len(lens)
+        size = max(size, m.gated_delta_pack_fwd_scratch_bytes(T, n, Hk, Hv, Dk, Dv, BF),
+                   m.gated_delta_pack_bwd_scratch_bytes(T, n, Hk, Hv, Dk, Dv, BF))
+        kept = torch.empty(m.gated_delta_pack_saved_bytes(T, n, Hk, Hv, Dk, Dv), dtype=torch.uint8, device="cuda")
+        out = {"out": nan_like(d["v"]), "hT": nan_like(d["h0"]), "dh0": nan_like(d["h0"]),
+               "grads": {"dq": nan_like(d["q"]), "dk": nan_like(d["k"]), "dv": nan_like(d["v"]),
+                         "dg": nan_like(d["g"]), "dbeta": nan_like(d["beta"])}}
+        calls.append((d, dc.cu_of(lens).cuda(), kept, out))
+    scratch = torch.empty(size, dtype=torch.uint8, device="cuda")
+
+    def call(d, cu, kept, out):
+        m.gated_delta_pack_fwd(d["q"], d["k"], d["v"], d["g"], d["beta"], cu, initial_state=d["h0"],
+                               final_state=out["hT"], saved=kept, scratch=scratch, out=out["out"])
+        m.gated_delta_pack_bwd(d["q"], d["k"], d["g"], d["beta"], cu, d["dout"], kept, dfinal_state=d["dhT"],
+                               dinitial_state=out["dh0"], scratch=scratch, out=out["grads"])
+
+    flat = lambda out: {"out": out["out"], "hT": out["hT"], "dh0": out["dh0"], **out["grads"]}  # noqa: E731
+    graphs = []
+    for c in calls:
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            call(*c)
+        torch.cuda.current_stream().wait_stream(side)
+        torch.cuda.synchronize()
+        outs.append({n: t.clone() for n, t in flat(c[3]).items()})
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            call(*c)
+        graphs.append(graph)
+    for turn in range(3):
+        scratch.fill_(255)
+        for c in calls:
+            for t in flat(c[3]).values():
+                t.fill_(float("nan"))
+        for graph in graphs:
+            graph.replay()
+        torch.cuda.synchronize()
+        for c, want in zip(calls, outs):
+            for n, t in flat(c[3]).items():
+                assert torch.equal(t, want[n]), (turn, n)
