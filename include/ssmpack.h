@@ -454,7 +454,9 @@ int gated_delta_pack_fwd(const void *q, const void *k, const void *v, const floa
  *   dfinal_state    fp32 (nseq, Hv, Dk, Dv), nullable (zero)
  *   dinitial_state  fp32 (nseq, Hv, Dk, Dv) out, nullable
  *   dq, dk (T, Hk, Dk) dtype out, summed over the value heads of a key head;
- *   dv (T, Hv, Dv) dtype out; dg, dbeta fp32 (T, Hv) out
+ *   dv (T, Hv, Dv) dtype out; dg, dbeta fp32 (T, Hv) out. dg is the difference
+ *   of what reads and what writes a state (q.dq and k.dk), and errs by 32-bit
+ *   roundings of those: where they nearly cancel, by more of itself.
  *   scratch  gated_delta_pack_bwd_scratch_bytes(T, nseq, Hk, Hv, Dk, Dv, dtype)
  * Other arguments, conditions and errors as gated_delta_pack_fwd.
  */

@@ -239,12 +239,8 @@ constexpr int kExact = std::is_same<T, float>::value ? 3 : 1;
 template <typename T>
 constexpr int kOutP = std::is_same<T, float>::value ? 3 : 2;
 
-__device__ __forceinline__ void load8(const float* p, bool on, float (&v)[8]) {
-    f32x4 a = {0, 0, 0, 0}, b = {0, 0, 0, 0};
-    if (on) {
-        a = reinterpret_cast<const f32x4*>(p)[0];
-        b = reinterpret_cast<const f32x4*>(p)[1];
-    }
+__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
+    const f32x4 a = reinterpret_cast<const f32x4*>(p)[0], b = reinterpret_cast<const f32x4*>(p)[1];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         v[e] = a[e];
@@ -305,10 +301,6 @@ struct Unit<uint16_t> {
     __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t o) {
         w = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)o, 0, 0));
     }
-    __device__ __forceinline__ void load(const uint16_t* p, bool on) {
-        w = u32x4{0, 0, 0, 0};
-        if (on) w = *reinterpret_cast<const u32x4*>(p);
-    }
     __device__ __forceinline__ void put_half(uint16_t* p, int h) const {
         *reinterpret_cast<u32x2*>(p) = h ? u32x2{w[2], w[3]} : u32x2{w[0], w[1]};
     }
@@ -334,13 +326,6 @@ struct Unit<float> {
     __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t o) {
         w[0] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)o, 0, 0));
         w[1] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)(o + 16), 0, 0));
-    }
-    __device__ __forceinline__ void load(const float* p, bool on) {
-        w[0] = w[1] = f32x4{0, 0, 0, 0};
-        if (on) {
-            w[0] = reinterpret_cast<const f32x4*>(p)[0];
-            w[1] = reinterpret_cast<const f32x4*>(p)[1];
-        }
     }
     __device__ __forceinline__ void put_half(float* p, int h) const { *reinterpret_cast<f32x4*>(p) = w[h]; }
     __device__ __forceinline__ void pack(const float (&v)[8]) {
@@ -370,7 +355,7 @@ __device__ __forceinline__ Frag<1> tile_frag(const uint16_t* p) {
 }
 __device__ __forceinline__ Frag<3> tile_frag(const float* p) {
     float v[8];
-    load8(p, true, v);
+    load8(p, v);
     return split8<3>(v);
 }
 
