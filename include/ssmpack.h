@@ -427,7 +427,8 @@ int qk_norm_pack_bwd(const void *q, const void *k, const float *wq, const float 
  *            errors e): the only memory between the two calls
  *   scratch  used during the call only,
  *            gated_delta_pack_fwd_scratch_bytes(T, nseq, Hk, Hv, Dk, Dv, dtype)
- * States, and everything that enters them, are fp32 whatever the dtype.
+ * States, and everything between the tensors, are fp32 whatever the dtype; a
+ * bf16 result is rounded once, at the end.
  * Results are deterministic. Within a sequence, a NaN or an infinity of a
  * token may reach outputs up to 63 tokens before it (they share a chunk);
  * other sequences are not touched.

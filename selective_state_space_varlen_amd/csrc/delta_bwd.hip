@@ -32,7 +32,7 @@ template <typename T, int DKP, int NW, bool SUM>
 __global__ __launch_bounds__(NW * 64) void k_delta_chain_bwd(DeltaArgs a) {
     constexpr int NX = kExact<T>;
     constexpr int MT = DKP / 16;
-    using Loads = ChainLoads<T, DKP, 3, NW * 64>;
+    using Loads = ChainLoads<T, DKP, NW * 64>;
     constexpr int SETS = kSets<typename Loads::Tiles, DKP, NW>;
     __shared__ alignas(16) typename Loads::Tiles sets[SETS];
     constexpr int kCols = NW * kWaveCols;
@@ -236,13 +236,12 @@ template <typename T>
 __global__ __launch_bounds__(256, kExact<T> == 1 ? 2 : 1) void k_delta_grads(DeltaArgs a) {
     constexpr int NW = 4;
     constexpr int NX = kExact<T>;
-    constexpr int NK = kOutP<T>;  // planes of what enters dk alone: its rounding hides the third
     constexpr int KC = NW * 8;    // columns at a time
     constexpr int TT = (10 + NW - 1) / NW;  // tiles of a^T a wave has: w, w + NW, ...
     using Plane = Tile<uint16_t, KC>;
     using Square = Tile<uint16_t, kC>;
     constexpr int PT = kC * KC, MT = kC * kC;
-    constexpr int kPlanes = (NX + 6) * PT, kSquares = (3 + NK) * MT;
+    constexpr int kPlanes = (NX + 6) * PT, kSquares = 6 * MT;
     // planes of dOut, dE and U ([token][column]); after a head's columns, of a
     // or -b ([i][j]) and its transpose
     __shared__ alignas(16) __bf16 lds[kPlanes > kSquares ? kPlanes : kSquares];
@@ -331,13 +330,13 @@ __global__ __launch_bounds__(256, kExact<T> == 1 ? 2 : 1) void k_delta_grads(Del
                 }
             }
             Frag<3> sb[KC / 32];
-            Frag<NK> gb[KC / 32];
+            Frag<3> gb[KC / 32];
 #pragma unroll
             for (int s = 0; s < KC / 32; ++s) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) sd = fmaf(next.s0[s].w[e >> 2][e & 3], next.s1[s].w[e >> 2][e & 3], sd);
                 sb[s] = unit_planes(next.s0[s]);
-                gb[s] = split_tiles<NK>(next.s1[s].w[0], next.s1[s].w[1]);
+                gb[s] = split_tiles<3>(next.s1[s].w[0], next.s1[s].w[1]);
             }
             {
                 const bool more = v0 + KC < a.Dv;
@@ -353,11 +352,11 @@ __global__ __launch_bounds__(256, kExact<T> == 1 ? 2 : 1) void k_delta_grads(Del
                     const int o = Plane::at(m * 16 + l16, u);
                     const auto po = tile_planes<NX>(Op, PT, o);
                     const auto pe = tile_planes<3>(Ep, PT, o);
-                    const auto pu = tile_planes<NK>(Up, PT, o);
+                    const auto pu = tile_planes<3>(Up, PT, o);
                     static_for<6>([&](auto t) {
                         mma_term<3, t>(dr[m], pe, sb[s]);
                         mma_term<3, t>(dq[m], po, sb[s]);
-                        mma_term<NK, t>(dw[m], pu, gb[s]);
+                        mma_term<3, t>(dw[m], pu, gb[s]);
                     });
                     __builtin_amdgcn_sched_barrier(0);
                 }
@@ -390,7 +389,7 @@ __global__ __launch_bounds__(256, kExact<T> == 1 ? 2 : 1) void k_delta_grads(Del
             const int row = (w & 1) * 32 + (w >> 1) * 16 + r, k = kplace((w & 1) * 32 + (1 - (w >> 1)) * 16 + k4);
             const float zero[4] = {};
             if (w < 2) lds_put4<3>(M, MT, Square::at(row, k >> 3) + (k & 7), zero);
-            else lds_put4<NK>(Mt, MT, Square::at(row, k >> 3) + (k & 7), zero);
+            else lds_put4<3>(Mt, MT, Square::at(row, k >> 3) + (k & 7), zero);
         }
         float end = decay[0][kC - 1] * sd;
 #pragma unroll
@@ -435,7 +434,7 @@ __global__ __launch_bounds__(256, kExact<T> == 1 ? 2 : 1) void k_delta_grads(Del
                     uint32_t p[3];
                     split2<3>(v[r], v[r + 1], p);
 #pragma unroll
-                    for (int y = 0; y < NK; ++y) {
+                    for (int y = 0; y < 3; ++y) {
                         uint16_t* const to = reinterpret_cast<uint16_t*>(Mt) + y * MT;
                         to[Square::at(j + r, pi >> 3) + (pi & 7)] = (uint16_t)p[y];
                         to[Square::at(j + r + 1, pi >> 3) + (pi & 7)] = (uint16_t)(p[y] >> 16);
@@ -450,16 +449,16 @@ __global__ __launch_bounds__(256, kExact<T> == 1 ? 2 : 1) void k_delta_grads(Del
                 const auto kb = kt.token_frag(l, s, wave), qb = qt.token_frag(l, s, wave);
                 // rows 32 s .. of a, rows .. 32 s + 31 of its transpose
                 Frag<3> fm[4];
-                Frag<NK> ft[4];
+                Frag<3> ft[4];
 #pragma unroll
                 for (int m = 2 * s; m < 4; ++m) fm[m - 2 * s] = tile_planes<3>(M, MT, Square::at(m * 16 + l16, u));
                 if (s == 0) mma_tiles<3, 0, 4>(pass ? dr : dq, fm, kb);
                 else mma_tiles<3, 2, 4>(pass ? dr : dq, fm, kb);
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int m = 0; m < 2 + 2 * s; ++m) ft[m] = tile_planes<NK>(Mt, MT, Square::at(m * 16 + l16, u));
-                if (s == 0) mma_tiles<NK, 0, 2>(tk, ft, pass ? kb : qb);
-                else mma_tiles<NK, 0, 4>(tk, ft, pass ? kb : qb);
+                for (int m = 0; m < 2 + 2 * s; ++m) ft[m] = tile_planes<3>(Mt, MT, Square::at(m * 16 + l16, u));
+                if (s == 0) mma_tiles<3, 0, 2>(tk, ft, pass ? kb : qb);
+                else mma_tiles<3, 0, 4>(tk, ft, pass ? kb : qb);
             }
             if (pass == 0) __syncthreads();
         }

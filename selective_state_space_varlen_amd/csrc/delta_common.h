@@ -183,33 +183,19 @@ __device__ __forceinline__ void step_order() {
 }
 
 // Two values as bf16 planes, packed: v = p[0] + p[1] + ... Three planes take
-// the leading 8 bits that are left each, which holds all 24 of an fp32. (Cutting
-// off takes two thirds of the time of rounding: 34 against 52 cycles a pair on
-// one SIMD, and a chain spends more cycles on splitting than on its products.)
-// Two planes round each, so that what they leave out, 2^-16 of v at most, has
-// no sign of its own to add up in a sum.
+// the leading 8 bits that are left each, which holds all 24 of an fp32; one is
+// for values that are bf16 already. (Cutting off takes two thirds of the time of
+// rounding: 34 against 52 cycles a pair on one SIMD, and a chain spends more
+// cycles on splitting than on its products.)
 template <int NP>
 __device__ __forceinline__ void split2(float v0, float v1, uint32_t (&p)[NP]) {
-    if constexpr (NP == 3) {
 #pragma unroll
-        for (int i = 0; i < NP; ++i) {
-            const uint32_t a = __builtin_bit_cast(uint32_t, v0), b = __builtin_bit_cast(uint32_t, v1);
-            p[i] = __builtin_amdgcn_perm(b, a, 0x07060302u);
-            if (i + 1 < NP) {
-                v0 -= __builtin_bit_cast(float, a & 0xffff0000u);
-                v1 -= __builtin_bit_cast(float, b & 0xffff0000u);
-            }
-        }
-    } else {
-        typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-        typedef float f32x2 __attribute__((ext_vector_type(2)));
-#pragma unroll
-        for (int i = 0; i < NP; ++i) {
-            p[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{v0, v1}), bf16x2));
-            if (i + 1 < NP) {
-                v0 -= __builtin_bit_cast(float, p[i] << 16);
-                v1 -= __builtin_bit_cast(float, p[i] & 0xffff0000u);
-            }
+    for (int i = 0; i < NP; ++i) {
+        const uint32_t a = __builtin_bit_cast(uint32_t, v0), b = __builtin_bit_cast(uint32_t, v1);
+        p[i] = __builtin_amdgcn_perm(b, a, 0x07060302u);
+        if (i + 1 < NP) {
+            v0 -= __builtin_bit_cast(float, a & 0xffff0000u);
+            v1 -= __builtin_bit_cast(float, b & 0xffff0000u);
         }
     }
 }
@@ -232,12 +218,6 @@ __device__ __forceinline__ Frag<NP> split8(const float (&v)[8]) {
 // planes that hold an input of this type exactly
 template <typename T>
 constexpr int kExact = std::is_same<T, float>::value ? 3 : 1;
-
-// planes of what enters a result of this type alone: bf16's own rounding, 2^-8
-// of the result, hides what two planes leave out, 2^-14 of a term at most (the
-// first two of a cut value's three; 2^-16 of one that is split in two)
-template <typename T>
-constexpr int kOutP = std::is_same<T, float>::value ? 3 : 2;
 
 __device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
     const f32x4 a = reinterpret_cast<const f32x4*>(p)[0], b = reinterpret_cast<const f32x4*>(p)[1];

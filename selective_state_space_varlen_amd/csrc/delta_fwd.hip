@@ -21,7 +21,7 @@ namespace ssmp {
 // their way there, and those of the one after it under way in registers.
 // kKeep: keep S and E for the backward. kSum: the first walk over the parts of
 // split sequences (split_chunks), whose last columns are A's.
-// Bound by what a SIMD can issue: a wave's chunk (heads of 128, bf16) is 182
+// Bound by what a SIMD can issue: a wave's chunk (heads of 128, bf16) is 216
 // matrix instructions of 16 cycles, and the rest of its 10000 cycles in
 // splitting fp32 values into planes, reading LDS, storing, and the latency of
 // each upon the last. One prompt of 513 tokens x 32 heads takes 43 us, 4.3 a
@@ -30,10 +30,10 @@ namespace ssmp {
 enum ChainMode { kPlain, kKeep, kSum };
 template <typename T, int DKP, int NW, ChainMode MODE>
 __global__ __launch_bounds__(NW * 64) void k_delta_chain(DeltaArgs a) {
-    constexpr int NX = kExact<T>, NO = kOutP<T>;
+    constexpr int NX = kExact<T>;
     constexpr bool SAVE = MODE == kKeep, SUM = MODE == kSum;
     constexpr int MT = DKP / 16;  // 16-row tiles of the state
-    using Loads = ChainLoads<T, DKP, NO, NW * 64>;
+    using Loads = ChainLoads<T, DKP, NW * 64>;
     constexpr int SETS = kSets<typename Loads::Tiles, DKP, NW>;
     __shared__ alignas(16) typename Loads::Tiles sets[SETS];
     constexpr int kCols = NW * kWaveCols;
@@ -93,8 +93,8 @@ __global__ __launch_bounds__(NW * 64) void k_delta_chain(DeltaArgs a) {
             Frag<3> nb;
             if (s + 1 < DKP / 32) nb = split_tiles<3>(S[2 * s + 2], S[2 * s + 3]);
             mma_tiles<3, 0, 4>(x, ka, sb);
-            if constexpr (!SUM) mma_tiles<NO, 0, 4>(o, qa, sb);
-            if constexpr (NX == 1 && !SUM) step_order<8, 20, 3>();
+            if constexpr (!SUM) mma_tiles<3, 0, 4>(o, qa, sb);
+            if constexpr (NX == 1 && !SUM) step_order<8, 24, 3>();
             sb = nb;
         }
         __builtin_amdgcn_sched_barrier(0);
@@ -145,7 +145,7 @@ __global__ __launch_bounds__(NW * 64) void k_delta_chain(DeltaArgs a) {
         }
         // S += K^T W, out += P U
         Frag<3> wb = split_tiles<3>(w[0], w[1]);
-        Frag<NO> ub = split_tiles<NO>(E[0], E[1]);
+        Frag<3> ub = split_tiles<3>(E[0], E[1]);
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
             __builtin_amdgcn_sched_barrier(0);
@@ -153,10 +153,10 @@ __global__ __launch_bounds__(NW * 64) void k_delta_chain(DeltaArgs a) {
 #pragma unroll
             for (int m = 0; m < MT; ++m) ka[m] = lds.k.token_frag(l, s, m);
             Frag<3> wn;
-            Frag<NO> un;
+            Frag<3> un;
             if (s == 0) {
                 wn = split_tiles<3>(w[2], w[3]);
-                un = split_tiles<NO>(E[2], E[3]);
+                un = split_tiles<3>(E[2], E[3]);
             }
             if constexpr (SETS == 2) {  // the next chunk's operands
                 if (s == 0) next.put_rows(other);
@@ -166,11 +166,11 @@ __global__ __launch_bounds__(NW * 64) void k_delta_chain(DeltaArgs a) {
             if constexpr (NX == 1) step_order<2 * MT, 3 * MT, 3>();
             __builtin_amdgcn_sched_barrier(0);
             if constexpr (!SUM) {
-                Frag<NO> pa[4];
+                Frag<3> pa[4];
 #pragma unroll
-                for (int m = 2 * s; m < 4; ++m) pa[m - 2 * s] = tri_frag<NO>(lds.att, s * 32 + m * 16 + l16, l4);
-                if (s == 0) mma_tiles<NO, 0, 4>(o, pa, ub);
-                else mma_tiles<NO, 2, 4>(o, pa, ub);
+                for (int m = 2 * s; m < 4; ++m) pa[m - 2 * s] = tri_frag<3>(lds.att, s * 32 + m * 16 + l16, l4);
+                if (s == 0) mma_tiles<3, 0, 4>(o, pa, ub);
+                else mma_tiles<3, 2, 4>(o, pa, ub);
             }
             wb = wn;
             ub = un;

@@ -179,13 +179,12 @@ int launch_delta_prepare(const DeltaArgs& a, hipStream_t s) {
 // ---------------------------------------------------------------------------
 // The operands of one chunk that a chain holds in LDS for all its waves, and
 // the registers in which the next chunk's are under way meanwhile: keys and
-// queries, the inverse (3 planes) and the products (NP planes). 62 to 68 KB
-// for bf16 heads of 128.
-template <typename T, int DKP, int NP>
+// queries, the inverse and the products. 68 KB for bf16 heads of 128.
+template <typename T, int DKP>
 struct ChainTiles {
     RowTile<T, DKP> k, q;
     __bf16 inv[3 * kTri];
-    __bf16 att[NP * kTri];
+    __bf16 att[3 * kTri];
     float eg[kC], el[kC], beta[kC];
 };
 
@@ -215,9 +214,9 @@ struct ChainAt {
     }
 };
 
-template <typename T, int DKP, int NP, int THREADS>
+template <typename T, int DKP, int THREADS>
 struct ChainLoads {
-    using Tiles = ChainTiles<T, DKP, NP>;
+    using Tiles = ChainTiles<T, DKP>;
     static constexpr int kN = DKP * kC / 8 / THREADS;                         // units of 8 elements a thread
     static constexpr int kM = (kTri / 4 + THREADS - 1) / THREADS;             // units of 4 of a triangle
     static __device__ __forceinline__ bool tri_on(int x) {
@@ -267,7 +266,7 @@ struct ChainLoads {
         for (int x = 0; x < kM; ++x)
             if (tri_on(x)) {
                 tri_put4<3>(t.inv, tid + x * THREADS, inv[x].w);
-                tri_put4<NP>(t.att, tid + x * THREADS, att[x].w);
+                tri_put4<3>(t.att, tid + x * THREADS, att[x].w);
             }
         if (tid < kC) t.eg[tid] = Elt<float>::cvt(dec);
         else if (tid < 2 * kC) t.el[tid - kC] = Elt<float>::cvt(dec);
