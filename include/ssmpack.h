@@ -386,7 +386,7 @@ enum ssmp_norm {
  *   dwq, dwk  fp32 (D) out, nullable; must be NULL where the weight is.
  *             Their sums over tokens and heads are deterministic.
  * The backward's workspace, qk_norm_pack_bwd_workspace_bytes(T, Hq, Hk, D)
- * bytes, is used only when dwq or dwk is given.
+ * bytes, is used only when dwq or dwk is given. The size does not fall as T grows.
  * Supports D a multiple of 8 up to 512, rot a multiple of 16 (of 2 when
  * interleaved) up to D. Activation pointers must be multiples of 16 bytes.
  * A row of zeros with eps = 0 gives NaN, as the formula does.
@@ -435,6 +435,8 @@ int qk_norm_pack_bwd(const void *q, const void *k, const float *wq, const float 
  * Supports Dk a multiple of 8 up to 128, Dv a multiple of 8, Hv a multiple
  * of Hk. Pointers other than g, beta, cu_seqlens must be multiples of 16 bytes.
  * Buffers must not overlap.
+ * The sizes do not fall as T or nseq grow: memory made for the most tokens and
+ * sequences serves all smaller packs.
  * Errors: SSMP_ERR_SHAPE (also Hv > 65535, Hk * Dk or Hv * Dv > 2^20, nseq >
  * 2^24, T * Hv * max(Dk, Dv) >= 2^40, or more than 2^23 pairs of a chunk, or of
  * a sequence and 128 columns, with a value head), SSMP_ERR_UNSUPPORTED, SSMP_ERR_NULL, SSMP_ERR_ALIGN,

@@ -336,10 +336,22 @@ __host__ __device__ inline int64_t split_parts(const DeltaArgs& a) { return a.T 
 // A part's matrix in `joint`: DKP rows of B's columns (whole waves of them; the
 // state that enters, once it is known), then A's.
 __host__ __device__ inline int joint_b(int Dv) { return (Dv + 63) / 64 * 64; }
+// Room for the parts of every pack of up to T tokens and nseq sequences, so that
+// a scratch made for the largest pack serves the smaller ones: fewer tokens may
+// have more parts, and fewer sequences may be split where these are not. With
+// `per` chains a sequence, packs of n <= kSplitChains / per sequences of kSplitChunks
+// chunks or more are split, and they have at most T / (4 kC) + n parts. With
+// q = chunks n per / (kCUs / 2) a part has at least max(4, 4 q / 5) chunks, so that
+// there are at most (kCUs / 2) 5 / 4 (1 + 1 / kSplitChunks) / per + n parts as well.
+constexpr int kMaxParts = kCUs / 2 * 5 / 4 * (kSplitChunks + 1) / kSplitChunks;
 inline size_t joint_bytes(int64_t T, int32_t nseq, int32_t Hv, int dkp, int32_t Dv) {
-    const int split = split_chunks(T, nseq, Hv, Dv);
-    if (!split) return 0;
-    return round256((size_t)(T / ((int64_t)kC * split) + nseq) * Hv * dkp * (joint_b(Dv) + dkp) * sizeof(float));
+    const int64_t per = (int64_t)Hv * ((Dv + 63) / 64);
+    int64_t n = T / kC / kSplitChunks;
+    if (n > nseq) n = nseq;
+    if (n > kSplitChains / per) n = kSplitChains / per;
+    if (n < 1) return 0;
+    const int64_t parts = T / (4 * kC) < kMaxParts / per ? T / (4 * kC) : kMaxParts / per;
+    return round256((size_t)(parts + n) * Hv * dkp * (joint_b(Dv) + dkp) * sizeof(float));
 }
 
 inline unsigned chain_blocks(const DeltaArgs& a, int waves) {

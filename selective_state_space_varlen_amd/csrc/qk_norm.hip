@@ -318,6 +318,14 @@ inline int64_t norm_bwd_blocks(int64_t T, int hsplit) {
     const int64_t b = (T * hsplit + kNormWaves - 1) / kNormWaves;
     return b < kNormBwdBlocks ? b : kNormBwdBlocks;
 }
+// The most of them for any number of tokens up to T, so that a workspace made
+// for T serves fewer: T hsplit is at most T + 2047 below 2048 tokens, then T.
+inline int64_t norm_bwd_rows(int64_t T, int heads, int D) {
+    const int rpw = kWave / norm_lanes(D), full = (heads + rpw - 1) / rpw;
+    int64_t most = (T < 2047 ? T : 2047) + 2047;
+    if (most < T) most = T;
+    return norm_bwd_blocks(T * full < most ? T * full : most, 1);
+}
 
 template <typename T, int LPR>
 void launch_norm(const NormArgs& a, bool bwd, bool dw, int64_t blocks, hipStream_t s) {
@@ -407,7 +415,7 @@ extern "C" int qk_norm_pack_fwd(const void* q, const void* k, const float* wq, c
 extern "C" size_t qk_norm_pack_bwd_workspace_bytes(int64_t T, int32_t Hq, int32_t Hk, int32_t D) {
     using namespace ssmp;
     if (!norm_sizes_ok(T, Hq, Hk, D) || D > kNormMaxD || T == 0) return 0;
-    return (size_t)norm_bwd_blocks(T, norm_hsplit(T, Hq + Hk, D)) * 2 * D * sizeof(float);
+    return (size_t)norm_bwd_rows(T, Hq + Hk, D) * 2 * D * sizeof(float);
 }
 
 extern "C" int qk_norm_pack_bwd(const void* q, const void* k, const float* wq, const float* wk, const int32_t* pos,

@@ -1,0 +1,75 @@
+"""CPU: memory sized for the largest pack serves every smaller one: no size
+query falls as the tokens or the sequences grow. And what the parts of split
+sequences take, by the rule that splits them, lies inside the scratch."""
+from __future__ import annotations
+
+import random
+
+import pytest
+
+HEADS = [  # Hk, Hv, Dk, Dv
+    (4, 4, 128, 128), (1, 1, 8, 8), (1, 2, 64, 72), (2, 4, 40, 200), (1, 3, 128, 64), (8, 16, 128, 128), (1, 32, 64, 64),
+    (16, 32, 128, 128), (1, 1, 128, 2048),
+]
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from selective_state_space_varlen_amd import binding
+    return binding.load()
+
+
+def queries(lib, heads):
+    return {"saved": lambda T, n: lib.gated_delta_pack_saved_bytes(T, n, *heads),
+            "fwd": lambda T, n: lib.gated_delta_pack_fwd_scratch_bytes(T, n, *heads, 1),
+            "bwd": lambda T, n: lib.gated_delta_pack_bwd_scratch_bytes(T, n, *heads, 1)}
+
+
+@pytest.mark.parametrize("heads", HEADS)
+def test_rule_sizes_never_fall(lib, heads):
+    tokens = sorted(set(range(0, 40000, 61)) | {64 * i + j for i in range(28, 36) for j in (-1, 0, 1)}
+                    | {2048 * i for i in range(1, 40)} | {1 << 17, 1 << 18, 1 << 19})
+    for name, f in queries(lib, heads).items():
+        for n in (1, 2, 3, 4, 7, 8, 15, 16, 31, 32, 33, 100):
+            sizes = [f(T, n) for T in tokens]
+            assert sizes == sorted(sizes), (name, n)
+        for T in (1, 63, 2047, 2048, 4096, 4160, 8192, 16384, 16385, 33000, 65536, 1 << 18):
+            sizes = [f(T, n) for n in range(1, 130)]
+            assert sizes == sorted(sizes), (name, T)
+
+
+@pytest.mark.parametrize("heads", [(16, 16, 128), (1, 1, 64), (8, 0, 128), (1, 1, 8), (40, 8, 512), (3, 2, 72), (64, 64, 256)])
+def test_norm_sizes_never_fall(lib, heads):
+    sizes = [lib.qk_norm_pack_bwd_workspace_bytes(T, *heads) for T in list(range(0, 6000)) + [1 << 14, 1 << 20]]
+    assert sizes == sorted(sizes)
+
+
+def round256(n):
+    return -(-n // 256) * 256
+
+
+def split_chunks(T, n, Hv, Dv):
+    """Chunks of a part: what decides where few long sequences are split."""
+    chains, chunks = n * Hv * -(-Dv // 64), T // 64 // n
+    if chains > 32 or chunks < 32:
+        return 0
+    p = max(chunks * chains // 128, 4)
+    while 2 * p * p < chunks:
+        p += 1
+    return p
+
+
+@pytest.mark.parametrize("heads", HEADS)
+def test_parts_fit_the_scratch(lib, heads):
+    Hk, Hv, Dk, Dv = heads
+    rng, split = random.Random(5), 0
+    for _ in range(4000):
+        T, n = int(2 ** rng.uniform(10, 21)), rng.choice([1, 1, 2, 3, 5, 8, 16, 32])
+        p = split_chunks(T, n, Hv, Dv)
+        dkp = 64 if Dk <= 64 else 128
+        parts = (T // (64 * p) + n) * Hv * dkp * (-(-Dv // 64) * 64 + dkp) * 4 if p else 0
+        slots = (T // 64 + n) * Hv
+        rest = round256(slots * 1024) + 2 * round256(slots * 12288) + round256(n * 4)
+        assert lib.gated_delta_pack_fwd_scratch_bytes(T, n, *heads, 1) >= rest + parts, (T, n)
+        split += p > 0
+    assert split or Hv * -(-Dv // 64) > 32
