@@ -34,7 +34,7 @@ __device__ __forceinline__ float dpp_add(float v) {
 __device__ __forceinline__ float sum8(float v) { return dpp_add<0x141>(dpp_add<0x4E>(dpp_add<0xB1>(v))); }
 __device__ __forceinline__ float sum16(float v) { return dpp_add<0x140>(sum8(v)); }
 
-// A launch takes fewer than 2^32 threads: this many workgroups of 256 at most.
+// A launch takes fewer than 2^32 threads: fewer than this many workgroups of 256.
 constexpr int64_t kMaxBlocks = int64_t(1) << 24;
 
 // ---------------------------------------------------------------------------

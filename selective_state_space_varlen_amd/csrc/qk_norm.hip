@@ -355,7 +355,7 @@ void launch_norm_d(const NormArgs& a, bool bwd, bool dw, int64_t blocks, hipStre
 }
 
 inline bool norm_sizes_ok(int64_t T, int32_t Hq, int32_t Hk, int32_t D) {
-    return T >= 0 && T < kMaxBlocks * kNormWaves && Hq >= 0 && Hk >= 0 && Hq <= 65536 && Hk <= 65536 && Hq + Hk >= 1 &&
+    return T >= 0 && T <= (kMaxBlocks - 1) * kNormWaves && Hq >= 0 && Hk >= 0 && Hq <= 65536 && Hk <= 65536 && Hq + Hk >= 1 &&
            D >= 1 && T * ((int64_t)Hq + Hk) * D < (int64_t(1) << 40);
 }
 inline int norm_check(int64_t T, int32_t Hq, int32_t Hk, int32_t D, int32_t rot, int32_t dtype, int32_t norm,

@@ -3,6 +3,7 @@ query falls as the tokens or the sequences grow. And what the parts of split
 sequences take, by the rule that splits them, lies inside the scratch."""
 from __future__ import annotations
 
+import ctypes
 import random
 
 import pytest
@@ -42,6 +43,21 @@ def test_rule_sizes_never_fall(lib, heads):
 def test_norm_sizes_never_fall(lib, heads):
     sizes = [lib.qk_norm_pack_bwd_workspace_bytes(T, *heads) for T in list(range(0, 6000)) + [1 << 14, 1 << 20]]
     assert sizes == sorted(sizes)
+
+
+def test_the_most_tokens_of_a_norm(lib):
+    """Four tokens a workgroup of 256, and a launch takes fewer than 2^32 threads."""
+    fake, odd = ctypes.c_void_p(0x1000), ctypes.c_void_p(0x1008)  # never dereferenced: every call is refused
+
+    def forward(T):
+        return lib.qk_norm_pack_fwd(fake, fake, None, None, None, None, fake, odd, T, 1, 0, 8, 0, 1, 0, 1e-6, 0, None)
+
+    top = (1 << 26) - 4
+    assert forward(top) == 8  # past the sizes' check: an unaligned pointer is what is wrong with it
+    for T in (top + 1, top + 2, top + 3, 1 << 26):
+        assert forward(T) == 2, T
+        assert lib.qk_norm_pack_bwd_workspace_bytes(T, 1, 0, 8) == 0
+    assert lib.qk_norm_pack_bwd_workspace_bytes(top, 1, 0, 8) > 0
 
 
 def round256(n):
