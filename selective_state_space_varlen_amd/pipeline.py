@@ -97,10 +97,15 @@ def delta_forward(x: tuple, w: tuple, b: Optional[tuple], g: torch.Tensor, beta:
                   cu_seqlens: torch.Tensor, Hk: int, Hv: int, pos: Optional[torch.Tensor] = None,
                   scale: Optional[float] = None, norm: int = _b.SSMP_NORM_L2, eps: float = 1e-6,
                   norm_weights: tuple = (None, None), inv_freq: Optional[torch.Tensor] = None,
-                  initial_states: Optional[dict] = None, final_states: bool = False, save: bool = True) -> dict:
+                  initial_states: Optional[dict] = None, final_states: bool = False, save: bool = True,
+                  interleaved: bool = False) -> dict:
     """x = (xq (T, Hk * Dk), xk (T, Hk * Dk), xv (T, Hv * Dv)) with conv weights w
     and biases b (None, or a tuple) in the same order; g, beta fp32 (T, Hv).
     Returns {'out' (T, Hv, Dv), ...}; keep it for delta_backward (save=True).
+
+    norm, eps, norm_weights (of the query and the key heads, either None),
+    inv_freq and interleaved go to qk_norm_pack_fwd, with pos (default: the
+    positions inside the pack's sequences) where inv_freq turns the heads.
 
     Sequences continued from an earlier pack take initial_states = {'delta':
     (nseq, Hv, Dk, Dv) fp32, 'conv': three contexts (nseq, W-1, .)} (either may
@@ -127,7 +132,7 @@ def delta_forward(x: tuple, w: tuple, b: Optional[tuple], g: torch.Tensor, beta:
         u.append(y)
     q, k, v = (u[i].view(T, n, u[i].shape[1] // n) for i, n in enumerate((Hk, Hk, Hv)))
     nk = dict(wq=norm_weights[0], wk=norm_weights[1], pos=starts if pos is None else pos, inv_freq=inv_freq,
-              norm=norm, eps=eps)
+              norm=norm, eps=eps, interleaved=interleaved)
     qn, kn = _b.qk_norm_pack_fwd(q, k, **nk)
     out, saved, hT = _b.gated_delta_pack_fwd(qn, kn, v, g, beta, cu_seqlens, scale=scale,
                                              initial_state=st.get("delta"), final_state=carry, save=save)
