@@ -89,3 +89,61 @@ def test_parts_fit_the_scratch(lib, heads):
         assert lib.gated_delta_pack_fwd_scratch_bytes(T, n, *heads, 1) >= rest + parts, (T, n)
         split += p > 0
     assert split or Hv * -(-Dv // 64) > 32
+
+
+def find(cu, n, T, slot, size):
+    """The chunk (or part) in a slot, by the device's search: 64 boundaries at a
+    time, each clamped. None, or (first token, tokens, sequence, number)."""
+    clamp = lambda x: min(max(x, 0), T)  # noqa: E731
+    lo, hi = 0, n
+    while True:
+        step = -(-(hi - lo) // 64)
+        at = [lo + lane * step for lane in range(64)]
+        assert all(0 <= min(i, n) <= n for i in at)
+        a = [clamp(cu[min(i, n)]) for i in at]
+        k = max(sum(i < hi and x // size + i <= slot for i, x in zip(at, a)), 1)
+        if step > 1:
+            lo, hi = lo + (k - 1) * step, min(lo + k * step, hi)
+            continue
+        seq, first = lo + k - 1, a[k - 1]
+        assert 0 <= seq < n
+        end = a[k] if k < 64 else clamp(cu[seq + 1])
+        number = slot - (first // size + seq)
+        start = first + number * size
+        if number < 0 or start >= end:
+            return None
+        return start, min(size, end - start), seq, number
+
+
+def test_any_boundaries_lead_inside():
+    """Chunks, parts and walks of whole sequences, for any content of cu_seqlens."""
+    rng = random.Random(8)
+    for _ in range(300):
+        T, n, p = rng.choice([1, 63, 64, 65, 200, 4200]), rng.choice([1, 2, 3, 5, 70, 200]), rng.choice([4, 5, 9])
+        kind = rng.randrange(3)
+        if kind == 0:
+            cu = sorted(rng.randint(0, T) for _ in range(n + 1))
+        elif kind == 1:
+            cu = [rng.randint(-T, 3 * T) for _ in range(n + 1)]
+        else:
+            cu = [rng.choice([2 ** 31 - 1, -2 ** 31, 0, T]) for _ in range(n + 1)]
+        slots, parts = T // 64 + n, T // (64 * p) + n
+        seen = 0
+        for slot in range(slots):
+            c = find(cu, n, T, slot, 64)
+            if c:
+                assert 0 <= c[0] and c[0] + c[1] <= T and 0 < c[1] <= 64
+                seen += c[1]
+        if kind == 0:
+            assert seen == cu[-1] - cu[0]
+        for part in range(parts):
+            w = find(cu, n, T, part, 64 * p)
+            if w:
+                start, tokens, seq, number = w
+                slot0 = (start - number * 64 * p) // 64 + seq + number * p
+                assert 0 <= slot0 and slot0 + -(-tokens // 64) <= slots and start + tokens <= T
+        for s in range(n):  # a chain over a whole sequence, and the join of its parts
+            a = min(max(cu[s], 0), T)
+            b = max(a, min(max(cu[s + 1], 0), T))
+            assert a // 64 + s + -(-(b - a) // 64) <= slots
+            assert a // (64 * p) + s + -(-(b - a) // (64 * p)) <= parts
