@@ -148,8 +148,11 @@ def delta_backward(x: tuple, w: tuple, b: Optional[tuple], g: torch.Tensor, beta
     """Gradients of sum(dout * out) (+ sum(dfinal * final) for carried states):
     'dx', 'dw', 'db' (tuples in the order q, k, v; db None without biases),
     'dg', 'dbeta', 'dwq', 'dwk' (the norm weights'), and with carried states
-    'dinitial_states', to hand to the earlier pack's backward."""
+    'dinitial_states', to hand to the earlier pack's backward. dfinal_states
+    is refused where the forward gave no final states."""
     cu, carry, st, dfs = fwd["cu_seqlens"], fwd["carry"], fwd["initial_states"], dfinal_states or {}
+    if not carry and any(t is not None for t in dfs.values()):
+        raise ValueError("dfinal_states: the forward gave no final states (initial_states, or final_states=True)")
     G = _b.gated_delta_pack_bwd(fwd["qn"], fwd["kn"], g, beta, cu, dout, fwd["saved"], scale=fwd["scale"],
                                 dfinal_state=dfs.get("delta"), dinitial_state=carry)
     N = _b.qk_norm_pack_bwd(fwd["q"], fwd["k"], G["dq"], G["dk"], **fwd["norm"])
