@@ -17,6 +17,7 @@ the scan through SiLU (Mamba-1's block order).
 """
 from __future__ import annotations
 
+import functools
 from typing import Optional
 
 import torch
@@ -93,6 +94,16 @@ def backward(x: torch.Tensor, w: torch.Tensor, b: Optional[torch.Tensor], delta:
     return g
 
 
+def _on_its_device(f):
+    """f with the device of its first argument's first tensor current, as the convs' launches need it to be."""
+    @functools.wraps(f)
+    def on_device(x, *args, **kw):
+        with torch.cuda.device_of(x[0]):
+            return f(x, *args, **kw)
+    return on_device
+
+
+@_on_its_device
 def delta_forward(x: tuple, w: tuple, b: Optional[tuple], g: torch.Tensor, beta: torch.Tensor,
                   cu_seqlens: torch.Tensor, Hk: int, Hv: int, pos: Optional[torch.Tensor] = None,
                   scale: Optional[float] = None, norm: int = _b.SSMP_NORM_L2, eps: float = 1e-6,
@@ -143,6 +154,7 @@ def delta_forward(x: tuple, w: tuple, b: Optional[tuple], g: torch.Tensor, beta:
     return res
 
 
+@_on_its_device
 def delta_backward(x: tuple, w: tuple, b: Optional[tuple], g: torch.Tensor, beta: torch.Tensor, fwd: dict,
                    dout: torch.Tensor, dfinal_states: Optional[dict] = None) -> dict:
     """Gradients of sum(dout * out) (+ sum(dfinal * final) for carried states):
