@@ -105,8 +105,10 @@ __device__ __forceinline__ NormAt norm_at(const NormArgs& a, int64_t t, int h, i
 
 // The turn of a lane's components at one position: y_e = x_e c_e + p_e s_e with
 // p_e the other member of e's pair and the sign in s_e. The angle in turns is
-// formed in 64 bits (a 32-bit one is off by radians at positions near 1e7)
-// and reduced to half a turn either way before it is rounded to 32. The wave's
+// formed in 64 bits (a 32-bit one is off by radians at positions near 1e7) and
+// reduced to half a turn either way; what its rounding to 32 leaves out, up to
+// 2^-25 of a half turn, turns the result once more to first order, so that small
+// cosines and sines have all their bits. The wave's
 // lanes form one angle each (rot / 2 of them in all) and pass them on through
 // LDS: formed where they are used, they would take longer than the heads do
 // (16384 tokens of 40 heads of 128, half turned: 118 us against 87).
@@ -120,9 +122,11 @@ __device__ __forceinline__ void make_turn(Turn& t, const NormArgs& a, int32_t po
     wave_sync();  // the last token's have been read
     for (int i = lane; i < half; i += kWave) {
         const double turns = (double)pos * (double)a.inv_freq[i] * 0.15915494309189533577;
+        const double halves = 2.0 * (turns - rint(turns));
+        const float main = (float)halves, rest = (float)((halves - (double)main) * 3.14159265358979323846);
         float sn, co;
-        sincospif((float)(2.0 * (turns - rint(turns))), &sn, &co);
-        cs[i] = make_float2(co, sn);
+        sincospif(main, &sn, &co);
+        cs[i] = make_float2(fmaf(-sn, rest, co), fmaf(co, rest, sn));
     }
     wave_sync();
     t.on = col < a.rot;
