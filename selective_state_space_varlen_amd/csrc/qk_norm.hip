@@ -115,7 +115,7 @@ __device__ __forceinline__ NormAt norm_at(const NormArgs& a, int64_t t, int h, i
 struct Turn {
     float c[kNormVec], s[kNormVec];
     int partner;  // lane that holds the other members (half-split pairs)
-    bool on;      // this lane holds turned components
+    int n;        // how many of this lane's components are turned (in adjacent pairs perhaps not all)
 };
 __device__ __forceinline__ void make_turn(Turn& t, const NormArgs& a, int32_t pos, int lane, int col, float2* cs) {
     const int half = a.rot >> 1;
@@ -129,9 +129,9 @@ __device__ __forceinline__ void make_turn(Turn& t, const NormArgs& a, int32_t po
         cs[i] = make_float2(fmaf(-sn, rest, co), fmaf(co, rest, sn));
     }
     wave_sync();
-    t.on = col < a.rot;
+    t.n = a.rot - col;
     t.partner = lane;
-    if (!a.interleaved && t.on) t.partner = col < half ? lane + half / kNormVec : lane - half / kNormVec;
+    if (!a.interleaved && t.n > 0) t.partner = col < half ? lane + half / kNormVec : lane - half / kNormVec;
 #pragma unroll
     for (int e = 0; e < kNormVec; ++e) {
         const int d = col + e;
@@ -155,7 +155,7 @@ __device__ __forceinline__ void apply_turn(const Turn& t, int interleaved, float
 #pragma unroll
     for (int e = 0; e < kNormVec; ++e) {
         const float turned = BACK ? fmaf(-p[e], t.s[e], v[e] * t.c[e]) : fmaf(p[e], t.s[e], v[e] * t.c[e]);
-        v[e] = t.on ? turned : v[e];
+        v[e] = e < t.n ? turned : v[e];
     }
 }
 
