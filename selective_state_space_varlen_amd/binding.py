@@ -130,12 +130,16 @@ def _stream(t: torch.Tensor):
     return ctypes.c_void_p(torch.cuda.current_stream(t.device).cuda_stream)
 
 
-def _dtype_code(t: torch.Tensor) -> int:
-    if t.dtype == torch.bfloat16:
+def _code_of(dtype: torch.dtype) -> int:
+    if dtype == torch.bfloat16:
         return SSMP_BF16
-    if t.dtype == torch.float32:
+    if dtype == torch.float32:
         return SSMP_F32
-    raise TypeError(f"unsupported dtype {t.dtype} (bfloat16 or float32)")
+    raise TypeError(f"unsupported dtype {dtype} (bfloat16 or float32)")
+
+
+def _dtype_code(t: torch.Tensor) -> int:
+    return _code_of(t.dtype)
 
 
 def _check(t: Optional[torch.Tensor], name: str, shape=None, dtype=None, device=None):
@@ -702,14 +706,12 @@ def gated_delta_pack_saved_bytes(T: int, nseq: int, Hk: int, Hv: int, Dk: int, D
 
 def gated_delta_pack_fwd_scratch_bytes(T: int, nseq: int, Hk: int, Hv: int, Dk: int, Dv: int,
                                        dtype: torch.dtype) -> int:
-    code = SSMP_BF16 if dtype == torch.bfloat16 else SSMP_F32
-    return int(load().gated_delta_pack_fwd_scratch_bytes(T, nseq, Hk, Hv, Dk, Dv, code))
+    return int(load().gated_delta_pack_fwd_scratch_bytes(T, nseq, Hk, Hv, Dk, Dv, _code_of(dtype)))
 
 
 def gated_delta_pack_bwd_scratch_bytes(T: int, nseq: int, Hk: int, Hv: int, Dk: int, Dv: int,
                                        dtype: torch.dtype) -> int:
-    code = SSMP_BF16 if dtype == torch.bfloat16 else SSMP_F32
-    return int(load().gated_delta_pack_bwd_scratch_bytes(T, nseq, Hk, Hv, Dk, Dv, code))
+    return int(load().gated_delta_pack_bwd_scratch_bytes(T, nseq, Hk, Hv, Dk, Dv, _code_of(dtype)))
 
 
 def gated_delta_pack_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor,

@@ -60,6 +60,16 @@ def test_the_most_tokens_of_a_norm(lib):
     assert lib.qk_norm_pack_bwd_workspace_bytes(top, 1, 0, 8) > 0
 
 
+def test_sizes_of_an_unsupported_type_are_refused():
+    import torch
+    import selective_state_space_varlen_amd as m
+    for f in (m.gated_delta_pack_fwd_scratch_bytes, m.gated_delta_pack_bwd_scratch_bytes):
+        assert f(100, 1, 1, 1, 64, 64, torch.bfloat16) > 0 and f(100, 1, 1, 1, 64, 64, torch.float32) > 0
+        for dtype in (torch.float16, torch.float64):
+            with pytest.raises(TypeError, match="unsupported dtype"):
+                f(100, 1, 1, 1, 64, 64, dtype)
+
+
 def round256(n):
     return -(-n // 256) * 256
 
