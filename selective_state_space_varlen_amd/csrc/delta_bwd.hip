@@ -25,8 +25,8 @@
 
 namespace ssmp {
 
-// As k_delta_chain, from the last chunk to the first, with the same bound: 730
-// us for 32768 tokens x 32 heads of 128 x 128 in bf16.
+// As k_delta_chain, from the last chunk to the first, with the same bound: 635
+// to 655 us for 32768 tokens x 32 heads of 128 x 128 in bf16.
 // SUM: the first walk over the parts of split sequences.
 template <typename T, int DKP, int NW, bool SUM>
 __global__ __launch_bounds__(NW * 64) void k_delta_chain_bwd(DeltaArgs a) {
@@ -188,9 +188,9 @@ __global__ __launch_bounds__(NW * 64) void k_delta_chain_bwd(DeltaArgs a) {
 // dOut, dE, U, S and dS' 32 columns at a time, the next ones (of the next head
 // too) under way in registers meanwhile. Two workgroups share a CU and fill
 // each other's waits at barriers: one of eight waves with all columns of a
-// head, which stages each chunk once instead of twice, takes 1660 us where
-// these take 1415 to 1480 (32768 tokens, 32 heads of 128 x 128 on 16 key heads).
-// That is 4.5 GB of memory's traffic at 3.1 TB/s, 60 % of what a copy reaches,
+// head, which stages each chunk once instead of twice, took 1660 us where these
+// took 1415 (32768 tokens, 32 heads of 128 x 128 on 16 key heads; 1390 now).
+// That is 4.5 GB of memory's traffic at 3.2 TB/s, 60 % of what a copy reaches,
 // beside the matrix instructions and the splitting, which a workgroup cannot
 // put wholly in the other's waits.
 // The rows of q.dq + k.dkread over these columns go to a.rows, with what the

@@ -111,9 +111,10 @@ __device__ __forceinline__ bool chunk_at(const int32_t* __restrict__ cu, int32_t
 // Matrix products. States, the chunk's inverse and every value derived from
 // them are fp32; v_mfma_f32_16x16x32_bf16 multiplies bf16. An fp32 operand is
 // split into bf16 planes x = x0 + x1 + x2 (8 bits each, together fp32's 24),
-// and a product adds the plane products down to the bits that count: with
-// three planes a side 6 of 9 (error 2^-24 relative to the factors), with one
-// side exactly bf16 3. That is 2.7 to 5.3 times the rate of the fp32 matrix
+// and a product adds the plane products down to the bits that count: with one
+// side exactly bf16 all 3; with three planes a side 6 of 9, which leaves out
+// 2^-24 of the product in the root mean square and 2^-21.1 at most (the planes
+// are cut off, so it is left out with the product's sign: 2^-24.6 on average). That is 2.7 to 5.3 times the rate of the fp32 matrix
 // instruction, whose rate is a sixteenth of bf16's.
 //
 // Operands: lane l of A holds row l % 16, elements k = 8 (l / 16) .. + 7; of B

@@ -24,9 +24,10 @@ namespace ssmp {
 // Bound by what a SIMD can issue: a wave's chunk (heads of 128, bf16) is 216
 // matrix instructions of 16 cycles, and the rest of its 10000 cycles in
 // splitting fp32 values into planes, reading LDS, storing, and the latency of
-// each upon the last. One prompt of 513 tokens x 32 heads takes 43 us, 4.3 a
-// chunk (6.1 with every CU at work, when the clock is lower, and 8.2 keeping S
-// and E); 32768 tokens x 32 heads 490 to 550 us, 710 keeping.
+// each upon the last. One prompt of 513 tokens x 32 heads takes 46 us; a long
+// chain 4.4 a chunk, 4.7 keeping S and E (with every CU at work, eight waves on
+// each and the clock lower, 7.4 and 10.5); 32768 tokens x 32 heads 480 to 500 us,
+// 670 to 690 keeping.
 enum ChainMode { kPlain, kKeep, kSum };
 template <typename T, int DKP, int NW, ChainMode MODE>
 __global__ __launch_bounds__(NW * 64) void k_delta_chain(DeltaArgs a) {

@@ -42,8 +42,8 @@ __device__ __forceinline__ void order_sequences(const DeltaArgs& a, int* h) {
 //   forward:  (I + L diag(beta))^-1 and P,           both lower triangular
 //   backward: (I + diag(beta) L)^-T and scale P^T,   both upper triangular
 // The inverse is one dependent sequence of small products, which four
-// workgroups a CU hide from each other: 198 us forward, 216 us backward for
-// 32768 tokens x 32 heads of 128 in bf16, 0.76 GB at 3.8 TB/s.
+// workgroups a CU hide from each other: 175 us forward, 183 us backward for
+// 32768 tokens x 32 heads of 128 in bf16, 0.76 GB at 4.2 TB/s.
 template <typename T, int DKP, bool BWD>
 __global__ __launch_bounds__(256, kExact<T> == 1 ? 4 : 1) void k_delta_prepare(DeltaArgs a) {
     constexpr int NX = kExact<T>;
@@ -276,10 +276,10 @@ struct ChainLoads {
 
 // Sets of a chain's operands in LDS: two where they fit and cost no workgroup
 // beside it, so that the next chunk's are put while this one's are read and a
-// chunk has one barrier. Against one set, at heads of 128 in bf16: 710 us
-// against 740 (keeping, 8 waves, 32768 tokens x 32 heads), 733 against 750
-// backward; 411 against 435 backward with 4 waves (16384 tokens x 12 heads).
-// What a start costs more: 43 us against 41 at 513 tokens.
+// chunk has one barrier. Against one set, keeping / backward, heads of 128 in
+// bf16 (us): 8 waves, 16 sequences of 2048 tokens x 32 heads, 670 / 634 against
+// 789 / 698; 4 waves, 6 sequences of 2731 x 12, 275 / 258 against 274 / 271;
+// one of 513 tokens x 32 heads 49 / 46 against 49 / 48.
 template <typename Tiles, int DKP, int NW>
 constexpr int kSets = 2 * sizeof(Tiles) <= 160 * 1024 && (DKP > 64 || NW == 8) ? 2 : 1;
 
@@ -287,11 +287,12 @@ constexpr int kSets = 2 * sizeof(Tiles) <= 160 * 1024 && (DKP > 64 || NW == 8) ?
 // once for a whole head and give each SIMD two waves, one of which works while
 // the other waits; while every workgroup of four finds a CU of its own, each
 // chunk of a chain ends sooner there. Keeping forward / backward in bf16, heads
-// of 128 (us, 32768 tokens): 128 chains 651 / 618 with eight and 525 / 507 with
-// four; 192 chains (24576 tokens) 378 / 354 and 477 / 461; 512 chains 764 / 738
-// and 1012 / 974. fp32 keys over 64 keep four: eight waves have half the
-// registers each and spill (512 chains of 512 tokens, 685 / 613 against 486 /
-// 508; keys of 64 fit, 214 / 237 against 306 / 321).
+// of 128 (us, 32768 tokens): 128 chains 654 / 587 with eight and 521 / 470 with
+// four; 192 chains (24576 tokens) 334 / 299 and 439 / 405; 512 chains 670 / 634
+// and 950 / 860. fp32 keys over 64 keep four: eight waves have half the registers
+// each, and 104 to 177 of them spill (512 chains of 512 tokens, 663 / 587 against
+// 427 / 441). With keys of 64, 4 to 13 spill, which costs less than four waves do
+// (199 / 219 against 278 / 279).
 constexpr int kCUs = 256;
 template <typename T, int DKP>
 constexpr bool kWide = kExact<T> == 1 || DKP <= 64;
@@ -303,8 +304,8 @@ int chain_waves(const DeltaArgs& a) {
     return kWide<T, DKP> && a.Dv > 4 * kWaveCols && chain_groups(a, 4) > kCUs ? 8 : 4;
 }
 // Whether the chains are started by length: where they are more than the CUs
-// take at once (31 sequences of 64 to 2048 tokens x 32 heads: 720 us against
-// 820 keeping, 751 against 847 backward).
+// take at once (31 sequences of 64 to 2048 tokens x 32 heads: 674 us against
+// 789 keeping, 650 against 750 backward).
 inline bool chain_ordered(const DeltaArgs& a, int waves) {
     return a.nseq > 1 && a.nseq <= kOrderMax && chain_groups(a, waves) > kCUs;
 }
@@ -317,12 +318,22 @@ inline bool chain_ordered(const DeltaArgs& a, int waves) {
 // That is (Dv + Dk) / Dv and 1 times the steps of the plain walk, so it takes
 // few chains and long ones. A part has at least the square root of half the
 // chunks (the walks take 2 parts' time, the join 5.5 us for each part), and
-// there are no more parts than CUs take at once. Forward / backward of one
-// sequence, heads of 128 x 128 in bf16 (us): 16384 tokens x 4 heads (8 chains)
-// 1017 / 1231 whole and 236 / 267 split; x 16 heads (32) 1062 / 1379 and 585 /
-// 721; x 32 heads (64) 1178 / 1355 and 1092 / 1320; 2048 tokens x 4 heads (32
-// chunks) 129 / 154 and 88 / 96; 1024 tokens 69 / 78 and 63 / 71, where two
-// more launches take what is gained.
+// there are no more parts than CUs take at once. Forward / keeping / backward of
+// one sequence, heads of 128 x 128 in bf16 (us):
+//   tokens x heads (chains)   whole                 split
+//   16384 x  4 (8)            1133 / 1202 / 1201     234 /  243 /  257
+//   16384 x 16 (32)           1228 / 1423 / 1285     587 /  666 /  679
+//   16384 x 24 (48)           1248 / 1435 / 1314     855 /  972 /  998
+//   16384 x 32 (64)           1251 / 1472 / 1347    1126 / 1292 / 1294
+//   16384 x 48 (96)           1261 / 1581 / 1407    1693 / 1945 / 1408
+//    4096 x 16 (32)            292 /  310 /  306     166 /  177 /  192
+//    4096 x 24 (48)            291 /  313 /  310     224 /  237 /  260
+//    4096 x 32 (64)            287 /  323 /  316     280 /  305 /  331
+//    2048 x  4 (8, 32 chunks)  145 /  155 /  149      89 /   93 /   94
+//    1024 x  4 (8, 16 chunks)   75 /   81 /   77      64 /   66 /   69
+// The two sides meet at 64 chains; the bound stands below that, and leaves whole
+// what has 33 to 63 of them, which the split would take a quarter from. At 16
+// chunks two more launches take most of what is gained.
 constexpr int kSplitChains = 32, kSplitChunks = 32;
 inline int split_chunks(int64_t T, int32_t nseq, int32_t Hv, int32_t Dv) {
     const int64_t chains = (int64_t)nseq * Hv * ((Dv + 63) / 64), chunks = T / kC / nseq;

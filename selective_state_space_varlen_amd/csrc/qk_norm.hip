@@ -10,8 +10,10 @@
 // Bound by HBM: each row is read and written once. A row lies across 1 to 64
 // lanes, 8 components in each, so that a wave reads 1 KiB (bf16) at a time;
 // a wave takes the heads of one token together, which turn by the same
-// angles, and forms its lanes' cosines and sines once. 32768 tokens of 32 heads
-// of 128 in bf16: 97 us forward and 155 us backward, 5.5 and 5.2 TB/s.
+// angles, and forms its lanes' cosines and sines once. In bf16, heads of 128:
+// 32768 tokens of 32 heads 94 us forward and 157 us backward, 5.7 and 5.1 TB/s;
+// 16384 tokens of 40, with weights and half turned, 85 us forward (3.9 TB/s) and
+// 105 + 7 us backward (4.5 TB/s), the angles in 64 bits on top.
 #include "delta_common.h"
 
 namespace ssmp {
