@@ -13,7 +13,7 @@
 // angles, and forms its lanes' cosines and sines once. In bf16, heads of 128:
 // 32768 tokens of 32 heads 94 us forward and 157 us backward, 5.7 and 5.1 TB/s;
 // 16384 tokens of 40, with weights and half turned, 85 us forward (3.9 TB/s) and
-// 105 + 7 us backward (4.5 TB/s), the angles in 64 bits on top.
+// 111 + 7 us backward (4.3 TB/s), the angles in 64 bits on top.
 #include "delta_common.h"
 
 namespace ssmp {
@@ -206,11 +206,17 @@ __global__ __launch_bounds__(kNormWaves* kWave) void k_qk_norm_fwd(NormArgs a) {
 }
 
 // As the forward; a wave goes over tokens with a fixed stride and keeps its
-// lanes' weight sums in registers, which the workgroup adds in a fixed order.
+// lanes' weight sums in registers, which the workgroup adds in a fixed order. A
+// lane may have thousands of rows, so the sums of kNormRun tokens go to sums of 64
+// bits in LDS. 16384 tokens of 40 turned heads of 128 in bf16 take 111 us so, 105
+// with sums of 32 bits alone, and 141 with those of 64 in registers, which leave
+// a SIMD three waves instead of four.
+constexpr int kNormRun = 8;
 template <typename T, int LPR, bool ROT, bool DW>
 __global__ __launch_bounds__(kNormWaves* kWave) void k_qk_norm_bwd(NormArgs a) {
     constexpr int RPW = kWave / LPR;
     __shared__ float2 cs[ROT ? kNormWaves : 1][ROT ? kNormMaxD / 2 : 1];
+    __shared__ double sums[DW ? kNormWaves : 1][2][DW ? LPR * kNormVec : 1];
     const int lane = lane_id(), wave = threadIdx.x >> 6;
     const int col = (lane & (LPR - 1)) * kNormVec;
     const bool in = col < a.D;
@@ -222,7 +228,21 @@ __global__ __launch_bounds__(kNormWaves* kWave) void k_qk_norm_bwd(NormArgs a) {
         for (int e = 0; e < kNormVec; ++e) {
             w[n][e] = a.w[n] && in ? a.w[n][col + e] : 1.0f;
             dw[n][e] = 0.0f;
+            if (DW && lane < LPR) sums[wave][n][col + e] = 0.0;
         }
+    const auto put_sums = [&] {  // each lane to places of its own
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int e = 0; e < kNormVec; ++e) {
+                float s = dw[n][e];
+#pragma unroll
+                for (int m = LPR; m < kWave; m <<= 1) s += __shfl_xor(s, m);
+                if (lane < LPR) sums[wave][n][col + e] += (double)s;
+                dw[n][e] = 0.0f;
+            }
+    };
+    int run = 0;
     const int64_t tasks = a.T * a.hsplit;
     for (int64_t task = (int64_t)blockIdx.x * kNormWaves + wave; task < tasks; task += (int64_t)gridDim.x * kNormWaves) {
         const int64_t t = task / a.hsplit;
@@ -269,25 +289,21 @@ __global__ __launch_bounds__(kNormWaves* kWave) void k_qk_norm_bwd(NormArgs a) {
             xr = xn;
             gr = gn;
         }
+        if constexpr (DW)
+            if (++run == kNormRun) {
+                put_sums();
+                run = 0;
+            }
     }
     if constexpr (DW) {
-        __shared__ float sums[kNormWaves][2][LPR * kNormVec];
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-            for (int e = 0; e < kNormVec; ++e) {
-                float s = dw[n][e];
-#pragma unroll
-                for (int m = LPR; m < kWave; m <<= 1) s += __shfl_xor(s, m);
-                if (lane < LPR) sums[wave][n][col + e] = s;
-            }
+        put_sums();
         __syncthreads();
         for (int i = threadIdx.x; i < 2 * a.D; i += blockDim.x) {
             const int n = i / a.D, d = i % a.D;
-            float s = 0.0f;
+            double s = 0.0;
 #pragma unroll
             for (int q = 0; q < kNormWaves; ++q) s += sums[q][n][d];
-            a.part[(size_t)blockIdx.x * 2 * a.D + i] = s;
+            a.part[(size_t)blockIdx.x * 2 * a.D + i] = (float)s;
         }
     }
 }
