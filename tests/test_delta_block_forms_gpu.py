@@ -144,3 +144,37 @@ def test_turned_block_in_two_packs(inter):
     b = block(slice(cut, n), a["final_states"], torch.arange(cut, n, dtype=torch.int32, device="cuda"))
     torch.cuda.synchronize()
     dc.check(torch.cat([a["out"], b["out"]]), whole["out"].cpu(), 8 * dc.tol32(n, DK + W), "out")
+
+
+def test_block_captured_and_replayed():
+    """Forward and backward in one graph, over other values and another division of the rows."""
+    d = inputs(BF, True, True, (True, True), True)
+    inv = torch.tensor([1.0, 0.3, 0.05, 0.01, 0.9, 0.2, 0.002, 0.5]).cuda()
+    m, cu = ssp(), dc.cu_of(LENS).cuda()
+    x = tree(d, lambda t: t.cuda())
+
+    def once():
+        F = m.delta_forward(x["x"], x["w"], x["b"], x["g"], x["beta"], cu, HK, HV, norm_weights=x["nw"], inv_freq=inv,
+                            interleaved=True, initial_states=x["states"])
+        G = m.delta_backward(x["x"], x["w"], x["b"], x["g"], x["beta"], F, x["dout"], dfinal_states=x["dstates"])
+        return leaves({"out": F["out"], "states": F["final_states"], "G": G})
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        once()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = once()
+    for lens in ([70, 1, 0, 33], [5, 64, 35, 0], [0, 0, 0, 104], [70, 1, 0, 33]):
+        cu.copy_(dc.cu_of(lens))
+        x["x"][0].mul_(-0.5)
+        graph.replay()
+        torch.cuda.synchronize()
+        mine = [t.clone() for t in got]
+        want = once()
+        torch.cuda.synchronize()
+        for a, b in zip(mine, want, strict=True):
+            assert torch.equal(a, b)
