@@ -389,7 +389,9 @@ enum ssmp_norm {
  * bytes, is used only when dwq or dwk is given. The size does not fall as T grows.
  * Supports D a multiple of 8 up to 512, rot a multiple of 16 (of 2 when
  * interleaved) up to D. Activation pointers must be multiples of 16 bytes.
- * A row of zeros with eps = 0 gives NaN, as the formula does.
+ * A row of zeros with eps = 0 gives NaN, as the formula does. Squares are added
+ * in 32 bits: a row whose sum passes their range (components near 1e19) gives
+ * zeros.
  * Errors: SSMP_ERR_SHAPE (also T > 2^26 - 4, more than 65536 heads, 2^40 elements
  * or more), SSMP_ERR_UNSUPPORTED, SSMP_ERR_NULL, SSMP_ERR_ALIGN,
  * SSMP_ERR_WORKSPACE.
