@@ -41,3 +41,14 @@ def test_infinite_components_that_are_not_turned(D, rot, inter, dtype):
     keep = torch.arange(D) != bad
     assert torch.equal(got["dwq"].cpu()[keep], clean["dwq"].cpu()[keep])
     assert not bool(got["dwq"].cpu()[bad].isfinite())
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_squares_out_of_range(dtype):
+    """Components of 2e19, whose squares pass 32 bits' range: zeros, in that row alone."""
+    x = torch.ones(4, 2, 64, dtype=dtype)
+    x[2, 1] = 2e19
+    y = ssp().qk_norm_pack_fwd(x.cuda(), x[:, :0].cuda(), eps=0.0)[0].cpu()
+    assert not bool(y[2, 1].any())
+    y[2, 1] = 0.125
+    assert bool((y == 0.125).all())  # 1 / sqrt 64
