@@ -61,9 +61,10 @@ const char *ssmp_status_string(int status);
  * or their meaning; 2 added the _ex scan entry points, 3 the host packer
  * varlen_pack_plan, 4 the scan and conv entry points with sequence states,
  * 5 the scan entry points with a checkpoint interval, 6 the forward scan
- * without allocation). qk_norm_pack_* and gated_delta_pack_* were added
- * beside version 6: they change nothing in it, and a caller that may meet a
- * library without them looks their symbols up. */
+ * without allocation). qk_norm_pack_*, gated_delta_pack_*, decay_attn_pack_*,
+ * layer_norm_pack_* and dropout_pack_* were added beside version 6: they change
+ * nothing in it, and a caller that may meet a library without them looks their
+ * symbols up. */
 int ssmp_abi_version(void);
 
 /*
@@ -500,6 +501,156 @@ int gated_delta_pack_step(const void *q, const void *k, const void *v, const flo
                           float *state, const int32_t *slots, void *out, int32_t B, int32_t nslots,
                           int32_t Hk, int32_t Hv, int32_t Dk, int32_t Dv, int32_t dtype, float scale,
                           void *stream);
+
+/*
+ * decay_attn_pack_fwd — linear attention with a decay for each head over
+ * packed sequences, the state reset (or taken from initial_state) at the start
+ * of each. Per value head h with key head h / (Hv / Hk), a_t = exp(g_t):
+ *   S_t = a_t S_{t-1} + k_t v_t^T          (S: Dk x Dv)
+ *   out_t = scale * S_t^T q_t
+ *   q, k     (T, Hk, Dk) dtype; as given (no norm is applied here)
+ *   v, out   (T, Hv, Dv) dtype
+ *   g        fp32, the log of the decay (-infinity: a reset): (T, Hv) with
+ *            per_token nonzero, (Hv), one decay for a head, otherwise. Meant to
+ *            be at most 0; a chunk's sum above 88 gives infinities.
+ *   cu_seqlens  device int32 [nseq+1]: non-decreasing, cu[0] = 0; cu[nseq] may
+ *            be less than T, and tokens from it on are neither read nor
+ *            written. Any other content gives meaningless values, but no
+ *            access outside the buffers.
+ *   initial_state  fp32 (nseq, Hv, Dk, Dv), nullable (zero)
+ *   final_state    fp32 (nseq, Hv, Dk, Dv) out, nullable
+ *   scratch  used during the call only,
+ *            decay_attn_pack_fwd_scratch_bytes(T, nseq, Hk, Hv, Dk, Dv) bytes
+ *            (states between segments of long sequences)
+ * States, and everything between the tensors, are fp32 whatever the dtype; a
+ * bf16 result is rounded once, at the end. Results are deterministic. Within a
+ * sequence, a NaN or an infinity of a token may reach outputs up to 63 tokens
+ * before it (they share a chunk); other sequences are not touched.
+ * Supports Dk a multiple of 8 up to 128, Dv a multiple of 8, Hv a multiple
+ * of Hk. Pointers other than g and cu_seqlens must be multiples of 16 bytes.
+ * Buffers must not overlap. The sizes do not fall as T or nseq grow: memory
+ * made for the most tokens and sequences serves all smaller packs.
+ * Errors: SSMP_ERR_SHAPE (also Hv > 65535, Hk * Dk, Hv * Dv or Hv * Dk *
+ * ceil(Dv / 128) > 2^20, nseq > 2^24, T * Hv * max(Dk, Dv) >= 2^40, or more
+ * than 2^23 pairs of a chunk of 64 tokens, or of a sequence and 128 columns,
+ * with a value head), SSMP_ERR_UNSUPPORTED, SSMP_ERR_NULL, SSMP_ERR_ALIGN,
+ * SSMP_ERR_WORKSPACE. The size queries return 0 for arguments out of range.
+ */
+size_t decay_attn_pack_fwd_scratch_bytes(int64_t T, int32_t nseq, int32_t Hk, int32_t Hv, int32_t Dk, int32_t Dv);
+int decay_attn_pack_fwd(const void *q, const void *k, const void *v, const float *g,
+                        const int32_t *cu_seqlens, int32_t nseq, void *out, int64_t T, int32_t Hk,
+                        int32_t Hv, int32_t Dk, int32_t Dv, int32_t dtype, int32_t per_token, float scale,
+                        const float *initial_state, float *final_state, void *scratch,
+                        size_t scratch_bytes, void *stream);
+
+/*
+ * decay_attn_pack_bwd — gradients of decay_attn_pack_fwd given dout. Nothing
+ * is kept from the forward: the inputs are the forward's.
+ *   dfinal_state    fp32 (nseq, Hv, Dk, Dv), nullable (zero)
+ *   dinitial_state  fp32 (nseq, Hv, Dk, Dv) out, nullable
+ *   dq, dk (T, Hk, Dk) dtype out, summed over the value heads of a key head;
+ *   dv (T, Hv, Dv) dtype out; dg fp32 out, nullable, of g's shape (with one
+ *   decay for a head, summed over the tokens). dg is the difference of what
+ *   reads and what writes a state (q.dq and k.dk), added up over up to 256
+ *   tokens, and errs by 32-bit roundings of those.
+ *   scratch  decay_attn_pack_bwd_scratch_bytes(T, nseq, Hk, Hv, Dk, Dv)
+ * Within a sequence, a NaN or an infinity of a token may reach gradients of up
+ * to 63 tokens on its other side (they share a chunk), and those of g up to 255
+ * tokens behind it. Other arguments, conditions and errors as decay_attn_pack_fwd.
+ */
+size_t decay_attn_pack_bwd_scratch_bytes(int64_t T, int32_t nseq, int32_t Hk, int32_t Hv, int32_t Dk, int32_t Dv);
+int decay_attn_pack_bwd(const void *q, const void *k, const void *v, const float *g,
+                        const int32_t *cu_seqlens, int32_t nseq, const void *dout, int64_t T, int32_t Hk,
+                        int32_t Hv, int32_t Dk, int32_t Dv, int32_t dtype, int32_t per_token, float scale,
+                        const float *initial_state, const float *dfinal_state, float *dinitial_state,
+                        void *dq, void *dk, void *dv, float *dg, void *scratch, size_t scratch_bytes,
+                        void *stream);
+
+/*
+ * decay_attn_pack_step — one new token for each of B rows of a serving batch,
+ * on states in a pool, updated in place (a workspace-free form of
+ * decay_attn_pack_fwd for sequences of one token).
+ *   q, k (B, Hk, Dk), v, out (B, Hv, Dv) dtype; g fp32 (B, Hv), or (Hv)
+ *   without per_token
+ *   state  fp32 (nslots, Hv, Dk, Dv), read and written: the states of the
+ *          slots that are named, no others
+ *   slots  device int32 [B], nullable (row b uses slot b): the state of each
+ *          row. Rows that name the same slot are applied in their order. A row
+ *          whose slot is outside [0, nslots) is skipped: its out is left as
+ *          it was.
+ * Supports Dk a multiple of 8 up to 128, Dv a multiple of 8. Buffers must not
+ * overlap. Allocates and needs nothing. Errors: SSMP_ERR_SHAPE (also B > nslots
+ * without slots, Hv or Dv > 65536, B * Hv * ceil(Dv / 32) >= 2^24),
+ * SSMP_ERR_UNSUPPORTED, SSMP_ERR_NULL, SSMP_ERR_ALIGN.
+ */
+int decay_attn_pack_step(const void *q, const void *k, const void *v, const float *g, float *state,
+                         const int32_t *slots, void *out, int32_t B, int32_t nslots, int32_t Hk,
+                         int32_t Hv, int32_t Dk, int32_t Dv, int32_t dtype, int32_t per_token, float scale,
+                         void *stream);
+
+/*
+ * layer_norm_pack_fwd / layer_norm_pack_bwd — the layer norm of rows, or of
+ * the heads of packed tokens, with the residual sum and dropout that precede
+ * it in the same pass. Over the D components of each row,
+ *   h = residual + drop(x);  y = (h - mean(h)) (var(h) + eps)^(-1/2) w + b
+ *   x, residual, y, h  (T, H, D) dtype (H = 1: rows); residual nullable
+ *              (zero); h out, nullable (not stored): the sum, rounded once. y
+ *              is formed from the sum before it is rounded.
+ *   w, b       fp32 (H, D), nullable (ones, zeros)
+ *   rng, p     as dropout_pack_fwd, the element's index being (t H + h) D + d;
+ *              p = 0: no dropout, rng is not read
+ * The backward takes dL/dy and, where h goes on past the norm, dL/dh
+ * (nullable: zero), and h as the forward stored it (its x where there was
+ * neither residual nor dropout):
+ *   dx         dtype out, dL/dx; dresidual dtype out, nullable: dL/dresidual,
+ *              which without dropout is dx as well
+ *   dw, db     fp32 (H, D) out, nullable; dw must be NULL where w is. Their
+ *              sums over tokens are deterministic.
+ * Its workspace, layer_norm_pack_bwd_workspace_bytes(T, H, D) bytes, is used
+ * only when dw or db is given. The size does not fall as T grows.
+ * y and h may be the same buffers as x or residual, dx and dresidual as dy, h
+ * or dh (y and h, dx and dresidual apart from each other). Supports D up to
+ * 16384; rows of a multiple of 8 components are read in wide pieces. Activation
+ * pointers must be multiples of 16 bytes. A row of equal components with
+ * eps = 0 gives NaN, as the formula does. Sums are formed in 32 bits: a row
+ * whose squares pass their range (components near 1e19) gives zeros.
+ * Errors: SSMP_ERR_SHAPE (also H > 65536, T >= 2^31, 2^40 elements or more, p
+ * as dropout_pack_fwd), SSMP_ERR_UNSUPPORTED, SSMP_ERR_NULL, SSMP_ERR_ALIGN,
+ * SSMP_ERR_WORKSPACE.
+ */
+int layer_norm_pack_fwd(const void *x, const void *residual, const float *w, const float *b,
+                        const uint64_t *rng, void *y, void *h, int64_t T, int32_t H, int32_t D,
+                        int32_t dtype, double p, float eps, void *stream);
+size_t layer_norm_pack_bwd_workspace_bytes(int64_t T, int32_t H, int32_t D);
+int layer_norm_pack_bwd(const void *dy, const void *h, const float *w, const void *dh, const uint64_t *rng,
+                        void *dx, void *dresidual, float *dw, float *db, void *workspace,
+                        size_t workspace_bytes, int64_t T, int32_t H, int32_t D, int32_t dtype, double p,
+                        float eps, void *stream);
+
+/*
+ * dropout_pack_fwd / dropout_pack_bwd — dropout from a counter: which elements
+ * are kept follows from their index, so no mask is stored.
+ *   y[e] = residual[e] + (u(e) >= c ? x[e] / (1 - c / 65536) : 0)
+ *   dx[e] = u(e) >= c ? dy[e] / (1 - c / 65536) : 0
+ * with c = 65536 p rounded to the nearest (ties to even): p is taken in steps
+ * of 2^-16, and what is kept is divided by the share that is kept. u(e) is the
+ * 16-bit number e % 8, lower halves first, of Philox4x32-10 (Salmon et al.
+ * 2011) with key rng[0] and counter (e / 8, rng[1]), lower words first.
+ *   x, residual, y, dy, dx  n elements of dtype; residual nullable (zero). y
+ *          may be the same buffer as x or residual, dx as dy.
+ *   rng    device uint64 [2]: seed and stream, read when the kernel runs, so a
+ *          captured call takes the numbers that stand there at each replay.
+ *          Forward and backward must find the same; a training step that drops
+ *          at several places gives each its own stream.
+ * A dropped element is zero whatever it was. Activation pointers must be
+ * multiples of 16 bytes. Errors: SSMP_ERR_SHAPE (n < 0 or n >= 2^40; p < 0, not
+ * a number, or 1 at that resolution), SSMP_ERR_UNSUPPORTED, SSMP_ERR_NULL,
+ * SSMP_ERR_ALIGN.
+ */
+int dropout_pack_fwd(const void *x, const void *residual, const uint64_t *rng, void *y, int64_t n,
+                     int32_t dtype, double p, void *stream);
+int dropout_pack_bwd(const void *dy, const uint64_t *rng, void *dx, int64_t n, int32_t dtype, double p,
+                     void *stream);
 
 /* Packing strategies of varlen_pack_plan. */
 enum ssmp_pack_strategy {

@@ -1,6 +1,6 @@
 """Packed variable-length sequence operators of linear-time blocks (Mamba-1's
-conv and selective scan, the gated delta rule with its head norms) on MI355X
-(gfx950).
+conv and selective scan, the gated delta rule with its head norms, linear
+attention with a decay, layer norm and dropout) on MI355X (gfx950).
 
 The operators are HIP kernels in libssmpack.so behind a C ABI
 (include/ssmpack.h); this package is the thin Python binding over it plus a
@@ -16,12 +16,22 @@ from .binding import (  # noqa: F401
     conv1d_pack_bwd_states_workspace_bytes,
     conv1d_pack_bwd_workspace_bytes,
     conv1d_pack_fwd,
+    decay_attn_pack_bwd,
+    decay_attn_pack_bwd_scratch_bytes,
+    decay_attn_pack_fwd,
+    decay_attn_pack_fwd_scratch_bytes,
+    decay_attn_pack_step,
+    dropout_pack_bwd,
+    dropout_pack_fwd,
     gated_delta_pack_bwd,
     gated_delta_pack_bwd_scratch_bytes,
     gated_delta_pack_fwd,
     gated_delta_pack_fwd_scratch_bytes,
     gated_delta_pack_saved_bytes,
     gated_delta_pack_step,
+    layer_norm_pack_bwd,
+    layer_norm_pack_bwd_workspace_bytes,
+    layer_norm_pack_fwd,
     load,
     qk_norm_pack_bwd,
     qk_norm_pack_bwd_workspace_bytes,

@@ -89,6 +89,19 @@ _SIGNATURES = {
     "gated_delta_pack_bwd": (ctypes.c_int, [_c_vp] * 5 + [_c_i32, _c_vp, _c_i64] + [_c_i32] * 5
                              + [_c_f32] + [_c_vp] * 8 + [_c_sz, _c_vp, _c_sz, _c_vp]),
     "gated_delta_pack_step": (ctypes.c_int, [_c_vp] * 8 + [_c_i32] * 7 + [_c_f32, _c_vp]),
+    "decay_attn_pack_fwd_scratch_bytes": (_c_sz, [_c_i64] + [_c_i32] * 5),
+    "decay_attn_pack_fwd": (ctypes.c_int, [_c_vp] * 5 + [_c_i32, _c_vp, _c_i64] + [_c_i32] * 6
+                            + [_c_f32, _c_vp, _c_vp, _c_vp, _c_sz, _c_vp]),
+    "decay_attn_pack_bwd_scratch_bytes": (_c_sz, [_c_i64] + [_c_i32] * 5),
+    "decay_attn_pack_bwd": (ctypes.c_int, [_c_vp] * 5 + [_c_i32, _c_vp, _c_i64] + [_c_i32] * 6
+                            + [_c_f32] + [_c_vp] * 8 + [_c_sz, _c_vp]),
+    "decay_attn_pack_step": (ctypes.c_int, [_c_vp] * 7 + [_c_i32] * 8 + [_c_f32, _c_vp]),
+    "layer_norm_pack_fwd": (ctypes.c_int, [_c_vp] * 7 + [_c_i64] + [_c_i32] * 3 + [ctypes.c_double, _c_f32, _c_vp]),
+    "layer_norm_pack_bwd_workspace_bytes": (_c_sz, [_c_i64, _c_i32, _c_i32]),
+    "layer_norm_pack_bwd": (ctypes.c_int, [_c_vp] * 10 + [_c_sz, _c_i64] + [_c_i32] * 3
+                            + [ctypes.c_double, _c_f32, _c_vp]),
+    "dropout_pack_fwd": (ctypes.c_int, [_c_vp] * 4 + [_c_i64, _c_i32, ctypes.c_double, _c_vp]),
+    "dropout_pack_bwd": (ctypes.c_int, [_c_vp] * 3 + [_c_i64, _c_i32, ctypes.c_double, _c_vp]),
     "varlen_pack_plan": (ctypes.c_int, [_c_vp, _c_i32, _c_i32, _c_i32, _c_i32, _c_vp, _c_vp, _c_vp, _c_vp,
                                         _c_vp, _c_vp]),
 }
@@ -796,3 +809,201 @@ def gated_delta_pack_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: 
              _arg(slots, "slots", (B,), torch.int32, dev), _arg(out, "out", (B, Hv, Dv), q.dtype, dev), B, n, Hk, Hv,
              Dk, Dv, code, float(Dk ** -0.5 if scale is None else scale))
     return out
+
+
+# ---------------------------------------------------------------------------
+# Linear attention with a decay for each head
+def _decay_args(q, k, v, name, g):
+    """Checks of what the linear attention's calls share: sizes (tokens, Hk,
+    Hv, Dk, Dv), the addresses of q, k, v (or what has its shape, `name`) and
+    g, the dtype's code, and whether g is by token."""
+    T, Hk, Dk = _heads(q, "q")
+    _, Hv, Dv = _heads(v, name)
+    dev, dt = q.device, q.dtype
+    code = _dtype_code(q)
+    per_token = g.dim() == 2
+    return (T, Hk, Hv, Dk, Dv), (_arg(q, "q", (T, Hk, Dk), dt, dev), _arg(k, "k", (T, Hk, Dk), dt, dev),
+                                 _arg(v, name, (T, Hv, Dv), dt, dev),
+                                 _arg(g, "g", (T, Hv) if per_token else (Hv,), torch.float32, dev)), code, int(per_token)
+
+
+def decay_attn_pack_fwd_scratch_bytes(T: int, nseq: int, Hk: int, Hv: int, Dk: int, Dv: int) -> int:
+    return int(load().decay_attn_pack_fwd_scratch_bytes(T, nseq, Hk, Hv, Dk, Dv))
+
+
+def decay_attn_pack_bwd_scratch_bytes(T: int, nseq: int, Hk: int, Hv: int, Dk: int, Dv: int) -> int:
+    return int(load().decay_attn_pack_bwd_scratch_bytes(T, nseq, Hk, Hv, Dk, Dv))
+
+
+def decay_attn_pack_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, cu_seqlens: torch.Tensor,
+                        scale: Optional[float] = None, initial_state: Optional[torch.Tensor] = None,
+                        final_state=False, scratch: Optional[torch.Tensor] = None,
+                        out: Optional[torch.Tensor] = None):
+    """Linear attention with a decay over the sequences of cu_seqlens: q, k
+    (T, Hk, Dk), v (T, Hv, Dv), log decay g fp32 (T, Hv), or (Hv) for one decay
+    a head; states fp32 (nseq, Hv, Dk, Dv). scale defaults to Dk ** -0.5.
+    Returns (out, final_state or None); nothing is kept for the backward. The
+    scratch is free again once the call's work on the current stream is done.
+    Rows behind cu_seqlens[-1] are left as they were."""
+    sizes, (pq, pk, pv, pg), code, per_token = _decay_args(q, k, v, "v", g)
+    T, Hk, Hv, Dk, Dv = sizes
+    dev, f32 = q.device, torch.float32
+    nseq = _nseq(cu_seqlens, dev)
+    state = (nseq, Hv, Dk, Dv)
+    fs = _out_or_new(final_state, state, f32, dev)
+    ws = _buffer(scratch, "scratch", decay_attn_pack_fwd_scratch_bytes(T, nseq, Hk, Hv, Dk, Dv) if scratch is None else 0,
+                 dev)
+    o = torch.empty_like(v) if out is None else out
+    _call_on(dev, "decay_attn_pack_fwd", pq, pk, pv, pg, cu_seqlens.data_ptr(), nseq,
+             _arg(o, "out", (T, Hv, Dv), q.dtype, dev), *sizes, code, per_token,
+             float(Dk ** -0.5 if scale is None else scale), _arg(initial_state, "initial_state", state, f32, dev),
+             _arg(fs, "final_state", state, f32, dev), ws[1], ws[2])
+    return o, fs
+
+
+def decay_attn_pack_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, cu_seqlens: torch.Tensor,
+                        dout: torch.Tensor, scale: Optional[float] = None,
+                        initial_state: Optional[torch.Tensor] = None, dfinal_state: Optional[torch.Tensor] = None,
+                        dinitial_state=False, want_dg: bool = True, scratch: Optional[torch.Tensor] = None,
+                        out: Optional[dict] = None) -> dict:
+    """Gradients of sum(dout * out) (+ sum(dfinal_state * final_state)):
+    {"dq", "dk", "dv", "dg", "dinitial_state"} (dg None with want_dg=False; the
+    last None unless asked for: True, or an output tensor). The inputs are the
+    forward's. `out` may supply the first four."""
+    sizes, (pq, pk, pv, pg), code, per_token = _decay_args(q, k, v, "v", g)
+    T, Hk, Hv, Dk, Dv = sizes
+    dev, dt, f32 = q.device, q.dtype, torch.float32
+    nseq = _nseq(cu_seqlens, dev)
+    state = (nseq, Hv, Dk, Dv)
+    di = _out_or_new(dinitial_state, state, f32, dev)
+    ws = _buffer(scratch, "scratch", decay_attn_pack_bwd_scratch_bytes(T, nseq, Hk, Hv, Dk, Dv) if scratch is None else 0,
+                 dev)
+    if out is None:
+        out = {"dq": torch.empty_like(q), "dk": torch.empty_like(k), "dv": torch.empty_like(v),
+               "dg": torch.empty_like(g) if want_dg else None}
+    dq, dk, dv, dg = (out[n] for n in ("dq", "dk", "dv", "dg"))
+    _call_on(dev, "decay_attn_pack_bwd", pq, pk, pv, pg, cu_seqlens.data_ptr(), nseq,
+             _arg(dout, "dout", v.shape, dt, dev), *sizes, code, per_token,
+             float(Dk ** -0.5 if scale is None else scale), _arg(initial_state, "initial_state", state, f32, dev),
+             _arg(dfinal_state, "dfinal_state", state, f32, dev), _arg(di, "dinitial_state", state, f32, dev),
+             _arg(dq, "dq", q.shape, dt, dev), _arg(dk, "dk", q.shape, dt, dev), _arg(dv, "dv", v.shape, dt, dev),
+             _arg(dg, "dg", g.shape, f32, dev), ws[1], ws[2])
+    return {"dq": dq, "dk": dk, "dv": dv, "dg": dg, "dinitial_state": di}
+
+
+def decay_attn_pack_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, state: torch.Tensor,
+                         slots: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                         out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """One token for each row: q, k (B, Hk, Dk), v (B, Hv, Dv), g (B, Hv) or
+    (Hv); state fp32 (nslots, Hv, Dk, Dv) is updated in place at slots (int32
+    (B); None: row b uses slot b). Returns out (B, Hv, Dv). A row whose slot
+    lies outside the pool is skipped: its out is left as it was, which for an
+    `out` made here is unset memory."""
+    sizes, ptrs, code, per_token = _decay_args(q, k, v, "v", g)
+    B, Hk, Hv, Dk, Dv = sizes
+    dev = q.device
+    if state.dim() != 4:
+        raise ValueError(f"state has shape {tuple(state.shape)}, expected (slots, heads, Dk, Dv)")
+    n = state.shape[0]
+    if out is None:
+        out = torch.empty_like(v)
+    _call_on(dev, "decay_attn_pack_step", *ptrs, _arg(state, "state", (n, Hv, Dk, Dv), torch.float32, dev),
+             _arg(slots, "slots", (B,), torch.int32, dev), _arg(out, "out", (B, Hv, Dv), q.dtype, dev), B, n, Hk, Hv,
+             Dk, Dv, code, per_token, float(Dk ** -0.5 if scale is None else scale))
+    return out
+
+
+# ---------------------------------------------------------------------------
+# Layer norm, dropout
+def _rows(x: torch.Tensor, name: str):
+    """Sizes (T, H, D) of rows (T, D), for which H is 1, or heads (T, H, D)."""
+    if x.dim() not in (2, 3):
+        raise ValueError(f"{name} has shape {tuple(x.shape)}, expected (tokens, size) or (tokens, heads, size)")
+    return x.shape if x.dim() == 3 else (x.shape[0], 1, x.shape[1])
+
+
+def _rng_arg(p: float, rng: Optional[torch.Tensor], dev) -> Optional[int]:
+    if p and rng is None:
+        raise ValueError("dropout (p) needs rng")
+    return _arg(rng, "rng", (2,), torch.int64, dev) if p else None
+
+
+def layer_norm_pack_fwd(x: torch.Tensor, w: Optional[torch.Tensor] = None, b: Optional[torch.Tensor] = None,
+                        eps: float = 1e-5, residual: Optional[torch.Tensor] = None, p: float = 0.0,
+                        rng: Optional[torch.Tensor] = None, out: Optional[tuple] = None):
+    """h = residual + drop(x), y = the layer norm of h over its last dimension,
+    times w, plus b. x (T, D) with w, b fp32 (D), or heads (T, H, D) with w, b
+    (H, D). p and rng (int64 (2): seed, stream) are dropout_pack_fwd's. Returns
+    (y, h), h None where it would be x itself (no residual, p = 0). `out` may
+    supply both (x and residual themselves included; h None: not stored)."""
+    T, H, D = _rows(x, "x")
+    dev, dt, par = x.device, x.dtype, x.shape[1:]
+    code = _dtype_code(x)
+    if out is None:
+        out = torch.empty_like(x), torch.empty_like(x) if residual is not None or p else None
+    y, h = out
+    _call_on(dev, "layer_norm_pack_fwd", _arg(x, "x", x.shape, dt, dev), _arg(residual, "residual", x.shape, dt, dev),
+             _arg(w, "w", par, torch.float32, dev), _arg(b, "b", par, torch.float32, dev), _rng_arg(p, rng, dev),
+             _arg(y, "y", x.shape, dt, dev), _arg(h, "h", x.shape, dt, dev), T, H, D, code, float(p), float(eps))
+    return y, h
+
+
+def layer_norm_pack_bwd_workspace_bytes(T: int, H: int, D: int) -> int:
+    return int(load().layer_norm_pack_bwd_workspace_bytes(T, H, D))
+
+
+def layer_norm_pack_bwd(dy: torch.Tensor, h: torch.Tensor, w: Optional[torch.Tensor] = None,
+                        dh: Optional[torch.Tensor] = None, eps: float = 1e-5, p: float = 0.0,
+                        rng: Optional[torch.Tensor] = None, bias: bool = False, residual: bool = False,
+                        workspace: Optional[torch.Tensor] = None, out: Optional[dict] = None) -> dict:
+    """Gradients of sum(dy * y) (+ sum(dh * h)) at h, the forward's sum as it
+    was stored (or its x): {"dx", "dresidual", "dw", "db"}; dresidual None
+    without residual=True, dw None without w, db None without bias=True.
+    Without dropout dresidual is dx, the same tensor. `out` may supply them (dx
+    and dresidual may be dy, h or dh)."""
+    T, H, D = _rows(h, "h")
+    dev, dt, par, f32 = h.device, h.dtype, h.shape[1:], torch.float32
+    code = _dtype_code(h)
+    if out is None:
+        out = {"dx": torch.empty_like(h), "dresidual": torch.empty_like(h) if residual and p else None,
+               "dw": None if w is None else torch.empty_like(w),
+               "db": torch.empty(par, dtype=f32, device=dev) if bias else None}
+        same = residual and not p
+    else:
+        same = False
+    dx, dres, dw, db = (out[n] for n in ("dx", "dresidual", "dw", "db"))
+    ws = (workspace, None, 0)
+    if workspace is not None or dw is not None or db is not None:
+        ws = _buffer(workspace, "workspace", layer_norm_pack_bwd_workspace_bytes(T, H, D) if workspace is None else 0, dev)
+    _call_on(dev, "layer_norm_pack_bwd", _arg(dy, "dy", h.shape, dt, dev), _arg(h, "h", h.shape, dt, dev),
+             _arg(w, "w", par, f32, dev), _arg(dh, "dh", h.shape, dt, dev), _rng_arg(p, rng, dev),
+             _arg(dx, "dx", h.shape, dt, dev), _arg(dres, "dresidual", h.shape, dt, dev), _arg(dw, "dw", par, f32, dev),
+             _arg(db, "db", par, f32, dev), ws[1], ws[2], T, H, D, code, float(p), float(eps))
+    return {"dx": dx, "dresidual": dx if same else dres, "dw": dw, "db": db}
+
+
+def dropout_pack_fwd(x: torch.Tensor, p: float, rng: torch.Tensor, residual: Optional[torch.Tensor] = None,
+                     out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """residual + x, an element of x dropped with probability p (in steps of
+    2^-16) and divided by 1 - p otherwise, by the numbers that follow from rng
+    (int64 (2): seed, stream) and the element's index. Any shape. `out` may be
+    x or residual."""
+    y = torch.empty_like(x) if out is None else out
+    dev = x.device
+    code = _dtype_code(x)
+    _call_on(dev, "dropout_pack_fwd", _arg(x, "x", x.shape, x.dtype, dev),
+             _arg(residual, "residual", x.shape, x.dtype, dev), _arg(rng, "rng", (2,), torch.int64, dev),
+             _arg(y, "out", x.shape, x.dtype, dev), x.numel(), code, float(p))
+    return y
+
+
+def dropout_pack_bwd(dy: torch.Tensor, p: float, rng: torch.Tensor, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The gradient of x, with the forward's p and rng (the residual's is dy
+    itself). `out` may be dy."""
+    dx = torch.empty_like(dy) if out is None else out
+    dev = dy.device
+    code = _dtype_code(dy)
+    _call_on(dev, "dropout_pack_bwd", _arg(dy, "dy", dy.shape, dy.dtype, dev),
+             _arg(rng, "rng", (2,), torch.int64, dev), _arg(dx, "out", dy.shape, dy.dtype, dev), dy.numel(), code,
+             float(p))
+    return dx

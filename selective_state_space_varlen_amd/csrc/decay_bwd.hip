@@ -1,0 +1,221 @@
+// decay_attn_pack_bwd: gradients of linear attention with a decay for each
+// head. Nothing is kept from the forward: dq's walk forms the states again as
+// it goes, and those between segments are summed again.
+#include "decay_walk.h"
+
+namespace ssmp {
+
+template <>
+int launch_decay_walk<kOut>(const DecayArgs&, int32_t, hipStream_t);
+template <>
+int launch_decay_walk<kSumS>(const DecayArgs&, int32_t, hipStream_t);
+template <>
+int launch_decay_walk<kDq>(const DecayArgs&, int32_t, hipStream_t);
+template <>
+int launch_decay_walk<kDk>(const DecayArgs&, int32_t, hipStream_t);
+template <>
+int launch_decay_walk<kDv>(const DecayArgs& a, int32_t dtype, hipStream_t s) {
+    return launch_decay_walk_of<kDv, false>(a, dtype, s);
+}
+template <>
+int launch_decay_walk<kSumD>(const DecayArgs& a, int32_t dtype, hipStream_t s) {
+    return launch_decay_walk_of<kSumD, false>(a, dtype, s);
+}
+
+// dg of one piece of kPiece tokens, lane = value head: back from the anchor at
+// its end, d g_t = d g_{t+1} + q_t.dq_t - k_t.dk_t, in 64 bits. The anchors
+// keep the roundings of the terms, which nearly cancel where decays are
+// strong, from adding up along a sequence. Where a token's decay is zero, so
+// is its gradient, and the sum starts again.
+__global__ __launch_bounds__(64) void k_decay_dg(DecayArgs p, int parts) {
+    const int hb = (p.Hv + 63) / 64;
+    const int64_t slot = blockIdx.x / hb;
+    const int hv = blockIdx.x % hb * 64 + threadIdx.x;
+    Chunk c;
+    const bool any = chunk_at(p.cu, p.nseq, p.T, slot, c, kPiece);
+    if (hv >= p.Hv) return;
+    double acc = 0.0, sum = 0.0;
+    if (any) {
+        const float* const meet = p.meet + ((size_t)slot * p.Hv + hv) * parts;
+        if (!c.last || p.dhT)
+            for (int i = 0; i < parts; ++i) acc += (double)meet[i];
+        constexpr int kBatch = 8;
+        for (int t1 = c.n; t1 > 0; t1 -= kBatch) {
+            float r[kBatch], g[kBatch];
+#pragma unroll
+            for (int x = 0; x < kBatch; ++x) {
+                const int t = t1 - 1 - x;
+                r[x] = g[x] = 0.0f;
+                if (t >= 0) {
+                    const size_t at = (size_t)(c.start + t) * p.Hv + hv;
+                    for (int i = 0; i < parts; ++i)
+                        r[x] += p.rows[0][(size_t)i * p.T * p.Hv + at] - p.rows[1][(size_t)i * p.T * p.Hv + at];
+                    g[x] = p.g[p.gstride ? at : hv];
+                }
+            }
+#pragma unroll
+            for (int x = 0; x < kBatch; ++x) {
+                const int t = t1 - 1 - x;
+                if (t < 0) continue;
+                acc += (double)r[x];
+                if (g[x] * kLog2e < -126.0f) acc = 0.0;
+                if (p.gstride) p.dg[(size_t)(c.start + t) * p.Hv + hv] = (float)acc;
+                sum += acc;
+            }
+        }
+    }
+    if (!p.gstride) p.dgsum[(size_t)slot * p.Hv + hv] = sum;
+}
+
+// one decay for a head: its gradient, in a fixed order
+__global__ __launch_bounds__(64) void k_decay_dg_sum(DecayArgs p, int64_t slots) {
+    const int hv = blockIdx.x, lane = threadIdx.x;
+    double s = 0.0;
+    for (int64_t i = lane; i < slots; i += 64) s += p.dgsum[(size_t)i * p.Hv + hv];
+    for (int d = 32; d; d >>= 1) s += __shfl_xor(s, d);
+    if (lane == 0) p.dg[hv] = (float)s;
+}
+
+// dq or dk: the sum of its parts by value head and slice, up to the last sequence's end
+template <typename T>
+__global__ __launch_bounds__(256) void k_decay_add(DecayArgs p, const float* __restrict__ part, void* out, int members) {
+    int64_t end = p.cu[p.nseq];
+    end = end < 0 ? 0 : end > p.T ? p.T : end;
+    const int per = p.Dk / 4;
+    const int64_t n = end * p.Hk * per;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+        const float* at = part + (i / per) * members * (int64_t)p.Dk + i % per * 4;
+        f32x4 s = {0, 0, 0, 0};
+        for (int m = 0; m < members; ++m) s += *reinterpret_cast<const f32x4*>(at + (int64_t)m * p.Dk);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) Elt<T>::st(static_cast<T*>(out), (size_t)i * 4 + x, s[x]);
+    }
+}
+int launch_decay_add(const DecayArgs& a, int i, int32_t dtype, hipStream_t s) {
+    const int64_t want = (a.T * a.Hk * (a.Dk / 4) + 255) / 256;
+    const unsigned blocks = (unsigned)(want < 8192 ? want : 8192);
+    void* const out = i ? a.dk : a.dq;
+    const int members = a.Hv / a.Hk * a.slices;
+    if (dtype == SSMP_F32) k_decay_add<float><<<blocks, 256, 0, s>>>(a, a.part[i], out, members);
+    else k_decay_add<uint16_t><<<blocks, 256, 0, s>>>(a, a.part[i], out, members);
+    SSMP_LAUNCH_CHECK();
+    return SSMP_OK;
+}
+
+struct DecayBwdLayout {
+    size_t joint[2], decay[2], part[2], rows[2], snap, meet, dgsum, total;
+};
+inline DecayBwdLayout decay_bwd_layout(int64_t T, int32_t nseq, int32_t Hk, int32_t Hv, int32_t Dk, int32_t Dv) {
+    DecayBwdLayout L;
+    const size_t slices = (Dv + kDecayMaxDb - 1) / kDecayMaxDb;
+    const DecayJoint j = decay_joint(T, Hv, Dk, Dv, Hv);
+    size_t at = 0;
+    const auto take = [&](size_t bytes) {
+        const size_t here = at;
+        at += round256(bytes);
+        return here;
+    };
+    for (int i = 0; i < 2; ++i) {
+        const size_t here = take(j.total);
+        L.joint[i] = here + j.joint;
+        L.decay[i] = here + j.decay;
+    }
+    const bool partial = (size_t)(Hv / Hk) * slices > 1;
+    for (int i = 0; i < 2; ++i) L.part[i] = take(partial ? (size_t)T * Hv * slices * Dk * sizeof(float) : 0);
+    for (int i = 0; i < 2; ++i) L.rows[i] = take(slices * T * Hv * sizeof(float));
+    const size_t db = Dv > 64 ? 128 : 64, dc = decay_cols(Dk);
+    L.snap = take((size_t)(T / kPiece) * Hv * slices * db * dc * sizeof(float));
+    L.meet = take((size_t)(T / kPiece + nseq) * Hv * slices * sizeof(float));
+    L.dgsum = take((size_t)(T / kPiece + nseq) * Hv * sizeof(double));
+    L.total = at;
+    return L;
+}
+
+}  // namespace ssmp
+
+extern "C" size_t decay_attn_pack_bwd_scratch_bytes(int64_t T, int32_t nseq, int32_t Hk, int32_t Hv, int32_t Dk,
+                                                    int32_t Dv) {
+    using namespace ssmp;
+    if (decay_check(T, nseq, Hk, Hv, Dk, Dv, SSMP_F32) || T == 0) return 0;
+    return decay_bwd_layout(T, nseq, Hk, Hv, Dk, Dv).total;
+}
+
+extern "C" int decay_attn_pack_bwd(const void* q, const void* k, const void* v, const float* g,
+                                   const int32_t* cu_seqlens, int32_t nseq, const void* dout, int64_t T, int32_t Hk,
+                                   int32_t Hv, int32_t Dk, int32_t Dv, int32_t dtype, int32_t per_token, float scale,
+                                   const float* initial_state, const float* dfinal_state, float* dinitial_state,
+                                   void* dq, void* dk, void* dv, float* dg, void* scratch, size_t scratch_bytes,
+                                   void* stream) {
+    using namespace ssmp;
+    if (const int st = decay_check(T, nseq, Hk, Hv, Dk, Dv, dtype)) return st;
+    if (!cu_seqlens) return SSMP_ERR_NULL;
+    if (T > 0 && (!q || !k || !v || !g || !dout || !dq || !dk || !dv)) return SSMP_ERR_NULL;
+    if (!aligned16(q, k, v, dout, dq, dk, dv, initial_state, dfinal_state, dinitial_state, scratch))
+        return SSMP_ERR_ALIGN;
+    if (T > 0 && (!scratch || scratch_bytes < decay_attn_pack_bwd_scratch_bytes(T, nseq, Hk, Hv, Dk, Dv)))
+        return SSMP_ERR_WORKSPACE;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    DecayArgs a = {};
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.dout = dout;
+    a.g = g;
+    a.cu = cu_seqlens;
+    a.dq = dq;
+    a.dk = dk;
+    a.dv = dv;
+    a.dg = dg;
+    a.h0 = initial_state;
+    a.dhT = dfinal_state;
+    a.dh0 = dinitial_state;
+    a.T = T;
+    a.nseq = nseq;
+    a.Hk = Hk;
+    a.Hv = Hv;
+    a.Dk = Dk;
+    a.Dv = Dv;
+    a.gstride = per_token ? Hv : 0;
+    a.scale = scale;
+    a.slices = (Dv + kDecayMaxDb - 1) / kDecayMaxDb;
+    a.seg = decay_segment(T, Hv);
+    if (T == 0) {
+        if (!per_token)
+            if (const int st = zero_f32(dg, Hv, s)) return st;
+        return dinitial_state ? launch_decay_walk<kDv>(a, dtype, s) : SSMP_OK;
+    }
+    const DecayBwdLayout L = decay_bwd_layout(T, nseq, Hk, Hv, Dk, Dv);
+    char* const ws = static_cast<char*>(scratch);
+    const bool partial = Hv / Hk * a.slices > 1;
+    for (int i = 0; i < 2; ++i) {
+        a.joint[i] = reinterpret_cast<float*>(ws + L.joint[i]);
+        a.seg_decay[i] = reinterpret_cast<float*>(ws + L.decay[i]);
+        a.part[i] = reinterpret_cast<float*>(ws + L.part[i]);
+        a.rows[i] = reinterpret_cast<float*>(ws + L.rows[i]);
+    }
+    a.snap = reinterpret_cast<float*>(ws + L.snap);
+    a.meet = reinterpret_cast<float*>(ws + L.meet);
+    a.dgsum = reinterpret_cast<double*>(ws + L.dgsum);
+    if (T > a.seg) {
+        if (const int st = launch_decay_walk<kSumS>(a, dtype, s)) return st;
+        if (const int st = launch_decay_join<false>(a, s)) return st;
+        if (const int st = launch_decay_walk<kSumD>(a, dtype, s)) return st;
+        if (const int st = launch_decay_join<true>(a, s)) return st;
+    }
+    if (const int st = launch_decay_walk<kDq>(a, dtype, s)) return st;
+    if (const int st = launch_decay_walk<kDk>(a, dtype, s)) return st;
+    if (const int st = launch_decay_walk<kDv>(a, dtype, s)) return st;
+    if (dg) {
+        const int64_t slots = T / kPiece + nseq;
+        k_decay_dg<<<(unsigned)(slots * ((Hv + 63) / 64)), 64, 0, s>>>(a, a.slices);
+        SSMP_LAUNCH_CHECK();
+        if (!per_token) {
+            k_decay_dg_sum<<<(unsigned)Hv, 64, 0, s>>>(a, slots);
+            SSMP_LAUNCH_CHECK();
+        }
+    }
+    if (partial)
+        for (int i = 0; i < 2; ++i)
+            if (const int st = launch_decay_add(a, i, dtype, s)) return st;
+    return SSMP_OK;
+}

@@ -1,0 +1,11 @@
+// decay_attn_pack_bwd: the walk that forms dq.
+#include "decay_walk.h"
+
+namespace ssmp {
+
+template <>
+int launch_decay_walk<kDq>(const DecayArgs& a, int32_t dtype, hipStream_t s) {
+    return a.dg ? launch_decay_walk_of<kDq, true>(a, dtype, s) : launch_decay_walk_of<kDq, false>(a, dtype, s);
+}
+
+}  // namespace ssmp

@@ -64,7 +64,8 @@ __device__ __forceinline__ Seq seq_at(const int32_t* __restrict__ cu, int s, int
 // The chunk in a slot: false where the slot holds none. Called by whole waves;
 // 64 boundaries are looked at in one step, so one trip to memory finds a
 // sequence among 64, two among 4096. (Pieces of another size than kC lie in
-// slots by the same rule.)
+// slots by the same rule. `empties`: a sequence without tokens counts as one of
+// no tokens, in the slot that it has all the same.)
 struct Chunk {
     int64_t start;   // its first token
     int32_t n;       // tokens
@@ -73,7 +74,7 @@ struct Chunk {
     bool last;       // of its sequence
 };
 __device__ __forceinline__ bool chunk_at(const int32_t* __restrict__ cu, int32_t nseq, int64_t T, int64_t slot,
-                                         Chunk& c, int size = kC) {
+                                         Chunk& c, int size = kC, bool empties = false) {
     const int top = (int)T, lane = lane_id();
     int lo = 0, hi = nseq;
     while (true) {
@@ -98,7 +99,7 @@ __device__ __forceinline__ bool chunk_at(const int32_t* __restrict__ cu, int32_t
         }
         c.index = slot - (first / size + lo);
         const int64_t at = c.index * size;
-        if (at < 0 || at >= end - first) return false;
+        if (at < 0 || (at >= end - first && !(empties && at == 0))) return false;
         c.start = first + at;
         c.last = end - first - at <= size;
         c.n = c.last ? (int32_t)(end - first - at) : size;
