@@ -22,49 +22,65 @@ int launch_decay_walk<kSumD>(const DecayArgs& a, int32_t dtype, hipStream_t s) {
     return launch_decay_walk_of<kSumD, false>(a, dtype, s);
 }
 
-// dg of one piece of kPiece tokens, lane = value head: back from the anchor at
-// its end, d g_t = d g_{t+1} + q_t.dq_t - k_t.dk_t, in 64 bits. The anchors
-// keep the roundings of the terms, which nearly cancel where decays are
-// strong, from adding up along a sequence. Where a token's decay is zero, so
-// is its gradient, and the sum starts again.
+// exp(g) in 32 bits without its smallest numbers, as the walks form it
+__device__ __forceinline__ bool decay_is_zero(float g) { return g * kLog2e < -126.0f; }
+
+// dg of one piece of kPiece tokens, a wave for 64 / kDgChunks heads, a lane
+// for one chunk of a head: back from the anchor at the chunk's end, d g_t =
+// d g_{t+1} + q_t.dq_t - k_t.dk_t, in 64 bits. Where a token's decay is zero,
+// so is its gradient, and the sum starts again.
+constexpr int kDgChunks = kPiece / kC, kDgHeads = 64 / kDgChunks;
 __global__ __launch_bounds__(64) void k_decay_dg(DecayArgs p, int parts) {
-    const int hb = (p.Hv + 63) / 64;
+    const int hb = (p.Hv + kDgHeads - 1) / kDgHeads;
     const int64_t slot = blockIdx.x / hb;
-    const int hv = blockIdx.x % hb * 64 + threadIdx.x;
+    const int hv = blockIdx.x % hb * kDgHeads + threadIdx.x % kDgHeads, ch = threadIdx.x / kDgHeads;
     Chunk c;
-    const bool any = chunk_at(p.cu, p.nseq, p.T, slot, c, kPiece);
-    if (hv >= p.Hv) return;
-    double acc = 0.0, sum = 0.0;
-    if (any) {
-        const float* const meet = p.meet + ((size_t)slot * p.Hv + hv) * parts;
+    const bool any = chunk_at(p.cu, p.nseq, p.T, slot, c, kPiece) && hv < p.Hv;
+    double sum = 0.0;
+    if (any && ch * kC < c.n) {
+        double acc = 0.0;
         if (!c.last || p.dhT)
-            for (int i = 0; i < parts; ++i) acc += (double)meet[i];
-        constexpr int kBatch = 8;
-        for (int t1 = c.n; t1 > 0; t1 -= kBatch) {
+            for (int i = 0; i < parts; ++i) acc += (double)p.meet[((size_t)slot * p.Hv + hv) * parts + i];
+        // what crosses between this chunk and those behind it in the piece
+        const int64_t first = c.start - c.index * kPiece, chunk0 = first / kC + c.seq + c.index * (kPiece / kC);
+        const int64_t chunks = (c.n + kC - 1) / kC;
+        for (int64_t i = chunks - 1; i > ch; --i) {
+            const size_t at = ((size_t)(chunk0 + i) * p.Hv + hv) * parts;
+            for (int j = 0; j < parts; ++j) acc += (double)p.chunk[0][at + j] - (double)p.chunk[1][at + j];
+        }
+        constexpr int kBatch = 16;
+        const int64_t t0 = c.start + ch * kC;
+        for (int t1 = min(c.n - ch * kC, kC); t1 > 0; t1 -= kBatch) {
             float r[kBatch], g[kBatch];
 #pragma unroll
             for (int x = 0; x < kBatch; ++x) {
                 const int t = t1 - 1 - x;
-                r[x] = g[x] = 0.0f;
-                if (t >= 0) {
-                    const size_t at = (size_t)(c.start + t) * p.Hv + hv;
-                    for (int i = 0; i < parts; ++i)
-                        r[x] += p.rows[0][(size_t)i * p.T * p.Hv + at] - p.rows[1][(size_t)i * p.T * p.Hv + at];
-                    g[x] = p.g[p.gstride ? at : hv];
-                }
+                const size_t at = (size_t)(t0 + (t < 0 ? 0 : t)) * p.Hv + hv;
+                r[x] = p.rows[0][at] - p.rows[1][at];
+                g[x] = p.g[p.gstride ? at : hv];
             }
+            for (int i = 1; i < parts; ++i)
+#pragma unroll
+                for (int x = 0; x < kBatch; ++x) {
+                    const int t = t1 - 1 - x;
+                    const size_t at = ((size_t)i * p.T + t0 + (t < 0 ? 0 : t)) * p.Hv + hv;
+                    r[x] += p.rows[0][at] - p.rows[1][at];
+                }
 #pragma unroll
             for (int x = 0; x < kBatch; ++x) {
                 const int t = t1 - 1 - x;
                 if (t < 0) continue;
                 acc += (double)r[x];
-                if (g[x] * kLog2e < -126.0f) acc = 0.0;
-                if (p.gstride) p.dg[(size_t)(c.start + t) * p.Hv + hv] = (float)acc;
+                if (decay_is_zero(g[x])) acc = 0.0;
+                if (p.gstride) p.dg[(size_t)(t0 + t) * p.Hv + hv] = (float)acc;
                 sum += acc;
             }
         }
     }
-    if (!p.gstride) p.dgsum[(size_t)slot * p.Hv + hv] = sum;
+    if (!p.gstride) {
+        for (int d = kDgHeads; d < 64; d *= 2) sum += __shfl_xor(sum, d);
+        if (threadIdx.x < kDgHeads && hv < p.Hv) p.dgsum[(size_t)slot * p.Hv + hv] = sum;
+    }
 }
 
 // one decay for a head: its gradient, in a fixed order
@@ -103,7 +119,7 @@ int launch_decay_add(const DecayArgs& a, int i, int32_t dtype, hipStream_t s) {
 }
 
 struct DecayBwdLayout {
-    size_t joint[2], decay[2], part[2], rows[2], snap, meet, dgsum, total;
+    size_t joint[2], decay[2], part[2], rows[2], chunk[2], snap, meet, dgsum, total;
 };
 inline DecayBwdLayout decay_bwd_layout(int64_t T, int32_t nseq, int32_t Hk, int32_t Hv, int32_t Dk, int32_t Dv) {
     DecayBwdLayout L;
@@ -123,6 +139,7 @@ inline DecayBwdLayout decay_bwd_layout(int64_t T, int32_t nseq, int32_t Hk, int3
     const bool partial = (size_t)(Hv / Hk) * slices > 1;
     for (int i = 0; i < 2; ++i) L.part[i] = take(partial ? (size_t)T * Hv * slices * Dk * sizeof(float) : 0);
     for (int i = 0; i < 2; ++i) L.rows[i] = take(slices * T * Hv * sizeof(float));
+    for (int i = 0; i < 2; ++i) L.chunk[i] = take((size_t)delta_slots(T, nseq) * Hv * slices * sizeof(float));
     const size_t db = Dv > 64 ? 128 : 64, dc = decay_cols(Dk);
     L.snap = take((size_t)(T / kPiece) * Hv * slices * db * dc * sizeof(float));
     L.meet = take((size_t)(T / kPiece + nseq) * Hv * slices * sizeof(float));
@@ -192,6 +209,7 @@ extern "C" int decay_attn_pack_bwd(const void* q, const void* k, const void* v, 
         a.seg_decay[i] = reinterpret_cast<float*>(ws + L.decay[i]);
         a.part[i] = reinterpret_cast<float*>(ws + L.part[i]);
         a.rows[i] = reinterpret_cast<float*>(ws + L.rows[i]);
+        a.chunk[i] = reinterpret_cast<float*>(ws + L.chunk[i]);
     }
     a.snap = reinterpret_cast<float*>(ws + L.snap);
     a.meet = reinterpret_cast<float*>(ws + L.meet);
@@ -207,7 +225,7 @@ extern "C" int decay_attn_pack_bwd(const void* q, const void* k, const void* v, 
     if (const int st = launch_decay_walk<kDv>(a, dtype, s)) return st;
     if (dg) {
         const int64_t slots = T / kPiece + nseq;
-        k_decay_dg<<<(unsigned)(slots * ((Hv + 63) / 64)), 64, 0, s>>>(a, a.slices);
+        k_decay_dg<<<(unsigned)(slots * ((Hv + kDgHeads - 1) / kDgHeads)), 64, 0, s>>>(a, a.slices);
         SSMP_LAUNCH_CHECK();
         if (!per_token) {
             k_decay_dg_sum<<<(unsigned)Hv, 64, 0, s>>>(a, slots);

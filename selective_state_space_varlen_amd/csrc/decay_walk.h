@@ -10,7 +10,13 @@
 // and rows of `c` are added up, forwards in time or backwards. Its state is
 // X = sum of decayed b c^T: S, S^T, and their gradients dS^T, dS.
 //   d g_t = (dS_t . a_t S_{t-1}), and since (dS_t . S_t) is d g_t + k_t.dk_t as
-// well as d g_{t+1} + q_t.dq_t:  d g_t = d g_{t+1} + q_t.dq_t - k_t.dk_t.
+// well as d g_{t+1} + q_t.dq_t:  d g_t = d g_{t+1} + q_t.dq_t - k_t.dk_t,
+// from (dS . S) at a sequence's end. The terms nearly cancel where decays are
+// strong, so roundings must not add up along the sequence: (dS . S) is formed
+// anew after every kPiece tokens, where dq's walk leaves S for dk's, and goes
+// from chunk to chunk by what crosses between chunks alone: (dS . S) before a
+// chunk is that behind it + sum q.dq' - sum k.dk', dq' and dk' being the parts
+// that come through the states.
 #pragma once
 
 #include "delta_common.h"
@@ -66,7 +72,8 @@ struct DecayArgs {
     // backward
     int32_t slices;       // of 128 rows that Dv has in dq and dk
     float* part[2];       // dq, dk by value head and slice: [T][Hk][members][Dk]; null where there is one
-    float* rows[2];       // q.dq and k.dk: [parts][T][Hv]; null without dg
+    float* rows[2];       // q.dq and k.dk: [parts][T][Hv]
+    float* chunk[2];      // what a chunk's rows of them get from and give to other chunks: [T / 64 + nseq][Hv][parts]
     float* snap;          // S^T after every kPiece-th token, in the walk's layout
     float* meet;          // (dS . S) at the ends of the pieces: [T / kPiece + nseq][Hv][parts]
     double* dgsum;        // one decay for a head: dg by piece, [T / kPiece + nseq][Hv]
@@ -75,6 +82,48 @@ struct DecayArgs {
 constexpr bool decay_reverse(int kind) { return kind == kDk || kind == kDv || kind == kSumD; }
 constexpr bool decay_by_key(int kind) { return kind == kDq || kind == kDk; }  // c and the result have key heads
 
+// The r-th segment of a walk, longest first, where there are at most 64
+// sequences: a launch takes as long as the workgroup that ends last, and a
+// long segment that starts last is waited for alone. Whole segments come
+// first, then what remains of each sequence by its length (and sequences
+// without tokens). Lane s looks at sequence s.
+__device__ __forceinline__ bool segment_at(const DecayArgs& p, int64_t r, Chunk& c) {
+    if (p.nseq > 64) return chunk_at(p.cu, p.nseq, p.T, r, c, p.seg, true);
+    const int l = lane_id();
+    const Seq q = l < p.nseq ? seq_at(p.cu, l, p.T) : Seq{0, 0, 0};
+    const int whole = q.len / p.seg, rest = l < p.nseq && (q.len == 0 || q.len % p.seg) ? q.len % p.seg : -1;
+    int before = whole;  // running sum of the whole ones
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+        const int v = __shfl_up(before, d);
+        before += l >= d ? v : 0;
+    }
+    const int all = __builtin_amdgcn_readlane(before, 63);
+    int at, index;
+    if (r < all) {
+        at = __popcll(__ballot(before <= r));
+        index = (int)r - __builtin_amdgcn_readlane(before - whole, at);
+    } else {
+        int rank = 0;
+        for (int s = 0; s < p.nseq; ++s) {
+            const int v = __builtin_amdgcn_readlane(rest, s);
+            rank += v > rest || (v == rest && s < l);
+        }
+        const uint64_t hit = __ballot(rest >= 0 && rank == (int)r - all);
+        if (!hit) return false;
+        at = __ffsll((unsigned long long)hit) - 1;
+        index = __builtin_amdgcn_readlane(whole, at);
+    }
+    const int len = __builtin_amdgcn_readlane(q.len, at);
+    const int start = __builtin_amdgcn_readlane((int)q.start, at);
+    c.start = (int64_t)start + (int64_t)index * p.seg;
+    c.n = min(len - index * p.seg, p.seg);
+    c.seq = at;
+    c.index = index;
+    c.last = len - index * p.seg <= p.seg;
+    return true;
+}
+
 // One side's rows: those of head h of H, columns off .. off + width - 1 of D
 template <typename T>
 struct Side {
@@ -82,42 +131,81 @@ struct Side {
     int stride, width;
     __device__ __forceinline__ Side(const void* base, int64_t start, int H, int h, int D, int off, int w)
         : p(static_cast<const T*>(base) + ((size_t)start * H + h) * D + off), stride(H * D), width(w) {}
+    // byte offset of column c of row i, which a multiple of rows may be added to
+    __device__ __forceinline__ uint32_t at(int i, int c) const {
+        return c < width ? (uint32_t)(i * stride + c) * (uint32_t)sizeof(T) : kNowhere;
+    }
+    __device__ __forceinline__ uint32_t rows(int n) const { return (uint32_t)(n * stride) * (uint32_t)sizeof(T); }
 };
+
+// The same in every lane, as a scalar: buffer resources are to be made of it
+__device__ __forceinline__ int32_t uniform(int32_t v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ int64_t uniform(int64_t v) {
+    return (int64_t)(((uint64_t)(uint32_t)uniform((int32_t)(v >> 32)) << 32) | (uint32_t)uniform((int32_t)v));
+}
 
 // 64 rows of a side on their way to LDS, W columns of it
 template <typename T, int W, int THREADS>
 struct SideLoads {
-    static constexpr int kN = kC * W / 8 / THREADS;
+    static constexpr int kN = kC * W / 8 / THREADS, kRows = THREADS / (W / 8);  // rows between a thread's units
     Unit<T> u[kN];
+    uint32_t o;  // of its first
+    __device__ __forceinline__ explicit SideLoads(const Side<T>& s) : o(s.at(threadIdx.x / (W / 8), threadIdx.x % (W / 8) * 8)) {}
     __device__ __forceinline__ void load(const Side<T>& s, int64_t row, int n) {
         const auto r = rows_rsrc(s.p + row * s.stride, n, s.stride, s.width);
+        const uint32_t at = fresh(o);
 #pragma unroll
-        for (int x = 0; x < kN; ++x) {
-            const int i = (threadIdx.x + x * THREADS) / (W / 8), c = (threadIdx.x + x * THREADS) % (W / 8);
-            u[x].load(r, c * 8 < s.width ? (uint32_t)(i * s.stride + c * 8) * (uint32_t)sizeof(T) : kNowhere);
-        }
+        for (int x = 0; x < kN; ++x) u[x].load(r, at + s.rows(x * kRows));
     }
-    // columns in places (they are a product's k), or as they come
-    __device__ __forceinline__ void put_places(RowTile<T, W>& t) const {
-#pragma unroll
-        for (int x = 0; x < kN; ++x)
-            t.put((threadIdx.x + x * THREADS) / (W / 8), (threadIdx.x + x * THREADS) % (W / 8), u[x]);
-    }
-    __device__ __forceinline__ void put_plain(RowTile<T, W>& t) const {
+    __device__ __forceinline__ void put(RowTile<T, W>& t) const {
 #pragma unroll
         for (int x = 0; x < kN; ++x) {
             T* const p = t.x + RowTile<T, W>::L::at((threadIdx.x + x * THREADS) / (W / 8), (threadIdx.x + x * THREADS) % (W / 8));
-            u[x].put_half(p, 0);
-            u[x].put_half(p + 4, 1);
+            if constexpr (sizeof(T) == 2) {
+                *reinterpret_cast<u32x4*>(p) = u[x].w;
+            } else {
+                u[x].put_half(p, 0);
+                u[x].put_half(p + 4, 1);
+            }
         }
     }
 };
 
-// Columns of c: in a tile that is stored plain, the reading that gives columns
-// 16 m + n of one in places gives 32 (m / 2) + 8 (n / 4) + 4 (m % 2) + n % 4.
-// A result whose rows are those of tiles m = 2 i and 2 i + 1 then leaves in
-// each lane eight columns that lie together, 32 i + 8 (l / 16) .. + 7.
+// Tiles hold their columns as they come. RowTile's reading of columns 16 m + n
+// then gives columns 32 (m / 2) + 8 (n / 4) + 4 (m % 2) + n % 4, so that what
+// tiles m = 2 i and 2 i + 1 of a result leave in a lane are eight rows that lie
+// together, 32 i + 8 (l / 16) .. + 7: the order in which the next product takes
+// its k, and columns of out that are stored together.
 __device__ __forceinline__ int decay_col(int m, int n) { return (m >> 1) * 32 + (n >> 2) * 8 + (m & 1) * 4 + (n & 3); }
+
+__device__ __forceinline__ void unit_values(const Unit<uint16_t>& u, float (&v)[8]) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        v[2 * e] = bf16_to_f32(u.w[e]);
+        v[2 * e + 1] = bf16_hi_to_f32(u.w[e]);
+    }
+}
+__device__ __forceinline__ void unit_values(const Unit<float>& u, float (&v)[8]) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = u.w[e >> 2][e & 3];
+}
+// the values that an operand's planes hold
+__device__ __forceinline__ void frag_values(const Frag<1>& f, float (&v)[8]) {
+    const u32x4 w = __builtin_bit_cast(u32x4, f.p[0]);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        v[2 * e] = bf16_to_f32(w[e]);
+        v[2 * e + 1] = bf16_hi_to_f32(w[e]);
+    }
+}
+__device__ __forceinline__ void frag_values(const Frag<3>& f, float (&v)[8]) {
+    float a[8], b[8];
+    frag_values(Frag<1>{{f.p[2]}}, v);
+    frag_values(Frag<1>{{f.p[1]}}, a);
+    frag_values(Frag<1>{{f.p[0]}}, b);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = (v[e] + a[e]) + b[e];
+}
 
 __device__ __forceinline__ float wave_sum(float v) {
     v = sum16(v);
@@ -125,15 +213,19 @@ __device__ __forceinline__ float wave_sum(float v) {
     return v + __shfl_xor(v, 32);
 }
 
+// Of one chunk: G and its exponentials
+struct DecayRows {
+    double G[kC];
+    float into[kC], onto[kC];     // decay from the state to a row, and from a row to the state
+    float whole;                  // of the chunk
+};
 template <typename T, int DBP, int CT, int NP>
 struct DecayTiles {
     RowTile<T, DBP> a, b;
     RowTile<T, 64 * CT> c;
     u32x4 P[8 * NP][64];          // [row tile][block of 32 columns][plane]: as one lane reads them
-    double G[kC];
-    float into[kC], onto[kC];     // decay from the state to a row, and from a row to the state
-    float whole;                  // of the chunk
-    float red[4][kC];
+    DecayRows rows[2];            // this chunk's and the next one's
+    float dot[4][kC], sum[2][4];  // by wave: dg's row sums; the anchor and the chunk's sum
 };
 
 // One workgroup of four waves per (segment, value head, slice of the state's
@@ -142,10 +234,12 @@ struct DecayTiles {
 // The state's columns do not meet, so a wave keeps its own in registers; the
 // decayed products P = D . A B^T are shared through LDS, a row tile from each
 // wave. The products leave rows of the state as rows of a register, which is
-// how the next product takes them (kplace), and rows of out along the lanes.
-// kDots: rows of out times rows of q or k, for dg.
+// how the next product takes them (decay_col), and rows of out along the lanes.
+// The next chunk's rows are under way in registers meanwhile, those of a in
+// the first half of a chunk and those of b and c in the second, so that two
+// workgroups share a CU. DOTS: rows of out times rows of q or k, for dg.
 template <typename T, int KIND, int DBP, int CT, bool DOTS>
-__global__ __launch_bounds__(256) void k_decay_walk(DecayArgs p) {
+__global__ __launch_bounds__(256, kExact<T> == 1 ? 2 : 1) void k_decay_walk(DecayArgs p) {
     constexpr int NX = kExact<T>;
     // Planes of P and of the state where out is formed: two hold 16 bits, of
     // which a bf16 result keeps 8; dg and fp32 results see all three. What is
@@ -153,19 +247,22 @@ __global__ __launch_bounds__(256) void k_decay_walk(DecayArgs p) {
     constexpr int NP = NX == 3 || DOTS ? 3 : 2;
     constexpr bool REV = decay_reverse(KIND), SUM = KIND == kSumS || KIND == kSumD, KEYS = decay_by_key(KIND);
     constexpr int MT = DBP / 16, KS = DBP / 32, COLS = 64 * CT;
+    constexpr int kFew = REV ? 3 : 0;  // the wave with the fewest tiles of P has G to do
     __shared__ alignas(16) DecayTiles<T, DBP, CT, NP> lds;
     const int Dc = KEYS ? p.Dk : p.Dv, Db = KEYS ? p.Dv : p.Dk;
     const int ncb = (Dc + COLS - 1) / COLS, slices = KEYS ? p.slices : 1, group = p.Hv / p.Hk;
     const Spread sp = spread(blockIdx.x, group * slices * ncb);
     if (sp.group >= (p.T / p.seg + p.nseq) * (int64_t)p.Hk) return;
     Chunk sg;
-    if (!chunk_at(p.cu, p.nseq, p.T, sp.group / p.Hk, sg, p.seg, true)) return;
+    if (!segment_at(p, sp.group / p.Hk, sg)) return;
+    sg = {uniform(sg.start), uniform(sg.n), uniform(sg.seq), uniform(sg.index), uniform((int32_t)sg.last) != 0};
     if (SUM && (REV ? sg.index == 0 : sg.last)) return;
     const int hk = (int)(sp.group % p.Hk), cb = sp.member % ncb, slice = sp.member / ncb % slices;
     const int hv = hk * group + sp.member / (ncb * slices);
     const int wave = wave_id(), l = lane_id(), l16 = l & 15, l4 = l >> 4;
     const int col0 = cb * COLS, off = slice * kDecayMaxDb, db = min(Db - off, DBP), parts = slices * ncb;
-    const int64_t state0 = (sg.start - sg.index * p.seg) / p.seg + sg.index;  // of the state behind this segment
+    const int64_t first = sg.start - sg.index * p.seg;    // of the sequence
+    const int64_t state0 = first / p.seg + sg.index;      // of the state behind this segment
     // a and b by the heads that have them
     const void* const ta = KIND == kOut ? p.q : KIND == kDq ? p.dout : KIND == kDk ? p.v : p.k;
     const void* const tb = KIND == kOut || KIND == kSumS ? p.k : KIND == kDq ? p.v : KIND == kDk ? p.dout : p.q;
@@ -173,279 +270,351 @@ __global__ __launch_bounds__(256) void k_decay_walk(DecayArgs p) {
     const int Hb = KEYS ? p.Hv : p.Hk, hb = KEYS ? hv : hk, Hc = KEYS ? p.Hk : p.Hv, hc = KEYS ? hk : hv;
     const Side<T> sa(ta, sg.start, Hb, hb, Db, off, db), sb(tb, sg.start, Hb, hb, Db, off, db);
     const Side<T> sc(tc, sg.start, Hc, hc, Dc, col0, min(Dc - col0, COLS));
-    // the state's element (row of b, column of c) in tensors of [Dk][Dv]
-    const auto element = [&](int row, int col) { return KEYS ? (size_t)col * p.Dv + row : (size_t)row * p.Dv + col; };
-    const auto state_ptr = [&](const float* base, int64_t n) { return base + ((size_t)n * p.Hv + hv) * p.Dk * p.Dv; };
-    const auto each = [&](auto f) {  // of the lane's elements
+    // a lane's columns of out: 4 CT from here on
+    const int col = col0 + (CT == 2 ? wave * 32 + l4 * 8 : (wave >> 1) * 32 + l4 * 8 + (wave & 1) * 4);
+    // The state in a tensor of [Dk][Dv], of which this workgroup has rows off ..
+    // of b and columns col0 .. of c: a lane's elements at(m, ct, r), four rows
+    // r of b together where b is v's or dout's
+    f32x4 S[MT][CT] = {};
+    const auto state_rsrc = [&](const float* base, int64_t n) {
+        return bytes_rsrc(base + ((size_t)n * p.Hv + hv) * p.Dk * p.Dv, (uint32_t)(p.Dk * p.Dv) * 4u);
+    };
+    const auto at = [&](int m, int ct, int r) {
+        const int row = decay_col(m, l4 * 4 + r), c = col0 + decay_col(wave * CT + ct, l16);
+        return row < db && c < Dc ? (uint32_t)(KEYS ? c * p.Dv + off + row : (off + row) * p.Dv + c) * 4u : kNowhere;
+    };
+    const auto state_at = [&](__amdgpu_buffer_rsrc_t r, int m, int ct) {
+        if constexpr (KEYS) return __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)at(m, ct, 0), 0, 0));
+        f32x4 v;
 #pragma unroll
-        for (int ct = 0; ct < CT; ++ct)
+        for (int x = 0; x < 4; ++x) v[x] = Elt<float>::cvt(Elt<float>::raw_rsrc(r, at(m, ct, x)));
+        return v;
+    };
+    const auto store_state = [&](const float* base, int64_t n) {
+        const auto r = state_rsrc(base, n);
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) Elt<float>::st_rsrc<0>(r, at(m, ct, x), S[m][ct][x]);
+    };
+    if constexpr (!SUM) {
+        const float* from = nullptr;
+        int64_t n = 0;
+        if (REV ? !sg.last : sg.index > 0) {
+            from = p.joint[REV];
+            n = REV ? state0 : state0 - 1;
+        } else {
+            from = REV ? p.dhT : p.h0;
+            n = sg.seq;
+        }
+        if (from) {
+            const auto r = state_rsrc(from, n);
 #pragma unroll
             for (int m = 0; m < MT; ++m)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int row = m * 16 + l4 * 4 + r, col = col0 + decay_col(wave * CT + ct, l16);
-                    if (row < db && col < Dc) f(m, ct, r, element(off + row, col));
-                }
-    };
-    f32x4 S[MT][CT] = {};
-    if constexpr (!SUM) {
-        const float* from = nullptr;
-        if (!REV) from = sg.index > 0 ? state_ptr(p.joint[0], state0 - 1) : p.h0 ? state_ptr(p.h0, sg.seq) : nullptr;
-        else from = !sg.last ? state_ptr(p.joint[1], state0) : p.dhT ? state_ptr(p.dhT, sg.seq) : nullptr;
-        if (from) each([&](int m, int ct, int r, size_t e) { S[m][ct][r] = from[e]; });
+                for (int ct = 0; ct < CT; ++ct) S[m][ct] = state_at(r, m, ct);
+        }
     }
     const int chunks = (sg.n + kC - 1) / kC;
-    SideLoads<T, DBP, 256> la, lb;
-    SideLoads<T, COLS, 256> lc;
+    SideLoads<T, DBP, 256> la(sa), lb(sb);
+    SideLoads<T, COLS, 256> lc(sc);
     uint32_t lg;
-    const auto load = [&](int i) {  // the i-th chunk of the walk
-        const int ch = REV ? chunks - 1 - i : i;
-        const int n = i < chunks ? min(sg.n - ch * kC, kC) : 0;
-        if constexpr (!SUM) la.load(sa, (int64_t)ch * kC, n);
-        lb.load(sb, (int64_t)ch * kC, n);
-        lc.load(sc, (int64_t)ch * kC, n);
-        const int64_t t = sg.start + ch * kC;
+    const auto chunk = [&](int i) { return REV ? chunks - 1 - i : i; };  // the walk's i-th
+    const auto tokens = [&](int i) { return i < chunks ? min(sg.n - chunk(i) * kC, kC) : 0; };
+    const auto load_a = [&](int i) {
+        const int n = tokens(i);
+        if constexpr (!SUM) la.load(sa, (int64_t)chunk(i) * kC, n);
+        const int64_t t = sg.start + chunk(i) * kC;
         lg = Elt<float>::raw_rsrc(rows_rsrc(p.g + (p.gstride ? t * p.gstride : 0) + hv, n, p.gstride, 1),
                                   l < n ? (uint32_t)(l * p.gstride) * 4u : kNowhere);
     };
+    const auto load_bc = [&](int i) {
+        const int n = tokens(i);
+        lb.load(sb, (int64_t)chunk(i) * kC, n);
+        lc.load(sc, (int64_t)chunk(i) * kC, n);
+    };
     double total = 0.0;
-    load(0);
+    const auto put_rows = [&](int i) {
+        if (wave != kFew || i >= chunks) return;
+        DecayRows& to = lds.rows[i & 1];
+        const double G = chunk_decay_sum(l < tokens(i) ? Elt<float>::cvt(lg) : 0.0f), last = read_lane(G, kC - 1);
+        to.G[l] = G;
+        const float head = decay_of(G), tail = decay_of(last - G);
+        to.into[l] = REV ? tail : head * p.scale;
+        to.onto[l] = REV ? head * p.scale : tail;
+        if (l == 0) to.whole = decay_of(last);
+        total += last;
+    };
+    load_a(0);
+    load_bc(0);
+    if constexpr (!SUM) la.put(lds.a);
+    lb.put(lds.b);
+    lc.put(lds.c);
+    put_rows(0);
+    __syncthreads();
     for (int i = 0; i < chunks; ++i) {
-        const int ch = REV ? chunks - 1 - i : i, n = min(sg.n - ch * kC, kC);
-        const int64_t t0 = sg.start + ch * kC;
+        const int n = tokens(i);
+        const int64_t t0 = sg.start + chunk(i) * kC;
+        const DecayRows& rows = lds.rows[i & 1];
         // dg's anchors: the state S^T of dq's walk behind every piece meets dS^T of dk's
-        const int64_t from_seq = sg.index * p.seg + ch * kC;
-        const bool piece_end = (from_seq + kC) % kPiece == 0 && !(sg.last && ch == chunks - 1);
-        const int64_t pieces = (sg.start - sg.index * p.seg) / kPiece + from_seq / kPiece;
-        float* snap = nullptr;
-        if constexpr (DOTS)
-            snap = p.snap + (((size_t)pieces * p.Hv + hv) * parts + slice * ncb + cb) * (DBP * COLS) +
-                   (size_t)wave * (MT * CT * 256) + l * 4;
-        if constexpr (!SUM) la.put_places(lds.a);
-        lb.put_places(lds.b);
-        lc.put_plain(lds.c);
-        if (wave == 0) {
-            const double G = chunk_decay_sum(l < n ? Elt<float>::cvt(lg) : 0.0f), last = read_lane(G, kC - 1);
-            lds.G[l] = G;
-            const float head = decay_of(G), tail = decay_of(last - G);
-            lds.into[l] = REV ? tail : head * p.scale;
-            lds.onto[l] = REV ? head * p.scale : tail;
-            if (l == 0) lds.whole = decay_of(last);
-            total += last;
+        const int64_t from_seq = t0 - first, piece = first / kPiece + from_seq / kPiece;
+        const bool piece_end = DOTS && (from_seq + kC) % kPiece == 0 && !(sg.last && chunk(i) == chunks - 1);
+        const auto snap = [&]() {  // the wave's part of it; tile i lies 1024 i bytes on
+            return bytes_rsrc(p.snap + (((size_t)piece * p.Hv + hv) * parts + slice * ncb + cb) * (DBP * COLS) +
+                                  (size_t)wave * (MT * CT * 256), MT * CT * 1024);
+        };
+        Unit<T> dots[DOTS ? 4 : 1];
+        if constexpr (DOTS) {
+            const Side<T> sd(KIND == kDq ? p.q : p.k, t0, p.Hk, hk, p.Dk, 0, p.Dk);
+            const auto r = rows_rsrc(sd.p, n, sd.stride, sd.width);
+            const uint32_t at = sd.at(fresh(l16), col & ~7);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) dots[t].load(r, at + sd.rows(t * 16));
         }
+        load_a(i + 1);
         if constexpr (DOTS && KIND == kDk) {
             if (piece_end) {
                 float e = 0.0f;
+                const auto sr = snap();
 #pragma unroll
                 for (int m = 0; m < MT; ++m)
 #pragma unroll
                     for (int ct = 0; ct < CT; ++ct) {
-                        const f32x4 w = *reinterpret_cast<const f32x4*>(snap + (m * CT + ct) * 256);
+                        const f32x4 w = __builtin_bit_cast(
+                            f32x4, __builtin_amdgcn_raw_buffer_load_b128(sr, l * 16, (m * CT + ct) * 1024, 0));
 #pragma unroll
                         for (int r = 0; r < 4; ++r) e = fmaf(S[m][ct][r], w[r], e);
                     }
                 e = wave_sum(e);
-                if (l == 0) lds.red[wave][0] = e;
+                if (l == 0) lds.sum[0][wave] = e;
             }
         }
-        __syncthreads();
-        if constexpr (DOTS && KIND == kDk) {
-            if (piece_end && threadIdx.x == 0)
-                p.meet[((size_t)(pieces + sg.seq) * p.Hv + hv) * parts + slice * ncb + cb] =
-                    (lds.red[0][0] + lds.red[1][0]) + (lds.red[2][0] + lds.red[3][0]);
-        }
-        load(i + 1);
         f32x4 o[CT][4] = {};
+        // the lane's share of rows of out times rows of q or k, rows 16 t + l16
+        const auto dot_of = [&](int t) {
+            float v[8], e = 0.0f;
+            unit_values(dots[DOTS ? t : 0], v);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                if constexpr (CT == 2) e = fmaf(o[CT - 1][t][x], v[4 + x], fmaf(o[0][t][x], v[x], e));
+                else {
+                    const float lo = v[x], hi = v[4 + x];
+                    e = fmaf(o[0][t][x], wave & 1 ? hi : lo, e);
+                }
+            }
+            return e;
+        };
         if constexpr (!SUM) {
+            const int ml = (int)fresh((uint32_t)l), m16 = ml & 15, m4 = ml >> 4;  // addresses are this half's own
             // P: wave w has rows 16 w .. + 15 along its lanes
             f32x4 x[4] = {};
 #pragma unroll
             for (int s = 0; s < KS; ++s) {
-                const Frag<NX> fa = lds.a.frag(wave * 16 + l16, s * 4 + l4);
+                const Frag<NX> fa = lds.a.frag(wave * 16 + m16, s * 4 + m4);
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    if (REV ? j >= wave : j <= wave) mma<NX>(x[j], lds.b.frag(j * 16 + l16, s * 4 + l4), fa);
+                    if (REV ? j >= wave : j <= wave) mma<NX>(x[j], lds.b.frag(j * 16 + m16, s * 4 + m4), fa);
             }
-            const int row = wave * 16 + l16;
-            const double Gi = lds.G[row];
+            const int row = wave * 16 + m16;
+            const double Gi = rows.G[row];
 #pragma unroll
             for (int j = 0; j < 4; ++j)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    const int col = j * 16 + l4 * 4 + r;
-                    const float d = decay_of(REV ? lds.G[col] - Gi : Gi - lds.G[col]) * p.scale;
-                    x[j][r] = (REV ? col >= row : col <= row) ? d * x[j][r] : 0.0f;
+                    const int c = j * 16 + m4 * 4 + r;
+                    float d = decay_of(REV ? rows.G[c] - Gi : Gi - rows.G[c]) * p.scale;
+                    asm volatile("" : "+v"(d));  // formed for every element, without branches
+                    x[j][r] = (REV ? c >= row : c <= row) ? d * x[j][r] : 0.0f;
                 }
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
                 if (REV ? s == 0 && wave >= 2 : s == 1 && wave < 2) continue;
                 const Frag<NP> f = split_tiles<NP>(x[2 * s], x[2 * s + 1]);
 #pragma unroll
-                for (int i = 0; i < NP; ++i) lds.P[(wave * 2 + s) * NP + i][l] = __builtin_bit_cast(u32x4, f.p[i]);
+                for (int i = 0; i < NP; ++i) lds.P[(wave * 2 + s) * NP + i][ml] = __builtin_bit_cast(u32x4, f.p[i]);
             }
             // A X, rows of out along the lanes
 #pragma unroll
             for (int s = 0; s < KS; ++s) {
+                __builtin_amdgcn_sched_barrier(0);
                 Frag<NP> fs[CT];
 #pragma unroll
                 for (int ct = 0; ct < CT; ++ct) fs[ct] = split_tiles<NP>(S[2 * s][ct], S[2 * s + 1][ct]);
 #pragma unroll
                 for (int t = 0; t < 4; ++t) {
-                    const Frag<NX> fa = lds.a.frag(t * 16 + l16, s * 4 + l4);
+                    const Frag<NX> fa = lds.a.frag(t * 16 + m16, s * 4 + m4);
 #pragma unroll
                     for (int ct = 0; ct < CT; ++ct) mma<NP>(o[ct][t], fs[ct], fa);
                 }
             }
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
-                const float d = lds.into[t * 16 + l16];
+                const float d = rows.into[t * 16 + m16];
 #pragma unroll
                 for (int ct = 0; ct < CT; ++ct) o[ct][t] *= d;
             }
+            if constexpr (DOTS) {
+                float e = 0.0f;
+#pragma unroll
+                for (int t = 0; t < 4; ++t) e += dot_of(t);
+                e = wave_sum(e);
+                if (l == 0) lds.sum[1][wave] = e;
+            }
             __syncthreads();
+            if constexpr (DOTS) {
+                const float* const w = lds.sum[threadIdx.x & 1];
+                const float e = (w[0] + w[1]) + (w[2] + w[3]);
+                if (threadIdx.x == 1)
+                    p.chunk[REV][((size_t)(first / kC + sg.seq + from_seq / kC) * p.Hv + hv) * parts + slice * ncb + cb] = e;
+                if (KIND == kDk && threadIdx.x == 0 && piece_end)
+                    p.meet[((size_t)(piece + sg.seq) * p.Hv + hv) * parts + slice * ncb + cb] = e;
+            }
+            la.put(lds.a);
         }
-        const float whole = lds.whole;
+        load_bc(i + 1);
+        put_rows(i + 1);
+        const float whole = rows.whole;
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct) S[m][ct] *= whole;
+        const int ml = (int)fresh((uint32_t)l);
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            const f32x4 w0 = *reinterpret_cast<const f32x4*>(lds.onto + s * 32 + l4 * 4);
-            const f32x4 w1 = *reinterpret_cast<const f32x4*>(lds.onto + s * 32 + 16 + l4 * 4);
+            __builtin_amdgcn_sched_barrier(0);
             Frag<NX> fc[CT];
-            Frag<3> fw[CT];
 #pragma unroll
-            for (int ct = 0; ct < CT; ++ct) {
-                const int m = wave * CT + ct;
-                fc[ct] = lds.c.token_frag(l, s, m);
-                float c0[4], c1[4];
-                lds.c.values4(l, 2 * s, m, c0);
-                lds.c.values4(l, 2 * s + 1, m, c1);
-                fw[ct] = split8<3>({c0[0] * w0[0], c0[1] * w0[1], c0[2] * w0[2], c0[3] * w0[3], c1[0] * w1[0],
-                                    c1[1] * w1[1], c1[2] * w1[2], c1[3] * w1[3]});
-            }
+            for (int ct = 0; ct < CT; ++ct) fc[ct] = lds.c.token_frag(ml, s, wave * CT + ct);
             if constexpr (!SUM) {
 #pragma unroll
                 for (int t = 0; t < 4; ++t) {
                     if (REV ? s == 0 && t >= 2 : s == 1 && t < 2) continue;
                     Frag<NP> f;
 #pragma unroll
-                    for (int i = 0; i < NP; ++i) f.p[i] = __builtin_bit_cast(bf16x8, lds.P[(t * 2 + s) * NP + i][l]);
+                    for (int i = 0; i < NP; ++i) f.p[i] = __builtin_bit_cast(bf16x8, lds.P[(t * 2 + s) * NP + i][ml]);
 #pragma unroll
                     for (int ct = 0; ct < CT; ++ct) mma<NP>(o[ct][t], fc[ct], f);
                 }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            const f32x4 w0 = *reinterpret_cast<const f32x4*>(rows.onto + s * 32 + (ml >> 4) * 4);
+            const f32x4 w1 = *reinterpret_cast<const f32x4*>(rows.onto + s * 32 + 16 + (ml >> 4) * 4);
+            Frag<3> fw[CT];
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) {
+                float x[8];
+                frag_values(fc[ct], x);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    x[e] *= w0[e];
+                    x[4 + e] *= w1[e];
+                }
+                fw[ct] = split8<3>(x);
             }
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
-                const Frag<NX> fb = lds.b.token_frag(l, s, m);
+                const Frag<NX> fb = lds.b.token_frag(ml, s, m);
 #pragma unroll
                 for (int ct = 0; ct < CT; ++ct) mma<3>(S[m][ct], fb, fw[ct]);
             }
         }
+        __builtin_amdgcn_sched_barrier(0);
         if constexpr (!SUM) {
-            // out: a lane has 4 CT columns of the rows 16 t + l16
-            const int D = Dc, H = KEYS ? p.Hk : p.Hv, h = KEYS ? hk : hv;
-            const int col = col0 + (CT == 2 ? wave * 32 + l4 * 8 : (wave >> 1) * 32 + l4 * 8 + (wave & 1) * 4);
-            const int members = group * slices;
-            const bool partial = KEYS && members > 1;
-            if (partial) {
-                const int member = sp.member / ncb;
-                float* const base = p.part[REV] + (((size_t)t0 * H + h) * members + member) * D;
-                const auto r = rows_rsrc(base, n, H * members * D, D);
+            const int H = KEYS ? p.Hk : p.Hv, h = KEYS ? hk : hv, members = group * slices;
+            if (KEYS && members > 1) {
+                const Side<float> to(p.part[REV], t0, H * members, h * members + sp.member / ncb, Dc, 0, Dc);
+                const auto r = rows_rsrc(to.p, n, to.stride, Dc);
+                const uint32_t at = to.at(fresh(l16), col);
 #pragma unroll
                 for (int t = 0; t < 4; ++t)
 #pragma unroll
                     for (int ct = 0; ct < CT; ++ct)
-                        __builtin_amdgcn_raw_buffer_store_b128(
-                            __builtin_bit_cast(u32x4, o[ct][t]), r,
-                            (int)(col < D ? (uint32_t)((t * 16 + l16) * (H * members * D) + col + ct * 4) * 4u : kNowhere), 0, 0);
+                        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, o[ct][t]), r,
+                                                               (int)(at + to.rows(t * 16) + ct * 16), 0, 0);
             } else {
-                T* const base = static_cast<T*>(KIND == kOut ? p.out : KIND == kDq ? p.dq : KIND == kDk ? p.dk : p.dv) +
-                                ((size_t)t0 * H + h) * D;
-                const auto r = rows_rsrc(base, n, H * D, D);
+                const Side<T> to(KIND == kOut ? p.out : KIND == kDq ? p.dq : KIND == kDk ? p.dk : p.dv, t0, H, h, Dc, 0, Dc);
+                const auto r = rows_rsrc(to.p, n, to.stride, Dc);
+                const uint32_t at = to.at(fresh(l16), col);
 #pragma unroll
                 for (int t = 0; t < 4; ++t) {
-                    const uint32_t at = col < D ? (uint32_t)((t * 16 + l16) * H * D + col) * (uint32_t)sizeof(T) : kNowhere;
                     if constexpr (CT == 2) {
                         Unit<T> u;
                         const f32x4 y = o[0][t], z = o[CT - 1][t];
                         u.pack({y[0], y[1], y[2], y[3], z[0], z[1], z[2], z[3]});
-                        u.store(r, at);
+                        u.store(r, at + to.rows(t * 16));
                     } else if constexpr (NX == 3) {
-                        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, o[0][t]), r, (int)at, 0, 0);
+                        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, o[0][t]), r,
+                                                               (int)(at + to.rows(t * 16)), 0, 0);
                     } else {
                         const f32x4 y = o[0][t];
                         const u32x2 w = {(uint32_t)f32_to_bf16(y[0]) | ((uint32_t)f32_to_bf16(y[1]) << 16),
                                          (uint32_t)f32_to_bf16(y[2]) | ((uint32_t)f32_to_bf16(y[3]) << 16)};
-                        __builtin_amdgcn_raw_buffer_store_b64(w, r, (int)at, 0, 0);
+                        __builtin_amdgcn_raw_buffer_store_b64(w, r, (int)(at + to.rows(t * 16)), 0, 0);
                     }
                 }
             }
             if constexpr (DOTS) {
-                const Side<T> sd(KIND == kDq ? p.q : p.k, t0, p.Hk, hk, p.Dk, 0, p.Dk);
-                const auto r = rows_rsrc(sd.p, n, sd.stride, sd.width);
 #pragma unroll
                 for (int t = 0; t < 4; ++t) {
-                    float e = 0.0f;
-#pragma unroll
-                    for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-                        for (int x = 0; x < 4; ++x) {
-                            const uint32_t at = col < D ? (uint32_t)((t * 16 + l16) * sd.stride + col + ct * 4 + x) * (uint32_t)sizeof(T) : kNowhere;
-                            e = fmaf(o[ct][t][x], Elt<T>::cvt(Elt<T>::raw_rsrc(r, at)), e);
-                        }
+                    float e = dot_of(t);
                     e += __shfl_xor(e, 16);
                     e += __shfl_xor(e, 32);
-                    if (l4 == 0) lds.red[wave][t * 16 + l16] = e;
+                    if (l4 == 0) lds.dot[wave][t * 16 + l16] = e;
                 }
                 if constexpr (KIND == kDq) {
                     if (piece_end) {
+                        const auto sr = snap();
 #pragma unroll
                         for (int m = 0; m < MT; ++m)
 #pragma unroll
                             for (int ct = 0; ct < CT; ++ct)
-                                *reinterpret_cast<f32x4*>(snap + (m * CT + ct) * 256) = S[m][ct];
+                                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, S[m][ct]), sr, l * 16,
+                                                                       (m * CT + ct) * 1024, 0);
                     }
                 }
             }
         }
         __syncthreads();
+        lb.put(lds.b);
+        lc.put(lds.c);
         if constexpr (DOTS) {
             if (threadIdx.x < n) {
                 const int x = threadIdx.x;
                 p.rows[REV][((size_t)(slice * ncb + cb) * p.T + t0 + x) * p.Hv + hv] =
-                    (lds.red[0][x] + lds.red[1][x]) + (lds.red[2][x] + lds.red[3][x]);
+                    (lds.dot[0][x] + lds.dot[1][x]) + (lds.dot[2][x] + lds.dot[3][x]);
             }
-            __syncthreads();
         }
+        __syncthreads();
     }
     if constexpr (SUM) {
-        float* const to = const_cast<float*>(state_ptr(p.joint[REV], state0 - REV));
-        each([&](int m, int ct, int r, size_t e) { to[e] = S[m][ct][r]; });
-        if (threadIdx.x == 0 && cb == 0) p.seg_decay[REV][(size_t)(state0 - REV) * p.Hv + hv] = decay_of(total);
+        store_state(p.joint[REV], state0 - REV);
+        if (wave == kFew && l == 0 && cb == 0) p.seg_decay[REV][(size_t)(state0 - REV) * p.Hv + hv] = decay_of(total);
     } else if constexpr (KIND == kOut) {
-        if (p.hT && sg.last) {
-            float* const to = const_cast<float*>(state_ptr(p.hT, sg.seq));
-            each([&](int m, int ct, int r, size_t e) { to[e] = S[m][ct][r]; });
-        }
+        if (p.hT && sg.last) store_state(p.hT, sg.seq);
     } else if constexpr (KIND == kDv) {
-        if (p.dh0 && sg.index == 0) {
-            float* const to = const_cast<float*>(state_ptr(p.dh0, sg.seq));
-            each([&](int m, int ct, int r, size_t e) { to[e] = S[m][ct][r]; });
-        }
+        if (p.dh0 && sg.index == 0) store_state(p.dh0, sg.seq);
     } else if constexpr (DOTS && KIND == kDq) {
         if (p.dhT && sg.last) {  // the last piece's anchor
-            const float* const w = state_ptr(p.dhT, sg.seq);
+            const auto r = state_rsrc(p.dhT, sg.seq);
             float e = 0.0f;
-            each([&](int m, int ct, int r, size_t at) { e = fmaf(S[m][ct][r], w[at], e); });
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) {
+                    const f32x4 w = state_at(r, m, ct);
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) e = fmaf(S[m][ct][x], w[x], e);
+                }
             e = wave_sum(e);
-            if (l == 0) lds.red[wave][0] = e;
+            if (l == 0) lds.sum[0][wave] = e;
             __syncthreads();
-            const int64_t first = sg.start - sg.index * p.seg, len = sg.index * p.seg + sg.n;
+            const int64_t len = sg.start - first + sg.n;
             if (threadIdx.x == 0 && len > 0)
                 p.meet[((size_t)(first / kPiece + sg.seq + (len - 1) / kPiece) * p.Hv + hv) * parts + slice * ncb + cb] =
-                    (lds.red[0][0] + lds.red[1][0]) + (lds.red[2][0] + lds.red[3][0]);
+                    (lds.sum[0][0] + lds.sum[0][1]) + (lds.sum[0][2] + lds.sum[0][3]);
         }
     }
 }

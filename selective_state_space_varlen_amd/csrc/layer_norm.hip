@@ -282,20 +282,30 @@ __global__ __launch_bounds__(kLnThreads) void k_layer_norm_bwd(LnArgs a) {
         if (!again || added) flush();
 }
 
-// The groups' sums of one head, 32 columns a workgroup
+// The groups' sums of one head, 32 columns a workgroup, every 32nd group a lane
+constexpr int kLnDwThreads = 1024, kLnDwLanes = kLnDwThreads / 32;
 template <typename S>
-__global__ __launch_bounds__(256) void k_layer_norm_dw(LnArgs a, int64_t groups) {
+__global__ __launch_bounds__(kLnDwThreads) void k_layer_norm_dw(LnArgs a, int64_t groups) {
     const int cols = 2 * a.D, nb = (cols + 31) / 32, head = blockIdx.x / nb, c = blockIdx.x % nb * 32 + threadIdx.x % 32;
     const int lane = threadIdx.x / 32;
     const S* const part = static_cast<const S*>(a.part);
     double s = 0.0;
-    if (c < cols)
-        for (int64_t g = head + (int64_t)lane * a.H; g < groups; g += (int64_t)8 * a.H) s += (double)part[(size_t)g * cols + c];
-    __shared__ double lds[8][32];
+    if (c < cols) {
+        constexpr int kBatch = 16;  // loads under way
+        const int64_t step = (int64_t)kLnDwLanes * a.H;
+        for (int64_t g = head + (int64_t)lane * a.H; g < groups; g += kBatch * step) {
+            S v[kBatch];
+#pragma unroll
+            for (int x = 0; x < kBatch; ++x) v[x] = g + x * step < groups ? part[(size_t)(g + x * step) * cols + c] : S(0);
+#pragma unroll
+            for (int x = 0; x < kBatch; ++x) s += (double)v[x];
+        }
+    }
+    __shared__ double lds[kLnDwLanes][32];
     lds[lane][threadIdx.x % 32] = s;
     __syncthreads();
     if (lane == 0 && c < cols) {
-        for (int i = 1; i < 8; ++i) s += lds[i][threadIdx.x];
+        for (int i = 1; i < kLnDwLanes; ++i) s += lds[i][threadIdx.x];
         float* const to = c < a.D ? a.dw : a.db;
         if (to) to[(size_t)head * a.D + (c < a.D ? c : c - a.D)] = (float)s;
     }
@@ -383,7 +393,7 @@ inline int ln_check(int64_t T, int32_t H, int32_t D, int32_t dtype) {
         T * H * D >= (int64_t(1) << 40))
         return SSMP_ERR_SHAPE;
     if (D > kLnMaxD) return SSMP_ERR_UNSUPPORTED;
-    if ((int64_t)H * ((2 * D + 31) / 32) >= kMaxBlocks) return SSMP_ERR_SHAPE;
+    if ((int64_t)H * ((2 * D + 31) / 32) >= kMaxBlocks / 4) return SSMP_ERR_SHAPE;  // k_layer_norm_dw's workgroups of 1024
     if (dtype != SSMP_F32 && dtype != SSMP_BF16) return SSMP_ERR_UNSUPPORTED;
     return SSMP_OK;
 }
@@ -475,8 +485,8 @@ extern "C" int layer_norm_pack_bwd(const void* dy, const void* h, const float* w
     if (sums) {
         const unsigned n = (unsigned)((int64_t)H * ((2 * D + 31) / 32));
         const int64_t groups = blocks * (kLnThreads / ln_form(D).lanes);
-        if (a.wide) k_layer_norm_dw<double><<<n, 256, 0, s>>>(a, groups);
-        else k_layer_norm_dw<float><<<n, 256, 0, s>>>(a, groups);
+        if (a.wide) k_layer_norm_dw<double><<<n, kLnDwThreads, 0, s>>>(a, groups);
+        else k_layer_norm_dw<float><<<n, kLnDwThreads, 0, s>>>(a, groups);
         SSMP_LAUNCH_CHECK();
     }
     return SSMP_OK;
