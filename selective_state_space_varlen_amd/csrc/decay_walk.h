@@ -207,6 +207,21 @@ __device__ __forceinline__ void frag_values(const Frag<3>& f, float (&v)[8]) {
     for (int e = 0; e < 8; ++e) v[e] = (v[e] + a[e]) + b[e];
 }
 
+// d[ct][t] += x[ct] a[t], one plane product after the other over all tiles
+template <int LIM, int NA, int NB, int CT>
+__device__ __forceinline__ void decay_mma(f32x4 (&d)[CT][4], const Frag<NA> (&x)[CT], const Frag<NB> (&a)[4]) {
+#pragma unroll
+    for (int s = LIM - 1; s >= 0; --s)
+#pragma unroll
+        for (int i = 0; i < NA; ++i)
+            if (s - i >= 0 && s - i < NB)
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct)
+                        d[ct][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[ct].p[i], a[t].p[s - i], d[ct][t], 0, 0, 0);
+}
+
 __device__ __forceinline__ float wave_sum(float v) {
     v = sum16(v);
     v += __shfl_xor(v, 16);
@@ -247,6 +262,9 @@ __global__ __launch_bounds__(256, kExact<T> == 1 ? 2 : 1) void k_decay_walk(Deca
     constexpr int NP = NX == 3 || DOTS ? 3 : 2;
     constexpr bool REV = decay_reverse(KIND), SUM = KIND == kSumS || KIND == kSumD, KEYS = decay_by_key(KIND);
     constexpr int MT = DBP / 16, KS = DBP / 32, COLS = 64 * CT;
+    // Vector operations of the next product in the shadow of one's matrix
+    // instructions; three planes leave no registers for it.
+    constexpr bool kAhead = NP == 2;
     constexpr int kFew = REV ? 3 : 0;  // the wave with the fewest tiles of P has G to do
     __shared__ alignas(16) DecayTiles<T, DBP, CT, NP> lds;
     const int Dc = KEYS ? p.Dk : p.Dv, Db = KEYS ? p.Dv : p.Dk;
@@ -254,7 +272,7 @@ __global__ __launch_bounds__(256, kExact<T> == 1 ? 2 : 1) void k_decay_walk(Deca
     const Spread sp = spread(blockIdx.x, group * slices * ncb);
     if (sp.group >= (p.T / p.seg + p.nseq) * (int64_t)p.Hk) return;
     Chunk sg;
-    if (!segment_at(p, sp.group / p.Hk, sg)) return;
+    if (SUM ? !chunk_at(p.cu, p.nseq, p.T, sp.group / p.Hk, sg, p.seg) : !segment_at(p, sp.group / p.Hk, sg)) return;
     sg = {uniform(sg.start), uniform(sg.n), uniform(sg.seq), uniform(sg.index), uniform((int32_t)sg.last) != 0};
     if (SUM && (REV ? sg.index == 0 : sg.last)) return;
     const int hk = (int)(sp.group % p.Hk), cb = sp.member % ncb, slice = sp.member / ncb % slices;
@@ -410,23 +428,30 @@ __global__ __launch_bounds__(256, kExact<T> == 1 ? 2 : 1) void k_decay_walk(Deca
             const int ml = (int)fresh((uint32_t)l), m16 = ml & 15, m4 = ml >> 4;  // addresses are this half's own
             // P: wave w has rows 16 w .. + 15 along its lanes
             f32x4 x[4] = {};
+            const auto has = [&](int j) { return REV ? j >= wave : j <= wave; };  // row tile w meets rows of tile j of b
+            {
+                Frag<NX> fa[KS];
 #pragma unroll
-            for (int s = 0; s < KS; ++s) {
-                const Frag<NX> fa = lds.a.frag(wave * 16 + m16, s * 4 + m4);
+                for (int s = 0; s < KS; ++s) fa[s] = lds.a.frag(wave * 16 + m16, s * 4 + m4);
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    if (REV ? j >= wave : j <= wave) mma<NX>(x[j], lds.b.frag(j * 16 + m16, s * 4 + m4), fa);
+                    if (has(j))
+#pragma unroll
+                        for (int s = 0; s < KS; ++s) mma<NX>(x[j], lds.b.frag(j * 16 + m16, s * 4 + m4), fa[s]);
             }
-            const int row = wave * 16 + m16;
-            const double Gi = rows.G[row];
+            const double Gi = rows.G[wave * 16 + m16];
 #pragma unroll
             for (int j = 0; j < 4; ++j)
+                if (has(j)) {
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int c = j * 16 + m4 * 4 + r;
-                    float d = decay_of(REV ? rows.G[c] - Gi : Gi - rows.G[c]) * p.scale;
-                    asm volatile("" : "+v"(d));  // formed for every element, without branches
-                    x[j][r] = (REV ? c >= row : c <= row) ? d * x[j][r] : 0.0f;
+                    for (int r = 0; r < 4; ++r) {
+                        const double Gj = rows.G[j * 16 + m4 * 4 + r];
+                        x[j][r] *= decay_of(REV ? Gj - Gi : Gi - Gj) * p.scale;
+                    }
+                    if (j == wave)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            if (REV ? m4 * 4 + r < m16 : m4 * 4 + r > m16) x[j][r] = 0.0f;
                 }
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
@@ -435,19 +460,34 @@ __global__ __launch_bounds__(256, kExact<T> == 1 ? 2 : 1) void k_decay_walk(Deca
 #pragma unroll
                 for (int i = 0; i < NP; ++i) lds.P[(wave * 2 + s) * NP + i][ml] = __builtin_bit_cast(u32x4, f.p[i]);
             }
-            // A X, rows of out along the lanes
+            // A X, rows of out along the lanes; in its shadow the state decays
+            const float whole = rows.whole;
+            Frag<NP> fs[CT], next[CT];
+            const auto planes = [&](int s, Frag<NP> (&f)[CT]) {
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) f[ct] = split_tiles<NP>(S[2 * s][ct], S[2 * s + 1][ct]);
+            };
+            if constexpr (kAhead) planes(0, next);
 #pragma unroll
             for (int s = 0; s < KS; ++s) {
                 __builtin_amdgcn_sched_barrier(0);
-                Frag<NP> fs[CT];
+                Frag<NX> fa[4];
 #pragma unroll
-                for (int ct = 0; ct < CT; ++ct) fs[ct] = split_tiles<NP>(S[2 * s][ct], S[2 * s + 1][ct]);
+                for (int t = 0; t < 4; ++t) fa[t] = lds.a.frag(t * 16 + m16, s * 4 + m4);
+                if constexpr (kAhead) {
 #pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    const Frag<NX> fa = lds.a.frag(t * 16 + m16, s * 4 + m4);
-#pragma unroll
-                    for (int ct = 0; ct < CT; ++ct) mma<NP>(o[ct][t], fs[ct], fa);
+                    for (int ct = 0; ct < CT; ++ct) fs[ct] = next[ct];
+                    if (s + 1 < KS) planes(s + 1, next);
+                } else {
+                    planes(s, fs);
                 }
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) {
+                    S[2 * s][ct] *= whole;
+                    S[2 * s + 1][ct] *= whole;
+                }
+                decay_mma<NP>(o, fs, fa);
+                if constexpr (kAhead) step_order<4, 4 * CT * NP, 4>();
             }
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -476,33 +516,20 @@ __global__ __launch_bounds__(256, kExact<T> == 1 ? 2 : 1) void k_decay_walk(Deca
         }
         load_bc(i + 1);
         put_rows(i + 1);
-        const float whole = rows.whole;
+        if constexpr (SUM) {
+            const float whole = rows.whole;
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+            for (int m = 0; m < MT; ++m)
 #pragma unroll
-            for (int ct = 0; ct < CT; ++ct) S[m][ct] *= whole;
+                for (int ct = 0; ct < CT; ++ct) S[m][ct] *= whole;
+        }
+        // P C and B^T (onto . C), 32 tokens at a time
         const int ml = (int)fresh((uint32_t)l);
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            __builtin_amdgcn_sched_barrier(0);
-            Frag<NX> fc[CT];
-#pragma unroll
-            for (int ct = 0; ct < CT; ++ct) fc[ct] = lds.c.token_frag(ml, s, wave * CT + ct);
-            if constexpr (!SUM) {
-#pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    if (REV ? s == 0 && t >= 2 : s == 1 && t < 2) continue;
-                    Frag<NP> f;
-#pragma unroll
-                    for (int i = 0; i < NP; ++i) f.p[i] = __builtin_bit_cast(bf16x8, lds.P[(t * 2 + s) * NP + i][ml]);
-#pragma unroll
-                    for (int ct = 0; ct < CT; ++ct) mma<NP>(o[ct][t], fc[ct], f);
-                }
-                __builtin_amdgcn_sched_barrier(0);
-            }
+        Frag<NX> fc[CT];
+        Frag<3> fw[CT];
+        const auto weigh = [&](int s) {
             const f32x4 w0 = *reinterpret_cast<const f32x4*>(rows.onto + s * 32 + (ml >> 4) * 4);
             const f32x4 w1 = *reinterpret_cast<const f32x4*>(rows.onto + s * 32 + 16 + (ml >> 4) * 4);
-            Frag<3> fw[CT];
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct) {
                 float x[8];
@@ -514,11 +541,55 @@ __global__ __launch_bounds__(256, kExact<T> == 1 ? 2 : 1) void k_decay_walk(Deca
                 }
                 fw[ct] = split8<3>(x);
             }
+        };
 #pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                const Frag<NX> fb = lds.b.token_frag(ml, s, m);
+        for (int s = 0; s < 2; ++s) {
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int ct = 0; ct < CT; ++ct) mma<3>(S[m][ct], fb, fw[ct]);
+            for (int ct = 0; ct < CT; ++ct) fc[ct] = lds.c.token_frag(ml, s, wave * CT + ct);
+            if constexpr (kAhead) weigh(s);
+            if constexpr (!SUM) {
+                constexpr int kFrom[2] = {0, REV ? 0 : 2}, kTo[2] = {REV ? 2 : 4, 4};  // row tiles that meet this block
+                constexpr int kStep = kAhead ? 4 : 1;  // of them at a time
+#pragma unroll
+                for (int t0 = kFrom[s]; t0 < kTo[s]; t0 += kStep) {
+                    Frag<NP> f[kStep];
+#pragma unroll
+                    for (int t = t0; t < t0 + kStep && t < kTo[s]; ++t)
+#pragma unroll
+                        for (int i = 0; i < NP; ++i)
+                            f[t - t0].p[i] = __builtin_bit_cast(bf16x8, lds.P[(t * 2 + s) * NP + i][ml]);
+#pragma unroll
+                    for (int i = NP - 1; i >= 0; --i)
+#pragma unroll
+                        for (int j = 0; j < NX; ++j)
+                            if (i + j < NP)
+#pragma unroll
+                                for (int t = t0; t < t0 + kStep && t < kTo[s]; ++t)
+#pragma unroll
+                                    for (int ct = 0; ct < CT; ++ct)
+                                        o[ct][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fc[ct].p[j], f[t - t0].p[i],
+                                                                                           o[ct][t], 0, 0, 0);
+                }
+            }
+            if constexpr (!kAhead) {
+                __builtin_amdgcn_sched_barrier(0);
+                weigh(s);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int m = 0; m < MT; m += 2) {
+                const Frag<NX> fb[2] = {lds.b.token_frag(ml, s, m), lds.b.token_frag(ml, s, m + 1)};
+#pragma unroll
+                for (int i = 2; i >= 0; --i)
+#pragma unroll
+                    for (int j = 0; j < NX; ++j)
+                        if (i + j < 3)
+#pragma unroll
+                            for (int y = 0; y < 2; ++y)
+#pragma unroll
+                                for (int ct = 0; ct < CT; ++ct)
+                                    S[m + y][ct] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[y].p[j], fw[ct].p[i], S[m + y][ct], 0, 0, 0);
             }
         }
         __builtin_amdgcn_sched_barrier(0);
