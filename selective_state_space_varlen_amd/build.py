@@ -17,8 +17,8 @@ LIB = os.path.join(HERE, "libssmpack.so")
 BUILD = os.path.join(ROOT, "_build")
 
 SOURCES = ["pack_indices.hip", "conv1d_pack.hip", "scan_fwd.hip", "scan_bwd.hip", "qk_norm.hip",
-           "delta_fwd.hip", "delta_bwd.hip", "delta_step.hip", "decay_fwd.hip", "decay_dq.hip", "decay_dk.hip",
-           "decay_bwd.hip", "decay_step.hip", "layer_norm.hip", "dropout.hip", "pack_plan.cpp"]
+           "delta_fwd.hip", "delta_bwd.hip", "delta_step.hip", "decay_fwd.hip", "decay_dq.hip", "decay_dkv.hip",
+           "decay_bwd.hip", "decay_step.hip", "layer_norm_fwd.hip", "layer_norm_bwd.hip", "dropout.hip", "pack_plan.cpp"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 CXX = os.environ.get("CXX", "g++")

@@ -5,23 +5,6 @@
 
 namespace ssmp {
 
-template <>
-int launch_decay_walk<kOut>(const DecayArgs&, int32_t, hipStream_t);
-template <>
-int launch_decay_walk<kSumS>(const DecayArgs&, int32_t, hipStream_t);
-template <>
-int launch_decay_walk<kDq>(const DecayArgs&, int32_t, hipStream_t);
-template <>
-int launch_decay_walk<kDk>(const DecayArgs&, int32_t, hipStream_t);
-template <>
-int launch_decay_walk<kDv>(const DecayArgs& a, int32_t dtype, hipStream_t s) {
-    return launch_decay_walk_of<kDv, false>(a, dtype, s);
-}
-template <>
-int launch_decay_walk<kSumD>(const DecayArgs& a, int32_t dtype, hipStream_t s) {
-    return launch_decay_walk_of<kSumD, false>(a, dtype, s);
-}
-
 // exp(g) in 32 bits without its smallest numbers, as the walks form it
 __device__ __forceinline__ bool decay_is_zero(float g) { return g * kLog2e < -126.0f; }
 
@@ -92,9 +75,11 @@ __global__ __launch_bounds__(64) void k_decay_dg_sum(DecayArgs p, int64_t slots)
     if (lane == 0) p.dg[hv] = (float)s;
 }
 
-// dq or dk: the sum of its parts by value head and slice, up to the last sequence's end
+// dq and dk: the sums of their parts by value head and slice, up to the last sequence's end
 template <typename T>
-__global__ __launch_bounds__(256) void k_decay_add(DecayArgs p, const float* __restrict__ part, void* out, int members) {
+__global__ __launch_bounds__(256) void k_decay_add(DecayArgs p, int members) {
+    const float* __restrict__ const part = p.part[blockIdx.y];
+    T* const out = static_cast<T*>(blockIdx.y ? p.dk : p.dq);
     int64_t end = p.cu[p.nseq];
     end = end < 0 ? 0 : end > p.T ? p.T : end;
     const int per = p.Dk / 4;
@@ -104,18 +89,8 @@ __global__ __launch_bounds__(256) void k_decay_add(DecayArgs p, const float* __r
         f32x4 s = {0, 0, 0, 0};
         for (int m = 0; m < members; ++m) s += *reinterpret_cast<const f32x4*>(at + (int64_t)m * p.Dk);
 #pragma unroll
-        for (int x = 0; x < 4; ++x) Elt<T>::st(static_cast<T*>(out), (size_t)i * 4 + x, s[x]);
+        for (int x = 0; x < 4; ++x) Elt<T>::st(out, (size_t)i * 4 + x, s[x]);
     }
-}
-int launch_decay_add(const DecayArgs& a, int i, int32_t dtype, hipStream_t s) {
-    const int64_t want = (a.T * a.Hk * (a.Dk / 4) + 255) / 256;
-    const unsigned blocks = (unsigned)(want < 8192 ? want : 8192);
-    void* const out = i ? a.dk : a.dq;
-    const int members = a.Hv / a.Hk * a.slices;
-    if (dtype == SSMP_F32) k_decay_add<float><<<blocks, 256, 0, s>>>(a, a.part[i], out, members);
-    else k_decay_add<uint16_t><<<blocks, 256, 0, s>>>(a, a.part[i], out, members);
-    SSMP_LAUNCH_CHECK();
-    return SSMP_OK;
 }
 
 struct DecayBwdLayout {
@@ -195,11 +170,12 @@ extern "C" int decay_attn_pack_bwd(const void* q, const void* k, const void* v, 
     a.gstride = per_token ? Hv : 0;
     a.scale = scale;
     a.slices = (Dv + kDecayMaxDb - 1) / kDecayMaxDb;
-    a.seg = decay_segment(T, Hv);
+    a.seg = decay_segment(T, nseq, Hv);
     if (T == 0) {
         if (!per_token)
             if (const int st = zero_f32(dg, Hv, s)) return st;
-        return dinitial_state ? launch_decay_walk<kDv>(a, dtype, s) : SSMP_OK;
+        a.dg = nullptr;
+        return dinitial_state ? launch_decay_dkv(a, dtype, s) : SSMP_OK;  // hands on dfinal_state
     }
     const DecayBwdLayout L = decay_bwd_layout(T, nseq, Hk, Hv, Dk, Dv);
     char* const ws = static_cast<char*>(scratch);
@@ -215,14 +191,11 @@ extern "C" int decay_attn_pack_bwd(const void* q, const void* k, const void* v, 
     a.meet = reinterpret_cast<float*>(ws + L.meet);
     a.dgsum = reinterpret_cast<double*>(ws + L.dgsum);
     if (T > a.seg) {
-        if (const int st = launch_decay_walk<kSumS>(a, dtype, s)) return st;
-        if (const int st = launch_decay_join<false>(a, s)) return st;
-        if (const int st = launch_decay_walk<kSumD>(a, dtype, s)) return st;
-        if (const int st = launch_decay_join<true>(a, s)) return st;
+        if (const int st = launch_decay_pair<kSumS, false, kSumD>(a, dtype, s)) return st;
+        if (const int st = launch_decay_join(a, 2, s)) return st;
     }
-    if (const int st = launch_decay_walk<kDq>(a, dtype, s)) return st;
-    if (const int st = launch_decay_walk<kDk>(a, dtype, s)) return st;
-    if (const int st = launch_decay_walk<kDv>(a, dtype, s)) return st;
+    if (const int st = launch_decay_dq(a, dtype, s)) return st;
+    if (const int st = launch_decay_dkv(a, dtype, s)) return st;
     if (dg) {
         const int64_t slots = T / kPiece + nseq;
         k_decay_dg<<<(unsigned)(slots * ((Hv + kDgHeads - 1) / kDgHeads)), 64, 0, s>>>(a, a.slices);
@@ -232,8 +205,13 @@ extern "C" int decay_attn_pack_bwd(const void* q, const void* k, const void* v, 
             SSMP_LAUNCH_CHECK();
         }
     }
-    if (partial)
-        for (int i = 0; i < 2; ++i)
-            if (const int st = launch_decay_add(a, i, dtype, s)) return st;
+    if (partial) {
+        const int64_t want = (T * Hk * (Dk / 4) + 255) / 256;
+        const dim3 blocks((unsigned)(want < 8192 ? want : 8192), 2);
+        const int members = Hv / Hk * a.slices;
+        if (dtype == SSMP_F32) k_decay_add<float><<<blocks, 256, 0, s>>>(a, members);
+        else k_decay_add<uint16_t><<<blocks, 256, 0, s>>>(a, members);
+        SSMP_LAUNCH_CHECK();
+    }
     return SSMP_OK;
 }

@@ -3,9 +3,8 @@
 
 namespace ssmp {
 
-template <>
-int launch_decay_walk<kDq>(const DecayArgs& a, int32_t dtype, hipStream_t s) {
-    return a.dg ? launch_decay_walk_of<kDq, true>(a, dtype, s) : launch_decay_walk_of<kDq, false>(a, dtype, s);
+int launch_decay_dq(const DecayArgs& a, int32_t dtype, hipStream_t s) {
+    return a.dg ? launch_decay_walk<kDq, true>(a, dtype, s) : launch_decay_walk<kDq, false>(a, dtype, s);
 }
 
 }  // namespace ssmp

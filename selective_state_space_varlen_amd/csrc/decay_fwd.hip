@@ -1,20 +1,6 @@
 // decay_attn_pack_fwd: linear attention with a decay for each head over packed
-// sequences, and the sums of the states between segments that the backward
-// shares with it.
+// sequences.
 #include "decay_walk.h"
-
-namespace ssmp {
-
-template <>
-int launch_decay_walk<kOut>(const DecayArgs& a, int32_t dtype, hipStream_t s) {
-    return launch_decay_walk_of<kOut, false>(a, dtype, s);
-}
-template <>
-int launch_decay_walk<kSumS>(const DecayArgs& a, int32_t dtype, hipStream_t s) {
-    return launch_decay_walk_of<kSumS, false>(a, dtype, s);
-}
-
-}  // namespace ssmp
 
 extern "C" size_t decay_attn_pack_fwd_scratch_bytes(int64_t T, int32_t nseq, int32_t Hk, int32_t Hv, int32_t Dk,
                                                     int32_t Dv) {
@@ -56,15 +42,15 @@ extern "C" int decay_attn_pack_fwd(const void* q, const void* k, const void* v, 
     a.gstride = per_token ? Hv : 0;
     a.scale = scale;
     a.slices = 1;
-    a.seg = decay_segment(T, work);
+    a.seg = decay_segment(T, nseq, work);
     if (need) {
         a.joint[0] = reinterpret_cast<float*>(static_cast<char*>(scratch) + L.joint);
         a.seg_decay[0] = reinterpret_cast<float*>(static_cast<char*>(scratch) + L.decay);
     }
     hipStream_t s = static_cast<hipStream_t>(stream);
     if (T > a.seg) {
-        if (const int st = launch_decay_walk<kSumS>(a, dtype, s)) return st;
-        if (const int st = launch_decay_join<false>(a, s)) return st;
+        if (const int st = launch_decay_walk<kSumS, false>(a, dtype, s)) return st;
+        if (const int st = launch_decay_join(a, 1, s)) return st;
     }
-    return launch_decay_walk<kOut>(a, dtype, s);
+    return launch_decay_walk<kOut, false>(a, dtype, s);
 }

@@ -33,25 +33,29 @@ namespace ssmp {
 constexpr int kDecayCols = 128;     // columns of c a workgroup takes at most
 constexpr int kDecayMaxDb = 128;    // rows of the state a workgroup takes
 constexpr int kPiece = 256;         // tokens between the points where dg is anchored
-constexpr int kSegMin = 256, kSegMax = 2048;
-constexpr int kSegWork = 512;       // workgroups that a launch should have
+constexpr int kSegMin = 128, kSegMax = 2048;
+constexpr int kSegWork = 768;       // workgroups that a launch should have
 
 inline int decay_cols(int32_t Dc) { return Dc <= 64 ? 64 : kDecayCols; }
 inline int decay_col_blocks(int32_t Dc) { return (Dc + kDecayCols - 1) / kDecayCols; }
-// heads * column blocks: the workgroups that a segment has
-inline int32_t decay_segment(int64_t T, int64_t work) {
+// work: heads * column blocks, the workgroups that a segment has. Enough
+// sequences are walked whole, as the first walk costs a third of the forward;
+// a longest segment bounds what one long sequence among them takes. 16384
+// tokens in 6 sequences x 24 heads of 128 x 64, segments of 768, 512, 384 and
+// 256 tokens: forward 164, 133, 143 and 139 us, backward 711, 583, 633 and 609.
+inline int32_t decay_segment(int64_t T, int32_t nseq, int64_t work) {
+    if (nseq * work >= kSegWork) return kSegMax;
     const int64_t n = T * work / kSegWork / kSegMin * kSegMin;
     return (int32_t)(n < kSegMin ? kSegMin : n > kSegMax ? kSegMax : n);
 }
-// The most T' / decay_segment(T') for T' <= T, plus one: below kSegMax a
-// segment is at least half of T' work / kSegWork long.
+// The most T' / decay_segment(T', any nseq) for T' <= T, plus one: below kSegMax
+// a segment is at least half of T' work / kSegWork long.
 inline int64_t decay_states(int64_t T, int64_t work) {
     const int64_t few = T / kSegMin, many = 2 * kSegWork / work, least = T / kSegMax;
     const int64_t n = few < many ? few : many;
     return (n > least ? n : least) + 1;
 }
 
-// kOut, kSumS: decay_fwd.hip; kDq: decay_dq.hip; kDk: decay_dk.hip; kDv, kSumD: decay_bwd.hip
 enum DecayKind { kOut, kDq, kDk, kDv, kSumS, kSumD };
 
 struct DecayArgs {
@@ -124,6 +128,12 @@ __device__ __forceinline__ bool segment_at(const DecayArgs& p, int64_t r, Chunk&
     return true;
 }
 
+// fresh(), of a scalar
+__device__ __forceinline__ int fresh_scalar(int v) {
+    asm volatile("" : "+s"(v));
+    return v;
+}
+
 // One side's rows: those of head h of H, columns off .. off + width - 1 of D
 template <typename T>
 struct Side {
@@ -149,11 +159,9 @@ template <typename T, int W, int THREADS>
 struct SideLoads {
     static constexpr int kN = kC * W / 8 / THREADS, kRows = THREADS / (W / 8);  // rows between a thread's units
     Unit<T> u[kN];
-    uint32_t o;  // of its first
-    __device__ __forceinline__ explicit SideLoads(const Side<T>& s) : o(s.at(threadIdx.x / (W / 8), threadIdx.x % (W / 8) * 8)) {}
-    __device__ __forceinline__ void load(const Side<T>& s, int64_t row, int n) {
+    __device__ __forceinline__ void load(const Side<T>& s, int64_t row, int n, int tid) {
         const auto r = rows_rsrc(s.p + row * s.stride, n, s.stride, s.width);
-        const uint32_t at = fresh(o);
+        const uint32_t at = s.at(tid / (W / 8), tid % (W / 8) * 8);
 #pragma unroll
         for (int x = 0; x < kN; ++x) u[x].load(r, at + s.rows(x * kRows));
     }
@@ -234,6 +242,11 @@ struct DecayRows {
     float into[kC], onto[kC];     // decay from the state to a row, and from a row to the state
     float whole;                  // of the chunk
 };
+// Planes of P and of the state where out is formed: two hold 16 bits, of
+// which a bf16 result keeps 8; dg and fp32 results see all three. What is
+// added to the state has three always.
+template <typename T, bool DOTS>
+constexpr int kDecayPlanes = kExact<T> == 3 || DOTS ? 3 : 2;
 template <typename T, int DBP, int CT, int NP>
 struct DecayTiles {
     RowTile<T, DBP> a, b;
@@ -254,22 +267,18 @@ struct DecayTiles {
 // the first half of a chunk and those of b and c in the second, so that two
 // workgroups share a CU. DOTS: rows of out times rows of q or k, for dg.
 template <typename T, int KIND, int DBP, int CT, bool DOTS>
-__global__ __launch_bounds__(256, kExact<T> == 1 ? 2 : 1) void k_decay_walk(DecayArgs p) {
-    constexpr int NX = kExact<T>;
-    // Planes of P and of the state where out is formed: two hold 16 bits, of
-    // which a bf16 result keeps 8; dg and fp32 results see all three. What is
-    // added to the state has three always.
-    constexpr int NP = NX == 3 || DOTS ? 3 : 2;
+__device__ __forceinline__ void decay_walk(const DecayArgs& p, int64_t block,
+                                           DecayTiles<T, DBP, CT, kDecayPlanes<T, DOTS>>& lds) {
+    constexpr int NX = kExact<T>, NP = kDecayPlanes<T, DOTS>;
     constexpr bool REV = decay_reverse(KIND), SUM = KIND == kSumS || KIND == kSumD, KEYS = decay_by_key(KIND);
     constexpr int MT = DBP / 16, KS = DBP / 32, COLS = 64 * CT;
     // Vector operations of the next product in the shadow of one's matrix
     // instructions; three planes leave no registers for it.
     constexpr bool kAhead = NP == 2;
     constexpr int kFew = REV ? 3 : 0;  // the wave with the fewest tiles of P has G to do
-    __shared__ alignas(16) DecayTiles<T, DBP, CT, NP> lds;
     const int Dc = KEYS ? p.Dk : p.Dv, Db = KEYS ? p.Dv : p.Dk;
     const int ncb = (Dc + COLS - 1) / COLS, slices = KEYS ? p.slices : 1, group = p.Hv / p.Hk;
-    const Spread sp = spread(blockIdx.x, group * slices * ncb);
+    const Spread sp = spread(block, group * slices * ncb);
     if (sp.group >= (p.T / p.seg + p.nseq) * (int64_t)p.Hk) return;
     Chunk sg;
     if (SUM ? !chunk_at(p.cu, p.nseq, p.T, sp.group / p.Hk, sg, p.seg) : !segment_at(p, sp.group / p.Hk, sg)) return;
@@ -289,7 +298,10 @@ __global__ __launch_bounds__(256, kExact<T> == 1 ? 2 : 1) void k_decay_walk(Deca
     const Side<T> sa(ta, sg.start, Hb, hb, Db, off, db), sb(tb, sg.start, Hb, hb, Db, off, db);
     const Side<T> sc(tc, sg.start, Hc, hc, Dc, col0, min(Dc - col0, COLS));
     // a lane's columns of out: 4 CT from here on
-    const int col = col0 + (CT == 2 ? wave * 32 + l4 * 8 : (wave >> 1) * 32 + l4 * 8 + (wave & 1) * 4);
+    const auto column = [&]() {
+        const int quarter = (int)(fresh(l) >> 4);
+        return col0 + (CT == 2 ? wave * 32 + quarter * 8 : (wave >> 1) * 32 + quarter * 8 + (wave & 1) * 4);
+    };
     // The state in a tensor of [Dk][Dv], of which this workgroup has rows off ..
     // of b and columns col0 .. of c: a lane's elements at(m, ct, r), four rows
     // r of b together where b is v's or dout's
@@ -336,33 +348,35 @@ __global__ __launch_bounds__(256, kExact<T> == 1 ? 2 : 1) void k_decay_walk(Deca
         }
     }
     const int chunks = (sg.n + kC - 1) / kC;
-    SideLoads<T, DBP, 256> la(sa), lb(sb);
-    SideLoads<T, COLS, 256> lc(sc);
+    SideLoads<T, DBP, 256> la, lb;
+    SideLoads<T, COLS, 256> lc;
     uint32_t lg;
     const auto chunk = [&](int i) { return REV ? chunks - 1 - i : i; };  // the walk's i-th
     const auto tokens = [&](int i) { return i < chunks ? min(sg.n - chunk(i) * kC, kC) : 0; };
     const auto load_a = [&](int i) {
         const int n = tokens(i);
-        if constexpr (!SUM) la.load(sa, (int64_t)chunk(i) * kC, n);
+        if constexpr (!SUM) la.load(sa, (int64_t)chunk(i) * kC, n, wave * 64 + (int)fresh(l));
         const int64_t t = sg.start + chunk(i) * kC;
         lg = Elt<float>::raw_rsrc(rows_rsrc(p.g + (p.gstride ? t * p.gstride : 0) + hv, n, p.gstride, 1),
-                                  l < n ? (uint32_t)(l * p.gstride) * 4u : kNowhere);
+                                  l < n ? fresh(l) * (uint32_t)p.gstride * 4u : kNowhere);
     };
     const auto load_bc = [&](int i) {
         const int n = tokens(i);
-        lb.load(sb, (int64_t)chunk(i) * kC, n);
-        lc.load(sc, (int64_t)chunk(i) * kC, n);
+        const int tid = wave * 64 + (int)fresh(l);
+        lb.load(sb, (int64_t)chunk(i) * kC, n, tid);
+        lc.load(sc, (int64_t)chunk(i) * kC, n, tid);
     };
     double total = 0.0;
     const auto put_rows = [&](int i) {
         if (wave != kFew || i >= chunks) return;
         DecayRows& to = lds.rows[i & 1];
         const double G = chunk_decay_sum(l < tokens(i) ? Elt<float>::cvt(lg) : 0.0f), last = read_lane(G, kC - 1);
-        to.G[l] = G;
+        const int row = (int)fresh(l);
+        to.G[row] = G;
         const float head = decay_of(G), tail = decay_of(last - G);
-        to.into[l] = REV ? tail : head * p.scale;
-        to.onto[l] = REV ? head * p.scale : tail;
-        if (l == 0) to.whole = decay_of(last);
+        to.into[row] = REV ? tail : head * p.scale;
+        to.onto[row] = REV ? head * p.scale : tail;
+        if (row == 0) to.whole = decay_of(last);
         total += last;
     };
     load_a(0);
@@ -373,7 +387,8 @@ __global__ __launch_bounds__(256, kExact<T> == 1 ? 2 : 1) void k_decay_walk(Deca
     put_rows(0);
     __syncthreads();
     for (int i = 0; i < chunks; ++i) {
-        const int n = tokens(i);
+        const int n = tokens(i), wv = fresh_scalar(wave), tid = wv * 64 + (int)fresh(l);  // or what follows from them fills registers
+
         const int64_t t0 = sg.start + chunk(i) * kC;
         const DecayRows& rows = lds.rows[i & 1];
         // dg's anchors: the state S^T of dq's walk behind every piece meets dS^T of dk's
@@ -381,13 +396,13 @@ __global__ __launch_bounds__(256, kExact<T> == 1 ? 2 : 1) void k_decay_walk(Deca
         const bool piece_end = DOTS && (from_seq + kC) % kPiece == 0 && !(sg.last && chunk(i) == chunks - 1);
         const auto snap = [&]() {  // the wave's part of it; tile i lies 1024 i bytes on
             return bytes_rsrc(p.snap + (((size_t)piece * p.Hv + hv) * parts + slice * ncb + cb) * (DBP * COLS) +
-                                  (size_t)wave * (MT * CT * 256), MT * CT * 1024);
+                                  (size_t)wv * (MT * CT * 256), MT * CT * 1024);
         };
         Unit<T> dots[DOTS ? 4 : 1];
         if constexpr (DOTS) {
             const Side<T> sd(KIND == kDq ? p.q : p.k, t0, p.Hk, hk, p.Dk, 0, p.Dk);
             const auto r = rows_rsrc(sd.p, n, sd.stride, sd.width);
-            const uint32_t at = sd.at(fresh(l16), col & ~7);
+            const uint32_t at = sd.at(fresh(l16), column() & ~7);
 #pragma unroll
             for (int t = 0; t < 4; ++t) dots[t].load(r, at + sd.rows(t * 16));
         }
@@ -406,7 +421,7 @@ __global__ __launch_bounds__(256, kExact<T> == 1 ? 2 : 1) void k_decay_walk(Deca
                         for (int r = 0; r < 4; ++r) e = fmaf(S[m][ct][r], w[r], e);
                     }
                 e = wave_sum(e);
-                if (l == 0) lds.sum[0][wave] = e;
+                if ((tid & 63) == 0) lds.sum[0][wv] = e;
             }
         }
         f32x4 o[CT][4] = {};
@@ -419,7 +434,7 @@ __global__ __launch_bounds__(256, kExact<T> == 1 ? 2 : 1) void k_decay_walk(Deca
                 if constexpr (CT == 2) e = fmaf(o[CT - 1][t][x], v[4 + x], fmaf(o[0][t][x], v[x], e));
                 else {
                     const float lo = v[x], hi = v[4 + x];
-                    e = fmaf(o[0][t][x], wave & 1 ? hi : lo, e);
+                    e = fmaf(o[0][t][x], wv & 1 ? hi : lo, e);
                 }
             }
             return e;
@@ -428,18 +443,18 @@ __global__ __launch_bounds__(256, kExact<T> == 1 ? 2 : 1) void k_decay_walk(Deca
             const int ml = (int)fresh((uint32_t)l), m16 = ml & 15, m4 = ml >> 4;  // addresses are this half's own
             // P: wave w has rows 16 w .. + 15 along its lanes
             f32x4 x[4] = {};
-            const auto has = [&](int j) { return REV ? j >= wave : j <= wave; };  // row tile w meets rows of tile j of b
+            const auto has = [&](int j) { return REV ? j >= wv : j <= wv; };  // row tile w meets rows of tile j of b
             {
                 Frag<NX> fa[KS];
 #pragma unroll
-                for (int s = 0; s < KS; ++s) fa[s] = lds.a.frag(wave * 16 + m16, s * 4 + m4);
+                for (int s = 0; s < KS; ++s) fa[s] = lds.a.frag(wv * 16 + m16, s * 4 + m4);
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     if (has(j))
 #pragma unroll
                         for (int s = 0; s < KS; ++s) mma<NX>(x[j], lds.b.frag(j * 16 + m16, s * 4 + m4), fa[s]);
             }
-            const double Gi = rows.G[wave * 16 + m16];
+            const double Gi = rows.G[wv * 16 + m16];
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 if (has(j)) {
@@ -448,17 +463,17 @@ __global__ __launch_bounds__(256, kExact<T> == 1 ? 2 : 1) void k_decay_walk(Deca
                         const double Gj = rows.G[j * 16 + m4 * 4 + r];
                         x[j][r] *= decay_of(REV ? Gj - Gi : Gi - Gj) * p.scale;
                     }
-                    if (j == wave)
+                    if (j == wv)
 #pragma unroll
                         for (int r = 0; r < 4; ++r)
                             if (REV ? m4 * 4 + r < m16 : m4 * 4 + r > m16) x[j][r] = 0.0f;
                 }
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
-                if (REV ? s == 0 && wave >= 2 : s == 1 && wave < 2) continue;
+                if (REV ? s == 0 && wv >= 2 : s == 1 && wv < 2) continue;
                 const Frag<NP> f = split_tiles<NP>(x[2 * s], x[2 * s + 1]);
 #pragma unroll
-                for (int i = 0; i < NP; ++i) lds.P[(wave * 2 + s) * NP + i][ml] = __builtin_bit_cast(u32x4, f.p[i]);
+                for (int i = 0; i < NP; ++i) lds.P[(wv * 2 + s) * NP + i][ml] = __builtin_bit_cast(u32x4, f.p[i]);
             }
             // A X, rows of out along the lanes; in its shadow the state decays
             const float whole = rows.whole;
@@ -501,15 +516,15 @@ __global__ __launch_bounds__(256, kExact<T> == 1 ? 2 : 1) void k_decay_walk(Deca
 #pragma unroll
                 for (int t = 0; t < 4; ++t) e += dot_of(t);
                 e = wave_sum(e);
-                if (l == 0) lds.sum[1][wave] = e;
+                if ((tid & 63) == 0) lds.sum[1][wv] = e;
             }
             __syncthreads();
             if constexpr (DOTS) {
-                const float* const w = lds.sum[threadIdx.x & 1];
+                const float* const w = lds.sum[tid & 1];
                 const float e = (w[0] + w[1]) + (w[2] + w[3]);
-                if (threadIdx.x == 1)
+                if (tid == 1)
                     p.chunk[REV][((size_t)(first / kC + sg.seq + from_seq / kC) * p.Hv + hv) * parts + slice * ncb + cb] = e;
-                if (KIND == kDk && threadIdx.x == 0 && piece_end)
+                if (KIND == kDk && tid == 0 && piece_end)
                     p.meet[((size_t)(piece + sg.seq) * p.Hv + hv) * parts + slice * ncb + cb] = e;
             }
             la.put(lds.a);
@@ -546,7 +561,7 @@ __global__ __launch_bounds__(256, kExact<T> == 1 ? 2 : 1) void k_decay_walk(Deca
         for (int s = 0; s < 2; ++s) {
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int ct = 0; ct < CT; ++ct) fc[ct] = lds.c.token_frag(ml, s, wave * CT + ct);
+            for (int ct = 0; ct < CT; ++ct) fc[ct] = lds.c.token_frag(ml, s, wv * CT + ct);
             if constexpr (kAhead) weigh(s);
             if constexpr (!SUM) {
                 constexpr int kFrom[2] = {0, REV ? 0 : 2}, kTo[2] = {REV ? 2 : 4, 4};  // row tiles that meet this block
@@ -577,9 +592,14 @@ __global__ __launch_bounds__(256, kExact<T> == 1 ? 2 : 1) void k_decay_walk(Deca
                 weigh(s);
             }
             __builtin_amdgcn_sched_barrier(0);
+            Frag<NX> fb[2] = {lds.b.token_frag(ml, s, 0), lds.b.token_frag(ml, s, 1)};
 #pragma unroll
             for (int m = 0; m < MT; m += 2) {
-                const Frag<NX> fb[2] = {lds.b.token_frag(ml, s, m), lds.b.token_frag(ml, s, m + 1)};
+                Frag<NX> now[2] = {fb[0], fb[1]};
+                if (m + 2 < MT) {
+                    fb[0] = lds.b.token_frag(ml, s, m + 2);
+                    fb[1] = lds.b.token_frag(ml, s, m + 3);
+                }
 #pragma unroll
                 for (int i = 2; i >= 0; --i)
 #pragma unroll
@@ -589,7 +609,8 @@ __global__ __launch_bounds__(256, kExact<T> == 1 ? 2 : 1) void k_decay_walk(Deca
                             for (int y = 0; y < 2; ++y)
 #pragma unroll
                                 for (int ct = 0; ct < CT; ++ct)
-                                    S[m + y][ct] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[y].p[j], fw[ct].p[i], S[m + y][ct], 0, 0, 0);
+                                    S[m + y][ct] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(now[y].p[j], fw[ct].p[i], S[m + y][ct], 0, 0, 0);
+                if constexpr (!kAhead) __builtin_amdgcn_sched_barrier(0);  // or reads pile up in registers
             }
         }
         __builtin_amdgcn_sched_barrier(0);
@@ -598,7 +619,7 @@ __global__ __launch_bounds__(256, kExact<T> == 1 ? 2 : 1) void k_decay_walk(Deca
             if (KEYS && members > 1) {
                 const Side<float> to(p.part[REV], t0, H * members, h * members + sp.member / ncb, Dc, 0, Dc);
                 const auto r = rows_rsrc(to.p, n, to.stride, Dc);
-                const uint32_t at = to.at(fresh(l16), col);
+                const uint32_t at = to.at(fresh(l16), column());
 #pragma unroll
                 for (int t = 0; t < 4; ++t)
 #pragma unroll
@@ -608,7 +629,7 @@ __global__ __launch_bounds__(256, kExact<T> == 1 ? 2 : 1) void k_decay_walk(Deca
             } else {
                 const Side<T> to(KIND == kOut ? p.out : KIND == kDq ? p.dq : KIND == kDk ? p.dk : p.dv, t0, H, h, Dc, 0, Dc);
                 const auto r = rows_rsrc(to.p, n, to.stride, Dc);
-                const uint32_t at = to.at(fresh(l16), col);
+                const uint32_t at = to.at(fresh(l16), column());
 #pragma unroll
                 for (int t = 0; t < 4; ++t) {
                     if constexpr (CT == 2) {
@@ -633,7 +654,7 @@ __global__ __launch_bounds__(256, kExact<T> == 1 ? 2 : 1) void k_decay_walk(Deca
                     float e = dot_of(t);
                     e += __shfl_xor(e, 16);
                     e += __shfl_xor(e, 32);
-                    if (l4 == 0) lds.dot[wave][t * 16 + l16] = e;
+                    if ((tid & 48) == 0) lds.dot[wv][t * 16 + l16] = e;
                 }
                 if constexpr (KIND == kDq) {
                     if (piece_end) {
@@ -652,10 +673,10 @@ __global__ __launch_bounds__(256, kExact<T> == 1 ? 2 : 1) void k_decay_walk(Deca
         lb.put(lds.b);
         lc.put(lds.c);
         if constexpr (DOTS) {
-            if (threadIdx.x < n) {
-                const int x = threadIdx.x;
-                p.rows[REV][((size_t)(slice * ncb + cb) * p.T + t0 + x) * p.Hv + hv] =
-                    (lds.dot[0][x] + lds.dot[1][x]) + (lds.dot[2][x] + lds.dot[3][x]);
+            if (wv == 0) {
+                const auto r = rows_rsrc(p.rows[REV] + ((size_t)(slice * ncb + cb) * p.T + t0) * p.Hv + hv, n, p.Hv, 1);
+                Elt<float>::st_rsrc<0>(r, (uint32_t)(tid * p.Hv) * 4u,
+                                       (lds.dot[0][tid] + lds.dot[1][tid]) + (lds.dot[2][tid] + lds.dot[3][tid]));
             }
         }
         __syncthreads();
@@ -690,32 +711,69 @@ __global__ __launch_bounds__(256, kExact<T> == 1 ? 2 : 1) void k_decay_walk(Deca
     }
 }
 
+template <typename T, int KIND, int DBP, int CT, bool DOTS>
+__global__ __launch_bounds__(256, kExact<T> == 1 ? 2 : 1) void k_decay_walk(DecayArgs p) {
+    __shared__ alignas(16) DecayTiles<T, DBP, CT, kDecayPlanes<T, DOTS>> lds;
+    decay_walk<T, KIND, DBP, CT, DOTS>(p, blockIdx.x, lds);
+}
+// Two walks that do not wait for each other in one launch, the first in the
+// first `blocks` workgroups, where all of them have a CU of their own: small
+// ones then run beside each other. (Compiled together they need more registers
+// than two workgroups a CU have: with spills, 32768 tokens x 32 heads take 920
+// us for dk and dv, 770 one after the other.)
+constexpr int kPairBlocks = 512;  // half of them, or more, without a segment
+template <typename T, int KIND, int DBP, int CT, bool DOTS, int KIND2, int DBP2, int CT2>
+__global__ __launch_bounds__(256, 1) void k_decay_pair(DecayArgs p, uint32_t blocks) {
+    using A = DecayTiles<T, DBP, CT, kDecayPlanes<T, DOTS>>;
+    using B = DecayTiles<T, DBP2, CT2, kDecayPlanes<T, false>>;
+    __shared__ alignas(16) char lds[sizeof(A) > sizeof(B) ? sizeof(A) : sizeof(B)];
+    if (blockIdx.x < blocks) decay_walk<T, KIND, DBP, CT, DOTS>(p, blockIdx.x, *reinterpret_cast<A*>(lds));
+    else decay_walk<T, KIND2, DBP2, CT2, false>(p, blockIdx.x - blocks, *reinterpret_cast<B*>(lds));
+}
+
 // Along the segments of each sequence that has several, in place: what a
-// segment adds becomes the state on its far side, X' = decay X + U. One
-// workgroup per (segment slot that is a sequence's first, head, block of
-// elements): each element is read and written once.
+// segment adds becomes the state on its far side, X' = decay X + U. A workgroup
+// per (sequence, head, block of elements): each element is read and written
+// once, kBatch states under way.
 template <bool REV>
-__global__ __launch_bounds__(256) void k_decay_join(DecayArgs p, int blocks) {
-    const int64_t slot = blockIdx.x / ((int64_t)p.Hv * blocks);
-    const int hv = blockIdx.x / blocks % p.Hv, block = blockIdx.x % blocks;
-    Chunk c;
-    if (!chunk_at(p.cu, p.nseq, p.T, slot, c, p.seg) || c.index != 0 || c.last) return;
-    const int64_t end = p.cu[c.seq + 1] < p.T ? p.cu[c.seq + 1] : p.T;
-    const int n = (int)((end - c.start + p.seg - 1) / p.seg) - 1;  // states between its segments
-    const int64_t state0 = c.start / p.seg;
+__device__ __forceinline__ void decay_join(const DecayArgs& p, int s, int hv, int block, int blocks) {
+    const Seq q = seq_at(p.cu, s, p.T);
+    const int n = (q.len - 1) / p.seg;  // states between its segments
+    if (q.len == 0 || n == 0) return;
+    const int64_t state0 = q.start / p.seg;
     const size_t size = (size_t)p.Dk * p.Dv, step = size * p.Hv;
     float* const x = p.joint[REV] + (size_t)state0 * step + hv * size;
     const float* const d = p.seg_decay[REV] + state0 * p.Hv + hv;
-    const float* const first = REV ? (p.dhT ? p.dhT + ((size_t)c.seq * p.Hv + hv) * size : nullptr)
-                                   : (p.h0 ? p.h0 + ((size_t)c.seq * p.Hv + hv) * size : nullptr);
+    const float* first = REV ? p.dhT : p.h0;
+    if (first) first += ((size_t)s * p.Hv + hv) * size;
     for (size_t e = ((size_t)block * 256 + threadIdx.x) * 4; e < size; e += (size_t)blocks * 1024) {
-        f32x4 s = first ? *reinterpret_cast<const f32x4*>(first + e) : f32x4{0, 0, 0, 0};
-        for (int i = 0; i < n; ++i) {
-            float* const at = x + (REV ? n - 1 - i : i) * step + e;
-            s = s * d[(REV ? n - 1 - i : i) * p.Hv] + *reinterpret_cast<const f32x4*>(at);
-            *reinterpret_cast<f32x4*>(at) = s;
+        f32x4 v = first ? *reinterpret_cast<const f32x4*>(first + e) : f32x4{0, 0, 0, 0};
+        constexpr int kBatch = 8;
+        for (int i = 0; i < n; i += kBatch) {
+            f32x4 u[kBatch];
+            float w[kBatch];
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) {
+                const int at = min(i + j, n - 1), to = REV ? n - 1 - at : at;
+                u[j] = *reinterpret_cast<const f32x4*>(x + to * step + e);
+                w[j] = d[to * p.Hv];
+            }
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j)
+                if (i + j < n) {
+                    v = v * w[j] + u[j];
+                    *reinterpret_cast<f32x4*>(x + (REV ? n - 1 - i - j : i + j) * step + e) = v;
+                }
         }
     }
+}
+// ways: 1 for S alone, 2 for dS as well
+template <int kUnused = 0>
+__global__ __launch_bounds__(256) void k_decay_join(DecayArgs p, int blocks, int ways) {
+    const int64_t i = blockIdx.x / ways;
+    const int s = (int)(i / ((int64_t)p.Hv * blocks)), hv = (int)(i / blocks % p.Hv), block = (int)(i % blocks);
+    if (ways == 1 || blockIdx.x % 2 == 0) decay_join<false>(p, s, hv, block, blocks);
+    else decay_join<true>(p, s, hv, block, blocks);
 }
 
 // The walks' workgroups, by kind: those of heads that share a and b, or c, on
@@ -725,44 +783,69 @@ inline int64_t decay_walk_blocks(const DecayArgs& a, int kind) {
     const int members = a.Hv / a.Hk * (decay_by_key(kind) ? a.slices : 1) * ((Dc + decay_cols(Dc) - 1) / decay_cols(Dc));
     return spread_blocks((a.T / a.seg + a.nseq) * a.Hk, members);
 }
-template <typename T, int KIND, bool DOTS>
-void launch_decay_walk_t(const DecayArgs& a, hipStream_t s) {
-    const unsigned n = (unsigned)decay_walk_blocks(a, KIND);
-    const int32_t Dc = decay_by_key(KIND) ? a.Dk : a.Dv, Db = decay_by_key(KIND) ? a.Dv : a.Dk;
+// f(rows of the state, column tiles), as constants, by heads of b and c
+template <typename F>
+void decay_dispatch(int32_t Db, int32_t Dc, F f) {
+    using C64 = std::integral_constant<int, 64>;
+    using C128 = std::integral_constant<int, 128>;
+    using One = std::integral_constant<int, 1>;
+    using Two = std::integral_constant<int, 2>;
     if (Db > 64) {
-        if (Dc > 64) k_decay_walk<T, KIND, 128, 2, DOTS><<<n, 256, 0, s>>>(a);
-        else k_decay_walk<T, KIND, 128, 1, DOTS><<<n, 256, 0, s>>>(a);
+        if (Dc > 64) f(C128{}, Two{});
+        else f(C128{}, One{});
     } else {
-        if (Dc > 64) k_decay_walk<T, KIND, 64, 2, DOTS><<<n, 256, 0, s>>>(a);
-        else k_decay_walk<T, KIND, 64, 1, DOTS><<<n, 256, 0, s>>>(a);
+        if (Dc > 64) f(C64{}, Two{});
+        else f(C64{}, One{});
     }
 }
 template <int KIND, bool DOTS>
-int launch_decay_walk_of(const DecayArgs& a, int32_t dtype, hipStream_t s) {
-    if (dtype == SSMP_F32) launch_decay_walk_t<float, KIND, DOTS>(a, s);
-    else launch_decay_walk_t<uint16_t, KIND, DOTS>(a, s);
+int launch_decay_walk(const DecayArgs& a, int32_t dtype, hipStream_t s) {
+    const unsigned n = (unsigned)decay_walk_blocks(a, KIND);
+    constexpr bool KEYS = decay_by_key(KIND);
+    decay_dispatch(KEYS ? a.Dv : a.Dk, KEYS ? a.Dk : a.Dv, [&](auto db, auto ct) {
+        constexpr int DBP = decltype(db)::value, CT = decltype(ct)::value;
+        if (dtype == SSMP_F32) k_decay_walk<float, KIND, DBP, CT, DOTS><<<n, 256, 0, s>>>(a);
+        else k_decay_walk<uint16_t, KIND, DBP, CT, DOTS><<<n, 256, 0, s>>>(a);
+    });
     SSMP_LAUNCH_CHECK();
     return SSMP_OK;
 }
-// each kind is compiled in the source that DecayKind's comment names
-template <int KIND>
-int launch_decay_walk(const DecayArgs& a, int32_t dtype, hipStream_t s);
-
-template <bool REV>
-int launch_decay_join(const DecayArgs& a, hipStream_t s) {
-    const int64_t slots = a.T / a.seg + a.nseq, per = (int64_t)a.Dk * a.Dv / 1024 + 1;
-    int64_t blocks = 2048 / (slots * a.Hv);
+// Both walks. KIND2's b and c have heads of Dk and Dv; KIND's those, or the other way round
+template <int KIND, bool DOTS, int KIND2>
+int launch_decay_pair(const DecayArgs& a, int32_t dtype, hipStream_t s) {
+    const unsigned n = (unsigned)decay_walk_blocks(a, KIND), m = n + (unsigned)decay_walk_blocks(a, KIND2);
+    if (m > kPairBlocks) {
+        if (const int st = launch_decay_walk<KIND, DOTS>(a, dtype, s)) return st;
+        return launch_decay_walk<KIND2, false>(a, dtype, s);
+    }
+    constexpr bool KEYS = decay_by_key(KIND);
+    decay_dispatch(a.Dk, a.Dv, [&](auto db, auto ct) {
+        constexpr int DBP2 = decltype(db)::value, CT2 = decltype(ct)::value;
+        constexpr int DBP = KEYS ? CT2 * 64 : DBP2, CT = KEYS ? DBP2 / 64 : CT2;
+        if (dtype == SSMP_F32) k_decay_pair<float, KIND, DBP, CT, DOTS, KIND2, DBP2, CT2><<<m, 256, 0, s>>>(a, n);
+        else k_decay_pair<uint16_t, KIND, DBP, CT, DOTS, KIND2, DBP2, CT2><<<m, 256, 0, s>>>(a, n);
+    });
+    SSMP_LAUNCH_CHECK();
+    return SSMP_OK;
+}
+inline int launch_decay_join(const DecayArgs& a, int ways, hipStream_t s) {
+    const int64_t per = ((int64_t)a.Dk * a.Dv + 1023) / 1024;  // blocks of an element a thread
+    int64_t blocks = 2048 / ((int64_t)a.nseq * a.Hv);
     blocks = blocks < 1 ? 1 : blocks > per ? per : blocks;
-    k_decay_join<REV><<<(unsigned)(slots * a.Hv * blocks), 256, 0, s>>>(a, (int)blocks);
+    k_decay_join<><<<(unsigned)((int64_t)a.nseq * a.Hv * blocks * ways), 256, 0, s>>>(a, (int)blocks, ways);
     SSMP_LAUNCH_CHECK();
     return SSMP_OK;
 }
+// compiled in sources of their own
+int launch_decay_dq(const DecayArgs& a, int32_t dtype, hipStream_t s);
+int launch_decay_dkv(const DecayArgs& a, int32_t dtype, hipStream_t s);
 
 inline int decay_check(int64_t T, int32_t nseq, int32_t Hk, int32_t Hv, int32_t Dk, int32_t Dv, int32_t dtype) {
     if (const int st = delta_check(T, nseq, Hk, Hv, Dk, Dv, dtype)) return st;
     const int64_t slices = (Dv + kDecayMaxDb - 1) / kDecayMaxDb;
     if (Hv * slices * Dk > kMaxRow) return SSMP_ERR_SHAPE;  // a row of dq's parts
-    if ((T / kPiece + nseq + 7) * (int64_t)Hv * slices >= kMaxBlocks) return SSMP_ERR_SHAPE;
+    // two walks in a launch, over segments of kSegMin at least; 128 columns of each
+    if ((T / kSegMin + nseq + 7) * (int64_t)Hv * slices * 2 >= kMaxBlocks) return SSMP_ERR_SHAPE;
     return SSMP_OK;
 }
 

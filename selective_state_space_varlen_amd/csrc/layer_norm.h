@@ -1,0 +1,209 @@
+// layer_norm_pack: the layer norm of rows or heads, with the residual sum and
+// dropout before it in the same pass, and its gradients. Over a row's D
+// components,
+//   h = residual + drop(x),  n = (h - mean) r,  r = (var + eps)^(-1/2),  y = n w + b;
+// with c = dy w the gradients are
+//   dh' = r (c - mean(c) - n mean(c n)) + dh,  dresidual = dh',  dx = drop(dh'),
+//   dw = sum_rows dy n,  db = sum_rows dy.
+// Bound by HBM: each row is read and written once, and lies in registers
+// between. The variance is formed from the differences from the mean, so that
+// no difference of large sums loses it.
+#pragma once
+
+#include "dropout.h"
+
+namespace ssmp {
+
+constexpr int kLnMaxD = 16384;
+// threads of a workgroup whose rows lie across so many lanes
+constexpr int ln_threads(int lanes) { return lanes > 256 ? lanes : 256; }
+constexpr int kLnWaves = 16;  // of the largest workgroup
+
+struct LnArgs {
+    const void *x, *residual, *dy, *dh;  // backward: x is h
+    const float *w, *b;
+    void *y, *h;                         // backward: dx, dresidual
+    float *dw, *db;
+    void* part;                          // backward: [group][2][D] sums
+    Drop drop;
+    int64_t rows;
+    int32_t H, D;
+    float eps;
+    int32_t wide;                        // the sums in `part` are doubles
+};
+
+// sum over the LANES lanes that share a row; a whole workgroup's through LDS
+template <int LANES>
+__device__ __forceinline__ float lane_sum(float v) {
+    if constexpr (LANES >= 2) v = dpp_add<0xB1>(v);
+    if constexpr (LANES >= 4) v = dpp_add<0x4E>(v);
+    if constexpr (LANES >= 8) v = dpp_add<0x141>(v);
+    if constexpr (LANES >= 16) v = dpp_add<0x140>(v);
+    if constexpr (LANES >= 32) v += __shfl_xor(v, 16);
+    if constexpr (LANES >= 64) v += __shfl_xor(v, 32);
+    return v;
+}
+template <int WAVES>
+__device__ __forceinline__ float waves_sum(const float* lds) {
+    float t[WAVES];
+#pragma unroll
+    for (int i = 0; i < WAVES; ++i) t[i] = lds[i];
+#pragma unroll
+    for (int d = 1; d < WAVES; d *= 2)
+#pragma unroll
+        for (int i = 0; i < WAVES; i += 2 * d) t[i] += t[i + d];
+    return t[0];
+}
+// several sums at one barrier
+template <int LANES, int N>
+__device__ __forceinline__ void row_sums(float (&v)[N], float (*lds)[kLnWaves]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = lane_sum<LANES>(v[i]);
+    if constexpr (LANES > 64) {
+        if ((threadIdx.x & 63) == 0)
+#pragma unroll
+            for (int i = 0; i < N; ++i) lds[i][threadIdx.x >> 6] = v[i];
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = waves_sum<LANES / 64>(lds[i]);
+    }
+}
+
+// A row of NV pieces of V in each of LANES lanes: piece j of lane i at column (j LANES + i) V
+template <typename T, int V, int LANES, int NV>
+struct LnRow {
+    Piece<T, V> u[NV];
+    __device__ __forceinline__ void load(const void* base, int64_t row, int D, int lane, bool on) {
+        const T* const p = static_cast<const T*>(base) + row * D;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int c = (j * LANES + lane) * V;
+            if (on && c < D) u[j].load(p + c);
+            else u[j].zero();
+        }
+    }
+    __device__ __forceinline__ void add(float (&v)[NV][V]) const {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            float t[V];
+            u[j].get(t);
+#pragma unroll
+            for (int e = 0; e < V; ++e) v[j][e] += t[e];
+        }
+    }
+    static __device__ __forceinline__ void store(void* base, int64_t row, int D, int lane, const float (&v)[NV][V]) {
+        T* const p = static_cast<T*>(base) + row * D;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int c = (j * LANES + lane) * V;
+            if (c < D) Piece<T, V>::store(p + c, v[j]);
+        }
+    }
+};
+template <int V, int LANES, int NV>
+__device__ __forceinline__ void drop_row(const Philox& ph, const Drop& d, int64_t row, int D, int lane, float (&v)[NV][V]) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const uint64_t e = (uint64_t)row * D + (j * LANES + lane) * V;
+        if constexpr (V == 8) drop8(ph, d, e >> 3, v[j]);
+        else v[j][0] = drop1(ph, d, e, v[j][0]);
+    }
+}
+// weights of a lane's columns, fill where there are none
+template <int V, int LANES, int NV>
+__device__ __forceinline__ void ln_weights(const float* w, int D, int lane, float fill, float (&v)[NV][V]) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            const int c = (j * LANES + lane) * V + e;
+            v[j][e] = w && c < D ? w[c] : fill;
+        }
+}
+// The reciprocal root of a row's variance from the sums of its differences
+// from a mean and of their squares. The first sum is what that mean was off by,
+// a rounding of its size, which may be far over the row's spread: `more`, to be
+// taken off the differences too.
+__device__ __forceinline__ float ln_root(const LnArgs& a, float sum, float squares, float& more) {
+    more = sum / (float)a.D;
+    const float var = squares / (float)a.D - more * more;
+    return 1.0f / sqrtf((var < 0.0f ? 0.0f : var) + a.eps);
+}
+
+// How a row lies: pieces of 8 elements where every row starts at a multiple of
+// 16 bytes, single ones otherwise; up to 512 (256) components in one wave or a
+// part of it, longer rows across a workgroup of as many lanes as leave each
+// one piece: more of them in a lane would leave too few waves a CU to hide the
+// loads (rows of 4096, backward: 512 lanes of one piece and 256 of two measured
+// below).
+struct LnForm {
+    int vec, lanes, nv;
+};
+inline LnForm ln_form(int32_t D) {
+    if (D % 8 == 0) {
+        for (int lanes = 4; lanes <= 64; lanes *= 2)
+            if (D <= lanes * 8) return {8, lanes, 1};
+        for (int lanes = 256; lanes <= 1024; lanes *= 2)
+            if (D <= lanes * 8) return {8, lanes, 1};
+        return {8, 1024, 2};
+    }
+    if (D <= 64) return {1, 64, 1};
+    if (D <= 256) return {1, 64, 4};
+    if (D <= 1024) return {1, 256, 4};
+    return {1, 1024, D <= 4096 ? 4 : D <= 8192 ? 8 : 16};
+}
+inline int ln_groups(int32_t D) { return ln_threads(ln_form(D).lanes) / ln_form(D).lanes; }  // of a workgroup
+// Workgroups: as many as have room at a time (`most` of 256 threads), a
+// multiple of what gives each group one head; at least `least` rows a group
+inline int64_t ln_blocks(int64_t rows, int32_t H, int32_t D, int64_t most, int64_t least = 1) {
+    const int sg = ln_groups(D);
+    most = most * 256 / ln_threads(ln_form(D).lanes);
+    int64_t a = H, b = sg;
+    while (b) {
+        const int64_t t = a % b;
+        a = b;
+        b = t;
+    }
+    const int64_t unit = H / a;  // groups = blocks * sg is then a multiple of H
+    int64_t n = (rows + sg * least - 1) / (sg * least);
+    n = n < most ? n : most;
+    return (n + unit - 1) / unit * unit;
+}
+constexpr int64_t kLnFwdBlocks = 2048, kLnBwdBlocks = 1024, kLnBwdRows = 4;
+
+// f(vector length, lanes, pieces) of a row's form, as constants
+template <int V, int L, int N>
+struct LnShape {
+    static constexpr int vec = V, lanes = L, nv = N;
+};
+template <typename F>
+void ln_dispatch(int32_t D, F f) {
+    const LnForm m = ln_form(D);
+    if (m.vec == 8) {
+        switch (m.lanes) {
+            case 4: return f(LnShape<8, 4, 1>{});
+            case 8: return f(LnShape<8, 8, 1>{});
+            case 16: return f(LnShape<8, 16, 1>{});
+            case 32: return f(LnShape<8, 32, 1>{});
+            case 64: return f(LnShape<8, 64, 1>{});
+            case 256: return f(LnShape<8, 256, 1>{});
+            case 512: return f(LnShape<8, 512, 1>{});
+        }
+        return m.nv == 1 ? f(LnShape<8, 1024, 1>{}) : f(LnShape<8, 1024, 2>{});
+    }
+    if (m.lanes == 64) return m.nv == 1 ? f(LnShape<1, 64, 1>{}) : f(LnShape<1, 64, 4>{});
+    if (m.lanes == 256) return f(LnShape<1, 256, 4>{});
+    if (m.nv == 4) return f(LnShape<1, 1024, 4>{});
+    return m.nv == 8 ? f(LnShape<1, 1024, 8>{}) : f(LnShape<1, 1024, 16>{});
+}
+
+inline int ln_check(int64_t T, int32_t H, int32_t D, int32_t dtype) {
+    if (T < 0 || H < 1 || D < 1 || H > 65536 || T >= (int64_t(1) << 31) || T * H >= (int64_t(1) << 40) ||
+        T * H * D >= (int64_t(1) << 40))
+        return SSMP_ERR_SHAPE;
+    if (D > kLnMaxD) return SSMP_ERR_UNSUPPORTED;
+    if ((int64_t)H * ((2 * D + 31) / 32) >= kMaxBlocks / 4) return SSMP_ERR_SHAPE;  // k_layer_norm_dw's workgroups of 1024
+    if (dtype != SSMP_F32 && dtype != SSMP_BF16) return SSMP_ERR_UNSUPPORTED;
+    return SSMP_OK;
+}
+}  // namespace ssmp
