@@ -48,4 +48,4 @@ from .binding import (  # noqa: F401
     varlen_pack_indices,
     varlen_pack_plan,
 )
-from .pipeline import backward, delta_backward, delta_forward, forward  # noqa: F401
+from .pipeline import backward, decay_backward, decay_forward, delta_backward, delta_forward, forward  # noqa: F401
