@@ -617,7 +617,7 @@ def _arg(t: Optional[torch.Tensor], name: str, shape, dtype, dev) -> Optional[in
     _check names what is wrong with one that is not."""
     if t is None:
         return None
-    if not (t.shape == shape and t.dtype is dtype and t.device == dev and t.is_contiguous()) or dev.type != "cuda":
+    if not (t.shape == shape and t.dtype is dtype and t.device == dev and t.is_contiguous() and t.is_cuda):
         _check(t, name, shape, dtype, dev)
     return t.data_ptr()
 

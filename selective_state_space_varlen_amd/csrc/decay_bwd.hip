@@ -98,7 +98,7 @@ struct DecayBwdLayout {
 };
 inline DecayBwdLayout decay_bwd_layout(int64_t T, int32_t nseq, int32_t Hk, int32_t Hv, int32_t Dk, int32_t Dv) {
     DecayBwdLayout L;
-    const size_t slices = (Dv + kDecayMaxDb - 1) / kDecayMaxDb;
+    const size_t slices = (Dv + kDecayMaxDb - 1) / kDecayMaxDb, parts = slices * (Dk > 64 ? 2 : 1);
     const DecayJoint j = decay_joint(T, Hv, Dk, Dv, Hv);
     size_t at = 0;
     const auto take = [&](size_t bytes) {
@@ -113,11 +113,11 @@ inline DecayBwdLayout decay_bwd_layout(int64_t T, int32_t nseq, int32_t Hk, int3
     }
     const bool partial = (size_t)(Hv / Hk) * slices > 1;
     for (int i = 0; i < 2; ++i) L.part[i] = take(partial ? (size_t)T * Hv * slices * Dk * sizeof(float) : 0);
-    for (int i = 0; i < 2; ++i) L.rows[i] = take(slices * T * Hv * sizeof(float));
-    for (int i = 0; i < 2; ++i) L.chunk[i] = take((size_t)delta_slots(T, nseq) * Hv * slices * sizeof(float));
-    const size_t db = Dv > 64 ? 128 : 64, dc = decay_cols(Dk);
+    for (int i = 0; i < 2; ++i) L.rows[i] = take(parts * T * Hv * sizeof(float));
+    for (int i = 0; i < 2; ++i) L.chunk[i] = take((size_t)delta_slots(T, nseq) * Hv * parts * sizeof(float));
+    const size_t db = Dv > 64 ? 128 : 64, dc = Dk > 64 ? 128 : 64;
     L.snap = take((size_t)(T / kPiece) * Hv * slices * db * dc * sizeof(float));
-    L.meet = take((size_t)(T / kPiece + nseq) * Hv * slices * sizeof(float));
+    L.meet = take((size_t)(T / kPiece + nseq) * Hv * parts * sizeof(float));
     L.dgsum = take((size_t)(T / kPiece + nseq) * Hv * sizeof(double));
     L.total = at;
     return L;
@@ -171,6 +171,7 @@ extern "C" int decay_attn_pack_bwd(const void* q, const void* k, const void* v, 
     a.scale = scale;
     a.slices = (Dv + kDecayMaxDb - 1) / kDecayMaxDb;
     a.seg = decay_segment(T, nseq, Hv);
+    a.few = T / a.seg <= kFewStates;
     if (T == 0) {
         if (!per_token)
             if (const int st = zero_f32(dg, Hv, s)) return st;
@@ -198,7 +199,7 @@ extern "C" int decay_attn_pack_bwd(const void* q, const void* k, const void* v, 
     if (const int st = launch_decay_dkv(a, dtype, s)) return st;
     if (dg) {
         const int64_t slots = T / kPiece + nseq;
-        k_decay_dg<<<(unsigned)(slots * ((Hv + kDgHeads - 1) / kDgHeads)), 64, 0, s>>>(a, a.slices);
+        k_decay_dg<<<(unsigned)(slots * ((Hv + kDgHeads - 1) / kDgHeads)), 64, 0, s>>>(a, a.slices * decay_blocks_of(Dv, Dk, dtype));
         SSMP_LAUNCH_CHECK();
         if (!per_token) {
             k_decay_dg_sum<<<(unsigned)Hv, 64, 0, s>>>(a, slots);

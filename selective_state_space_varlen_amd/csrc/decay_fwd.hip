@@ -43,6 +43,7 @@ extern "C" int decay_attn_pack_fwd(const void* q, const void* k, const void* v, 
     a.scale = scale;
     a.slices = 1;
     a.seg = decay_segment(T, nseq, work);
+    a.few = T / a.seg <= kFewStates;
     if (need) {
         a.joint[0] = reinterpret_cast<float*>(static_cast<char*>(scratch) + L.joint);
         a.seg_decay[0] = reinterpret_cast<float*>(static_cast<char*>(scratch) + L.decay);

@@ -36,7 +36,6 @@ constexpr int kPiece = 256;         // tokens between the points where dg is anc
 constexpr int kSegMin = 128, kSegMax = 2048;
 constexpr int kSegWork = 768;       // workgroups that a launch should have
 
-inline int decay_cols(int32_t Dc) { return Dc <= 64 ? 64 : kDecayCols; }
 inline int decay_col_blocks(int32_t Dc) { return (Dc + kDecayCols - 1) / kDecayCols; }
 // work: heads * column blocks, the workgroups that a segment has. Enough
 // sequences are walked whole, as the first walk costs a third of the forward;
@@ -73,6 +72,7 @@ struct DecayArgs {
     int32_t seg;
     float *joint[2];      // states S, dS between segments: [state][Hv][Dk][Dv]
     float* seg_decay[2];  // [state][Hv]: e^(sum of g over the segment)
+    int32_t few;          // few segments: each walk adds up what the others left (no k_decay_join)
     // backward
     int32_t slices;       // of 128 rows that Dv has in dq and dk
     float* part[2];       // dq, dk by value head and slice: [T][Hk][members][Dk]; null where there is one
@@ -154,6 +154,33 @@ __device__ __forceinline__ int64_t uniform(int64_t v) {
     return (int64_t)(((uint64_t)(uint32_t)uniform((int32_t)(v >> 32)) << 32) | (uint32_t)uniform((int32_t)v));
 }
 
+// 64 rows in LDS as bf16 planes, for fp32 three: splitting at every read, in
+// every wave, took more time than the products (1237 tokens x 6 heads of 40 x
+// 72 in fp32: forward 39 us, now 27). The two readings are RowTile's.
+template <typename T, int W>
+struct DecayTile {
+    static constexpr int NX = kExact<T>;
+    RowTile<uint16_t, W> p[NX];
+    __device__ __forceinline__ void put(int i, int unit, const Unit<T>& u) {
+        const Frag<NX> f = unit_planes(u);
+#pragma unroll
+        for (int x = 0; x < NX; ++x)
+            *reinterpret_cast<u32x4*>(p[x].x + RowTile<uint16_t, W>::L::at(i, unit)) = __builtin_bit_cast(u32x4, f.p[x]);
+    }
+    __device__ __forceinline__ Frag<NX> frag(int token, int unit) const {
+        Frag<NX> f;
+#pragma unroll
+        for (int x = 0; x < NX; ++x) f.p[x] = p[x].frag(token, unit).p[0];
+        return f;
+    }
+    __device__ __forceinline__ Frag<NX> token_frag(int l, int s, int m) const {
+        Frag<NX> f;
+#pragma unroll
+        for (int x = 0; x < NX; ++x) f.p[x] = p[x].token_frag(l, s, m).p[0];
+        return f;
+    }
+};
+
 // 64 rows of a side on their way to LDS, W columns of it
 template <typename T, int W, int THREADS>
 struct SideLoads {
@@ -165,21 +192,13 @@ struct SideLoads {
 #pragma unroll
         for (int x = 0; x < kN; ++x) u[x].load(r, at + s.rows(x * kRows));
     }
-    __device__ __forceinline__ void put(RowTile<T, W>& t) const {
+    __device__ __forceinline__ void put(DecayTile<T, W>& t) const {
 #pragma unroll
-        for (int x = 0; x < kN; ++x) {
-            T* const p = t.x + RowTile<T, W>::L::at((threadIdx.x + x * THREADS) / (W / 8), (threadIdx.x + x * THREADS) % (W / 8));
-            if constexpr (sizeof(T) == 2) {
-                *reinterpret_cast<u32x4*>(p) = u[x].w;
-            } else {
-                u[x].put_half(p, 0);
-                u[x].put_half(p + 4, 1);
-            }
-        }
+        for (int x = 0; x < kN; ++x) t.put((threadIdx.x + x * THREADS) / (W / 8), (threadIdx.x + x * THREADS) % (W / 8), u[x]);
     }
 };
 
-// Tiles hold their columns as they come. RowTile's reading of columns 16 m + n
+// Tiles hold their columns as they come. Their reading of columns 16 m + n
 // then gives columns 32 (m / 2) + 8 (n / 4) + 4 (m % 2) + n % 4, so that what
 // tiles m = 2 i and 2 i + 1 of a result leave in a lane are eight rows that lie
 // together, 32 i + 8 (l / 16) .. + 7: the order in which the next product takes
@@ -249,8 +268,8 @@ template <typename T, bool DOTS>
 constexpr int kDecayPlanes = kExact<T> == 3 || DOTS ? 3 : 2;
 template <typename T, int DBP, int CT, int NP>
 struct DecayTiles {
-    RowTile<T, DBP> a, b;
-    RowTile<T, 64 * CT> c;
+    DecayTile<T, DBP> a, b;
+    DecayTile<T, 64 * CT> c;
     u32x4 P[8 * NP][64];          // [row tile][block of 32 columns][plane]: as one lane reads them
     DecayRows rows[2];            // this chunk's and the next one's
     float dot[4][kC], sum[2][4];  // by wave: dg's row sums; the anchor and the chunk's sum
@@ -330,21 +349,30 @@ __device__ __forceinline__ void decay_walk(const DecayArgs& p, int64_t block,
                 for (int x = 0; x < 4; ++x) Elt<float>::st_rsrc<0>(r, at(m, ct, x), S[m][ct][x]);
     };
     if constexpr (!SUM) {
-        const float* from = nullptr;
-        int64_t n = 0;
-        if (REV ? !sg.last : sg.index > 0) {
-            from = p.joint[REV];
-            n = REV ? state0 : state0 - 1;
-        } else {
-            from = REV ? p.dhT : p.h0;
-            n = sg.seq;
-        }
-        if (from) {
-            const auto r = state_rsrc(from, n);
+        const auto from = [&](const float* base, int64_t n) {
+            const auto r = state_rsrc(base, n);
 #pragma unroll
             for (int m = 0; m < MT; ++m)
 #pragma unroll
                 for (int ct = 0; ct < CT; ++ct) S[m][ct] = state_at(r, m, ct);
+        };
+        const float* const given = REV ? p.dhT : p.h0;
+        const bool inner = REV ? !sg.last : sg.index > 0;  // the state is another segment's
+        if (inner && !p.few) from(p.joint[REV], REV ? state0 : state0 - 1);
+        else if (given) from(given, sg.seq);
+        if (inner && p.few) {  // what each segment on the way has added to the given one
+            const int64_t all = first / p.seg;
+            const int ends = uniform((int32_t)((seq_at(p.cu, sg.seq, p.T).len - 1) / p.seg));  // states between segments
+            const int n = REV ? ends - (int)sg.index : (int)sg.index;
+            for (int j = 0; j < n; ++j) {
+                const int64_t at_j = all + (REV ? ends - 1 - j : j);
+                const auto r = state_rsrc(p.joint[REV], at_j);
+                const float d = p.seg_decay[REV][at_j * p.Hv + hv];
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct) S[m][ct] = S[m][ct] * d + state_at(r, m, ct);
+            }
         }
     }
     const int chunks = (sg.n + kC - 1) / kC;
@@ -776,59 +804,76 @@ __global__ __launch_bounds__(256) void k_decay_join(DecayArgs p, int blocks, int
     else decay_join<true>(p, s, hv, block, blocks);
 }
 
+// Columns of c that a workgroup takes, in tiles of 16 a wave: two, or one where
+// there are no more or where fp32's planes of rows over 64 leave LDS for no more
+template <typename T>
+constexpr int decay_tiles(bool wide_b, bool wide_c) {
+    return wide_c && !(kExact<T> == 3 && wide_b) ? 2 : 1;
+}
+inline int decay_blocks_of(int32_t Db, int32_t Dc, int32_t dtype) {
+    const int cols = 64 * (dtype == SSMP_F32 ? decay_tiles<float>(Db > 64, Dc > 64) : decay_tiles<uint16_t>(Db > 64, Dc > 64));
+    return (Dc + cols - 1) / cols;
+}
 // The walks' workgroups, by kind: those of heads that share a and b, or c, on
 // one XCD.
-inline int64_t decay_walk_blocks(const DecayArgs& a, int kind) {
-    const int32_t Dc = decay_by_key(kind) ? a.Dk : a.Dv;
-    const int members = a.Hv / a.Hk * (decay_by_key(kind) ? a.slices : 1) * ((Dc + decay_cols(Dc) - 1) / decay_cols(Dc));
-    return spread_blocks((a.T / a.seg + a.nseq) * a.Hk, members);
+inline int64_t decay_walk_blocks(const DecayArgs& a, int kind, int32_t dtype) {
+    const bool keys = decay_by_key(kind);
+    const int blocks = keys ? a.slices * decay_blocks_of(a.Dv, a.Dk, dtype) : decay_blocks_of(a.Dk, a.Dv, dtype);
+    return spread_blocks((a.T / a.seg + a.nseq) * a.Hk, a.Hv / a.Hk * blocks);
 }
-// f(rows of the state, column tiles), as constants, by heads of b and c
+// f(fp32, Dk over 64, Dv over 64), as constants
 template <typename F>
-void decay_dispatch(int32_t Db, int32_t Dc, F f) {
-    using C64 = std::integral_constant<int, 64>;
-    using C128 = std::integral_constant<int, 128>;
-    using One = std::integral_constant<int, 1>;
-    using Two = std::integral_constant<int, 2>;
-    if (Db > 64) {
-        if (Dc > 64) f(C128{}, Two{});
-        else f(C128{}, One{});
-    } else {
-        if (Dc > 64) f(C64{}, Two{});
-        else f(C64{}, One{});
-    }
+void decay_dispatch(const DecayArgs& a, int32_t dtype, F f) {
+    using Y = std::true_type;
+    using N = std::false_type;
+    const auto with = [&](auto t) {
+        if (a.Dk > 64) a.Dv > 64 ? f(t, Y{}, Y{}) : f(t, Y{}, N{});
+        else a.Dv > 64 ? f(t, N{}, Y{}) : f(t, N{}, N{});
+    };
+    if (dtype == SSMP_F32) with(Y{});
+    else with(N{});
 }
+template <int KIND, bool WK, bool WV, typename T>
+struct DecayForm {  // of a walk, for heads of Dk and Dv over 64 or not
+    static constexpr bool B = decay_by_key(KIND) ? WV : WK, C = decay_by_key(KIND) ? WK : WV;
+    static constexpr int DBP = B ? 128 : 64, CT = decay_tiles<T>(B, C);
+};
+template <bool FP32>
+using DecayType = typename std::conditional<FP32, float, uint16_t>::type;
 template <int KIND, bool DOTS>
 int launch_decay_walk(const DecayArgs& a, int32_t dtype, hipStream_t s) {
-    const unsigned n = (unsigned)decay_walk_blocks(a, KIND);
-    constexpr bool KEYS = decay_by_key(KIND);
-    decay_dispatch(KEYS ? a.Dv : a.Dk, KEYS ? a.Dk : a.Dv, [&](auto db, auto ct) {
-        constexpr int DBP = decltype(db)::value, CT = decltype(ct)::value;
-        if (dtype == SSMP_F32) k_decay_walk<float, KIND, DBP, CT, DOTS><<<n, 256, 0, s>>>(a);
-        else k_decay_walk<uint16_t, KIND, DBP, CT, DOTS><<<n, 256, 0, s>>>(a);
+    const unsigned n = (unsigned)decay_walk_blocks(a, KIND, dtype);
+    decay_dispatch(a, dtype, [&](auto fp32, auto wk, auto wv) {
+        using T = DecayType<decltype(fp32)::value>;
+        using F = DecayForm<KIND, decltype(wk)::value, decltype(wv)::value, T>;
+        k_decay_walk<T, KIND, F::DBP, F::CT, DOTS><<<n, 256, 0, s>>>(a);
     });
     SSMP_LAUNCH_CHECK();
     return SSMP_OK;
 }
-// Both walks. KIND2's b and c have heads of Dk and Dv; KIND's those, or the other way round
+// Both walks, beside each other where they are small
 template <int KIND, bool DOTS, int KIND2>
 int launch_decay_pair(const DecayArgs& a, int32_t dtype, hipStream_t s) {
-    const unsigned n = (unsigned)decay_walk_blocks(a, KIND), m = n + (unsigned)decay_walk_blocks(a, KIND2);
+    const unsigned n = (unsigned)decay_walk_blocks(a, KIND, dtype), m = n + (unsigned)decay_walk_blocks(a, KIND2, dtype);
     if (m > kPairBlocks) {
         if (const int st = launch_decay_walk<KIND, DOTS>(a, dtype, s)) return st;
         return launch_decay_walk<KIND2, false>(a, dtype, s);
     }
-    constexpr bool KEYS = decay_by_key(KIND);
-    decay_dispatch(a.Dk, a.Dv, [&](auto db, auto ct) {
-        constexpr int DBP2 = decltype(db)::value, CT2 = decltype(ct)::value;
-        constexpr int DBP = KEYS ? CT2 * 64 : DBP2, CT = KEYS ? DBP2 / 64 : CT2;
-        if (dtype == SSMP_F32) k_decay_pair<float, KIND, DBP, CT, DOTS, KIND2, DBP2, CT2><<<m, 256, 0, s>>>(a, n);
-        else k_decay_pair<uint16_t, KIND, DBP, CT, DOTS, KIND2, DBP2, CT2><<<m, 256, 0, s>>>(a, n);
+    decay_dispatch(a, dtype, [&](auto fp32, auto wk, auto wv) {
+        using T = DecayType<decltype(fp32)::value>;
+        using F = DecayForm<KIND, decltype(wk)::value, decltype(wv)::value, T>;
+        using G = DecayForm<KIND2, decltype(wk)::value, decltype(wv)::value, T>;
+        k_decay_pair<T, KIND, F::DBP, F::CT, DOTS, KIND2, G::DBP, G::CT><<<m, 256, 0, s>>>(a, n);
     });
     SSMP_LAUNCH_CHECK();
     return SSMP_OK;
 }
+// Up to so many states between segments are added up by the walks themselves,
+// each reading those on its way: a prompt of 513 tokens x 32 heads of 128 x 128
+// in 5 segments takes 33 us with a join between the walks and 29 without.
+constexpr int kFewStates = 5;
 inline int launch_decay_join(const DecayArgs& a, int ways, hipStream_t s) {
+    if (a.few) return SSMP_OK;
     const int64_t per = ((int64_t)a.Dk * a.Dv + 1023) / 1024;  // blocks of an element a thread
     int64_t blocks = 2048 / ((int64_t)a.nseq * a.Hv);
     blocks = blocks < 1 ? 1 : blocks > per ? per : blocks;
