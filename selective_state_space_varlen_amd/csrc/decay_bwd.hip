@@ -19,45 +19,51 @@ __global__ __launch_bounds__(64) void k_decay_dg(DecayArgs p, int parts) {
     const int hv = blockIdx.x % hb * kDgHeads + threadIdx.x % kDgHeads, ch = threadIdx.x / kDgHeads;
     Chunk c;
     const bool any = chunk_at(p.cu, p.nseq, p.T, slot, c, kPiece) && hv < p.Hv;
-    double sum = 0.0;
-    if (any && ch * kC < c.n) {
-        double acc = 0.0;
+    const int n = any ? min(c.n - ch * kC, kC) : 0;  // tokens of this lane's chunk
+    const int64_t t0 = c.start + ch * kC;
+    double acc = 0.0, sum = 0.0, cross = 0.0;  // cross: what goes through the chunk's states
+    if (n > 0) {
         if (!c.last || p.dhT)
             for (int i = 0; i < parts; ++i) acc += (double)p.meet[((size_t)slot * p.Hv + hv) * parts + i];
-        // what crosses between this chunk and those behind it in the piece
-        const int64_t first = c.start - c.index * kPiece, chunk0 = first / kC + c.seq + c.index * (kPiece / kC);
-        const int64_t chunks = (c.n + kC - 1) / kC;
-        for (int64_t i = chunks - 1; i > ch; --i) {
-            const size_t at = ((size_t)(chunk0 + i) * p.Hv + hv) * parts;
-            for (int j = 0; j < parts; ++j) acc += (double)p.chunk[0][at + j] - (double)p.chunk[1][at + j];
+        const int64_t first = c.start - c.index * kPiece, chunk = first / kC + c.seq + c.index * kDgChunks + ch;
+        for (int i = 0; i < parts; ++i) {
+            const size_t at = ((size_t)chunk * p.Hv + hv) * parts + i;
+            cross += (double)p.chunk[0][at] - (double)p.chunk[1][at];
         }
-        constexpr int kBatch = 16;
-        const int64_t t0 = c.start + ch * kC;
-        for (int t1 = min(c.n - ch * kC, kC); t1 > 0; t1 -= kBatch) {
-            float r[kBatch], g[kBatch];
+    }
+    // the anchor at this chunk's end: that of the piece's, and what crosses the chunks between
+    double behind = cross;
+#pragma unroll
+    for (int d = kDgHeads; d < 64; d *= 2) {
+        const double v = __shfl_down(behind, d);
+        behind += threadIdx.x + d < 64 ? v : 0.0;
+    }
+    acc += behind - cross;
+    constexpr int kBatch = 32;  // tokens' loads under way
+    for (int t1 = n; t1 > 0; t1 -= kBatch) {
+        float r[kBatch], g[kBatch];
+#pragma unroll
+        for (int x = 0; x < kBatch; ++x) {
+            const int t = t1 - 1 - x;
+            const size_t at = (size_t)(t0 + (t < 0 ? 0 : t)) * p.Hv + hv;
+            r[x] = p.rows[0][at] - p.rows[1][at];
+            g[x] = p.g[p.gstride ? at : hv];
+        }
+        for (int i = 1; i < parts; ++i)
 #pragma unroll
             for (int x = 0; x < kBatch; ++x) {
                 const int t = t1 - 1 - x;
-                const size_t at = (size_t)(t0 + (t < 0 ? 0 : t)) * p.Hv + hv;
-                r[x] = p.rows[0][at] - p.rows[1][at];
-                g[x] = p.g[p.gstride ? at : hv];
+                const size_t at = ((size_t)i * p.T + t0 + (t < 0 ? 0 : t)) * p.Hv + hv;
+                r[x] += p.rows[0][at] - p.rows[1][at];
             }
-            for (int i = 1; i < parts; ++i)
 #pragma unroll
-                for (int x = 0; x < kBatch; ++x) {
-                    const int t = t1 - 1 - x;
-                    const size_t at = ((size_t)i * p.T + t0 + (t < 0 ? 0 : t)) * p.Hv + hv;
-                    r[x] += p.rows[0][at] - p.rows[1][at];
-                }
-#pragma unroll
-            for (int x = 0; x < kBatch; ++x) {
-                const int t = t1 - 1 - x;
-                if (t < 0) continue;
-                acc += (double)r[x];
-                if (decay_is_zero(g[x])) acc = 0.0;
-                if (p.gstride) p.dg[(size_t)(t0 + t) * p.Hv + hv] = (float)acc;
-                sum += acc;
-            }
+        for (int x = 0; x < kBatch; ++x) {
+            const int t = t1 - 1 - x;
+            if (t < 0) continue;
+            acc += (double)r[x];
+            if (decay_is_zero(g[x])) acc = 0.0;
+            if (p.gstride) p.dg[(size_t)(t0 + t) * p.Hv + hv] = (float)acc;
+            sum += acc;
         }
     }
     if (!p.gstride) {
