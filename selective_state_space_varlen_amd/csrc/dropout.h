@@ -72,18 +72,32 @@ __device__ __forceinline__ float drop1(const Philox& ph, const Drop& d, uint64_t
     return (e & 1 ? x >> 16 : x & 0xffffu) >= d.cut ? v * d.by : 0.0f;
 }
 
-// V elements of a row on their way: 8 as two or one wide access, or a single one
+// V elements of a row on their way: 8 as two or one wide access, or a single
+// one. ONCE: with a temporal hint that nothing of it is to stay in the caches.
 template <typename T, int V>
 struct Piece;
 template <typename T>
 struct Piece<T, 8> {
     Unit<T> u;
+    using W = typename std::conditional<sizeof(T) == 2, u32x4, f32x4>::type;  // of a wide access
+    template <bool ONCE = false>
+    static __device__ __forceinline__ W wide(const W* p) {
+        if constexpr (ONCE) return __builtin_nontemporal_load(p);
+        else return *p;
+    }
+    template <bool ONCE = false>
+    static __device__ __forceinline__ void wide(W* p, const W& w) {
+        if constexpr (ONCE) __builtin_nontemporal_store(w, p);
+        else *p = w;
+    }
+    template <bool ONCE = false>
     __device__ __forceinline__ void load(const T* p) {
+        const W* const at = reinterpret_cast<const W*>(p);
         if constexpr (sizeof(T) == 2) {
-            u.w = *reinterpret_cast<const u32x4*>(p);
+            u.w = wide<ONCE>(at);
         } else {
-            u.w[0] = reinterpret_cast<const f32x4*>(p)[0];
-            u.w[1] = reinterpret_cast<const f32x4*>(p)[1];
+            u.w[0] = wide<ONCE>(at);
+            u.w[1] = wide<ONCE>(at + 1);
         }
     }
     __device__ __forceinline__ void zero() { u = {}; }
@@ -99,14 +113,16 @@ struct Piece<T, 8> {
             for (int e = 0; e < 8; ++e) v[e] = u.w[e >> 2][e & 3];
         }
     }
+    template <bool ONCE = false>
     static __device__ __forceinline__ void store(T* p, const float (&v)[8]) {
         Unit<T> o;
         o.pack(v);
+        W* const at = reinterpret_cast<W*>(p);
         if constexpr (sizeof(T) == 2) {
-            *reinterpret_cast<u32x4*>(p) = o.w;
+            wide<ONCE>(at, o.w);
         } else {
-            reinterpret_cast<f32x4*>(p)[0] = o.w[0];
-            reinterpret_cast<f32x4*>(p)[1] = o.w[1];
+            wide<ONCE>(at, o.w[0]);
+            wide<ONCE>(at + 1, o.w[1]);
         }
     }
 };

@@ -203,6 +203,35 @@ def test_dropout_share_streams_and_far_elements():
         assert [bool(v) for v in (y[at:at + 8] != 0).cpu()] == [u >= 32768 for u in k]
 
 
+@pytest.mark.parametrize("dtype,n", [(F32, (1 << 25) + 5), (BF, (1 << 26) + 5)])
+def test_dropout_of_what_no_cache_holds(dtype, n):
+    """Accesses of large tensors are others: the first elements as in a small
+    call, the last ones, behind the last eight, by the definition."""
+    m, few = ssp(), 4096
+    x = torch.randn(n, device="cuda", generator=torch.Generator("cuda").manual_seed(1)).to(dtype)
+    r = x.flip(0)
+    for res in (None, r):
+        y = m.dropout_pack_fwd(x, 0.5, rng(9, 4), residual=res)
+        assert torch.equal(y[:few], m.dropout_pack_fwd(x[:few], 0.5, rng(9, 4), residual=None if res is None else res[:few]))
+        at = n // 8 * 8 - 8
+        kept = torch.tensor([u >= 32768 for c in (at // 8, at // 8 + 1) for u in philox_of([c, 0], 9, 4)][:n - at])
+        want = torch.where(kept, 2 * x[at:].cpu().float(), torch.zeros(()))  # p = 1/2: twice what is kept, exactly
+        if res is not None:
+            want = want + res[at:].cpu().float()
+        assert torch.equal(y[at:].cpu(), want.to(dtype))
+
+
+def test_rows_past_32_bits_of_elements():
+    m, D = ssp(), 16384
+    T, few = (1 << 18) + 3, 5
+    o = dict(dtype=BF, device="cuda", generator=torch.Generator("cuda").manual_seed(2))
+    x, dy, w = torch.randn(T, D, **o), torch.randn(T, D, **o), torch.rand(D, device="cuda")
+    y, _ = m.layer_norm_pack_fwd(x, w)
+    dx = m.layer_norm_pack_bwd(dy, x, w)["dx"]
+    assert torch.equal(y[-few:], m.layer_norm_pack_fwd(x[-few:].clone(), w)[0])
+    assert torch.equal(dx[-few:], m.layer_norm_pack_bwd(dy[-few:].clone(), x[-few:].clone(), w)["dx"])
+
+
 def philox_of(c, seed, stream):
     low = 0xffffffff
     c, k = c + [stream & low, stream >> 32], [seed & low, seed >> 32]
