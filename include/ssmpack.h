@@ -528,7 +528,9 @@ int gated_delta_pack_step(const void *q, const void *k, const void *v, const flo
  * before it (they share a chunk); other sequences are not touched.
  * Supports Dk a multiple of 8 up to 128, Dv a multiple of 8, Hv a multiple
  * of Hk. Pointers other than g and cu_seqlens must be multiples of 16 bytes.
- * Buffers must not overlap. The sizes do not fall as T or nseq grow: memory
+ * Buffers must not overlap (one buffer as initial and final state is refused:
+ * SSMP_ERR_UNSUPPORTED, as is one that holds dinitial_state and either of the
+ * states that go into the backward). The sizes do not fall as T or nseq grow: memory
  * made for the most tokens and sequences serves all smaller packs.
  * Errors: SSMP_ERR_SHAPE (also Hv > 65535, Hk * Dk, Hv * Dv or Hv * Dk *
  * ceil(Dv / 128) > 2^20, nseq > 2^24, T * Hv * max(Dk, Dv) >= 2^40, or more

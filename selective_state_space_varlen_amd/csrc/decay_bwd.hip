@@ -146,6 +146,7 @@ extern "C" int decay_attn_pack_bwd(const void* q, const void* k, const void* v, 
                                    void* stream) {
     using namespace ssmp;
     if (const int st = decay_check(T, nseq, Hk, Hv, Dk, Dv, dtype)) return st;
+    if (dinitial_state && (dinitial_state == initial_state || dinitial_state == dfinal_state)) return SSMP_ERR_UNSUPPORTED;  // segments of a sequence start from the one while the first writes the other
     if (!cu_seqlens) return SSMP_ERR_NULL;
     if (T > 0 && (!q || !k || !v || !g || !dout || !dq || !dk || !dv)) return SSMP_ERR_NULL;
     if (!aligned16(q, k, v, dout, dq, dk, dv, initial_state, dfinal_state, dinitial_state, scratch))

@@ -16,6 +16,7 @@ extern "C" int decay_attn_pack_fwd(const void* q, const void* k, const void* v, 
                                    size_t scratch_bytes, void* stream) {
     using namespace ssmp;
     if (const int st = decay_check(T, nseq, Hk, Hv, Dk, Dv, dtype)) return st;
+    if (initial_state && initial_state == final_state) return SSMP_ERR_UNSUPPORTED;  // segments of a sequence start from the one while the last writes the other
     if (!cu_seqlens) return SSMP_ERR_NULL;
     if (T > 0 && (!q || !k || !v || !g || !out)) return SSMP_ERR_NULL;
     if (!aligned16(q, k, v, out, initial_state, final_state, scratch)) return SSMP_ERR_ALIGN;

@@ -52,6 +52,13 @@ def test_attention_refusals(lib):
     assert fwd(lib, T=0, q=NULL, k=NULL, v=NULL, g=NULL, out=NULL, scratch=NULL, nscratch=0) == OK  # nothing to do
 
 
+def test_one_buffer_for_two_states_is_refused(lib):
+    """Segments of a sequence run beside each other: one would read what another has written."""
+    assert fwd(lib, h0=FAKE, hT=FAKE) == E_UNSUP
+    assert bwd(lib, h0=FAKE, dh0=FAKE) == E_UNSUP
+    assert bwd(lib, dhT=FAKE, dh0=FAKE) == E_UNSUP
+
+
 def test_more_than_a_launch_takes_is_refused(lib):
     assert fwd(lib, T=1 << 30, Hv=1, Dk=8, Dv=8) == E_SHAPE
     assert fwd(lib, T=100, nseq=1 << 23, Hv=1, Dk=8, Dv=8) == E_SHAPE

@@ -246,3 +246,46 @@ def test_steps_follow_a_prompt():
         y = m.decay_attn_pack_step(*(d[k][at].contiguous() for k in ("q", "k", "v", "g")), state)
         dc.check(y, whole[at].cpu().to(ck.F64), tol + 2.0 ** -13 + 2.0 ** -8, "out")  # both are rounded to bf16
     dc.check(state, hT.cpu(), tol, "state")
+
+
+def test_offsets_past_32_bits():
+    """2.3e9 elements of v (4.6e9 bytes): the last three sequences as alone. 768
+    workgroups or more walk sequences whole, so that both take the same steps."""
+    m = ssp()
+    L, n, Hv, Dk, Dv, few = 2000, 35, 256, 8, 128, 3
+    T = L * n
+    assert T * Hv * Dv > 1 << 31 and few * Hv >= 768
+    gen = torch.Generator("cuda").manual_seed(6)
+    o = dict(device="cuda", generator=gen)
+    q, k = torch.randn(T, 1, Dk, **o).to(BF), torch.randn(T, 1, Dk, **o).to(BF)
+    v, dout = (torch.randn(T, Hv, Dv, dtype=BF, **o) for _ in range(2))
+    g = -torch.rand(T, Hv, **o) * 0.1
+    h0, dhT = (torch.randn(n, Hv, Dk, Dv, **o) for _ in range(2))
+
+    def run_(s, states):
+        t = [x[s] for x in (q, k, v, g)]
+        count = t[0].shape[0] // L
+        cu = dc.cu_of([L] * count).cuda()
+        out, hT = m.decay_attn_pack_fwd(*t, cu, initial_state=h0[states].clone(), final_state=True)
+        G = m.decay_attn_pack_bwd(*t, cu, dout[s], initial_state=h0[states].clone(), dfinal_state=dhT[states].clone(),
+                                  dinitial_state=True)
+        return dict(G, out=out, hT=hT)
+
+    whole = run_(slice(0, T), slice(0, n))
+    alone = run_(slice(T - few * L, T), slice(n - few, n))
+    for name, t in alone.items():
+        assert torch.equal(whole[name][-t.shape[0]:], t), name
+
+
+def test_step_on_a_pool_past_32_bits():
+    m = ssp()
+    Hv, D, slots = 32, 128, 8200
+    assert slots * Hv * D * D > 1 << 32
+    d = dev(ck.inputs(8, [3], Hv, Hv, D, D, BF, False, True))
+    state = torch.empty(slots, Hv, D, D, device="cuda")
+    at = torch.tensor([8199, 0, 8192], dtype=torch.int32, device="cuda")
+    small = torch.randn(3, Hv, D, D, device="cuda", generator=torch.Generator("cuda").manual_seed(9))
+    state[at.long()] = small
+    a = m.decay_attn_pack_step(d["q"], d["k"], d["v"], d["g"], state, at)
+    b = m.decay_attn_pack_step(d["q"], d["k"], d["v"], d["g"], small)
+    assert torch.equal(a, b) and torch.equal(state[at.long()], small)
