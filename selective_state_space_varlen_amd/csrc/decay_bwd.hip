@@ -179,6 +179,7 @@ extern "C" int decay_attn_pack_bwd(const void* q, const void* k, const void* v, 
     a.slices = (Dv + kDecayMaxDb - 1) / kDecayMaxDb;
     a.seg = decay_segment(T, nseq, Hv);
     a.few = T / a.seg <= kFewStates;
+    a.heads = decay_heads_of(a, dtype);
     if (T == 0) {
         if (!per_token)
             if (const int st = zero_f32(dg, Hv, s)) return st;
@@ -187,7 +188,6 @@ extern "C" int decay_attn_pack_bwd(const void* q, const void* k, const void* v, 
     }
     const DecayBwdLayout L = decay_bwd_layout(T, nseq, Hk, Hv, Dk, Dv);
     char* const ws = static_cast<char*>(scratch);
-    const bool partial = Hv / Hk * a.slices > 1;
     for (int i = 0; i < 2; ++i) {
         a.joint[i] = reinterpret_cast<float*>(ws + L.joint[i]);
         a.seg_decay[i] = reinterpret_cast<float*>(ws + L.decay[i]);
@@ -213,10 +213,10 @@ extern "C" int decay_attn_pack_bwd(const void* q, const void* k, const void* v, 
             SSMP_LAUNCH_CHECK();
         }
     }
-    if (partial) {
+    const int members = Hv / Hk / a.heads * a.slices;
+    if (members > 1) {
         const int64_t want = (T * Hk * (Dk / 4) + 255) / 256;
         const dim3 blocks((unsigned)(want < 8192 ? want : 8192), 2);
-        const int members = Hv / Hk * a.slices;
         if (dtype == SSMP_F32) k_decay_add<float><<<blocks, 256, 0, s>>>(a, members);
         else k_decay_add<uint16_t><<<blocks, 256, 0, s>>>(a, members);
         SSMP_LAUNCH_CHECK();

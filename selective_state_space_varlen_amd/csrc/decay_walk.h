@@ -75,6 +75,7 @@ struct DecayArgs {
     int32_t few;          // few segments: each walk adds up what the others left (no k_decay_join)
     // backward
     int32_t slices;       // of 128 rows that Dv has in dq and dk
+    int32_t heads;        // of a key head that a workgroup of dq's and dk's walks has
     float* part[2];       // dq, dk by value head and slice: [T][Hk][members][Dk]; null where there is one
     float* rows[2];       // q.dq and k.dk: [parts][T][Hv]
     float* chunk[2];      // what a chunk's rows of them get from and give to other chunks: [T / 64 + nseq][Hv][parts]
@@ -194,7 +195,10 @@ struct SideLoads {
     }
     __device__ __forceinline__ void put(DecayTile<T, W>& t) const {
 #pragma unroll
-        for (int x = 0; x < kN; ++x) t.put((threadIdx.x + x * THREADS) / (W / 8), (threadIdx.x + x * THREADS) % (W / 8), u[x]);
+        for (int x = 0; x < kN; ++x) {
+            const int at = (int)(threadIdx.x % THREADS) + x * THREADS;
+            t.put(at / (W / 8), at % (W / 8), u[x]);
+        }
     }
 };
 
@@ -285,9 +289,12 @@ struct DecayTiles {
 // The next chunk's rows are under way in registers meanwhile, those of a in
 // the first half of a chunk and those of b and c in the second, so that two
 // workgroups share a CU. DOTS: rows of out times rows of q or k, for dg.
-template <typename T, int KIND, int DBP, int CT, bool DOTS>
+// HEADS = 2 (dq, dk): both value heads of a key head in a workgroup of eight
+// waves, which add up what they have formed, so that there are no parts: each
+// four waves hand those rows to the others that the others store.
+template <typename T, int KIND, int DBP, int CT, bool DOTS, int HEADS = 1>
 __device__ __forceinline__ void decay_walk(const DecayArgs& p, int64_t block,
-                                           DecayTiles<T, DBP, CT, kDecayPlanes<T, DOTS>>& lds) {
+                                           DecayTiles<T, DBP, CT, kDecayPlanes<T, DOTS>>* tiles) {
     constexpr int NX = kExact<T>, NP = kDecayPlanes<T, DOTS>;
     constexpr bool REV = decay_reverse(KIND), SUM = KIND == kSumS || KIND == kSumD, KEYS = decay_by_key(KIND);
     constexpr int MT = DBP / 16, KS = DBP / 32, COLS = 64 * CT;
@@ -297,15 +304,17 @@ __device__ __forceinline__ void decay_walk(const DecayArgs& p, int64_t block,
     constexpr int kFew = REV ? 3 : 0;  // the wave with the fewest tiles of P has G to do
     const int Dc = KEYS ? p.Dk : p.Dv, Db = KEYS ? p.Dv : p.Dk;
     const int ncb = (Dc + COLS - 1) / COLS, slices = KEYS ? p.slices : 1, group = p.Hv / p.Hk;
-    const Spread sp = spread(block, group * slices * ncb);
+    const Spread sp = spread(block, group / HEADS * slices * ncb);  // (HEADS = 2: one group, one slice)
+    const int mine = HEADS == 2 ? wave_id() >> 2 : 0;  // of the workgroup's heads
+    DecayTiles<T, DBP, CT, kDecayPlanes<T, DOTS>>& lds = tiles[mine];
     if (sp.group >= (p.T / p.seg + p.nseq) * (int64_t)p.Hk) return;
     Chunk sg;
     if (SUM ? !chunk_at(p.cu, p.nseq, p.T, sp.group / p.Hk, sg, p.seg) : !segment_at(p, sp.group / p.Hk, sg)) return;
     sg = {uniform(sg.start), uniform(sg.n), uniform(sg.seq), uniform(sg.index), uniform((int32_t)sg.last) != 0};
     if (SUM && (REV ? sg.index == 0 : sg.last)) return;
     const int hk = (int)(sp.group % p.Hk), cb = sp.member % ncb, slice = sp.member / ncb % slices;
-    const int hv = hk * group + sp.member / (ncb * slices);
-    const int wave = wave_id(), l = lane_id(), l16 = l & 15, l4 = l >> 4;
+    const int hv = hk * group + sp.member / (ncb * slices) * HEADS + mine;
+    const int wave = HEADS == 2 ? wave_id() & 3 : wave_id(), l = lane_id(), l16 = l & 15, l4 = l >> 4;
     const int col0 = cb * COLS, off = slice * kDecayMaxDb, db = min(Db - off, DBP), parts = slices * ncb;
     const int64_t first = sg.start - sg.index * p.seg;    // of the sequence
     const int64_t state0 = first / p.seg + sg.index;      // of the state behind this segment
@@ -642,40 +651,43 @@ __device__ __forceinline__ void decay_walk(const DecayArgs& p, int64_t block,
             }
         }
         __builtin_amdgcn_sched_barrier(0);
-        if constexpr (!SUM) {
-            const int H = KEYS ? p.Hk : p.Hv, h = KEYS ? hk : hv, members = group * slices;
+        // rows from .. from + 16 N - 1 of the result
+        const auto store = [&](const auto& y, int from) {
+            constexpr int N = 4 / HEADS;
+            const int H = KEYS ? p.Hk : p.Hv, h = KEYS ? hk : hv, members = HEADS == 2 ? 1 : group * slices;
             if (KEYS && members > 1) {
                 const Side<float> to(p.part[REV], t0, H * members, h * members + sp.member / ncb, Dc, 0, Dc);
                 const auto r = rows_rsrc(to.p, n, to.stride, Dc);
-                const uint32_t at = to.at(fresh(l16), column());
+                const uint32_t at = to.at(fresh(l16), column()) + to.rows(from);
 #pragma unroll
-                for (int t = 0; t < 4; ++t)
+                for (int t = 0; t < N; ++t)
 #pragma unroll
                     for (int ct = 0; ct < CT; ++ct)
-                        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, o[ct][t]), r,
+                        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, y[ct][t]), r,
                                                                (int)(at + to.rows(t * 16) + ct * 16), 0, 0);
-            } else {
-                const Side<T> to(KIND == kOut ? p.out : KIND == kDq ? p.dq : KIND == kDk ? p.dk : p.dv, t0, H, h, Dc, 0, Dc);
-                const auto r = rows_rsrc(to.p, n, to.stride, Dc);
-                const uint32_t at = to.at(fresh(l16), column());
+                return;
+            }
+            const Side<T> to(KIND == kOut ? p.out : KIND == kDq ? p.dq : KIND == kDk ? p.dk : p.dv, t0, H, h, Dc, 0, Dc);
+            const auto r = rows_rsrc(to.p, n, to.stride, Dc);
+            const uint32_t at = to.at(fresh(l16), column()) + to.rows(from);
 #pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    if constexpr (CT == 2) {
-                        Unit<T> u;
-                        const f32x4 y = o[0][t], z = o[CT - 1][t];
-                        u.pack({y[0], y[1], y[2], y[3], z[0], z[1], z[2], z[3]});
-                        u.store(r, at + to.rows(t * 16));
-                    } else if constexpr (NX == 3) {
-                        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, o[0][t]), r,
-                                                               (int)(at + to.rows(t * 16)), 0, 0);
-                    } else {
-                        const f32x4 y = o[0][t];
-                        const u32x2 w = {(uint32_t)f32_to_bf16(y[0]) | ((uint32_t)f32_to_bf16(y[1]) << 16),
-                                         (uint32_t)f32_to_bf16(y[2]) | ((uint32_t)f32_to_bf16(y[3]) << 16)};
-                        __builtin_amdgcn_raw_buffer_store_b64(w, r, (int)(at + to.rows(t * 16)), 0, 0);
-                    }
+            for (int t = 0; t < N; ++t) {
+                const f32x4 x = y[0][t], z = y[CT - 1][t];
+                if constexpr (CT == 2) {
+                    Unit<T> u;
+                    u.pack({x[0], x[1], x[2], x[3], z[0], z[1], z[2], z[3]});
+                    u.store(r, at + to.rows(t * 16));
+                } else if constexpr (NX == 3) {
+                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, x), r, (int)(at + to.rows(t * 16)), 0, 0);
+                } else {
+                    const u32x2 w = {(uint32_t)f32_to_bf16(x[0]) | ((uint32_t)f32_to_bf16(x[1]) << 16),
+                                     (uint32_t)f32_to_bf16(x[2]) | ((uint32_t)f32_to_bf16(x[3]) << 16)};
+                    __builtin_amdgcn_raw_buffer_store_b64(w, r, (int)(at + to.rows(t * 16)), 0, 0);
                 }
             }
+        };
+        if constexpr (!SUM) {
+            if constexpr (HEADS == 1) store(o, 0);
             if constexpr (DOTS) {
 #pragma unroll
                 for (int t = 0; t < 4; ++t) {
@@ -698,6 +710,14 @@ __device__ __forceinline__ void decay_walk(const DecayArgs& p, int64_t block,
             }
         }
         __syncthreads();
+        if constexpr (HEADS == 2) {  // P has been read: row tiles that the other head's waves store, at their places
+            u32x4* const give = &lds.P[0][0] + tid;
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct)
+                    give[(t * CT + ct) * 256] = __builtin_bit_cast(u32x4, mine ? o[ct][t] : o[ct][2 + t]);
+        }
         lb.put(lds.b);
         lc.put(lds.c);
         if constexpr (DOTS) {
@@ -708,6 +728,17 @@ __device__ __forceinline__ void decay_walk(const DecayArgs& p, int64_t block,
             }
         }
         __syncthreads();
+        if constexpr (HEADS == 2) {
+            const u32x4* const take = &tiles[mine ^ 1].P[0][0] + tid;
+            f32x4 y[CT][2];
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct)
+                    y[ct][t] = __builtin_bit_cast(f32x4, take[(t * CT + ct) * 256]) + (mine ? o[ct][2 + t] : o[ct][t]);
+            __syncthreads();  // before the next P
+            store(y, mine * 32);
+        }
     }
     if constexpr (SUM) {
         store_state(p.joint[REV], state0 - REV);
@@ -732,7 +763,7 @@ __device__ __forceinline__ void decay_walk(const DecayArgs& p, int64_t block,
             if (l == 0) lds.sum[0][wave] = e;
             __syncthreads();
             const int64_t len = sg.start - first + sg.n;
-            if (threadIdx.x == 0 && len > 0)
+            if (threadIdx.x % 256 == 0 && len > 0)
                 p.meet[((size_t)(first / kPiece + sg.seq + (len - 1) / kPiece) * p.Hv + hv) * parts + slice * ncb + cb] =
                     (lds.sum[0][0] + lds.sum[0][1]) + (lds.sum[0][2] + lds.sum[0][3]);
         }
@@ -742,7 +773,12 @@ __device__ __forceinline__ void decay_walk(const DecayArgs& p, int64_t block,
 template <typename T, int KIND, int DBP, int CT, bool DOTS>
 __global__ __launch_bounds__(256, kExact<T> == 1 ? 2 : 1) void k_decay_walk(DecayArgs p) {
     __shared__ alignas(16) DecayTiles<T, DBP, CT, kDecayPlanes<T, DOTS>> lds;
-    decay_walk<T, KIND, DBP, CT, DOTS>(p, blockIdx.x, lds);
+    decay_walk<T, KIND, DBP, CT, DOTS>(p, blockIdx.x, &lds);
+}
+template <int KIND, int DBP, int CT, bool DOTS>
+__global__ __launch_bounds__(512, 2) void k_decay_heads(DecayArgs p) {
+    __shared__ alignas(16) DecayTiles<uint16_t, DBP, CT, kDecayPlanes<uint16_t, DOTS>> lds[2];
+    decay_walk<uint16_t, KIND, DBP, CT, DOTS, 2>(p, blockIdx.x, lds);
 }
 // Two walks that do not wait for each other in one launch, the first in the
 // first `blocks` workgroups, where all of them have a CU of their own: small
@@ -755,8 +791,8 @@ __global__ __launch_bounds__(256, 1) void k_decay_pair(DecayArgs p, uint32_t blo
     using A = DecayTiles<T, DBP, CT, kDecayPlanes<T, DOTS>>;
     using B = DecayTiles<T, DBP2, CT2, kDecayPlanes<T, false>>;
     __shared__ alignas(16) char lds[sizeof(A) > sizeof(B) ? sizeof(A) : sizeof(B)];
-    if (blockIdx.x < blocks) decay_walk<T, KIND, DBP, CT, DOTS>(p, blockIdx.x, *reinterpret_cast<A*>(lds));
-    else decay_walk<T, KIND2, DBP2, CT2, false>(p, blockIdx.x - blocks, *reinterpret_cast<B*>(lds));
+    if (blockIdx.x < blocks) decay_walk<T, KIND, DBP, CT, DOTS>(p, blockIdx.x, reinterpret_cast<A*>(lds));
+    else decay_walk<T, KIND2, DBP2, CT2, false>(p, blockIdx.x - blocks, reinterpret_cast<B*>(lds));
 }
 
 // Along the segments of each sequence that has several, in place: what a
@@ -816,10 +852,10 @@ inline int decay_blocks_of(int32_t Db, int32_t Dc, int32_t dtype) {
 }
 // The walks' workgroups, by kind: those of heads that share a and b, or c, on
 // one XCD.
-inline int64_t decay_walk_blocks(const DecayArgs& a, int kind, int32_t dtype) {
+inline int64_t decay_walk_blocks(const DecayArgs& a, int kind, int32_t dtype, int heads = 1) {
     const bool keys = decay_by_key(kind);
     const int blocks = keys ? a.slices * decay_blocks_of(a.Dv, a.Dk, dtype) : decay_blocks_of(a.Dk, a.Dv, dtype);
-    return spread_blocks((a.T / a.seg + a.nseq) * a.Hk, a.Hv / a.Hk * blocks);
+    return spread_blocks((a.T / a.seg + a.nseq) * a.Hk, a.Hv / a.Hk / heads * blocks);
 }
 // f(fp32, Dk over 64, Dv over 64), as constants
 template <typename F>
@@ -842,6 +878,17 @@ template <bool FP32>
 using DecayType = typename std::conditional<FP32, float, uint16_t>::type;
 template <int KIND, bool DOTS>
 int launch_decay_walk(const DecayArgs& a, int32_t dtype, hipStream_t s) {
+    if constexpr (decay_by_key(KIND)) {
+        if (a.heads == 2) {
+            const unsigned n = (unsigned)decay_walk_blocks(a, KIND, dtype, 2);
+            decay_dispatch(a, SSMP_BF16, [&](auto, auto wk, auto wv) {
+                using F = DecayForm<KIND, decltype(wk)::value, decltype(wv)::value, uint16_t>;
+                k_decay_heads<KIND, F::DBP, F::CT, DOTS><<<n, 512, 0, s>>>(a);
+            });
+            SSMP_LAUNCH_CHECK();
+            return SSMP_OK;
+        }
+    }
     const unsigned n = (unsigned)decay_walk_blocks(a, KIND, dtype);
     decay_dispatch(a, dtype, [&](auto fp32, auto wk, auto wv) {
         using T = DecayType<decltype(fp32)::value>;
@@ -855,7 +902,7 @@ int launch_decay_walk(const DecayArgs& a, int32_t dtype, hipStream_t s) {
 template <int KIND, bool DOTS, int KIND2>
 int launch_decay_pair(const DecayArgs& a, int32_t dtype, hipStream_t s) {
     const unsigned n = (unsigned)decay_walk_blocks(a, KIND, dtype), m = n + (unsigned)decay_walk_blocks(a, KIND2, dtype);
-    if (m > kPairBlocks) {
+    if (m > kPairBlocks || (decay_by_key(KIND) && a.heads == 2)) {
         if (const int st = launch_decay_walk<KIND, DOTS>(a, dtype, s)) return st;
         return launch_decay_walk<KIND2, false>(a, dtype, s);
     }
@@ -880,6 +927,20 @@ inline int launch_decay_join(const DecayArgs& a, int ways, hipStream_t s) {
     k_decay_join<><<<(unsigned)((int64_t)a.nseq * a.Hv * blocks * ways), 256, 0, s>>>(a, (int)blocks, ways);
     SSMP_LAUNCH_CHECK();
     return SSMP_OK;
+}
+// Both value heads of a key head in a workgroup, where there are two, and more
+// workgroups than the card has at a time: no parts are written and added up,
+// while eight waves in step take about a fifth longer. Backward, in us, with
+// one head a workgroup and with two:
+//   tokens, sequences    2048, 8   4096, 8   8192, 8   32768, 35
+//   32 heads 128 x 128   189, 185  344, 320  537, 508  1505, 1365
+//   others: 16384, 1, 16 of 128 x 64: 397, 318; 8192, 8, 32 of 64 x 64: 250,
+//   257; 32768, 29, 32 of 64 x 64: 790, 778; 8192, 8, 8 of 128 x 128: 206, 215
+// (Two of 24 heads, which halves the parts: 16384, 8, of 128 x 64: 568, 551;
+// 4096: 191, 198; 32768: 995, 1013. fp32 walks have no room for it.)
+inline int decay_heads_of(const DecayArgs& a, int32_t dtype) {
+    if (dtype == SSMP_F32 || a.Hv != 2 * a.Hk || a.slices > 1) return 1;
+    return decay_walk_blocks(a, kDk, dtype) + decay_walk_blocks(a, kDv, dtype) > kPairBlocks ? 2 : 1;
 }
 // compiled in sources of their own
 int launch_decay_dq(const DecayArgs& a, int32_t dtype, hipStream_t s);

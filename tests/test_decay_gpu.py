@@ -99,6 +99,29 @@ def test_chunked_matches_definition(case, dtype, carry, per_token):
     compare(run(dev(d), dc.cu_of(lens).cuda(), carry), ref, d, lens, carry)
 
 
+# More workgroups than the card has at a time: then the value heads of a key
+# head that has two share one in dq's and dk's walks.
+SHORT = [1, 0, 5, 64, 3, 17, 2, 40]
+
+
+@pytest.mark.parametrize("dg", [True, False])
+@pytest.mark.parametrize("lens,Hk,Hv,Dk,Dv", [
+    (SHORT * 5 + [65, 300], 4, 8, 128, 128),
+    (SHORT * 5 + [257], 4, 8, 64, 64),
+    (SHORT * 5 + [64, 129], 6, 12, 128, 40),
+    (SHORT * 5 + [200], 4, 8, 40, 128),
+    (SHORT * 5, 6, 12, 8, 8),
+    (SHORT * 3 + [70, 1], 3, 6, 72, 136),      # wide value heads, in slices: each alone
+    (SHORT * 5 + [66], 2, 8, 72, 64),          # four
+])
+@pytest.mark.parametrize("carry,per_token", [(True, True), (False, False)])
+def test_heads_in_pairs(lens, Hk, Hv, Dk, Dv, carry, per_token, dg):
+    assert 2 * len(lens) * Hv * -(-Dv // 128) > 512
+    d = ck.inputs(9, lens, Hk, Hv, Dk, Dv, BF, carry, per_token)
+    ref = ck.reference(d, lens, 0.4)
+    compare(run(dev(d), dc.cu_of(lens).cuda(), carry, scale=0.4, dg=dg), ref, d, lens, carry, dg)
+
+
 @pytest.mark.parametrize("what", ["reset", "lowest", "fast", "slow", "none", "k0", "long_then_reset"])
 @pytest.mark.parametrize("dtype", [F32, BF])
 def test_limits_of_decays(what, dtype):

@@ -18,6 +18,7 @@ FORMS = [
     (131, 1, 1, 1, 8, 8),        # one, over a segment
     (700, 9, 2, 4, 128, 72),
     (1500, 70, 1, 2, 32, 136),   # more sequences than lanes; wide value heads
+    (600, 140, 1, 2, 128, 72),   # both value heads in a workgroup
 ]
 
 
