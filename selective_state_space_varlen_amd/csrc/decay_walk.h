@@ -157,7 +157,7 @@ __device__ __forceinline__ int64_t uniform(int64_t v) {
 
 // 64 rows in LDS as bf16 planes, for fp32 three: splitting at every read, in
 // every wave, took more time than the products (1237 tokens x 6 heads of 40 x
-// 72 in fp32: forward 39 us, now 27). The two readings are RowTile's.
+// 72 in fp32: the forward's walk 25.5 us, now 23.5). The two readings are RowTile's.
 template <typename T, int W>
 struct DecayTile {
     static constexpr int NX = kExact<T>;
@@ -289,6 +289,11 @@ struct DecayTiles {
 // The next chunk's rows are under way in registers meanwhile, those of a in
 // the first half of a chunk and those of b and c in the second, so that two
 // workgroups share a CU. DOTS: rows of out times rows of q or k, for dg.
+// What bounds it: 32768 tokens x 32 heads of 128 x 128 in bf16 take 290 us
+// forward, 220 at a copy's rate; copies of the walk that only load and store
+// take 253, that only compute 262, and eight waves a workgroup of 16 columns
+// each no less. dq 385 to 460, dk 430 to 505, dv 265 to 320 (what a launch takes
+// falls as the clock does under load).
 // HEADS = 2 (dq, dk): both value heads of a key head in a workgroup of eight
 // waves, which add up what they have formed, so that there are no parts: each
 // four waves hand those rows to the others that the others store.
@@ -917,7 +922,7 @@ int launch_decay_pair(const DecayArgs& a, int32_t dtype, hipStream_t s) {
 }
 // Up to so many states between segments are added up by the walks themselves,
 // each reading those on its way: a prompt of 513 tokens x 32 heads of 128 x 128
-// in 5 segments takes 33 us with a join between the walks and 29 without.
+// in 5 segments takes 36 us with a join between the walks and 30.5 without.
 constexpr int kFewStates = 5;
 inline int launch_decay_join(const DecayArgs& a, int ways, hipStream_t s) {
     if (a.few) return SSMP_OK;
