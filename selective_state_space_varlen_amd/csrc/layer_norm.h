@@ -136,18 +136,28 @@ __device__ __forceinline__ float ln_root(const LnArgs& a, float sum, float squar
 // How a row lies: pieces of 8 elements where every row starts at a multiple of
 // 16 bytes, single ones otherwise; up to 512 (256) components in one wave or a
 // part of it, longer rows across a workgroup of as many lanes as leave each one
-// piece: more of them in a lane leave the backward, which adds up the weights'
-// gradients too, too few waves a CU to hide the loads (32768 rows of 4096 in
+// piece, or two: more of them in a lane leave a backward that adds up the
+// weights' gradients too few waves a CU to hide the loads (32768 rows of 4096 in
 // bf16: 351 us with 512 lanes of one piece, 365 with 256 of two).
 struct LnForm {
     int vec, lanes, nv;
 };
-inline LnForm ln_form(int32_t D) {
+// The most lanes of a row in two pieces a lane, which waits at barriers with
+// half as many waves. bf16, in us, with one piece a lane and with two:
+//   rows x columns                32768 x 4096  32768 x 2560  16384 x 8192  4096 x 4096  1024 x 8192
+//   forward, residual, dropout    242, 227      175, 159      214, 204      35.2, 35.1   24.3, 24.5
+//   forward                       125, 115      110, 85       164, 115      26.2, 24.2   24.3, 20.6
+//   backward without dw, db       229, 207      200, 148      238, 281      32.5, 31.7   20.0, 20.2
+// With the weights' gradients it loses (above), and so do rows of fp32 (16384 x
+// 4096: forward 202 and 208, backward 196 and 212).
+constexpr int ln_two(bool bf16, bool backward, bool dw) { return !bf16 || dw ? 0 : backward ? 256 : 512; }
+inline LnForm ln_form(int32_t D, int two) {
     if (D % 8 == 0) {
         for (int lanes = 4; lanes <= 64; lanes *= 2)
             if (D <= lanes * 8) return {8, lanes, 1};
         for (int lanes = 256; lanes <= 1024; lanes *= 2)
-            if (D <= lanes * 8) return {8, lanes, 1};
+            for (int nv = 1; nv <= (lanes <= two ? 2 : 1); ++nv)
+                if (D <= lanes * 8 * nv) return {8, lanes, nv};
         return {8, 1024, 2};
     }
     if (D <= 64) return {1, 64, 1};
@@ -155,12 +165,13 @@ inline LnForm ln_form(int32_t D) {
     if (D <= 1024) return {1, 256, 4};
     return {1, 1024, D <= 4096 ? 4 : D <= 8192 ? 8 : 16};
 }
-inline int ln_groups(int32_t D) { return ln_threads(ln_form(D).lanes) / ln_form(D).lanes; }  // of a workgroup
+inline int ln_groups(int32_t D, int two) { return ln_threads(ln_form(D, two).lanes) / ln_form(D, two).lanes; }  // of a workgroup
 // Workgroups: as many as have room at a time (`most` of 256 threads), a
 // multiple of what gives each group one head; at least `least` rows a group
-inline int64_t ln_blocks(int64_t rows, int32_t H, int32_t D, int64_t most, int64_t least = 1) {
-    const int sg = ln_groups(D);
-    most = most * 256 / ln_threads(ln_form(D).lanes);
+inline int64_t ln_blocks(int64_t rows, int32_t H, int32_t D, int two, int64_t most, int64_t least = 1) {
+    const LnForm m = ln_form(D, two);
+    const int sg = ln_groups(D, two);
+    most = most * 256 / ln_threads(m.lanes);
     int64_t a = H, b = sg;
     while (b) {
         const int64_t t = a % b;
@@ -172,6 +183,8 @@ inline int64_t ln_blocks(int64_t rows, int32_t H, int32_t D, int64_t most, int64
     n = n < most ? n : most;
     return (n + unit - 1) / unit * unit;
 }
+// Forward half as many workgroups where a lane has two pieces, which are all that
+// a CU has room for: more of them start late (4096 x 4096: 35 us, 45 with as many).
 // Backward four rows a group at least, or the groups' sums take longer than the
 // rows (1237 tokens x 6 heads of 72: rows 10.2 and sums 7.2 us, 11.2 and 16.8
 // with a row a group).
@@ -182,9 +195,13 @@ template <int V, int L, int N>
 struct LnShape {
     static constexpr int vec = V, lanes = L, nv = N;
 };
-template <typename F>
+template <int TWO, typename F>
 void ln_dispatch(int32_t D, F f) {
-    const LnForm m = ln_form(D);
+    const LnForm m = ln_form(D, TWO);
+    if constexpr (TWO >= 256)
+        if (m.vec == 8 && m.lanes == 256 && m.nv == 2) return f(LnShape<8, 256, 2>{});
+    if constexpr (TWO >= 512)
+        if (m.vec == 8 && m.lanes == 512 && m.nv == 2) return f(LnShape<8, 512, 2>{});
     if (m.vec == 8) {
         switch (m.lanes) {
             case 4: return f(LnShape<8, 4, 1>{});

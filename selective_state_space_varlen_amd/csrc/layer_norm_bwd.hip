@@ -136,31 +136,25 @@ __global__ __launch_bounds__(kLnDwThreads) void k_layer_norm_dw(LnArgs a, int64_
     }
 }
 
-template <typename T>
-void launch_ln_bwd(const LnArgs& a, bool dw, int64_t blocks, hipStream_t s) {
-    ln_dispatch(a.D, [&](auto f) {
+template <typename T, bool DW>
+void launch_ln_bwd(const LnArgs& a, int64_t blocks, hipStream_t s) {
+    ln_dispatch<ln_two(sizeof(T) == 2, true, DW)>(a.D, [&](auto f) {
         constexpr int V = decltype(f)::vec, L = decltype(f)::lanes, N = decltype(f)::nv;
         const dim3 g((unsigned)blocks), b(ln_threads(L));
-        const bool drop = a.drop.cut > 0;
-        if (dw) {
-            if (drop) k_layer_norm_bwd<T, V, L, N, true, true><<<g, b, 0, s>>>(a);
-            else k_layer_norm_bwd<T, V, L, N, false, true><<<g, b, 0, s>>>(a);
-        } else {
-            if (drop) k_layer_norm_bwd<T, V, L, N, true, false><<<g, b, 0, s>>>(a);
-            else k_layer_norm_bwd<T, V, L, N, false, false><<<g, b, 0, s>>>(a);
-        }
+        if (a.drop.cut) k_layer_norm_bwd<T, V, L, N, true, DW><<<g, b, 0, s>>>(a);
+        else k_layer_norm_bwd<T, V, L, N, false, DW><<<g, b, 0, s>>>(a);
     });
 }
 
 // The backward's sums for any number of rows up to T H: a group adds at most
 // kLnFlush rows in 32 bits, and keeps doubles where it has more.
 inline bool ln_wide(int64_t rows, int64_t blocks, int32_t D) {
-    const int64_t groups = blocks * ln_groups(D);
+    const int64_t groups = blocks * ln_groups(D, 0);
     return (rows + groups - 1) / groups > kLnFlush;
 }
 inline size_t ln_part_bytes(int64_t rows, int32_t H, int32_t D) {
-    const int64_t blocks = ln_blocks(rows, H, D, kLnBwdBlocks, kLnBwdRows);
-    return (size_t)blocks * ln_groups(D) * 2 * D * (ln_wide(rows, blocks, D) ? 8 : 4);
+    const int64_t blocks = ln_blocks(rows, H, D, 0, kLnBwdBlocks, kLnBwdRows);
+    return (size_t)blocks * ln_groups(D, 0) * 2 * D * (ln_wide(rows, blocks, D) ? 8 : 4);
 }
 
 }  // namespace ssmp
@@ -204,14 +198,19 @@ extern "C" int layer_norm_pack_bwd(const void* dy, const void* h, const float* w
     a.H = H;
     a.D = D;
     a.eps = eps;
-    const int64_t blocks = ln_blocks(a.rows, H, D, kLnBwdBlocks, kLnBwdRows);
+    const int64_t blocks = ln_blocks(a.rows, H, D, ln_two(dtype == SSMP_BF16, true, sums), kLnBwdBlocks, kLnBwdRows);
     a.wide = ln_wide(a.rows, blocks, D);
-    if (dtype == SSMP_F32) launch_ln_bwd<float>(a, sums, blocks, s);
-    else launch_ln_bwd<uint16_t>(a, sums, blocks, s);
+    const auto launch = [&](auto dw) {
+        constexpr bool DW = decltype(dw)::value;
+        if (dtype == SSMP_F32) launch_ln_bwd<float, DW>(a, blocks, s);
+        else launch_ln_bwd<uint16_t, DW>(a, blocks, s);
+    };
+    if (sums) launch(std::true_type{});
+    else launch(std::false_type{});
     SSMP_LAUNCH_CHECK();
     if (sums) {
         const unsigned n = (unsigned)((int64_t)H * ((2 * D + 31) / 32));
-        const int64_t groups = blocks * ln_groups(D);
+        const int64_t groups = blocks * ln_groups(D, 0);
         if (a.wide) k_layer_norm_dw<double><<<n, kLnDwThreads, 0, s>>>(a, groups);
         else k_layer_norm_dw<float><<<n, kLnDwThreads, 0, s>>>(a, groups);
         SSMP_LAUNCH_CHECK();

@@ -68,7 +68,7 @@ __global__ __launch_bounds__(ln_threads(LANES)) void k_layer_norm_fwd(LnArgs a) 
 
 template <typename T>
 void launch_ln_fwd(const LnArgs& a, int64_t blocks, hipStream_t s) {
-    ln_dispatch(a.D, [&](auto f) {
+    ln_dispatch<ln_two(sizeof(T) == 2, false, false)>(a.D, [&](auto f) {
         constexpr int V = decltype(f)::vec, L = decltype(f)::lanes, N = decltype(f)::nv;
         const dim3 g((unsigned)blocks), b(ln_threads(L));
         if (a.drop.cut) k_layer_norm_fwd<T, V, L, N, true><<<g, b, 0, s>>>(a);
@@ -98,7 +98,9 @@ extern "C" int layer_norm_pack_fwd(const void* x, const void* residual, const fl
     a.H = H;
     a.D = D;
     a.eps = eps;
-    const int64_t blocks = ln_blocks(a.rows, H, D, kLnFwdBlocks);
+    const int two = ln_two(dtype == SSMP_BF16, false, false);
+    const LnForm m = ln_form(D, two);
+    const int64_t blocks = ln_blocks(a.rows, H, D, two, m.vec == 8 && m.lanes <= two ? kLnFwdBlocks / m.nv : kLnFwdBlocks);
     hipStream_t s = static_cast<hipStream_t>(stream);
     if (dtype == SSMP_F32) launch_ln_fwd<float>(a, blocks, s);
     else launch_ln_fwd<uint16_t>(a, blocks, s);
