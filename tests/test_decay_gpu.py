@@ -312,3 +312,39 @@ def test_step_on_a_pool_past_32_bits():
     a = m.decay_attn_pack_step(d["q"], d["k"], d["v"], d["g"], state, at)
     b = m.decay_attn_pack_step(d["q"], d["k"], d["v"], d["g"], small)
     assert torch.equal(a, b) and torch.equal(state[at.long()], small)
+
+
+def test_many_sequences_without_tokens():
+    """Nothing to walk, in more workgroups than the card has at a time: states and gradients go through."""
+    m, n, Hk, Hv, D = ssp(), 300, 2, 4, 64
+    q, v = (torch.empty(0, h, D, dtype=BF, device="cuda") for h in (Hk, Hv))
+    g, cu = torch.empty(0, Hv, device="cuda"), torch.zeros(n + 1, dtype=torch.int32, device="cuda")
+    h = torch.randn(n, Hv, D, D, device="cuda", generator=torch.Generator("cuda").manual_seed(3))
+    _, hT = m.decay_attn_pack_fwd(q, q, v, g, cu, initial_state=h, final_state=True)
+    G = m.decay_attn_pack_bwd(q, q, v, g, cu, v, initial_state=h, dfinal_state=h, dinitial_state=True)
+    assert torch.equal(hT, h) and torch.equal(G["dinitial_state"], h)
+
+
+def test_heads_in_pairs_captured_and_replayed():
+    m, n, Hk, Hv, D = ssp(), 80, 2, 4, 64
+    lens = [1 + 7 * i % 90 for i in range(n)]
+    assert 2 * n * Hv > 512
+    d = dev(ck.inputs(12, lens, Hk, Hv, D, D, BF, False, True))
+    cu = dc.cu_of(lens).cuda()
+    args = (d["q"], d["k"], d["v"], d["g"], cu, d["dout"])
+    want = m.decay_attn_pack_bwd(*args)
+    ws = poison(m.decay_attn_pack_bwd_scratch_bytes(sum(lens), n, Hk, Hv, D, D))
+    out = {k: nan_like(want[k]) for k in ("dq", "dk", "dv", "dg")}
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        m.decay_attn_pack_bwd(*args, scratch=ws, out=out)
+    for _ in range(3):
+        ws.fill_(255)
+        for t in out.values():
+            t.fill_(float("nan"))
+        graph.replay()
+        eager = m.decay_attn_pack_bwd(*args)
+        torch.cuda.synchronize()
+        for k, t in out.items():
+            assert torch.equal(t, want[k]) and torch.equal(eager[k], want[k]), k
