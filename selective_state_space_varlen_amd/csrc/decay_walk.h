@@ -265,16 +265,15 @@ struct DecayRows {
     float into[kC], onto[kC];     // decay from the state to a row, and from a row to the state
     float whole;                  // of the chunk
 };
-// Planes of P and of the state where out is formed: two hold 16 bits, of
-// which a bf16 result keeps 8; dg and fp32 results see all three. What is
-// added to the state has three always.
-template <typename T, bool DOTS>
-constexpr int kDecayPlanes = kExact<T> == 3 || DOTS ? 3 : 2;
-template <typename T, int DBP, int CT, int NP>
+// Planes of P, of the state and of what is added to it: all 24 bits. (With two,
+// cut off, 5 bf16 results in 1000 are not the nearest to the exact value, 2.1e-4
+// of a tensor's norm; with three 0.12, 2.3e-5, as of any sums in 32 bits.)
+constexpr int kPlanes = 3;
+template <typename T, int DBP, int CT>
 struct DecayTiles {
     DecayTile<T, DBP> a, b;
     DecayTile<T, 64 * CT> c;
-    u32x4 P[8 * NP][64];          // [row tile][block of 32 columns][plane]: as one lane reads them
+    u32x4 P[8 * kPlanes][64];     // [row tile][block of 32 columns][plane]: as one lane reads them
     DecayRows rows[2];            // this chunk's and the next one's
     float dot[4][kC], sum[2][4];  // by wave: dg's row sums; the anchor and the chunk's sum
 };
@@ -299,19 +298,20 @@ struct DecayTiles {
 // four waves hand those rows to the others that the others store.
 template <typename T, int KIND, int DBP, int CT, bool DOTS, int HEADS = 1>
 __device__ __forceinline__ void decay_walk(const DecayArgs& p, int64_t block,
-                                           DecayTiles<T, DBP, CT, kDecayPlanes<T, DOTS>>* tiles) {
-    constexpr int NX = kExact<T>, NP = kDecayPlanes<T, DOTS>;
+                                           DecayTiles<T, DBP, CT>* tiles) {
+    constexpr int NX = kExact<T>, NP = kPlanes;
     constexpr bool REV = decay_reverse(KIND), SUM = KIND == kSumS || KIND == kSumD, KEYS = decay_by_key(KIND);
     constexpr int MT = DBP / 16, KS = DBP / 32, COLS = 64 * CT;
     // Vector operations of the next product in the shadow of one's matrix
-    // instructions; three planes leave no registers for it.
-    constexpr bool kAhead = NP == 2;
+    // instructions; dg's rows, or three planes of an input, leave no registers
+    // for it.
+    constexpr bool kAhead = !DOTS && NX == 1;
     constexpr int kFew = REV ? 3 : 0;  // the wave with the fewest tiles of P has G to do
     const int Dc = KEYS ? p.Dk : p.Dv, Db = KEYS ? p.Dv : p.Dk;
     const int ncb = (Dc + COLS - 1) / COLS, slices = KEYS ? p.slices : 1, group = p.Hv / p.Hk;
     const Spread sp = spread(block, group / HEADS * slices * ncb);  // (HEADS = 2: one group, one slice)
     const int mine = HEADS == 2 ? wave_id() >> 2 : 0;  // of the workgroup's heads
-    DecayTiles<T, DBP, CT, kDecayPlanes<T, DOTS>>& lds = tiles[mine];
+    DecayTiles<T, DBP, CT>& lds = tiles[mine];
     if (sp.group >= (p.T / p.seg + p.nseq) * (int64_t)p.Hk) return;
     Chunk sg;
     if (SUM ? !chunk_at(p.cu, p.nseq, p.T, sp.group / p.Hk, sg, p.seg) : !segment_at(p, sp.group / p.Hk, sg)) return;
@@ -777,12 +777,12 @@ __device__ __forceinline__ void decay_walk(const DecayArgs& p, int64_t block,
 
 template <typename T, int KIND, int DBP, int CT, bool DOTS>
 __global__ __launch_bounds__(256, kExact<T> == 1 ? 2 : 1) void k_decay_walk(DecayArgs p) {
-    __shared__ alignas(16) DecayTiles<T, DBP, CT, kDecayPlanes<T, DOTS>> lds;
+    __shared__ alignas(16) DecayTiles<T, DBP, CT> lds;
     decay_walk<T, KIND, DBP, CT, DOTS>(p, blockIdx.x, &lds);
 }
 template <int KIND, int DBP, int CT, bool DOTS>
 __global__ __launch_bounds__(512, 2) void k_decay_heads(DecayArgs p) {
-    __shared__ alignas(16) DecayTiles<uint16_t, DBP, CT, kDecayPlanes<uint16_t, DOTS>> lds[2];
+    __shared__ alignas(16) DecayTiles<uint16_t, DBP, CT> lds[2];
     decay_walk<uint16_t, KIND, DBP, CT, DOTS, 2>(p, blockIdx.x, lds);
 }
 // Two walks that do not wait for each other in one launch, the first in the
@@ -793,8 +793,8 @@ __global__ __launch_bounds__(512, 2) void k_decay_heads(DecayArgs p) {
 constexpr int kPairBlocks = 512;  // half of them, or more, without a segment
 template <typename T, int KIND, int DBP, int CT, bool DOTS, int KIND2, int DBP2, int CT2>
 __global__ __launch_bounds__(256, 1) void k_decay_pair(DecayArgs p, uint32_t blocks) {
-    using A = DecayTiles<T, DBP, CT, kDecayPlanes<T, DOTS>>;
-    using B = DecayTiles<T, DBP2, CT2, kDecayPlanes<T, false>>;
+    using A = DecayTiles<T, DBP, CT>;
+    using B = DecayTiles<T, DBP2, CT2>;
     __shared__ alignas(16) char lds[sizeof(A) > sizeof(B) ? sizeof(A) : sizeof(B)];
     if (blockIdx.x < blocks) decay_walk<T, KIND, DBP, CT, DOTS>(p, blockIdx.x, reinterpret_cast<A*>(lds));
     else decay_walk<T, KIND2, DBP2, CT2, false>(p, blockIdx.x - blocks, reinterpret_cast<B*>(lds));
