@@ -553,8 +553,8 @@ int decay_attn_pack_fwd(const void *q, const void *k, const void *v, const float
  *   dq, dk (T, Hk, Dk) dtype out, summed over the value heads of a key head;
  *   dv (T, Hv, Dv) dtype out; dg fp32 out, nullable, of g's shape (with one
  *   decay for a head, summed over the tokens). dg is the difference of what
- *   reads and what writes a state (q.dq and k.dk), added up over up to 256
- *   tokens, and errs by 32-bit roundings of those.
+ *   reads and what writes a state (q.dq and k.dk), added up in 64 bits over up
+ *   to 256 tokens, and errs by 32-bit roundings of those.
  *   scratch  decay_attn_pack_bwd_scratch_bytes(T, nseq, Hk, Hv, Dk, Dv)
  * Within a sequence, a NaN or an infinity of a token may reach gradients of up
  * to 63 tokens on its other side (they share a chunk), and those of g up to 255

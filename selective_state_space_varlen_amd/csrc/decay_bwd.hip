@@ -24,11 +24,11 @@ __global__ __launch_bounds__(64) void k_decay_dg(DecayArgs p, int parts) {
     double acc = 0.0, sum = 0.0, cross = 0.0;  // cross: what goes through the chunk's states
     if (n > 0) {
         if (!c.last || p.dhT)
-            for (int i = 0; i < parts; ++i) acc += (double)p.meet[((size_t)slot * p.Hv + hv) * parts + i];
+            for (int i = 0; i < parts; ++i) acc += p.meet[((size_t)slot * p.Hv + hv) * parts + i];
         const int64_t first = c.start - c.index * kPiece, chunk = first / kC + c.seq + c.index * kDgChunks + ch;
         for (int i = 0; i < parts; ++i) {
             const size_t at = ((size_t)chunk * p.Hv + hv) * parts + i;
-            cross += (double)p.chunk[0][at] - (double)p.chunk[1][at];
+            cross += p.chunk[0][at] - p.chunk[1][at];
         }
     }
     // the anchor at this chunk's end: that of the piece's, and what crosses the chunks between
@@ -41,12 +41,13 @@ __global__ __launch_bounds__(64) void k_decay_dg(DecayArgs p, int parts) {
     acc += behind - cross;
     constexpr int kBatch = 32;  // tokens' loads under way
     for (int t1 = n; t1 > 0; t1 -= kBatch) {
-        float r[kBatch], g[kBatch];
+        double r[kBatch];
+        float g[kBatch];
 #pragma unroll
         for (int x = 0; x < kBatch; ++x) {
             const int t = t1 - 1 - x;
             const size_t at = (size_t)(t0 + (t < 0 ? 0 : t)) * p.Hv + hv;
-            r[x] = p.rows[0][at] - p.rows[1][at];
+            r[x] = (double)p.rows[0][at] - (double)p.rows[1][at];
             g[x] = p.g[p.gstride ? at : hv];
         }
         for (int i = 1; i < parts; ++i)
@@ -54,13 +55,13 @@ __global__ __launch_bounds__(64) void k_decay_dg(DecayArgs p, int parts) {
             for (int x = 0; x < kBatch; ++x) {
                 const int t = t1 - 1 - x;
                 const size_t at = ((size_t)i * p.T + t0 + (t < 0 ? 0 : t)) * p.Hv + hv;
-                r[x] += p.rows[0][at] - p.rows[1][at];
+                r[x] += (double)p.rows[0][at] - (double)p.rows[1][at];
             }
 #pragma unroll
         for (int x = 0; x < kBatch; ++x) {
             const int t = t1 - 1 - x;
             if (t < 0) continue;
-            acc += (double)r[x];
+            acc += r[x];
             if (decay_is_zero(g[x])) acc = 0.0;
             if (p.gstride) p.dg[(size_t)(t0 + t) * p.Hv + hv] = (float)acc;
             sum += acc;
@@ -120,10 +121,10 @@ inline DecayBwdLayout decay_bwd_layout(int64_t T, int32_t nseq, int32_t Hk, int3
     const bool partial = (size_t)(Hv / Hk) * slices > 1;
     for (int i = 0; i < 2; ++i) L.part[i] = take(partial ? (size_t)T * Hv * slices * Dk * sizeof(float) : 0);
     for (int i = 0; i < 2; ++i) L.rows[i] = take(parts * T * Hv * sizeof(float));
-    for (int i = 0; i < 2; ++i) L.chunk[i] = take((size_t)delta_slots(T, nseq) * Hv * parts * sizeof(float));
+    for (int i = 0; i < 2; ++i) L.chunk[i] = take((size_t)delta_slots(T, nseq) * Hv * parts * sizeof(double));
     const size_t db = Dv > 64 ? 128 : 64, dc = Dk > 64 ? 128 : 64;
     L.snap = take((size_t)(T / kPiece) * Hv * slices * db * dc * sizeof(float));
-    L.meet = take((size_t)(T / kPiece + nseq) * Hv * parts * sizeof(float));
+    L.meet = take((size_t)(T / kPiece + nseq) * Hv * parts * sizeof(double));
     L.dgsum = take((size_t)(T / kPiece + nseq) * Hv * sizeof(double));
     L.total = at;
     return L;
@@ -193,10 +194,10 @@ extern "C" int decay_attn_pack_bwd(const void* q, const void* k, const void* v, 
         a.seg_decay[i] = reinterpret_cast<float*>(ws + L.decay[i]);
         a.part[i] = reinterpret_cast<float*>(ws + L.part[i]);
         a.rows[i] = reinterpret_cast<float*>(ws + L.rows[i]);
-        a.chunk[i] = reinterpret_cast<float*>(ws + L.chunk[i]);
+        a.chunk[i] = reinterpret_cast<double*>(ws + L.chunk[i]);
     }
     a.snap = reinterpret_cast<float*>(ws + L.snap);
-    a.meet = reinterpret_cast<float*>(ws + L.meet);
+    a.meet = reinterpret_cast<double*>(ws + L.meet);
     a.dgsum = reinterpret_cast<double*>(ws + L.dgsum);
     if (T > a.seg) {
         if (const int st = launch_decay_pair<kSumS, false, kSumD>(a, dtype, s)) return st;

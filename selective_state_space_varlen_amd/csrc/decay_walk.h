@@ -16,7 +16,10 @@
 // anew after every kPiece tokens, where dq's walk leaves S for dk's, and goes
 // from chunk to chunk by what crosses between chunks alone: (dS . S) before a
 // chunk is that behind it + sum q.dq' - sum k.dk', dq' and dk' being the parts
-// that come through the states.
+// that come through the states. Both are the start of many tokens' dg, so they
+// are summed in 64 bits (in 32: dg of 16384 tokens in long sequences errs by
+// 3.7e-7 of its norm, now by 3.0e-7, the sum over the tokens of short ones by
+// up to 8.3e-7, now 6.4e-7; the backward takes as long).
 #pragma once
 
 #include "delta_common.h"
@@ -78,9 +81,9 @@ struct DecayArgs {
     int32_t heads;        // of a key head that a workgroup of dq's and dk's walks has
     float* part[2];       // dq, dk by value head and slice: [T][Hk][members][Dk]; null where there is one
     float* rows[2];       // q.dq and k.dk: [parts][T][Hv]
-    float* chunk[2];      // what a chunk's rows of them get from and give to other chunks: [T / 64 + nseq][Hv][parts]
+    double* chunk[2];     // what a chunk's rows of them get from and give to other chunks: [T / 64 + nseq][Hv][parts]
     float* snap;          // S^T after every kPiece-th token, in the walk's layout
-    float* meet;          // (dS . S) at the ends of the pieces: [T / kPiece + nseq][Hv][parts]
+    double* meet;         // (dS . S) at the ends of the pieces: [T / kPiece + nseq][Hv][parts]
     double* dgsum;        // one decay for a head: dg by piece, [T / kPiece + nseq][Hv]
 };
 
@@ -253,8 +256,11 @@ __device__ __forceinline__ void decay_mma(f32x4 (&d)[CT][4], const Frag<NA> (&x)
                         d[ct][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[ct].p[i], a[t].p[s - i], d[ct][t], 0, 0, 0);
 }
 
-__device__ __forceinline__ float wave_sum(float v) {
-    v = sum16(v);
+__device__ __forceinline__ double wave_sum(double v) {
+    v = dpp_add_f64<0xB1>(v);
+    v = dpp_add_f64<0x4E>(v);
+    v = dpp_add_f64<0x141>(v);
+    v = dpp_add_f64<0x140>(v);
     v += __shfl_xor(v, 16);
     return v + __shfl_xor(v, 32);
 }
@@ -275,7 +281,8 @@ struct DecayTiles {
     DecayTile<T, 64 * CT> c;
     u32x4 P[8 * kPlanes][64];     // [row tile][block of 32 columns][plane]: as one lane reads them
     DecayRows rows[2];            // this chunk's and the next one's
-    float dot[4][kC], sum[2][4];  // by wave: dg's row sums; the anchor and the chunk's sum
+    float dot[4][kC];             // by wave: dg's row sums
+    double sum[2][4];             // the anchor and the chunk's sum
 };
 
 // One workgroup of four waves per (segment, value head, slice of the state's
@@ -451,7 +458,7 @@ __device__ __forceinline__ void decay_walk(const DecayArgs& p, int64_t block,
         load_a(i + 1);
         if constexpr (DOTS && KIND == kDk) {
             if (piece_end) {
-                float e = 0.0f;
+                double e = 0.0;
                 const auto sr = snap();
 #pragma unroll
                 for (int m = 0; m < MT; ++m)
@@ -460,7 +467,7 @@ __device__ __forceinline__ void decay_walk(const DecayArgs& p, int64_t block,
                         const f32x4 w = __builtin_bit_cast(
                             f32x4, __builtin_amdgcn_raw_buffer_load_b128(sr, l * 16, (m * CT + ct) * 1024, 0));
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) e = fmaf(S[m][ct][r], w[r], e);
+                        for (int r = 0; r < 4; ++r) e = fma((double)S[m][ct][r], (double)w[r], e);
                     }
                 e = wave_sum(e);
                 if ((tid & 63) == 0) lds.sum[0][wv] = e;
@@ -554,16 +561,16 @@ __device__ __forceinline__ void decay_walk(const DecayArgs& p, int64_t block,
                 for (int ct = 0; ct < CT; ++ct) o[ct][t] *= d;
             }
             if constexpr (DOTS) {
-                float e = 0.0f;
+                double e = 0.0;
 #pragma unroll
-                for (int t = 0; t < 4; ++t) e += dot_of(t);
+                for (int t = 0; t < 4; ++t) e += (double)dot_of(t);
                 e = wave_sum(e);
                 if ((tid & 63) == 0) lds.sum[1][wv] = e;
             }
             __syncthreads();
             if constexpr (DOTS) {
-                const float* const w = lds.sum[tid & 1];
-                const float e = (w[0] + w[1]) + (w[2] + w[3]);
+                const double* const w = lds.sum[tid & 1];
+                const double e = (w[0] + w[1]) + (w[2] + w[3]);
                 if (tid == 1)
                     p.chunk[REV][((size_t)(first / kC + sg.seq + from_seq / kC) * p.Hv + hv) * parts + slice * ncb + cb] = e;
                 if (KIND == kDk && tid == 0 && piece_end)
@@ -755,14 +762,14 @@ __device__ __forceinline__ void decay_walk(const DecayArgs& p, int64_t block,
     } else if constexpr (DOTS && KIND == kDq) {
         if (p.dhT && sg.last) {  // the last piece's anchor
             const auto r = state_rsrc(p.dhT, sg.seq);
-            float e = 0.0f;
+            double e = 0.0;
 #pragma unroll
             for (int m = 0; m < MT; ++m)
 #pragma unroll
                 for (int ct = 0; ct < CT; ++ct) {
                     const f32x4 w = state_at(r, m, ct);
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) e = fmaf(S[m][ct][x], w[x], e);
+                    for (int x = 0; x < 4; ++x) e = fma((double)S[m][ct][x], (double)w[x], e);
                 }
             e = wave_sum(e);
             if (l == 0) lds.sum[0][wave] = e;

@@ -77,3 +77,29 @@ def test_gradients_do_not_depend_on_whether_dg_is_asked_for(lens, Hk, Hv, Dk, Dv
     a, b = (run(d, dc.cu_of(lens).cuda(), True, dg=dg) for dg in (True, False))
     for n in ("dq", "dk", "dv", "dh0"):
         assert torch.equal(a[n], b[n]), n
+
+
+@pytest.mark.parametrize("dtype", [BF, torch.float32])
+@pytest.mark.parametrize("lens,Hk,Hv,Dk,Dv", [
+    ([1, 64, 600], 1, 2, 128, 128),
+    ([257, 0, 300], 2, 2, 40, 72),
+    ([520], 1, 1, 64, 264),
+    ([300, 7] * 25, 4, 8, 128, 64),           # both value heads of a key head in a workgroup
+])
+def test_what_dg_starts_from(lens, Hk, Hv, Dk, Dv, dtype):
+    """Queries and keys of zero and no decay: every token's dg is (dfinal_state . initial_state), a sum of
+    Dk Dv products that nearly cancel. It is formed in 64 bits and rounded once, whatever it starts from in the sequence."""
+    d = ck.inputs(50, lens, Hk, Hv, Dk, Dv, dtype, True)
+    d["q"].zero_(), d["k"].zero_(), d["g"].zero_()
+    want = (d["h0"].double() * d["dhT"].double()).sum((-1, -2))
+    size = (d["h0"].double() * d["dhT"].double()).abs().sum((-1, -2))
+    got = run(dev(d), dc.cu_of(lens).cuda(), True)["dg"].cpu().double()
+    one = run(dev(dict(d, g=torch.zeros(Hv))), dc.cu_of(lens).cuda(), True)["dg"].cpu().double()
+    t = 0
+    for s, n in enumerate(lens):
+        off_by = (got[t:t + n] - want[s]).abs()
+        assert bool((off_by <= 2.0 ** -24 * want[s].abs() + 2.0 ** -45 * size[s]).all()), (s, float(off_by.max()), want[s])
+        t += n
+    n = torch.tensor(lens, dtype=torch.float64)[:, None]
+    room = 2.0 ** -24 * (n * want).sum(0).abs() + 2.0 ** -40 * (n * size).sum(0)
+    assert bool(((one - (n * want).sum(0)).abs() <= room).all())
