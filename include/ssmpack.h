@@ -532,10 +532,10 @@ int gated_delta_pack_step(const void *q, const void *k, const void *v, const flo
  * SSMP_ERR_UNSUPPORTED, as is one that holds dinitial_state and either of the
  * states that go into the backward). The sizes do not fall as T or nseq grow: memory
  * made for the most tokens and sequences serves all smaller packs.
- * Errors: SSMP_ERR_SHAPE (also Hv > 65535, Hk * Dk, Hv * Dv or Hv * Dk *
- * ceil(Dv / 128) > 2^20, nseq > 2^24, T * Hv * max(Dk, Dv) >= 2^40, or more
- * than 2^23 pairs of a chunk of 64 tokens, or of a sequence and 128 columns,
- * with a value head), SSMP_ERR_UNSUPPORTED, SSMP_ERR_NULL, SSMP_ERR_ALIGN,
+ * Errors: SSMP_ERR_SHAPE (also T >= 2^31, Hv > 65535, Hk * Dk, Hv * Dv or Hv *
+ * Dk * ceil(Dv / 128) > 2^20, nseq > 2^24, T * Hv * max(Dk, Dv) >= 2^40,
+ * (T / 64 + nseq + 7) * Hv >= 2^23, or (T / 128 + nseq + 7) * Hv *
+ * ceil(Dv / 128) >= 2^23), SSMP_ERR_UNSUPPORTED, SSMP_ERR_NULL, SSMP_ERR_ALIGN,
  * SSMP_ERR_WORKSPACE. The size queries return 0 for arguments out of range.
  */
 size_t decay_attn_pack_fwd_scratch_bytes(int64_t T, int32_t nseq, int32_t Hk, int32_t Hv, int32_t Dk, int32_t Dv);

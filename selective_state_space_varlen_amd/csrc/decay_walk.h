@@ -962,7 +962,7 @@ inline int decay_check(int64_t T, int32_t nseq, int32_t Hk, int32_t Hv, int32_t 
     if (const int st = delta_check(T, nseq, Hk, Hv, Dk, Dv, dtype)) return st;
     const int64_t slices = (Dv + kDecayMaxDb - 1) / kDecayMaxDb;
     if (Hv * slices * Dk > kMaxRow) return SSMP_ERR_SHAPE;  // a row of dq's parts
-    // two walks in a launch, over segments of kSegMin at least; 128 columns of each
+    // a walk's workgroups: segments of kSegMin at least, blocks of 64 columns or more
     if ((T / kSegMin + nseq + 7) * (int64_t)Hv * slices * 2 >= kMaxBlocks) return SSMP_ERR_SHAPE;
     return SSMP_OK;
 }
