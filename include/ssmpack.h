@@ -617,7 +617,8 @@ int decay_attn_pack_step(const void *q, const void *k, const void *v, const floa
  * eps = 0 gives NaN, as the formula does. Sums are formed in 32 bits: a row
  * whose squares pass their range (components near 1e19) gives zeros.
  * Errors: SSMP_ERR_SHAPE (also H > 65536, T >= 2^31, 2^40 elements or more, p
- * as dropout_pack_fwd), SSMP_ERR_UNSUPPORTED, SSMP_ERR_NULL, SSMP_ERR_ALIGN,
+ * as dropout_pack_fwd; with dw or db H * ceil(D / 16) >= 2^22, for which the
+ * size query returns 0), SSMP_ERR_UNSUPPORTED, SSMP_ERR_NULL, SSMP_ERR_ALIGN,
  * SSMP_ERR_WORKSPACE.
  */
 int layer_norm_pack_fwd(const void *x, const void *residual, const float *w, const float *b,

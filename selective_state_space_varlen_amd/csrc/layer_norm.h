@@ -221,11 +221,9 @@ void ln_dispatch(int32_t D, F f) {
 }
 
 inline int ln_check(int64_t T, int32_t H, int32_t D, int32_t dtype) {
-    if (T < 0 || H < 1 || D < 1 || H > 65536 || T >= (int64_t(1) << 31) || T * H >= (int64_t(1) << 40) ||
-        T * H * D >= (int64_t(1) << 40))
-        return SSMP_ERR_SHAPE;
+    constexpr int64_t most = int64_t(1) << 40;
+    if (T < 0 || H < 1 || D < 1 || H > 65536 || T >= (int64_t(1) << 31) || T * H > (most - 1) / D) return SSMP_ERR_SHAPE;
     if (D > kLnMaxD) return SSMP_ERR_UNSUPPORTED;
-    if ((int64_t)H * ((2 * D + 31) / 32) >= kMaxBlocks / 4) return SSMP_ERR_SHAPE;  // k_layer_norm_dw's workgroups of 1024
     if (dtype != SSMP_F32 && dtype != SSMP_BF16) return SSMP_ERR_UNSUPPORTED;
     return SSMP_OK;
 }

@@ -152,6 +152,8 @@ inline bool ln_wide(int64_t rows, int64_t blocks, int32_t D) {
     const int64_t groups = blocks * ln_groups(D, 0);
     return (rows + groups - 1) / groups > kLnFlush;
 }
+// k_layer_norm_dw's workgroups are more than a launch takes
+inline bool ln_dw_over(int32_t H, int32_t D) { return (int64_t)H * ((2 * D + 31) / 32) >= kMaxBlocks * 256 / kLnDwThreads; }
 inline size_t ln_part_bytes(int64_t rows, int32_t H, int32_t D) {
     const int64_t blocks = ln_blocks(rows, H, D, 0, kLnBwdBlocks, kLnBwdRows);
     return (size_t)blocks * ln_groups(D, 0) * 2 * D * (ln_wide(rows, blocks, D) ? 8 : 4);
@@ -161,7 +163,7 @@ inline size_t ln_part_bytes(int64_t rows, int32_t H, int32_t D) {
 
 extern "C" size_t layer_norm_pack_bwd_workspace_bytes(int64_t T, int32_t H, int32_t D) {
     using namespace ssmp;
-    if (ln_check(T, H, D, SSMP_F32) || T == 0) return 0;
+    if (ln_check(T, H, D, SSMP_F32) || ln_dw_over(H, D) || T == 0) return 0;
     return ln_part_bytes(T * H, H, D);
 }
 
@@ -171,6 +173,7 @@ extern "C" int layer_norm_pack_bwd(const void* dy, const void* h, const float* w
                                    float eps, void* stream) {
     using namespace ssmp;
     if (const int st = ln_check(T, H, D, dtype)) return st;
+    if ((dw || db) && ln_dw_over(H, D)) return SSMP_ERR_SHAPE;
     LnArgs a = {};
     if (!make_drop(p, rng, a.drop)) return SSMP_ERR_SHAPE;
     if (dw && !w) return SSMP_ERR_NULL;
