@@ -9,6 +9,16 @@
 // between (32768 rows of 4096 in bf16 with residual and dropout: forward 205 us
 // or 5.2 TB/s, backward with the weights' gradients 341 and 9, 3.9 TB/s, which
 // is short of memory's by what two barriers and the generator take in a row).
+// That holds for pieces of 8 elements up to 8192 components, and a few registers
+// over for fp32 from 4096 on with the weights' gradients. Backward, rows of over
+// 8192 do not fit the 128 registers a lane of 1024 has, but for bf16 without the
+// weights' gradients, and pass through scratch memory: 4096 rows of 16384 take,
+// forward, backward, and backward with dw and db, 79, 96 and 396 us in bf16 (at
+// a copy's rate 55, 82, 82), 120, 273 and 478 in fp32 (110, 164, 164). Rows that
+// pieces of 8 do not divide are read by the element, of which each has ten rounds
+// of the generator to itself: 32768 x 4097 in bf16 takes 304, 451 and 467 us
+// (110, 164, 164), with residual and dropout 801 forward and 1130 backward (219,
+// 274); over 4096 they spill as well (4096 x 16383 with both: 483 and 1140).
 // The variance is formed from the differences from the mean, so that
 // no difference of large sums loses it.
 #pragma once
@@ -145,11 +155,17 @@ struct LnForm {
 // The most lanes of a row in two pieces a lane, which waits at barriers with
 // half as many waves. bf16, in us, with one piece a lane and with two:
 //   rows x columns                32768 x 4096  32768 x 2560  16384 x 8192  4096 x 4096  1024 x 8192
-//   forward, residual, dropout    242, 227      175, 159      214, 204      35.2, 35.1   24.3, 24.5
-//   forward                       125, 115      110, 85       164, 115      26.2, 24.2   24.3, 20.6
-//   backward without dw, db       229, 207      200, 148      238, 281      32.5, 31.7   20.0, 20.2
-// With the weights' gradients it loses (above), and so do rows of fp32 (16384 x
-// 4096: forward 202 and 208, backward 196 and 212).
+//   forward, residual, dropout    242, 227      175, 159      214, 204      32.4, 33.2   24.3, 24.5
+//   forward                       125, 115      110, 85       164, 115      26.5, 24.8   24.3, 20.6
+//   backward without dw, db       229, 207      200, 148      238, 281      29.2, 25.0   20.0, 20.2
+//   rows x columns                2048 x 4096   1024 x 4096   512 x 4096    256 x 4096   512 x 2560
+//   forward, residual, dropout    23.9, 25.1    20.0, 20.3    12.5, 12.7    9.7, 9.7     9.8, 9.9
+//   forward                       20.7, 20.5    18.8, 18.7    11.1, 11.0    8.5, 8.6     8.4, 8.4
+//   backward without dw, db       18.4, 17.0    11.9, 12.1    11.3, 11.4    11.2, 11.1   10.3, 10.2
+//   the same, residual, dropout   23.1, 23.4    15.5, 16.4    14.3, 15.2    13.8, 14.7   12.9, 13.5
+// So a few rows lose up to 7 % by it, 1 us, where the call waits for latency; the
+// rule looks at columns alone. With the weights' gradients it loses (above), and
+// so do rows of fp32 (16384 x 4096: forward 202 and 208, backward 196 and 212).
 constexpr int ln_two(bool bf16, bool backward, bool dw) { return !bf16 || dw ? 0 : backward ? 256 : 512; }
 inline LnForm ln_form(int32_t D, int two) {
     if (D % 8 == 0) {

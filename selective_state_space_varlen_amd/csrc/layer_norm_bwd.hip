@@ -11,14 +11,13 @@ constexpr int kLnFlush = 64;
 template <typename T, int V, int LANES, int NV, bool DROP, bool DW>
 __global__ __launch_bounds__(ln_threads(LANES)) void k_layer_norm_bwd(LnArgs a) {
     constexpr int SG = ln_threads(LANES) / LANES;
-    constexpr bool KEEP = NV * V <= 16;
     __shared__ float lds[2][5][kLnWaves];
     const int lane = threadIdx.x % LANES;
     const int64_t group = (int64_t)blockIdx.x * SG + threadIdx.x / LANES, groups = (int64_t)gridDim.x * SG;
     const int head = (int)(group % a.H);
     const float* const w = a.w ? a.w + (size_t)head * a.D : nullptr;
     float wv[NV][V], dw[NV][V] = {}, db[NV][V] = {};
-    if constexpr (KEEP) ln_weights<V, LANES, NV>(w, a.D, lane, 1.0f, wv);
+    ln_weights<V, LANES, NV>(w, a.D, lane, 1.0f, wv);
     LnRow<T, V, LANES, NV> x, dy, dh;
     int turn = 0, added = 0;
     bool again = false;
@@ -60,7 +59,6 @@ __global__ __launch_bounds__(ln_threads(LANES)) void k_layer_norm_bwd(LnArgs a) 
         if (a.dh) dh.add(d);
         load(row + groups);
         // mean(c n) = r (mean(c (h - m)) - (mean - m) mean(c)) for a mean m that is nearly right
-        if constexpr (!KEEP) ln_weights<V, LANES, NV>(w, a.D, lane, 1.0f, wv);
         float one[2] = {}, two[3] = {}, more;
 #pragma unroll
         for (int j = 0; j < NV; ++j)

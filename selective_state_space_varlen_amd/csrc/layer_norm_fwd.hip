@@ -8,7 +8,6 @@ namespace ssmp {
 template <typename T, int V, int LANES, int NV, bool DROP>
 __global__ __launch_bounds__(ln_threads(LANES)) void k_layer_norm_fwd(LnArgs a) {
     constexpr int SG = ln_threads(LANES) / LANES;
-    constexpr bool KEEP = NV * V <= 16;  // weights in registers
     __shared__ float lds[2][3][kLnWaves];
     const int lane = threadIdx.x % LANES;
     const int64_t group = (int64_t)blockIdx.x * SG + threadIdx.x / LANES, groups = (int64_t)gridDim.x * SG;
@@ -16,10 +15,8 @@ __global__ __launch_bounds__(ln_threads(LANES)) void k_layer_norm_fwd(LnArgs a) 
     const float* const w = a.w ? a.w + (size_t)head * a.D : nullptr;
     const float* const b = a.b ? a.b + (size_t)head * a.D : nullptr;
     float wv[NV][V], bv[NV][V];
-    if constexpr (KEEP) {
-        ln_weights<V, LANES, NV>(w, a.D, lane, 1.0f, wv);
-        ln_weights<V, LANES, NV>(b, a.D, lane, 0.0f, bv);
-    }
+    ln_weights<V, LANES, NV>(w, a.D, lane, 1.0f, wv);
+    ln_weights<V, LANES, NV>(b, a.D, lane, 0.0f, bv);
     LnRow<T, V, LANES, NV> x, res;
     int turn = 0;
     const auto load = [&](int64_t row) {
@@ -54,10 +51,6 @@ __global__ __launch_bounds__(ln_threads(LANES)) void k_layer_norm_fwd(LnArgs a) 
         row_sums<LANES>(two, lds[turn] + 1);
         const float r = ln_root(a, two[0], two[1], more);
         turn ^= 1;
-        if constexpr (!KEEP) {
-            ln_weights<V, LANES, NV>(w, a.D, lane, 1.0f, wv);
-            ln_weights<V, LANES, NV>(b, a.D, lane, 0.0f, bv);
-        }
 #pragma unroll
         for (int j = 0; j < NV; ++j)
 #pragma unroll
