@@ -615,7 +615,8 @@ int decay_attn_pack_step(const void *q, const void *k, const void *v, const floa
  * 16384; rows of a multiple of 8 components are read in wide pieces. Activation
  * pointers must be multiples of 16 bytes. A row of equal components with
  * eps = 0 gives NaN, as the formula does. Sums are formed in 32 bits: a row
- * whose squares pass their range (components near 1e19) gives zeros.
+ * whose squares pass their range (components near 1e19) counts as one of zeros,
+ * y = b with dL/dh alone handed on, and one whose sum does (near 3e38 / D) gives NaN.
  * Errors: SSMP_ERR_SHAPE (also H > 65536, T >= 2^31, 2^40 elements or more, p
  * as dropout_pack_fwd; with dw or db H * ceil(D / 16) >= 2^22, for which the
  * size query returns 0), SSMP_ERR_UNSUPPORTED, SSMP_ERR_NULL, SSMP_ERR_ALIGN,
