@@ -44,7 +44,7 @@ inline int decay_col_blocks(int32_t Dc) { return (Dc + kDecayCols - 1) / kDecayC
 // sequences are walked whole, as the first walk costs a third of the forward;
 // a longest segment bounds what one long sequence among them takes. 16384
 // tokens in 6 sequences x 24 heads of 128 x 64, segments of 768, 512, 384 and
-// 256 tokens: forward 164, 133, 143 and 139 us, backward 711, 583, 633 and 609.
+// 256 tokens: forward 177, 144, 158 and 153 us, backward 725, 583, 646 and 618.
 inline int32_t decay_segment(int64_t T, int32_t nseq, int64_t work) {
     if (nseq * work >= kSegWork) return kSegMax;
     const int64_t n = T * work / kSegWork / kSegMin * kSegMin;
@@ -295,11 +295,12 @@ struct DecayTiles {
 // The next chunk's rows are under way in registers meanwhile, those of a in
 // the first half of a chunk and those of b and c in the second, so that two
 // workgroups share a CU. DOTS: rows of out times rows of q or k, for dg.
-// What bounds it: 32768 tokens x 32 heads of 128 x 128 in bf16 take 290 us
-// forward, 220 at a copy's rate; copies of the walk that only load and store
-// take 253, that only compute 262, and eight waves a workgroup of 16 columns
-// each no less. dq 385 to 460, dk 430 to 505, dv 265 to 320 (what a launch takes
-// falls as the clock does under load).
+// What bounds it: 32768 tokens x 32 heads of 128 x 128 in bf16 take 296 to 325
+// us forward, 220 at a copy's rate; copies of the walk that only compute take
+// 292 to 303, that only load and store 252. With 16 key heads 296 to 311, 284 to
+// 292 and 187 (164 at a copy's rate): its arithmetic bounds it. (Eight waves a
+// workgroup of 16 columns each took no less.) In training dq 390 to 455, dk 440
+// to 510, dv 305 to 365 (a launch takes longer as the clock falls under load).
 // HEADS = 2 (dq, dk): both value heads of a key head in a workgroup of eight
 // waves, which add up what they have formed, so that there are no parts: each
 // four waves hand those rows to the others that the others store.
@@ -795,8 +796,8 @@ __global__ __launch_bounds__(512, 2) void k_decay_heads(DecayArgs p) {
 // Two walks that do not wait for each other in one launch, the first in the
 // first `blocks` workgroups, where all of them have a CU of their own: small
 // ones then run beside each other. (Compiled together they need more registers
-// than two workgroups a CU have: with spills, 32768 tokens x 32 heads take 920
-// us for dk and dv, 770 one after the other.)
+// than two workgroups a CU have: a backward of 32768 tokens x 32 heads of 128 x
+// 128 takes 1487 us with dk and dv in one launch, 1306 one after the other.)
 constexpr int kPairBlocks = 512;  // half of them, or more, without a segment
 template <typename T, int KIND, int DBP, int CT, bool DOTS, int KIND2, int DBP2, int CT2>
 __global__ __launch_bounds__(256, 1) void k_decay_pair(DecayArgs p, uint32_t blocks) {
@@ -929,7 +930,7 @@ int launch_decay_pair(const DecayArgs& a, int32_t dtype, hipStream_t s) {
 }
 // Up to so many states between segments are added up by the walks themselves,
 // each reading those on its way: a prompt of 513 tokens x 32 heads of 128 x 128
-// in 5 segments takes 36 us with a join between the walks and 30.5 without.
+// in 5 segments takes 38 us with a join between the walks and 29 without.
 constexpr int kFewStates = 5;
 inline int launch_decay_join(const DecayArgs& a, int ways, hipStream_t s) {
     if (a.few) return SSMP_OK;
@@ -943,11 +944,15 @@ inline int launch_decay_join(const DecayArgs& a, int ways, hipStream_t s) {
 // Both value heads of a key head in a workgroup, where there are two, and more
 // workgroups than the card has at a time: no parts are written and added up,
 // while eight waves in step take about a fifth longer. Backward, in us, with
-// one head a workgroup and with two:
+// one head a workgroup and with two; above the rule's border
 //   tokens, sequences    2048, 8   4096, 8   8192, 8   32768, 35
-//   32 heads 128 x 128   189, 185  344, 320  537, 508  1505, 1365
-//   others: 16384, 1, 16 of 128 x 64: 397, 318; 8192, 8, 32 of 64 x 64: 250,
-//   257; 32768, 29, 32 of 64 x 64: 790, 778; 8192, 8, 8 of 128 x 128: 206, 215
+//   32 heads 128 x 128   174, 161  333, 297  519, 467  1560, 1420
+//   others: 16384, 1, 16 of 128 x 64: 403, 326; 8192, 8, 32 of 64 x 64: 245,
+//   228; 32768, 29, 32 of 64 x 64: 795, 770; 8192, 8, 8 of 128 x 128: 184, 174
+// and below it
+//   513, 1, 32 of 128 x 128: 91, 125; 1024, 2, 16 of 128 x 128: 86, 114; 1024, 1,
+//   8 of 128 x 64: 68, 86; 1237, 12, 8 of 64 x 64: 51, 64; 600, 20, 8 of 128 x
+//   128: 50, 53
 // (Two of 24 heads, which halves the parts: 16384, 8, of 128 x 64: 568, 551;
 // 4096: 191, 198; 32768: 995, 1013. fp32 walks have no room for it.)
 inline int decay_heads_of(const DecayArgs& a, int32_t dtype) {
