@@ -303,7 +303,8 @@ struct DecayTiles {
 // to 510, dv 305 to 365 (a launch takes longer as the clock falls under load).
 // HEADS = 2 (dq, dk): both value heads of a key head in a workgroup of eight
 // waves, which add up what they have formed, so that there are no parts: each
-// four waves hand those rows to the others that the others store.
+// four waves hand those rows to the others that the others store. (dk of 128 x
+// 128 with dg spills 4 registers a lane in this form, none in the other.)
 template <typename T, int KIND, int DBP, int CT, bool DOTS, int HEADS = 1>
 __device__ __forceinline__ void decay_walk(const DecayArgs& p, int64_t block,
                                            DecayTiles<T, DBP, CT>* tiles) {

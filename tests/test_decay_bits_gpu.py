@@ -4,7 +4,8 @@ bits. Short sequences, where 32-bit sums err least and a part left out shows
 most: 2^-14 of a term moves 5 results in 1000 to their neighbours. The count
 of results that may lie beside the nearest value is that of the delta rule's test
 (`off`), whose errors are of the same kind: a state's product, decayed products
-and 32-bit roundings of each."""
+and 32-bit roundings of each. (What tests/decay_checks.py allows for two cut
+parts, `tol_parts`, is more than any result needs.)"""
 from __future__ import annotations
 
 import pytest
